@@ -1,0 +1,287 @@
+"""Row operators on the GPU against their 64-bit definitions: mxfp8_quantize
+(every code and scale equal), rmsnorm, rmsnorm_mxfp8 and rmsnorm_backward
+(within bounds derived from the roundings: tests/opsref.py), over all row
+types, single elements to rows past the register kernels, strides, rows that
+start at any element, in-place calls, and rows of zeros, infinities and NaN."""
+import numpy as np
+import pytest
+import torch
+
+import opsref as ref
+import tiled_dense_gemm_tile_amd as tg
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "f32": torch.float32}
+EPS = 1e-5
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def u8(t):
+    return t.contiguous().view(torch.uint8).cpu().numpy()
+
+
+def rows_of(seed, rows, n, kind, pad=0, off=0, scale=1.0):
+    """A (rows, n) device tensor of the type, `pad` elements between rows and
+    the first element `off` elements into its storage, with a few large
+    columns; the storage is returned with it."""
+    rng = np.random.default_rng(seed)
+    ld = n + pad
+    store = rng.standard_normal(off + rows * ld + 8) * scale
+    store[::37] *= 20
+    s = torch.from_numpy(store.astype(np.float32)).to(DEV).to(TYPES[kind])
+    return s[off:off + rows * ld].view(rows, ld)[:, :n]
+
+
+QUANT = [(1, 32, 0, 0), (3, 64, 0, 0), (7, 96, 5, 3), (257, 160, 0, 1), (33, 4096, 32, 0), (5, 14336, 0, 0),
+         (1000, 32, 1, 0)]
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("case", QUANT, ids=str)
+def test_quantize(case, kind):
+    rows, n, pad, off = case
+    x = rows_of(1, rows, n, kind, pad, off)
+    x[0, :32] = 0                                      # a block of zeros
+    if rows > 2:
+        x[2] *= 2.0 ** -13
+    q, sf = tg.mxfp8_quantize(x)
+    want, code = ref.quantize(f64(x))
+    assert np.array_equal(u8(sf), code)
+    assert np.array_equal(ref.e4m3(u8(q)), want)
+
+
+def test_quantize_borders():
+    """Block maxima at 448 * 2^e and one step to either side; elements halfway
+    between codes; the smallest and largest numbers."""
+    top = np.array([448.0, np.nextafter(np.float32(448), np.float32(0)), np.nextafter(np.float32(448), np.float32(1e9)),
+                    256.0, 1.0, 1.75, 1.7500001, 2.0 ** -118, 2.0 ** -126, 2.0 ** -149, 3.4e38, 2.0 ** 127], np.float32)
+    x = np.zeros((top.size, 32), np.float32)
+    x[:, 0] = top
+    for i in range(1, 31):                             # ties between neighbouring codes, of every binade
+        x[:, i] = -top / 2 ** (i % 20) * np.float32((17 + 2 * (i % 8)) / 32)
+    q, sf = tg.mxfp8_quantize(torch.from_numpy(x).to(DEV))
+    want, code = ref.quantize(x.astype(np.float64))
+    assert np.array_equal(u8(sf), code)
+    assert np.array_equal(ref.e4m3(u8(q)), want)
+    assert np.nanmax(np.abs(want)) <= 448
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_quantize_nonfinite(kind):
+    x = rows_of(2, 6, 96, kind)
+    x[0, 5], x[1, 40], x[2, 70] = float("nan"), float("inf"), float("-inf")
+    x[3, 32:64] = float("nan")
+    q, sf = tg.mxfp8_quantize(x)
+    want, code = ref.quantize(f64(x))
+    assert np.array_equal(u8(sf), code)
+    assert np.array_equal(ref.e4m3(u8(q)), want, equal_nan=True)
+    assert np.isnan(want).sum() == 35
+
+
+def test_quantize_leaves_padding():
+    x = rows_of(3, 40, 64, "bf16")
+    qs = torch.full((41, 80), 0x5A, dtype=torch.uint8, device=DEV)
+    ss = torch.full((41, 5), 0x5A, dtype=torch.uint8, device=DEV)
+    tg.mxfp8_quantize(x, Q=qs[:40, 3:67], SF=ss[:40, 1:3])
+    want, code = ref.quantize(f64(x))
+    q, s = u8(qs), u8(ss)
+    assert np.array_equal(ref.e4m3(q[:40, 3:67]), want) and np.array_equal(s[:40, 1:3], code)
+    q[:40, 3:67], s[:40, 1:3] = 0x5A, 0x5A
+    assert (q == 0x5A).all() and (s == 0x5A).all()
+
+
+def test_quantize_empty():
+    for shape in ((0, 64), (5, 0)):
+        q, sf = tg.mxfp8_quantize(torch.zeros(shape, dtype=torch.bfloat16, device=DEV))
+        assert q.shape == shape and sf.shape == (shape[0], shape[1] // 32)
+
+
+# (rows, n, pad, offset): a wave per row, a workgroup per row, the long kernel
+NORM = [(1, 1, 0, 0), (3, 7, 2, 1), (5, 32, 0, 0), (2, 257, 0, 3), (9, 1000, 0, 0), (1, 4096, 0, 0), (1030, 96, 0, 1),
+        (1027, 4096, 8, 0), (1025, 1001, 0, 0), (4, 8193, 1, 0), (3, 14336, 0, 5), (2, 16384, 0, 0), (2, 32768, 0, 0),
+        (2, 40001, 0, 1)]
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("case", NORM, ids=str)
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm(case, kind, residual):
+    rows, n, pad, off = case
+    x = rows_of(4, rows, n, kind, pad, off)
+    r = rows_of(5, rows, n, kind, 0, off) if residual else None
+    w = rows_of(6, 1, n, kind if n % 3 else "f32")[0].contiguous()
+    y, h, rstd = tg.rmsnorm(x, w, EPS, residual=r)
+    hv = f64(h)
+    if residual:
+        # the sum is formed in fp32 and rounded again: half a step, and fp32's
+        s = f64(x) + f64(r)
+        assert (np.abs(hv - s) <= (ref.HALF[kind] + (ref.U if kind != "f32" else 0)) * np.abs(s) + ref.TINY[kind]).all()
+    else:
+        assert h is x
+    want, rs = ref.norm(hv, f64(w), EPS)
+    assert (np.abs(f64(rstd) - rs) <= ref.rstd_bound(n) * rs).all()
+    # (h w) rstd: two roundings beside rstd's error, then the output's
+    bound = (ref.rstd_bound(n) + 2 * ref.U) * np.abs(want) + 2.0 ** -148
+    assert (np.abs(f64(y) - want) <= bound + ref.HALF[kind] * (np.abs(want) + bound) + ref.TINY[kind]).all()
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("case", [(1, 32, 0, 0), (3, 96, 1, 1), (7, 1024, 0, 0), (1025, 416, 0, 3), (1026, 4096, 0, 0),
+                                  (2, 8224, 0, 0), (3, 16384, 32, 0), (2, 40032, 0, 1)], ids=str)
+def test_norm_mxfp8(case, kind):
+    rows, n, pad, off = case
+    x, r = rows_of(7, rows, n, kind, pad, off), rows_of(8, rows, n, kind)
+    w = rows_of(9, 1, n, kind)[0].contiguous()
+    q, sf, h, rstd = tg.rmsnorm_mxfp8(x, w, EPS, residual=r)
+    y16, h16, rstd16 = tg.rmsnorm(x, w, EPS, residual=r)
+    assert torch.equal(h, h16) and torch.equal(rstd, rstd16)
+    want, rs = ref.norm(f64(h), f64(w), EPS)
+    assert (np.abs(f64(rstd) - rs) <= ref.rstd_bound(n) * rs).all()
+    d = (ref.rstd_bound(n) + 2 * ref.U) * np.abs(want)
+    e = u8(sf).astype(np.int64) - 127
+    amax, slack = np.abs(want).reshape(rows, -1, 32).max(axis=2), d.reshape(rows, -1, 32).max(axis=2)
+    # the least scale that clips nothing, of a maximum known to within `slack`
+    assert (amax - slack <= 448 * np.ldexp(1.0, e)).all()
+    assert ((amax + slack > 448 * np.ldexp(1.0, e - 1)) | (e == -127)).all()
+    # half a step of e4m3: 2^-4 of the value, or 2^-10 of the scale below its normal range
+    step = np.maximum(2.0 ** -4 * (np.abs(want) + d), np.repeat(np.ldexp(1.0, e - 10), 32, axis=1))
+    assert (np.abs(ref.dequant(u8(q), u8(sf)) - want) <= step + d).all()
+
+
+@pytest.mark.parametrize("where", ["x", "r", "y_over_x", "y_over_r"])
+@pytest.mark.parametrize("n", [96, 8192, 40000])
+def test_norm_in_place(where, n):
+    x, r = rows_of(10, 5, n, "bf16"), rows_of(11, 5, n, "bf16")
+    w = rows_of(12, 1, n, "bf16")[0].contiguous()
+    y0, h0, s0 = tg.rmsnorm(x, w, EPS, residual=r)
+    a, b = x.clone(), r.clone()
+    kw = {"x": dict(H=a), "r": dict(H=b), "y_over_x": dict(Y=a), "y_over_r": dict(Y=b)}[where]
+    y, h, s = tg.rmsnorm(a, w, EPS, residual=b, **kw)
+    assert torch.equal(y, y0) and torch.equal(h, h0) and torch.equal(s, s0)
+    assert (h if "H" in kw else y).data_ptr() == next(iter(kw.values())).data_ptr()
+
+
+def test_norm_special_rows():
+    x = rows_of(13, 6, 256, "f32")
+    x[0] = 0
+    x[1, 3] = float("nan")
+    x[2, 9] = float("inf")
+    w = torch.ones(256, device=DEV)
+    y, _, rstd = tg.rmsnorm(x, w, EPS)
+    assert (y[0] == 0).all() and abs(rstd[0].item() - EPS ** -0.5) < 1e-4 * EPS ** -0.5
+    assert torch.isnan(y[1]).all() and torch.isnan(y[2, 9])
+    want, _ = ref.norm(f64(x[3:]), np.ones(256), EPS)
+    assert np.abs(f64(y[3:]) - want).max() < 1e-5      # the other rows do not notice
+    q, sf, _, _ = tg.rmsnorm_mxfp8(x, w, EPS)
+    v = ref.e4m3(u8(q))
+    assert (v[0] == 0).all() and (u8(sf)[0] == 0).all()
+    assert np.isnan(v[1]).all() and np.isnan(v[2, 9]) and np.isfinite(v[3:]).all()
+
+
+def test_norm_leaves_padding():
+    x = rows_of(14, 9, 100, "bf16")
+    w = torch.ones(100, dtype=torch.bfloat16, device=DEV)
+    big = torch.full((10, 111), 3.5, dtype=torch.bfloat16, device=DEV)
+    hs = torch.full((10, 107), 4.5, dtype=torch.bfloat16, device=DEV)
+    y0, h0, _ = tg.rmsnorm(x, w, EPS, residual=x)
+    tg.rmsnorm(x, w, EPS, residual=x, Y=big[:9, 5:105], H=hs[:9, 1:101])
+    assert torch.equal(big[:9, 5:105], y0) and torch.equal(hs[:9, 1:101], h0)
+    big[:9, 5:105], hs[:9, 1:101] = 3.5, 4.5
+    assert (big == 3.5).all() and (hs == 4.5).all()
+
+
+BWD = [(1, 1, 0, 0), (3, 7, 2, 1), (5, 1000, 0, 0), (1500, 100, 0, 1), (2049, 2048, 0, 0), (1100, 4100, 4, 0),
+       (40, 8192, 0, 0), (9, 14336, 0, 3), (5, 16384, 0, 0), (70, 20001, 0, 1)]
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("case", BWD, ids=str)
+@pytest.mark.parametrize("extra", [False, True])
+def test_norm_backward(case, kind, extra):
+    rows, n, pad, off = case
+    h, dy = rows_of(20, rows, n, kind, pad, off), rows_of(21, rows, n, kind, 0, off, 0.1)
+    dh = rows_of(22, rows, n, kind, 3, 0, 0.1) if extra else None
+    w = rows_of(23, 1, n, kind if n % 3 else "f32")[0].contiguous()
+    rstd = torch.from_numpy((1 / np.sqrt((f64(h) ** 2).mean(1) + EPS)).astype(np.float32)).to(DEV)
+    dx, dw = tg.rmsnorm_backward(dy, h, w, rstd, dH=dh)
+    want, wdw, ag, au, adw = ref.norm_backward(f64(dy), f64(h), f64(w), f64(rstd), 0.0 if dh is None else f64(dh))
+    # g: a rounding; u = h rstd: one; the row's sum: its chain of n / 64 + 32,
+    # its terms' three roundings, the mean's division; u m, g - u m, the last
+    # product and sum: one each of at most their terms
+    bound = 4 * ref.U * ag + (n / 64 + 32 + 9) * ref.U * au + 2 * ref.U * np.abs(want)
+    assert (np.abs(f64(dx) - want) <= bound + ref.HALF[kind] * (np.abs(want) + bound) + ref.TINY[kind]).all()
+    # a column's chain: a group's rows (at least 64 groups, or a group a row),
+    # 32 partial sums a lane and 32 lanes; two roundings a term
+    assert (np.abs(f64(dw) - wdw) <= (rows / 64 + 1 + 64 + 2) * ref.U * adw).all()
+    dx2, none = tg.rmsnorm_backward(dy, h, w, rstd, dH=dh, weight_grad=False)
+    assert none is None and torch.equal(dx, dx2)
+
+
+@pytest.mark.parametrize("n", [96, 8192, 20000])
+def test_norm_backward_in_place(n):
+    h, dy, dh = (rows_of(s, 70, n, "bf16") for s in (24, 25, 26))
+    w = rows_of(27, 1, n, "bf16")[0].contiguous()
+    rstd = torch.rsqrt(h.float().square().mean(1) + EPS)
+    dx0, dw0 = tg.rmsnorm_backward(dy, h, w, rstd, dH=dh)
+    for over in ("dy", "dh"):
+        a, b = dy.clone(), dh.clone()
+        t = a if over == "dy" else b
+        dx, dw = tg.rmsnorm_backward(a, h, w, rstd, dH=b, dX=t)
+        assert dx.data_ptr() == t.data_ptr() and torch.equal(dx, dx0) and torch.equal(dw, dw0)
+
+
+def test_norm_backward_no_rows():
+    e = torch.zeros(0, 48, device=DEV)
+    dx, dw = tg.rmsnorm_backward(e, e, torch.ones(48, device=DEV), torch.zeros(0, device=DEV),
+                                 dW=torch.full((48,), 7.0, device=DEV))
+    assert dx.shape == (0, 48) and (dw == 0).all()
+
+
+def test_norm_backward_leaves_what_lies_behind():
+    h = rows_of(28, 300, 100, "bf16")
+    w = torch.ones(100, dtype=torch.bfloat16, device=DEV)
+    rstd = torch.ones(300, device=DEV)
+    need = tg.rmsnorm_backward_workspace_bytes(300, 100)
+    ws = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device=DEV)
+    dw, dx = torch.full((130,), 9.0, device=DEV), torch.full((301, 107), 4.5, dtype=torch.bfloat16, device=DEV)
+    tg.rmsnorm_backward(h, h, w, rstd, dX=dx[:300, 2:102], dW=dw[:100], workspace=ws[:need])
+    assert (ws[need:] == 0x5A).all() and (dw[100:] == 9).all()
+    dx[:300, 2:102] = 4.5
+    assert (dx == 4.5).all()
+
+
+def test_norm_gradient_against_differences():
+    """dx and dw along random directions against central differences of the
+    64-bit forward form.  With steps of 1e-4 of unit-variance rows the
+    difference's own error is of the order of 1e-8 of the loss's third
+    derivative; fp32's is (n / 64 + 41) u of the sums' magnitudes, under
+    1e-5 of |dy| |direction| here."""
+    rng = np.random.default_rng(30)
+    h, dy, w = rng.standard_normal((6, 640)), rng.standard_normal((6, 640)), 1 + 0.1 * rng.standard_normal(640)
+    h, dy, w = (a.astype(np.float32).astype(np.float64) for a in (h, dy, w))
+    d = [torch.from_numpy(a.astype(np.float32)).to(DEV) for a in (h, dy, w)]
+    _, _, rstd = tg.rmsnorm(d[0], d[2], EPS)
+    dx, dw = tg.rmsnorm_backward(d[1], d[0], d[2], rstd)
+    for seed in range(4):
+        r = np.random.default_rng(seed)
+        vh, vw = r.standard_normal(h.shape), r.standard_normal(w.shape)
+        for a, b, got in ((vh, 0 * vw, (f64(dx) * vh).sum()), (0 * vh, vw, (f64(dw) * vw).sum())):
+            loss = lambda t: (ref.norm(h + t * a, w + t * b, EPS)[0] * dy).sum()  # noqa: E731
+            num = (loss(1e-4) - loss(-1e-4)) / 2e-4
+            assert abs(got - num) <= 1e-5 * np.linalg.norm(dy) * max(np.linalg.norm(a), np.linalg.norm(b) * np.sqrt(6))
+
+
+def test_same_bits_every_call():
+    h, dy = rows_of(31, 3000, 1000, "bf16"), rows_of(32, 3000, 1000, "bf16")
+    w = rows_of(33, 1, 1000, "bf16")[0].contiguous()
+    y, _, rstd = tg.rmsnorm(h, w, EPS)
+    first = tg.rmsnorm_backward(dy, h, w, rstd)
+    for _ in range(3):
+        again = tg.rmsnorm_backward(dy, h, w, rstd)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+        assert torch.equal(y, tg.rmsnorm(h, w, EPS)[0])

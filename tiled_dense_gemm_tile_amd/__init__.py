@@ -12,6 +12,11 @@ Tensor conventions (same as the C ABI):
   (last stride 1) or MN-contiguous (first stride 1, e.g. ``X.t()`` of a
   contiguous K x M or K x N tensor); the binding passes the storage order to
   ``gemm_bf16_ex`` / ``gemm_fp16_ex`` when one is MN-contiguous.
+
+The operators around the block-scaled products (``include/tilegemm_ops.h``:
+``mxfp8_quantize``, ``rmsnorm``, ``rmsnorm_mxfp8``, ``rmsnorm_backward``,
+``gemm_wgrad_mxfp8``, ``gemv_mxfp4``) are bound in :mod:`.ops` and exported
+here.
 """
 from __future__ import annotations
 
@@ -21,7 +26,8 @@ import threading
 
 __all__ = ["gemm_bf16", "gemm_fp16", "gemm_bf16_splitk", "gemm_fp16_splitk", "splitk_workspace_bytes",
            "gemm_mxfp8", "gemm_mxfp4", "gemm_mxfp6", "gemm_mxfp8_splitk", "gemm_mxfp4_splitk", "gemm_mxfp6_splitk", "raw", "GemmError", "LibraryMissing",
-           "library_path", "STATUS"]
+           "library_path", "STATUS", "mxfp8_quantize", "rmsnorm", "rmsnorm_mxfp8", "rmsnorm_backward",
+           "rmsnorm_backward_workspace_bytes", "gemm_wgrad_mxfp8", "gemm_wgrad_mxfp8_workspace_bytes", "gemv_mxfp4"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libtilegemm.so")
@@ -120,8 +126,28 @@ def _load():
             L.gemm_status_string.argtypes = [ci]
             L.gemm_last_hip_error.restype = ci
             L.gemm_last_hip_error.argtypes = []
+            _declare_ops(L)
             _lib = L
     return _lib
+
+
+def _declare_ops(L):
+    """Signatures of include/tilegemm_ops.h."""
+    i64, vp, ci, sz, f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+    norm = [i64, i64, vp, i64, vp, i64, ci, vp, ci, f32, vp, i64]
+    for name, args in (
+            ("mxfp8_quantize", [i64, i64, vp, i64, ci, vp, i64, vp, i64, vp]),
+            ("rmsnorm", norm + [vp, i64, vp, vp]),
+            ("rmsnorm_mxfp8", norm + [vp, i64, vp, i64, vp, vp]),
+            ("rmsnorm_backward", [i64, i64, vp, i64, vp, i64, ci, vp, ci, vp, vp, i64, vp, i64, vp, vp, sz, vp]),
+            ("gemm_wgrad_mxfp8", [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, sz, vp]),
+            ("gemv_mxfp4", [i64, i64, i64, i64, vp, i64, ci, vp, i64, vp, i64, vp, i64, vp, i64, ci, vp])):
+        f = getattr(L, name)
+        f.restype, f.argtypes = ci, args
+    L.rmsnorm_backward_workspace_bytes.restype = sz
+    L.rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
+    L.gemm_wgrad_mxfp8_workspace_bytes.restype = sz
+    L.gemm_wgrad_mxfp8_workspace_bytes.argtypes = [i64, i64, i64]
 
 
 class _Raw:
@@ -655,3 +681,16 @@ def gemm_mxfp6_splitk(A, SFA, B, SFB, C=None, out_dtype=None, D=None, fmt="e2m3"
     groups (0: the library's choice); ``workspace`` as
     :func:`gemm_bf16_splitk`."""
     return _mx6("gemm_mxfp6_splitk", A, SFA, B, SFB, C, out_dtype, D, fmt, (splits, workspace))
+
+
+# The functions of ops.py, which needs torch at import, load with their first use.
+_OPS = ("mxfp8_quantize", "rmsnorm", "rmsnorm_mxfp8", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes",
+        "gemm_wgrad_mxfp8", "gemm_wgrad_mxfp8_workspace_bytes", "gemv_mxfp4")
+
+
+def __getattr__(name):
+    if name not in _OPS:
+        raise AttributeError("module %r has no attribute %r" % (__name__, name))
+    from . import ops
+    f = globals()[name] = getattr(ops, name)
+    return f

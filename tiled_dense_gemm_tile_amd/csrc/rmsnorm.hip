@@ -1,0 +1,300 @@
+// C ABI and kernels of the forward row operators: mxfp8_quantize, rmsnorm,
+// rmsnorm_mxfp8 (include/tilegemm_ops.h).
+//
+// One pass: a row's elements stay in registers between the sum of squares
+// and the output, so every element is read and written once and the bound is
+// the HBM rate.  Sums and products are fp32; h is rounded to the row type
+// before the sum because that stored h is what the backward pass and the next
+// layer read; y is formed as (h * w) * rstd -- for 16-bit h and w the first
+// product is exact -- and rounded once.
+#include <math.h>
+
+#include "rows.hpp"
+#include "rows_api.hpp"
+
+using namespace tg_api;
+
+namespace tg {
+
+struct NormArgs {
+    const void *X, *R, *W;
+    void *H, *Y;                                       // Y: the row type, or e4m3 codes
+    uint8_t *SF;
+    float *rstd;
+    int64_t ldx, ldr, ldh, ldy, ldsf;
+    int64_t rows;
+    int N;
+    float eps;
+    bool w_f32;
+};
+
+// TPR threads per row (64: a wave, four rows per workgroup; 256 or 1024: the
+// workgroup), VPT vectors of 16 bytes per thread: N <= TPR * VPT * VE.
+template <int T, bool MX, int TPR, int VPT>
+__global__ void __launch_bounds__(TPR == 64 ? 256 : TPR) rmsnorm_kernel(NormArgs p) {
+    typedef RowVec<T> RV;
+    constexpr int VE = RV::VE;
+    const int t = TPR == 64 ? threadIdx.x & 63 : threadIdx.x;
+    const int64_t row = TPR == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
+    if (TPR == 64 && row >= p.rows) return;
+    const int N = p.N;
+    const typename RV::S *x = (const typename RV::S *)p.X + row * p.ldx;
+    const typename RV::S *r = (const typename RV::S *)p.R + row * p.ldr;
+
+    typename RV::V h[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = (i * TPR + t) * VE;
+        h[i] = typename RV::V{};
+        if (c < N) h[i] = RV::load(x, c, N);
+    }
+    if (p.R) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (i * TPR + t) * VE;
+            if (c < N) {
+                const typename RV::V v = RV::load(r, c, N);
+#pragma unroll
+                for (int u = 0; u < VE; ++u)
+                    h[i][u] = Elem<T>::down(Elem<T>::up(h[i][u]) + Elem<T>::up(v[u]));
+            }
+        }
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        float s = 0.0f;
+#pragma unroll
+        for (int u = 0; u < VE; ++u) {
+            const float f = Elem<T>::up(h[i][u]);
+            s = fmaf(f, f, s);
+        }
+        ss += s;
+    }
+    ss = wave_sum(ss);
+    if constexpr (TPR > 64) {
+        __shared__ float part[TPR / 64];
+        if ((t & 63) == 0) part[t >> 6] = ss;
+        __syncthreads();
+        ss = 0.0f;
+#pragma unroll
+        for (int w = 0; w < TPR / 64; ++w) ss += part[w];
+    }
+    const float rstd = 1.0f / sqrtf(ss / (float)N + p.eps);
+    if (p.rstd && t == 0) p.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = (i * TPR + t) * VE;
+        if (c < N) {
+            if (p.H) RV::store((typename RV::S *)p.H + row * p.ldh, c, N, h[i]);
+            float w[VE], y[VE];
+            load_weights<T>(p.W, p.w_f32, c, N, w);
+#pragma unroll
+            for (int u = 0; u < VE; ++u) y[u] = Elem<T>::up(h[i][u]) * w[u] * rstd;
+            if constexpr (MX) {
+                mx_store<VE>(y, (uint8_t *)p.Y + row * p.ldy, p.SF + row * p.ldsf, c);
+            } else {
+                typename RV::V o;
+#pragma unroll
+                for (int u = 0; u < VE; ++u) o[u] = Elem<T>::down(y[u]);
+                RV::store((typename RV::S *)p.Y + row * p.ldy, c, N, o);
+            }
+        }
+    }
+}
+
+// Rows too long for the registers of one workgroup: two passes, the second
+// reading the row again (h from H where it was written, else x + r again).
+template <int T, bool MX>
+__global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs p) {
+    typedef RowVec<T> RV;
+    constexpr int VE = RV::VE;
+    const int64_t row = blockIdx.x;
+    const int N = p.N, t = threadIdx.x;
+    const typename RV::S *x = (const typename RV::S *)p.X + row * p.ldx;
+    const typename RV::S *r = (const typename RV::S *)p.R + row * p.ldr;
+    typename RV::S *hs = (typename RV::S *)p.H + row * p.ldh;
+    auto sum_at = [&](int64_t c) __attribute__((always_inline)) {
+        typename RV::V h = RV::load(x, (int)c, N);
+        if (p.R) {
+            const typename RV::V v = RV::load(r, (int)c, N);
+#pragma unroll
+            for (int u = 0; u < VE; ++u) h[u] = Elem<T>::down(Elem<T>::up(h[u]) + Elem<T>::up(v[u]));
+        }
+        return h;
+    };
+    float ss = 0.0f;
+    for (int64_t c = (int64_t)t * VE; c < N; c += 1024 * VE) {
+        const typename RV::V h = sum_at(c);
+        float s = 0.0f;
+#pragma unroll
+        for (int u = 0; u < VE; ++u) {
+            const float f = Elem<T>::up(h[u]);
+            s = fmaf(f, f, s);
+        }
+        ss += s;
+        if (p.H) RV::store(hs, (int)c, N, h);
+    }
+    __shared__ float part[16];
+    ss = wave_sum(ss);
+    if ((t & 63) == 0) part[t >> 6] = ss;
+    __syncthreads();
+    ss = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) ss += part[w];
+    const float rstd = 1.0f / sqrtf(ss / (float)N + p.eps);
+    if (p.rstd && t == 0) p.rstd[row] = rstd;
+    for (int64_t c = (int64_t)t * VE; c < N; c += 1024 * VE) {
+        const typename RV::V h = p.H ? RV::load(hs, (int)c, N) : sum_at(c);   // this thread's own stores
+        float w[VE], y[VE];
+        load_weights<T>(p.W, p.w_f32, (int)c, N, w);
+#pragma unroll
+        for (int u = 0; u < VE; ++u) y[u] = Elem<T>::up(h[u]) * w[u] * rstd;
+        if constexpr (MX) {
+            mx_store<VE>(y, (uint8_t *)p.Y + row * p.ldy, p.SF + row * p.ldsf, (int)c);
+        } else {
+            typename RV::V o;
+#pragma unroll
+            for (int u = 0; u < VE; ++u) o[u] = Elem<T>::down(y[u]);
+            RV::store((typename RV::S *)p.Y + row * p.ldy, (int)c, N, o);
+        }
+    }
+}
+
+// One vector of one row per thread and step; blocks of 32 elements are
+// independent, so rows need no workgroup of their own.
+template <int T>
+__global__ void __launch_bounds__(256)
+    quantize_kernel(const void *X, int64_t ldx, uint8_t *Q, int64_t ldq, uint8_t *SF, int64_t ldsf, int64_t rows,
+                    int nvec) {
+    typedef RowVec<T> RV;
+    constexpr int VE = RV::VE;
+    const int64_t total = rows * nvec;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / nvec;
+        const int c = (int)(i - row * nvec) * VE;
+        const typename RV::V v = RV::load((const typename RV::S *)X + row * ldx, c, c + VE);
+        float y[VE];
+#pragma unroll
+        for (int u = 0; u < VE; ++u) y[u] = Elem<T>::up(v[u]);
+        mx_store<VE>(y, Q + row * ldq, SF + row * ldsf, c);
+    }
+}
+
+template <int T, bool MX, int TPR, int VPT>
+hipError_t go(const NormArgs &p, hipStream_t s) {
+    const int64_t grid = TPR == 64 ? (p.rows + 3) / 4 : p.rows;
+    hipLaunchKernelGGL((rmsnorm_kernel<T, MX, TPR, VPT>), dim3((unsigned)grid), dim3(TPR == 64 ? 256 : TPR), 0, s, p);
+    return hipGetLastError();
+}
+
+template <int T, bool MX>
+hipError_t launch_norm(const NormArgs &p, hipStream_t s) {
+    const int nvec = (int)(((int64_t)p.N + kVE<T> - 1) / kVE<T>);
+    // A wave per row needs no barrier, but leaves a short batch of rows with
+    // too few loads in flight: below 1024 rows a workgroup takes each.
+    if (nvec <= 64 || (p.rows >= 1024 && nvec <= 512)) {
+        if (nvec <= 64) return go<T, MX, 64, 1>(p, s);
+        if (nvec <= 128) return go<T, MX, 64, 2>(p, s);
+        if (nvec <= 256) return go<T, MX, 64, 4>(p, s);
+        return go<T, MX, 64, 8>(p, s);
+    }
+    if (nvec <= 256) return go<T, MX, 256, 1>(p, s);
+    if (nvec <= 512) return go<T, MX, 256, 2>(p, s);
+    if (nvec <= 1024) return go<T, MX, 256, 4>(p, s);
+    if (nvec <= 2048) return go<T, MX, 256, 8>(p, s);
+    if (nvec <= 4096) return go<T, MX, 1024, 4>(p, s);
+    hipLaunchKernelGGL((rmsnorm_long_kernel<T, MX>), dim3((unsigned)p.rows), dim3(1024), 0, s, p);
+    return hipGetLastError();
+}
+
+}  // namespace tg
+
+namespace {
+
+gemm_status run_norm(bool mx, int64_t rows, int64_t N, const void *X, int64_t ldx, const void *R, int64_t ldr,
+                     int type, const void *W, int w_type, float eps, void *H, int64_t ldh, void *Y, int64_t ldy,
+                     void *SF, int64_t ldsf, float *rstd, hipStream_t s) {
+    bool none;
+    gemm_status st = check_rows(rows, N, &none);
+    if (st != GEMM_OK) return st;
+    if (!elem_type(type) || (w_type != type && w_type != GEMM_TYPE_F32)) return GEMM_ERR_UNSUPPORTED;
+    if (!(eps >= 0.0f) || !isfinite(eps) || (mx && N % 32 != 0)) return GEMM_ERR_UNSUPPORTED;
+    if (none) return GEMM_OK;
+    if (ldx < N || (R && ldr < N) || (H && ldh < N) || ldy < N || (mx && ldsf < N / 32)) return GEMM_ERR_BAD_LD;
+    if (!X || !W || !Y || (mx && !SF)) return GEMM_ERR_NULL_POINTER;
+    const int es = elem_size(type);
+    if (misaligned(X, es) || misaligned(R, es) || misaligned(H, es) || misaligned(Y, mx ? 1 : es) ||
+        misaligned(W, elem_size(w_type)) || misaligned(rstd, 4))
+        return GEMM_ERR_MISALIGNED;
+    if ((H && H == Y) || (H == X && ldh != ldx) || (H && H == R && ldh != ldr)) return GEMM_ERR_UNSUPPORTED;
+    if ((Y == X && ldy != ldx) || (Y == R && ldy != ldr) || (mx && (Y == X || Y == R))) return GEMM_ERR_UNSUPPORTED;
+    tg::NormArgs p;
+    p.X = X;
+    p.R = R;
+    p.W = W;
+    p.H = H;
+    p.Y = Y;
+    p.SF = (uint8_t *)SF;
+    p.rstd = rstd;
+    p.ldx = ldx;
+    p.ldr = ldr;
+    p.ldh = ldh;
+    p.ldy = ldy;
+    p.ldsf = ldsf;
+    p.rows = rows;
+    p.N = (int)N;
+    p.eps = eps;
+    p.w_f32 = w_type == GEMM_TYPE_F32;
+    hipError_t e;
+    switch (type) {
+    case GEMM_TYPE_F32: e = mx ? tg::launch_norm<0, true>(p, s) : tg::launch_norm<0, false>(p, s); break;
+    case GEMM_TYPE_BF16: e = mx ? tg::launch_norm<1, true>(p, s) : tg::launch_norm<1, false>(p, s); break;
+    default: e = mx ? tg::launch_norm<2, true>(p, s) : tg::launch_norm<2, false>(p, s); break;
+    }
+    return launched(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status rmsnorm(int64_t rows, int64_t N, const void *X, int64_t ldx, const void *R, int64_t ldr, int type,
+                    const void *W, int w_type, float eps, void *H, int64_t ldh, void *Y, int64_t ldy, float *rstd,
+                    hipStream_t stream) {
+    return run_norm(false, rows, N, X, ldx, R, ldr, type, W, w_type, eps, H, ldh, Y, ldy, nullptr, 0, rstd, stream);
+}
+
+gemm_status rmsnorm_mxfp8(int64_t rows, int64_t N, const void *X, int64_t ldx, const void *R, int64_t ldr, int type,
+                          const void *W, int w_type, float eps, void *H, int64_t ldh, void *Q, int64_t ldq, void *SF,
+                          int64_t ldsf, float *rstd, hipStream_t stream) {
+    return run_norm(true, rows, N, X, ldx, R, ldr, type, W, w_type, eps, H, ldh, Q, ldq, SF, ldsf, rstd, stream);
+}
+
+gemm_status mxfp8_quantize(int64_t rows, int64_t N, const void *X, int64_t ldx, int x_type, void *Q, int64_t ldq,
+                           void *SF, int64_t ldsf, hipStream_t stream) {
+    bool none;
+    gemm_status st = check_rows(rows, N, &none);
+    if (st != GEMM_OK) return st;
+    if (!elem_type(x_type) || N % 32 != 0) return GEMM_ERR_UNSUPPORTED;
+    if (none) return GEMM_OK;
+    if (ldx < N || ldq < N || ldsf < N / 32) return GEMM_ERR_BAD_LD;
+    if (!X || !Q || !SF) return GEMM_ERR_NULL_POINTER;
+    if (misaligned(X, elem_size(x_type))) return GEMM_ERR_MISALIGNED;
+    const int ve = x_type == GEMM_TYPE_F32 ? 4 : 8;
+    const int nvec = (int)(N / ve);
+    const int64_t want = (rows * nvec + 255) / 256;
+    const unsigned grid = (unsigned)(want < 16384 ? want : 16384);
+    switch (x_type) {
+#define TG_QUANT(t)                                                                                                  \
+    hipLaunchKernelGGL((tg::quantize_kernel<t>), dim3(grid), dim3(256), 0, stream, X, ldx, (uint8_t *)Q, ldq,        \
+                       (uint8_t *)SF, ldsf, rows, nvec)
+    case GEMM_TYPE_F32: TG_QUANT(0); break;
+    case GEMM_TYPE_BF16: TG_QUANT(1); break;
+    default: TG_QUANT(2); break;
+#undef TG_QUANT
+    }
+    return launched(hipGetLastError());
+}
+
+}  // extern "C"

@@ -1,0 +1,155 @@
+// Device-side pieces of the row operators (norm, quantisation): vectors of
+// 16 bytes at any element alignment, wave reductions, and the block-scaled
+// output of a row.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+
+namespace tg {
+
+// Row element types.
+template <int T> struct Elem;                          // gemm_elem_type
+template <> struct Elem<0> {
+    typedef float S;
+    static __device__ __forceinline__ float up(S v) { return v; }
+    static __device__ __forceinline__ S down(float v) { return v; }
+};
+template <> struct Elem<1> {
+    typedef __bf16 S;
+    static __device__ __forceinline__ float up(S v) { return (float)v; }
+    static __device__ __forceinline__ S down(float v) { return (S)v; }
+};
+template <> struct Elem<2> {
+    typedef _Float16 S;
+    static __device__ __forceinline__ float up(S v) { return (float)v; }
+    static __device__ __forceinline__ S down(float v) { return (S)v; }
+};
+
+// VE = 16 bytes' worth of row elements as fp32.  The memory vector is only
+// element-aligned: gfx950 serves a 16-byte access at any address, so rows
+// need no padding and no scalar variant.
+template <int T> constexpr int kVE = T == 0 ? 4 : 8;
+
+template <int T>
+struct RowVec {
+    static constexpr int VE = kVE<T>;
+    typedef typename Elem<T>::S S;
+    typedef S V __attribute__((ext_vector_type(VE)));
+    struct __attribute__((packed, aligned(sizeof(S)))) U {
+        V v;
+    };
+    // elements [c, c + VE) of a row of n; past the end: zeros
+    static __device__ __forceinline__ V load(const void *row, int c, int n) {
+        const S *p = (const S *)row + c;
+        if (c + VE <= n) return ((const U *)p)->v;
+        V v = {};
+        for (int i = 0; i < VE; ++i)
+            if (c + i < n) v[i] = p[i];
+        return v;
+    }
+    static __device__ __forceinline__ void store(void *row, int c, int n, V v) {
+        S *p = (S *)row + c;
+        if (c + VE <= n) {
+            ((U *)p)->v = v;
+            return;
+        }
+        for (int i = 0; i < VE; ++i)
+            if (c + i < n) p[i] = v[i];
+    }
+};
+
+// VE weights as fp32: of the row's type, or fp32.
+template <int T>
+__device__ __forceinline__ void load_weights(const void *w, bool w_f32, int c, int n, float (&out)[kVE<T>]) {
+    if constexpr (T != 0) {
+        if (w_f32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 v = RowVec<0>::load(w, c + 4 * h, n);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) out[4 * h + i] = v[i];
+            }
+            return;
+        }
+    }
+    const auto v = RowVec<T>::load(w, c, n);
+#pragma unroll
+    for (int i = 0; i < kVE<T>; ++i) out[i] = Elem<T>::up(v[i]);
+}
+
+// v of the lane at the other end of an exchange inside 16 lanes.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
+
+// Sum over the wave's 64 lanes, the same in every lane: exchanges inside 16
+// lanes run in the vector pipe, the last two through the LDS crossbar.
+__device__ __forceinline__ float wave_sum(float v) {
+    v += __builtin_bit_cast(float, dpp<kXor1>(__builtin_bit_cast(uint32_t, v)));
+    v += __builtin_bit_cast(float, dpp<kXor2>(__builtin_bit_cast(uint32_t, v)));
+    v += __builtin_bit_cast(float, dpp<kMirror8>(__builtin_bit_cast(uint32_t, v)));
+    v += __builtin_bit_cast(float, dpp<kMirror16>(__builtin_bit_cast(uint32_t, v)));
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    return v;
+}
+
+// Bits of |v|, or 0 for a NaN or an infinity: as unsigned numbers they order
+// like the magnitudes.
+__device__ __forceinline__ uint32_t finite_bits(float v) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v) & 0x7fffffffu;
+    return u < 0x7f800000u ? u : 0u;
+}
+
+// e8m0 code of the least power of two 2^e with amax <= 448 * 2^e = 1.75 *
+// 2^(e + 8): adding 0x1fffff to the bits carries into the exponent exactly
+// when the significand is above 1.75, and the exponent field less 8 is then
+// e + 127 (held at 0, 2^-127).
+__device__ __forceinline__ uint32_t mx_code(uint32_t amax_bits) {
+    const uint32_t f = (amax_bits + 0x1fffffu) >> 23;
+    return f > 8u ? f - 8u : 0u;
+}
+
+// 2^(127 - code), what an element is multiplied with before its rounding
+// (code <= 247: a normal number).
+__device__ __forceinline__ float mx_inverse(uint32_t code) {
+    return __builtin_bit_cast(float, (254u - code) << 23);
+}
+
+// VE consecutive elements of a row, their 32-element block spread over 32 /
+// VE neighbouring lanes: codes and scale of the row's block-scaled form.
+// (Values are at most 448 here, where the conversion neither saturates nor
+// makes a NaN of its own; infinities become the NaN code.)
+template <int VE>
+__device__ __forceinline__ void mx_store(const float (&y)[VE], uint8_t *q, uint8_t *sf, int c) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+        const uint32_t b = finite_bits(y[i]);
+        m = m > b ? m : b;
+    }
+    auto join = [&](uint32_t o) __attribute__((always_inline)) { m = m > o ? m : o; };
+    join(dpp<kXor1>(m));
+    join(dpp<kXor2>(m));
+    if constexpr (VE == 4) join(dpp<kMirror8>(m));
+    const uint32_t code = mx_code(m);
+    const float inv = mx_inverse(code);
+    struct __attribute__((packed, aligned(1))) Words {
+        uint32_t w[VE / 4];
+    } out;
+#pragma unroll
+    for (int i = 0; i < VE; i += 4) {
+        int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[i] * inv, y[i + 1] * inv, 0, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(y[i + 2] * inv, y[i + 3] * inv, w, true);
+        out.w[i / 4] = (uint32_t)w;
+    }
+    *(Words *)(q + c) = out;
+    if (c % 32 == 0) sf[c / 32] = (uint8_t)code;
+}
+
+}  // namespace tg
