@@ -11,6 +11,7 @@
 // that lane group g holds block g, and X is read with the same permutation.
 // The waves' sums are joined through LDS in wave order.
 #include "api.hpp"
+#include "pipeline.hpp"
 #include "rows.hpp"
 #include "../../include/tilegemm_ops.h"
 
@@ -81,111 +82,15 @@ __device__ __forceinline__ void split_f16(u32x4 x, u32x4 &hi, u32x4 &lo) {
     }
 }
 
-// MB: blocks of 16 rows of X per workgroup, NB: blocks of 16 weight rows.
-template <bool FP16, bool OUT_BF16, int MB, int NB>
-__global__ void __launch_bounds__(kGemvWaves * 64) gemv_mxfp4_kernel(GemvArgs p) {
-    __shared__ float red[kGemvWaves][MB * NB * 4][64];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int lc = lane & 15, lg = lane >> 4;
-    const int tn = blockIdx.x % p.tiles_n, tm = blockIdx.x / p.tiles_n;
-    const int n0 = tn * 16 * NB, m0 = tm * 16 * MB;
-    const int K = p.K;
-
-    const uint8_t *w[NB], *sf[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        // (rows past N: the last row again, never stored)
-        const int n = n0 + 16 * b + lc;
-        const int64_t row = n < p.N ? n : p.N - 1;
-        w[b] = p.W + row * p.ldw_bytes;
-        sf[b] = p.SF + row * p.ldsf;
-    }
-    const uint16_t *x[MB];
-    bool xin[MB];
-#pragma unroll
-    for (int a = 0; a < MB; ++a) {
-        const int m = m0 + 16 * a + lc;
-        xin[a] = m < p.M;
-        x[a] = (const uint16_t *)p.X + (int64_t)(xin[a] ? m : 0) * p.ldx;
-    }
-
-    f32x4 acc[MB][NB];
-#pragma unroll
-    for (int a = 0; a < MB; ++a)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    // wave w takes the K steps of 512 w, w + 8, ...: four tiles of 128
-    for (int64_t k0 = (int64_t)wave * 512; k0 < K; k0 += kGemvWaves * 512) {
-        u32x4 wq[NB][4];
-        uint32_t code[NB][4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int64_t k = k0 + t * 128 + lg * 32;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                wq[b][t] = u32x4{0u, 0u, 0u, 0u};
-                code[b][t] = 127u;
-                if (k < K) {
-                    wq[b][t] = ((const Bytes16 *)(w[b] + k / 2))->v;
-                    code[b][t] = sf[b][k >> p.kshift];
-                }
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int64_t k = k0 + t * 128 + lg * 32;
-            // fp16 holds a scaled weight exactly when its scale is 2^-23 ..
-            // 2^13 (subnormals included); a tile with another scale takes
-            // bf16 weights and X in two bf16 parts
-            bool direct = true;
-            if constexpr (FP16) {
-                bool in = true;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) in = in && code[b][t] >= 104u && code[b][t] <= 140u;
-                direct = __all(in);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                u32x4 xf[MB];
-#pragma unroll
-                for (int a = 0; a < MB; ++a) {
-                    xf[a] = u32x4{0u, 0u, 0u, 0u};
-                    if (xin[a] && k < K) xf[a] = ((const Halves8 *)(x[a] + k + 8 * j))->v;
-                }
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const float scale = __builtin_bit_cast(float, code[b][t] << 23);
-                    if (!FP16 || direct) {
-                        const u32x4 wf = fp4_up<FP16>(wq[b][t][j], scale);
-#pragma unroll
-                        for (int a = 0; a < MB; ++a) acc[a][b] = mfma16<FP16>(xf[a], wf, acc[a][b]);
-                    } else {
-                        const u32x4 wf = fp4_up<false>(wq[b][t][j], scale);
-#pragma unroll
-                        for (int a = 0; a < MB; ++a) {
-                            u32x4 hi, lo;
-                            split_f16(xf[a], hi, lo);
-                            acc[a][b] = mfma16<false>(hi, wf, acc[a][b]);
-                            acc[a][b] = mfma16<false>(lo, wf, acc[a][b]);
-                        }
-                    }
-                }
-            }
-        }
-    }
-
-    // lane l, register r of block (a, b): row 16 a + 4 (l / 16) + r, column 16 b + l % 16
-#pragma unroll
-    for (int a = 0; a < MB; ++a)
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) red[wave][(a * NB + b) * 4 + r][lane] = acc[a][b][r];
-    __syncthreads();
-    for (int i = threadIdx.x; i < MB * NB * 256; i += kGemvWaves * 64) {
-        const int l = i & 63, q = i >> 6, r = q & 3, b = (q >> 2) % NB, a = (q >> 2) / NB;
-        const int m = m0 + 16 * a + 4 * (l >> 4) + r, n = n0 + 16 * b + (l & 15);
+// The waves' sums of block a (16 rows of X) joined in wave order, plus C, to D.
+// red[wave][4 a + r][lane]: lane l, register r holds row 16 a + 4 (l / 16) + r
+// and column l % 16.
+template <bool OUT_BF16, int MB>
+__device__ __forceinline__ void gemv_join(const float (&red)[kGemvWaves][MB * 4][64], const GemvArgs &p, int m0,
+                                          int n0) {
+    for (int i = threadIdx.x; i < MB * 256; i += kGemvWaves * 64) {
+        const int l = i & 63, q = i >> 6, r = q & 3, a = q >> 2;
+        const int m = m0 + 16 * a + 4 * (l >> 4) + r, n = n0 + (l & 15);
         if (m >= p.M || n >= p.N) continue;
         float v = 0.0f;
 #pragma unroll
@@ -200,9 +105,200 @@ __global__ void __launch_bounds__(kGemvWaves * 64) gemv_mxfp4_kernel(GemvArgs p)
     }
 }
 
+// One MFMA of 32 K: 8 weights (a word of codes) of each lane against its x.
+template <bool FP16, int MB>
+__device__ __forceinline__ void gemv_step(const u32x4 (&xf)[MB], uint32_t w, uint32_t code, bool direct,
+                                          f32x4 (&acc)[MB]) {
+    const float scale = __builtin_bit_cast(float, code << 23);
+    if (!FP16 || direct) {
+        const u32x4 wf = fp4_up<FP16>(w, scale);
+#pragma unroll
+        for (int a = 0; a < MB; ++a) acc[a] = mfma16<FP16>(xf[a], wf, acc[a]);
+    } else {
+        const u32x4 wf = fp4_up<false>(w, scale);
+#pragma unroll
+        for (int a = 0; a < MB; ++a) {
+            u32x4 hi, lo;
+            split_f16(xf[a], hi, lo);
+            acc[a] = mfma16<false>(hi, wf, acc[a]);
+            acc[a] = mfma16<false>(lo, wf, acc[a]);
+        }
+    }
+}
+
+// fp16 holds a scaled weight exactly when its scale is 2^-23 .. 2^13
+// (subnormals included).
+__device__ __forceinline__ bool fp16_scale(uint32_t code) { return code >= 104u && code <= 140u; }
+
+// Weight rows 16-byte aligned: each wave's K step of 512 (16 rows of 256
+// bytes) goes straight to LDS in whole rows, sixteen lanes a row, and is
+// read back a word per lane in the MFMA's own order, so that X is read in
+// runs of 64 bytes and a step of 32 K has one scale.  Chunk c of row r sits
+// at chunk c ^ r: the 16 rows of a read fall on all 64 banks.
+template <bool FP16, bool OUT_BF16, int MB>
+__global__ void __launch_bounds__(kGemvWaves * 64) gemv_mxfp4_staged_kernel(GemvArgs p) {
+    __shared__ __attribute__((aligned(16))) char stage[kGemvWaves][4096];
+    __shared__ float red[kGemvWaves][MB * 4][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lc = lane & 15, lg = lane >> 4;
+    const int tn = blockIdx.x % p.tiles_n, tm = blockIdx.x / p.tiles_n;
+    const int n0 = tn * 16, m0 = tm * 16 * MB;
+    const int K = p.K;
+    const __amdgpu_buffer_rsrc_t rW = make_rsrc(p.W + (int64_t)n0 * p.ldw_bytes, span_bytes(p.N - n0, K / 2, p.ldw_bytes, 1));
+    char *ring = stage[wave];
+    const int64_t srow = n0 + lc < p.N ? n0 + lc : p.N - 1;
+    const uint8_t *sf = p.SF + srow * p.ldsf;
+    const uint16_t *x[MB];
+    bool xin[MB];
+#pragma unroll
+    for (int a = 0; a < MB; ++a) {
+        const int m = m0 + 16 * a + lc;
+        xin[a] = m < p.M;
+        x[a] = (const uint16_t *)p.X + (int64_t)(xin[a] ? m : 0) * p.ldx + 8 * lg;
+    }
+    f32x4 acc[MB];
+#pragma unroll
+    for (int a = 0; a < MB; ++a) acc[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    for (int k0 = wave * 512; k0 < K; k0 += kGemvWaves * 512) {
+        // four rows an instruction: lane L writes chunk L % 16 of row 4 i + L / 16
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 4 * i + lg, c = lc ^ row;
+            const int kb = k0 / 2 + c * 16;            // (rows past N lie past the resource)
+            dma_load<16>(rW, ring + i * 1024, kb < K / 2 ? (uint32_t)(row * p.ldw_bytes + kb) : kOOB);
+        }
+        // byte j of sc[t]: the scale of K block 4 t + j
+        uint32_t sc[4];
+        if (p.kshift == 5 && k0 + 512 <= K) {
+            const u32x4 v = ((const Bytes16 *)(sf + k0 / 32))->v;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) sc[t] = v[t];
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                sc[t] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = k0 + t * 128 + j * 32;
+                    sc[t] |= (k < K ? (uint32_t)sf[k >> p.kshift] : 127u) << (8 * j);
+                }
+            }
+        }
+        bool direct = true;
+        if constexpr (FP16) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) direct = direct && fp16_scale((sc[t] >> (8 * j)) & 0xffu);
+            direct = __all(direct);
+        }
+        u32x4 xf[4][MB];
+        auto load_x = [&](int t, int j) __attribute__((always_inline)) {
+            const int k = k0 + t * 128 + j * 32;
+#pragma unroll
+            for (int a = 0; a < MB; ++a) {
+                xf[j][a] = u32x4{0u, 0u, 0u, 0u};
+                if (xin[a] && k < K) xf[j][a] = ((const Halves8 *)(x[a] + k))->v;
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_x(0, j);
+        wait_vmcnt<0>();
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (t > 0) load_x(t, j);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t w = *(const uint32_t *)(ring + lc * 256 + (((4 * t + j) ^ lc) << 4) + 4 * lg);
+                gemv_step<FP16, MB>(xf[j], w, (sc[t] >> (8 * j)) & 0xffu, direct, acc);
+            }
+        }
+        wait_lgkmcnt0();                               // this step's reads done before the next overwrites it
+        asm volatile("" ::: "memory");
+    }
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) red[wave][a * 4 + r][lane] = acc[a][r];
+    __syncthreads();
+    gemv_join<OUT_BF16, MB>(red, p, m0, n0);
+}
+
+// Weight rows that start at any byte.
+template <bool FP16, bool OUT_BF16, int MB>
+__global__ void __launch_bounds__(kGemvWaves * 64) gemv_mxfp4_kernel(GemvArgs p) {
+    __shared__ float red[kGemvWaves][MB * 4][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lc = lane & 15, lg = lane >> 4;
+    const int tn = blockIdx.x % p.tiles_n, tm = blockIdx.x / p.tiles_n;
+    const int n0 = tn * 16, m0 = tm * 16 * MB;
+    const int K = p.K;
+    // (rows past N: the last row again, never stored)
+    const int64_t wrow = n0 + lc < p.N ? n0 + lc : p.N - 1;
+    const uint8_t *w = p.W + wrow * p.ldw_bytes, *sf = p.SF + wrow * p.ldsf;
+    const uint16_t *x[MB];
+    bool xin[MB];
+#pragma unroll
+    for (int a = 0; a < MB; ++a) {
+        const int m = m0 + 16 * a + lc;
+        xin[a] = m < p.M;
+        x[a] = (const uint16_t *)p.X + (int64_t)(xin[a] ? m : 0) * p.ldx;
+    }
+    f32x4 acc[MB];
+#pragma unroll
+    for (int a = 0; a < MB; ++a) acc[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // wave w takes the K steps of 512 w, w + 8, ...: four tiles of 128, of
+    // which lane group g loads block g, K permuted inside the tile
+    for (int64_t k0 = (int64_t)wave * 512; k0 < K; k0 += kGemvWaves * 512) {
+        u32x4 wq[4];
+        uint32_t code[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int64_t k = k0 + t * 128 + lg * 32;
+            wq[t] = u32x4{0u, 0u, 0u, 0u};
+            code[t] = 127u;
+            if (k < K) {
+                wq[t] = ((const Bytes16 *)(w + k / 2))->v;
+                code[t] = sf[k >> p.kshift];
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int64_t k = k0 + t * 128 + lg * 32;
+            const bool direct = !FP16 || __all(fp16_scale(code[t]));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                u32x4 xf[MB];
+#pragma unroll
+                for (int a = 0; a < MB; ++a) {
+                    xf[a] = u32x4{0u, 0u, 0u, 0u};
+                    if (xin[a] && k < K) xf[a] = ((const Halves8 *)(x[a] + k + 8 * j))->v;
+                }
+                gemv_step<FP16, MB>(xf, wq[t][j], code[t], direct, acc);
+            }
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) red[wave][a * 4 + r][lane] = acc[a][r];
+    __syncthreads();
+    gemv_join<OUT_BF16, MB>(red, p, m0, n0);
+}
+
 template <bool FP16, bool OUT_BF16, int MB>
 hipError_t go_gemv(const GemvArgs &p, unsigned grid, hipStream_t s) {
-    hipLaunchKernelGGL((gemv_mxfp4_kernel<FP16, OUT_BF16, MB, 1>), dim3(grid), dim3(kGemvWaves * 64), 0, s, p);
+    // 16-byte weight rows
+    if (((uintptr_t)p.W | (uintptr_t)p.ldw_bytes) % 16 == 0)
+        hipLaunchKernelGGL((gemv_mxfp4_staged_kernel<FP16, OUT_BF16, MB>), dim3(grid), dim3(kGemvWaves * 64), 0, s, p);
+    else
+        hipLaunchKernelGGL((gemv_mxfp4_kernel<FP16, OUT_BF16, MB>), dim3(grid), dim3(kGemvWaves * 64), 0, s, p);
     return hipGetLastError();
 }
 

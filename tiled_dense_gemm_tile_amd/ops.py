@@ -15,60 +15,90 @@ from __future__ import annotations
 
 import torch
 
-from . import OUT_BF16, OUT_F32, _check, _ld, _load, _on_device
+from . import OUT_BF16, OUT_F32, _check, _load
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 _E8M0 = (torch.float8_e8m0fnu, torch.uint8)
+_E2M1 = (torch.uint8, torch.float4_e2m1fn_x2)
+_F32 = (torch.float32,)
+_NONE = (None, 0)
 
 
-def _run(name, dev, *args):
+def _run(f, dev, *args):
     """The C call on torch's current stream of ``dev``, with ``dev`` current
     (a NULL stream means the current device's)."""
-    f = getattr(_load(), name)
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch.cuda.current_device() == dev.index:
-        _check(f(*args, stream))
+        status = f(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(f(*args, stream))
+            status = f(*args, stream)
+    if status:
+        _check(status)
 
 
-def _matrix(name, t, rows, cols, dtypes):
+def _device(X):
+    dev = X.device
+    if dev.type != "cuda":
+        raise ValueError("the tensors must be device tensors")
+    return dev
+
+
+def _matrix(name, t, shape, dtypes, dev):
+    """(pointer, leading dimension) of a matrix, checked."""
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError("%s must be (%d, %d)" % (name, rows, cols))
-    return t
+    if t.shape != shape:
+        raise ValueError("%s must be (%d, %d)" % (name, shape[0], shape[1]))
+    if t.device != dev:
+        raise ValueError("%s must be a device tensor on %s" % (name, dev))
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError("%s: the last stride must be 1" % name)
+    if shape[0] <= 1 and ld < shape[1]:
+        ld = shape[1]
+    return t.data_ptr(), ld
 
 
-def _vector(name, t, n, dtypes):
+def _vector(name, t, n, dtypes, dev):
+    """Pointer of a contiguous vector, checked."""
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError("%s must be a contiguous vector of %d" % (name, n))
-    return t
+    if t.device != dev:
+        raise ValueError("%s must be a device tensor on %s" % (name, dev))
+    return t.data_ptr()
 
 
-def _ptr_ld(t, cols):
-    return (None, 0) if t is None else (t.data_ptr(), _ld(t, cols))
-
-
-def _rows(X):
+def _rows(name, X):
+    """(shape, type code, device) of the first matrix of a row operator."""
     if X.dim() != 2 or X.dtype not in _TYPES:
-        raise TypeError("X must be a 2-D float32, bfloat16 or float16 tensor")
-    _on_device(X, X=X)
-    return X.shape[0], X.shape[1], X.dtype
+        raise TypeError("%s must be a 2-D float32, bfloat16 or float16 tensor" % name)
+    return tuple(X.shape), _TYPES[X.dtype], _device(X)
 
 
-def _scaled_out(X, rows, N, Q, SF):
+def _scaled_out(shape, dev, Q, SF):
+    rows, N = shape
     if N % 32:
         raise ValueError("block-scaled rows hold a multiple of 32 elements")
     if Q is None:
-        Q = torch.empty((rows, N), dtype=torch.float8_e4m3fn, device=X.device)
+        Q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
     if SF is None:
-        SF = torch.empty((rows, N // 32), dtype=torch.float8_e8m0fnu, device=X.device)
-    return _matrix("Q", Q, rows, N, _E4M3), _matrix("SF", SF, rows, N // 32, _E8M0)
+        SF = torch.empty((rows, N // 32), dtype=torch.float8_e8m0fnu, device=dev)
+    return Q, SF, _matrix("Q", Q, shape, _E4M3, dev) + _matrix("SF", SF, (rows, N // 32), _E8M0, dev)
+
+
+def _workspace(t, need, dev):
+    """(tensor to keep, pointer, bytes) of a workspace given or allocated here."""
+    if t is None:
+        if not need:
+            return None, None, 0
+        t = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif t.device != dev or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous device tensor on %s" % dev)
+    return t, t.data_ptr(), t.numel() * t.element_size()
 
 
 def mxfp8_quantize(X, Q=None, SF=None):
@@ -76,27 +106,28 @@ def mxfp8_quantize(X, Q=None, SF=None):
     scales SF (rows, N/32), as :func:`gemm_mxfp8` takes an operand.  N must
     be a multiple of 32.  The scale of a block is the least power of two that
     clips none of its elements.  Returns (Q, SF)."""
-    rows, N, dtype = _rows(X)
-    Q, SF = _scaled_out(X, rows, N, Q, SF)
-    _on_device(X, Q=Q, SF=SF)
-    _run("mxfp8_quantize", X.device, rows, N, X.data_ptr(), _ld(X, N), _TYPES[dtype], Q.data_ptr(), _ld(Q, N),
-         SF.data_ptr(), _ld(SF, N // 32))
+    shape, code, dev = _rows("X", X)
+    x = _matrix("X", X, shape, (X.dtype,), dev)
+    Q, SF, out = _scaled_out(shape, dev, Q, SF)
+    _run(_load().mxfp8_quantize, dev, *shape, *x, code, *out)
     return Q, SF
 
 
-def _norm_args(X, W, residual, H, rstd):
-    rows, N, dtype = _rows(X)
-    _vector("W", W, N, (dtype, torch.float32))
+def _norm(f, X, W, eps, residual, H, rstd, shape, code, dev, out):
+    """The norm's call; returns (H, rstd)."""
+    own = (X.dtype,)
+    x = _matrix("X", X, shape, own, dev)
+    w = _vector("W", W, shape[1], (X.dtype, torch.float32), dev)
+    r = _NONE
     if residual is not None:
-        _matrix("residual", residual, rows, N, (dtype,))
+        r = _matrix("residual", residual, shape, own, dev)
         if H is None:
-            H = torch.empty((rows, N), dtype=dtype, device=X.device)
-    if H is not None:
-        _matrix("H", H, rows, N, (dtype,))
+            H = torch.empty(shape, dtype=X.dtype, device=dev)
+    h = _NONE if H is None else _matrix("H", H, shape, own, dev)
     if rstd is None:
-        rstd = torch.empty(rows, dtype=torch.float32, device=X.device)
-    _vector("rstd", rstd, rows, (torch.float32,))
-    return rows, N, dtype, H, rstd
+        rstd = torch.empty(shape[0], dtype=torch.float32, device=dev)
+    _run(f, dev, *shape, *x, *r, code, w, _TYPES[W.dtype], eps, *h, *out, _vector("rstd", rstd, shape[0], _F32, dev))
+    return X if H is None else H, rstd
 
 
 def rmsnorm(X, W, eps, residual=None, Y=None, H=None, rstd=None):
@@ -105,16 +136,11 @@ def rmsnorm(X, W, eps, residual=None, Y=None, H=None, rstd=None):
     sqrt(mean(H^2) + eps).  W (N,) of X's type or float32.  H may be given as
     X or the residual (in place), and so may Y unless H is the same.
     Returns (Y, H, rstd), H being X when there is no residual and no H."""
-    rows, N, dtype, H, rstd = _norm_args(X, W, residual, H, rstd)
+    shape, code, dev = _rows("X", X)
     if Y is None:
-        Y = torch.empty((rows, N), dtype=dtype, device=X.device)
-    _matrix("Y", Y, rows, N, (dtype,))
-    _on_device(X, W=W, residual=residual, H=H, Y=Y, rstd=rstd)
-    rp, ldr = _ptr_ld(residual, N)
-    hp, ldh = _ptr_ld(H, N)
-    _run("rmsnorm", X.device, rows, N, X.data_ptr(), _ld(X, N), rp, ldr, _TYPES[dtype], W.data_ptr(),
-         _TYPES[W.dtype], float(eps), hp, ldh, Y.data_ptr(), _ld(Y, N), rstd.data_ptr())
-    return Y, X if H is None else H, rstd
+        Y = torch.empty(shape, dtype=X.dtype, device=dev)
+    out = _matrix("Y", Y, shape, (X.dtype,), dev)
+    return (Y, *_norm(_load().rmsnorm, X, W, eps, residual, H, rstd, shape, code, dev, out))
 
 
 def rmsnorm_mxfp8(X, W, eps, residual=None, Q=None, SF=None, H=None, rstd=None):
@@ -122,20 +148,14 @@ def rmsnorm_mxfp8(X, W, eps, residual=None, Q=None, SF=None, H=None, rstd=None):
     :func:`mxfp8_quantize`): the operand of :func:`gemm_mxfp8` and the 8-bit
     copy that :func:`gemm_wgrad_mxfp8` reads in the backward pass.  Returns
     (Q, SF, H, rstd)."""
-    rows, N, dtype, H, rstd = _norm_args(X, W, residual, H, rstd)
-    Q, SF = _scaled_out(X, rows, N, Q, SF)
-    _on_device(X, W=W, residual=residual, H=H, Q=Q, SF=SF, rstd=rstd)
-    rp, ldr = _ptr_ld(residual, N)
-    hp, ldh = _ptr_ld(H, N)
-    _run("rmsnorm_mxfp8", X.device, rows, N, X.data_ptr(), _ld(X, N), rp, ldr, _TYPES[dtype], W.data_ptr(),
-         _TYPES[W.dtype], float(eps), hp, ldh, Q.data_ptr(), _ld(Q, N), SF.data_ptr(), _ld(SF, N // 32),
-         rstd.data_ptr())
-    return Q, SF, X if H is None else H, rstd
+    shape, code, dev = _rows("X", X)
+    Q, SF, out = _scaled_out(shape, dev, Q, SF)
+    return (Q, SF, *_norm(_load().rmsnorm_mxfp8, X, W, eps, residual, H, rstd, shape, code, dev, out))
 
 
 def rmsnorm_backward_workspace_bytes(rows: int, N: int) -> int:
     """Workspace bytes :func:`rmsnorm_backward` needs for dW."""
-    return int(_load().rmsnorm_backward_workspace_bytes(rows, N))
+    return _load().rmsnorm_backward_workspace_bytes(rows, N)
 
 
 def rmsnorm_backward(dY, H, W, rstd, dH=None, dX=None, dW=None, workspace=None, weight_grad=True):
@@ -147,49 +167,45 @@ def rmsnorm_backward(dY, H, W, rstd, dH=None, dX=None, dW=None, workspace=None, 
     ``workspace``: a device byte tensor of at least
     :func:`rmsnorm_backward_workspace_bytes` bytes, 256-byte aligned
     (allocated per call when not given).  Returns (dX, dW)."""
-    rows, N, dtype = _rows(dY)
-    _matrix("H", H, rows, N, (dtype,))
-    _vector("W", W, N, (dtype, torch.float32))
-    _vector("rstd", rstd, rows, (torch.float32,))
-    if dH is not None:
-        _matrix("dH", dH, rows, N, (dtype,))
+    shape, code, dev = _rows("dY", dY)
+    rows, N = shape
+    own = (dY.dtype,)
+    dy = _matrix("dY", dY, shape, own, dev)
+    h = _matrix("H", H, shape, own, dev)
+    w = _vector("W", W, N, (dY.dtype, torch.float32), dev)
+    s = _vector("rstd", rstd, rows, _F32, dev)
+    dh = _NONE if dH is None else _matrix("dH", dH, shape, own, dev)
     if dX is None:
-        dX = torch.empty((rows, N), dtype=dtype, device=dY.device)
-    _matrix("dX", dX, rows, N, (dtype,))
-    wp, wb = None, 0
+        dX = torch.empty(shape, dtype=dY.dtype, device=dev)
+    dx = _matrix("dX", dX, shape, own, dev)
+    dw, ws = None, (None, 0)
     if weight_grad:
         if dW is None:
-            dW = torch.empty(N, dtype=torch.float32, device=dY.device)
-        _vector("dW", dW, N, (torch.float32,))
-        if workspace is None:
-            workspace = torch.empty(rmsnorm_backward_workspace_bytes(rows, N), dtype=torch.uint8, device=dY.device)
-        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            dW = torch.empty(N, dtype=torch.float32, device=dev)
+        dw = _vector("dW", dW, N, _F32, dev)
+        workspace, *ws = _workspace(workspace, workspace is None and rmsnorm_backward_workspace_bytes(rows, N), dev)
     elif dW is not None:
         raise ValueError("dW given with weight_grad=False")
-    _on_device(dY, H=H, W=W, rstd=rstd, dH=dH, dX=dX, dW=dW, workspace=workspace)
-    hp, ldh = _ptr_ld(dH, N)
-    _run("rmsnorm_backward", dY.device, rows, N, dY.data_ptr(), _ld(dY, N), H.data_ptr(), _ld(H, N), _TYPES[dtype],
-         W.data_ptr(), _TYPES[W.dtype], rstd.data_ptr(), hp, ldh, dX.data_ptr(), _ld(dX, N),
-         None if dW is None else dW.data_ptr(), wp, wb)
+    _run(_load().rmsnorm_backward, dev, rows, N, *dy, *h, code, w, _TYPES[W.dtype], s, *dh, *dx, dw, *ws)
     return dX, dW
 
 
-def _product_out(ref, M, N, C, D, out_dtype):
-    out_dtype = torch.float32 if out_dtype is None else out_dtype
-    if out_dtype not in (torch.float32, torch.bfloat16):
+def _product_out(shape, dev, C, D, out_dtype):
+    """(D, output type code, C's pointer and leading dimension, D's)."""
+    if out_dtype is None:
+        out_dtype = torch.float32
+    elif out_dtype != torch.float32 and out_dtype != torch.bfloat16:
         raise TypeError("out_dtype must be float32 or bfloat16")
     if D is None:
-        D = torch.empty((M, N), dtype=out_dtype, device=ref.device)
-    _matrix("D", D, M, N, (out_dtype,))
-    if C is not None:
-        _matrix("C", C, M, N, (out_dtype,))
-    return D, OUT_BF16 if out_dtype == torch.bfloat16 else OUT_F32
+        D = torch.empty(shape, dtype=out_dtype, device=dev)
+    c = _NONE if C is None else _matrix("C", C, shape, (out_dtype,), dev)
+    return D, OUT_BF16 if out_dtype == torch.bfloat16 else OUT_F32, c + _matrix("D", D, shape, (out_dtype,), dev)
 
 
 def gemm_wgrad_mxfp8_workspace_bytes(M: int, N: int, K: int) -> int:
     """Workspace bytes with which :func:`gemm_wgrad_mxfp8` may cut K (0: it
     would not)."""
-    return int(_load().gemm_wgrad_mxfp8_workspace_bytes(M, N, K))
+    return _load().gemm_wgrad_mxfp8_workspace_bytes(M, N, K)
 
 
 def gemm_wgrad_mxfp8(dY, Q, SF, C=None, out_dtype=None, D=None, workspace=None):
@@ -202,23 +218,17 @@ def gemm_wgrad_mxfp8(dY, Q, SF, C=None, out_dtype=None, D=None, workspace=None):
     not given; a smaller one runs without cutting K)."""
     if dY.dtype != torch.bfloat16 or dY.dim() != 2:
         raise TypeError("dY must be a 2-D bfloat16 tensor")
-    _on_device(dY, dY=dY)
-    K, M = dY.shape
     if Q.dim() != 2 or Q.shape[1] % 32:
         raise ValueError("Q must be (K, N) with N a multiple of 32")
+    dev = _device(dY)
+    K, M = dY.shape
     N = Q.shape[1]
-    _matrix("Q", Q, K, N, _E4M3)
-    _matrix("SF", SF, K, N // 32, _E8M0)
-    D, out = _product_out(dY, M, N, C, D, out_dtype)
-    if workspace is None:
-        need = gemm_wgrad_mxfp8_workspace_bytes(M, N, K)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dY.device)
-    _on_device(dY, Q=Q, SF=SF, C=C, D=D, workspace=workspace)
-    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    cp, ldc = _ptr_ld(C, N)
-    _run("gemm_wgrad_mxfp8", dY.device, M, N, K, dY.data_ptr(), _ld(dY, M), Q.data_ptr(), _ld(Q, N), SF.data_ptr(),
-         _ld(SF, N // 32), cp, ldc, D.data_ptr(), _ld(D, N), out, wp, wb)
+    a = _matrix("dY", dY, (K, M), (torch.bfloat16,), dev)
+    b = _matrix("Q", Q, (K, N), _E4M3, dev)
+    s = _matrix("SF", SF, (K, N // 32), _E8M0, dev)
+    D, out, cd = _product_out((M, N), dev, C, D, out_dtype)
+    workspace, *ws = _workspace(workspace, workspace is None and gemm_wgrad_mxfp8_workspace_bytes(M, N, K), dev)
+    _run(_load().gemm_wgrad_mxfp8, dev, M, N, K, *a, *b, *s, *cd, out, *ws)
     return D
 
 
@@ -229,21 +239,16 @@ def gemv_mxfp4(X, W, SFW, kblock=32, C=None, out_dtype=None, D=None):
     :func:`gemm_mx_kblock` take B and SFB.  X is not quantised.  Made for up
     to 16 rows, right for any number.  ``out_dtype`` float32 (default) or
     bfloat16; C of that type may be D."""
-    if X.dtype not in (torch.bfloat16, torch.float16) or X.dim() != 2:
+    if X.dim() != 2 or (X.dtype != torch.bfloat16 and X.dtype != torch.float16):
         raise TypeError("X must be a 2-D bfloat16 or float16 tensor")
-    _on_device(X, X=X)
+    dev = _device(X)
     M, K = X.shape
-    if W.dim() != 2:
-        raise ValueError("W must be (N, K/2) bytes")
+    if W.dim() != 2 or K % 2 or kblock <= 0:
+        raise ValueError("W must be (N, K/2) bytes, K even and kblock positive")
     N = W.shape[0]
-    if K % 2 or kblock <= 0:
-        raise ValueError("K must be even and kblock positive")
-    _matrix("W", W, N, K // 2, (torch.uint8, getattr(torch, "float4_e2m1fn_x2", torch.uint8)))
-    groups = -(-K // kblock)
-    _matrix("SFW", SFW, N, groups, _E8M0)
-    D, out = _product_out(X, M, N, C, D, out_dtype)
-    _on_device(X, W=W, SFW=SFW, C=C, D=D)
-    cp, ldc = _ptr_ld(C, N)
-    _run("gemv_mxfp4", X.device, M, N, K, int(kblock), X.data_ptr(), _ld(X, K), _TYPES[X.dtype], W.data_ptr(),
-         2 * _ld(W, K // 2), SFW.data_ptr(), _ld(SFW, groups), cp, ldc, D.data_ptr(), _ld(D, N), out)
+    x = _matrix("X", X, (M, K), (X.dtype,), dev)
+    wp, ldw = _matrix("W", W, (N, K // 2), _E2M1, dev)
+    s = _matrix("SFW", SFW, (N, -(-K // kblock)), _E8M0, dev)
+    D, out, cd = _product_out((M, N), dev, C, D, out_dtype)
+    _run(_load().gemv_mxfp4, dev, M, N, K, kblock, *x, _TYPES[X.dtype], wp, 2 * ldw, *s, *cd, out)
     return D
