@@ -137,18 +137,26 @@ size_t gemm_wgrad_mxfp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *     D[m][n] = C[m][n] + sum_{k<K} x[m][k] * e2m1(W, n*ldw + k) * 2^(SFW[n*ldsfw + k/kblock] - 127)
  * W and SFW as gemm_mxfp4 and gemm_mx_kblock take B and SFB (ldw in
  * elements, even); X is not quantised: the products of its 16-bit elements
- * with the weights are exact and summed in fp32.  One kernel, made for M up
- * to 16 and bound by the reading of W; any M is right.
+ * with the weights are exact and summed in fp32.  Made for M up
+ * to 16 and bound by the reading of W; any M up to 2^20 is right.
  *   x_type: GEMM_TYPE_BF16 or GEMM_TYPE_FP16    out_type as gemm_bf16 (C, D)
  *   K a multiple of 32; kblock as gemm_mx_kblock: 32 times a power of two, or
  *   any multiple of 32 that is at least K (GEMM_ERR_UNSUPPORTED otherwise)
  *   ldx, ldw >= K; ldsfw >= ceil(K / kblock); C NULL: 0; C == D with
  *   ldc == ldd accumulates in place.
+ *   workspace: device memory, 256-byte aligned, or NULL.  With at least
+ *     gemv_mxfp4_workspace_bytes(M, N, K) bytes, calls whose X exceeds the
+ *     LDS of a compute unit, and those of few rows of W, cut K into ranges
+ *     and sum the fp32 partial sums in order; a smaller one or NULL runs
+ *     uncut, slower (the same result up to summation order).
  * Scale code 0xFF gives NaN in the row's outputs.
  */
 gemm_status gemv_mxfp4(int64_t M, int64_t N, int64_t K, int64_t kblock, const void *X, int64_t ldx, int x_type,
                        const void *W, int64_t ldw, const void *SFW, int64_t ldsfw,
-                       const void *C, int64_t ldc, void *D, int64_t ldd, int out_type, hipStream_t stream);
+                       const void *C, int64_t ldc, void *D, int64_t ldd, int out_type,
+                       void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t gemv_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 #ifdef __cplusplus
 }

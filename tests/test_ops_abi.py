@@ -22,8 +22,8 @@ NAN, INF = float("nan"), float("inf")
 def test_header_functions_are_exported():
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = sorted(set(re.findall(r"^[A-Za-z_][\w\s\*]*?\b(\w+)\s*\(", text, flags=re.M)))
-    assert names == ["gemm_wgrad_mxfp8", "gemm_wgrad_mxfp8_workspace_bytes", "gemv_mxfp4", "mxfp8_quantize", "rmsnorm",
-                     "rmsnorm_backward", "rmsnorm_backward_workspace_bytes", "rmsnorm_mxfp8"]
+    assert names == ["gemm_wgrad_mxfp8", "gemm_wgrad_mxfp8_workspace_bytes", "gemv_mxfp4", "gemv_mxfp4_workspace_bytes",
+                     "mxfp8_quantize", "rmsnorm", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes", "rmsnorm_mxfp8"]
     out = subprocess.run(["nm", "-D", "--defined-only", tg.library_path()], capture_output=True, text=True,
                          check=True).stdout
     exported = {line.split()[-1] for line in out.splitlines() if " T " in line}
@@ -166,8 +166,8 @@ def test_wgrad_workspace_bytes():
 
 
 def gemv(M=2, N=64, K=64, kb=32, X=P, ldx=64, xt=BF16, W=P + (1 << 20), ldw=64, SF=P + (2 << 20), ldsf=2, C=None,
-         ldc=64, D=Q, ldd=64, out=F32):
-    return tg.raw.gemv_mxfp4(M, N, K, kb, X, ldx, xt, W, ldw, SF, ldsf, C, ldc, D, ldd, out, None)
+         ldc=64, D=Q, ldd=64, out=F32, ws=None, wb=0):
+    return tg.raw.gemv_mxfp4(M, N, K, kb, X, ldx, xt, W, ldw, SF, ldsf, C, ldc, D, ldd, out, ws, wb, None)
 
 
 def test_gemv_refusals():
@@ -191,6 +191,16 @@ def test_gemv_refusals():
     assert gemv(X=P + 1) == MISALIGNED
     assert gemv(D=Q + 2) == MISALIGNED
     assert gemv(C=Q, ldc=128) == UNSUPPORTED
+    assert gemv(ws=Q + 64, wb=1 << 20) == MISALIGNED
+    assert gemv(M=(1 << 20) + 1) == UNSUPPORTED
+
+
+def test_gemv_workspace_bytes():
+    assert tg.gemv_mxfp4_workspace_bytes(0, 64, 64) == 0
+    assert tg.gemv_mxfp4_workspace_bytes(1, 64, -32) == 0
+    assert tg.gemv_mxfp4_workspace_bytes(1, 14336, 4096) == 0
+    b = tg.gemv_mxfp4_workspace_bytes(16, 4096, 14336)
+    assert b > 0 and b % (16 * 4096 * 4) == 0
 
 
 def test_binding_refuses_host_tensors_and_types():

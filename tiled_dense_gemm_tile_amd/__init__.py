@@ -27,7 +27,7 @@ import threading
 __all__ = ["gemm_bf16", "gemm_fp16", "gemm_bf16_splitk", "gemm_fp16_splitk", "splitk_workspace_bytes",
            "gemm_mxfp8", "gemm_mxfp4", "gemm_mxfp6", "gemm_mxfp8_splitk", "gemm_mxfp4_splitk", "gemm_mxfp6_splitk", "raw", "GemmError", "LibraryMissing",
            "library_path", "STATUS", "mxfp8_quantize", "rmsnorm", "rmsnorm_mxfp8", "rmsnorm_backward",
-           "rmsnorm_backward_workspace_bytes", "gemm_wgrad_mxfp8", "gemm_wgrad_mxfp8_workspace_bytes", "gemv_mxfp4"]
+           "rmsnorm_backward_workspace_bytes", "gemm_wgrad_mxfp8", "gemm_wgrad_mxfp8_workspace_bytes", "gemv_mxfp4", "gemv_mxfp4_workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libtilegemm.so")
@@ -141,13 +141,15 @@ def _declare_ops(L):
             ("rmsnorm_mxfp8", norm + [vp, i64, vp, i64, vp, vp]),
             ("rmsnorm_backward", [i64, i64, vp, i64, vp, i64, ci, vp, ci, vp, vp, i64, vp, i64, vp, vp, sz, vp]),
             ("gemm_wgrad_mxfp8", [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, sz, vp]),
-            ("gemv_mxfp4", [i64, i64, i64, i64, vp, i64, ci, vp, i64, vp, i64, vp, i64, vp, i64, ci, vp])):
+            ("gemv_mxfp4", [i64, i64, i64, i64, vp, i64, ci, vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, sz, vp])):
         f = getattr(L, name)
         f.restype, f.argtypes = ci, args
     L.rmsnorm_backward_workspace_bytes.restype = sz
     L.rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
     L.gemm_wgrad_mxfp8_workspace_bytes.restype = sz
     L.gemm_wgrad_mxfp8_workspace_bytes.argtypes = [i64, i64, i64]
+    L.gemv_mxfp4_workspace_bytes.restype = sz
+    L.gemv_mxfp4_workspace_bytes.argtypes = [i64, i64, i64]
 
 
 class _Raw:
@@ -685,7 +687,7 @@ def gemm_mxfp6_splitk(A, SFA, B, SFB, C=None, out_dtype=None, D=None, fmt="e2m3"
 
 # The functions of ops.py, which needs torch at import, load with their first use.
 _OPS = ("mxfp8_quantize", "rmsnorm", "rmsnorm_mxfp8", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes",
-        "gemm_wgrad_mxfp8", "gemm_wgrad_mxfp8_workspace_bytes", "gemv_mxfp4")
+        "gemm_wgrad_mxfp8", "gemm_wgrad_mxfp8_workspace_bytes", "gemv_mxfp4", "gemv_mxfp4_workspace_bytes")
 
 
 def __getattr__(name):

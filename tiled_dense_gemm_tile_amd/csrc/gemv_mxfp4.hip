@@ -27,13 +27,29 @@ struct GemvArgs {
     int64_t ldx, ldw_bytes, ldsf, ldc, ldd;
     int M, N, K;
     int kshift;                                        // scale index of element k: k >> kshift
-    int tiles_n;
+    int tiles_n;                                       // blocks of 16 weight rows
+    bool out_bf16;
+    // staged kernel: 2^kwlog waves share one block's K; LDS bytes between
+    // rows of X; K per range, and where the ranges' sums go (null: one range):
+    // range s to the M x ldws matrix at ws + s * M * ldws
+    int kwlog, x_pitch, k_split;
+    float *ws;
+    int64_t ldws;
 };
 
 constexpr int kGemvWaves = 8;
 
 struct __attribute__((packed, aligned(1))) Bytes16 {
     u32x4 v;
+};
+struct __attribute__((packed, aligned(1))) Bytes8 {
+    u32x2 v;
+};
+struct __attribute__((packed, aligned(1))) Bytes2 {
+    uint16_t v;
+};
+struct __attribute__((packed, aligned(1))) Bytes4 {
+    uint32_t v;
 };
 struct __attribute__((packed, aligned(2))) Halves8 {
     u32x4 v;
@@ -82,26 +98,60 @@ __device__ __forceinline__ void split_f16(u32x4 x, u32x4 &hi, u32x4 &lo) {
     }
 }
 
-// The waves' sums of block a (16 rows of X) joined in wave order, plus C, to D.
+// A finished sum, with C to D, or one of a K range to the workspace.
+__device__ __forceinline__ void gemv_put(const GemvArgs &p, int split, int m, int n, float v) {
+    if (m >= p.M || n >= p.N) return;
+    if (p.ws) {
+        p.ws[((int64_t)split * p.M + m) * p.ldws + n] = v;
+    } else if (p.out_bf16) {
+        if (p.C) v += (float)((const __bf16 *)p.C)[(int64_t)m * p.ldc + n];
+        ((__bf16 *)p.D)[(int64_t)m * p.ldd + n] = (__bf16)v;
+    } else {
+        if (p.C) v += ((const float *)p.C)[(int64_t)m * p.ldc + n];
+        ((float *)p.D)[(int64_t)m * p.ldd + n] = v;
+    }
+}
+
+// The sums of each 2^kwlog neighbouring waves (one block of 16 weight rows; the
+// next: the next block) joined in wave order and put.
 // red[wave][4 a + r][lane]: lane l, register r holds row 16 a + 4 (l / 16) + r
 // and column l % 16.
-template <bool OUT_BF16, int MB>
-__device__ __forceinline__ void gemv_join(const float (&red)[kGemvWaves][MB * 4][64], const GemvArgs &p, int m0,
-                                          int n0) {
-    for (int i = threadIdx.x; i < MB * 256; i += kGemvWaves * 64) {
-        const int l = i & 63, q = i >> 6, r = q & 3, a = q >> 2;
-        const int m = m0 + 16 * a + 4 * (l >> 4) + r, n = n0 + (l & 15);
-        if (m >= p.M || n >= p.N) continue;
+template <int MB>
+__device__ __forceinline__ void gemv_join(float (&red)[kGemvWaves][MB * 4][64], const GemvArgs &p, int kwlog,
+                                          int split, int m0, int n0) {
+    // (through an empty asm: a persistent caller's addresses would otherwise be
+    // kept in registers through its main loop)
+    int first = threadIdx.x;
+    asm volatile("" : "+v"(first));
+    for (int i = first; i < (MB * 256 * kGemvWaves) >> kwlog; i += kGemvWaves * 64) {
+        const int l = i & 63, q = (i >> 6) % (MB * 4), rw = (i >> 6) / (MB * 4), r = q & 3, a = q >> 2;
+        const int m = m0 + 16 * a + 4 * (l >> 4) + r, n = n0 + 16 * rw + (l & 15);
+        // (reads in asm, each waited for in its own statement: a plain LDS read
+        // would also wait for the weights on their way into LDS)
+        uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const float *)&red[rw << kwlog][q][l];
         float v = 0.0f;
+        if (kwlog == 3) {
+            float s[8];
+            asm volatile(
+                "ds_read_b32 %0, %8\n\tds_read_b32 %1, %8 offset:%c9\n\tds_read_b32 %2, %8 offset:%c10\n\t"
+                "ds_read_b32 %3, %8 offset:%c11\n\tds_read_b32 %4, %8 offset:%c12\n\t"
+                "ds_read_b32 %5, %8 offset:%c13\n\tds_read_b32 %6, %8 offset:%c14\n\t"
+                "ds_read_b32 %7, %8 offset:%c15\n\ts_waitcnt lgkmcnt(0)"
+                : "=&v"(s[0]), "=&v"(s[1]), "=&v"(s[2]), "=&v"(s[3]), "=&v"(s[4]), "=&v"(s[5]), "=&v"(s[6]),
+                  "=&v"(s[7])
+                : "v"(at), "n"(MB * 1024), "n"(MB * 2048), "n"(MB * 3072), "n"(MB * 4096), "n"(MB * 5120),
+                  "n"(MB * 6144), "n"(MB * 7168)
+                : "memory");
 #pragma unroll
-        for (int s = 0; s < kGemvWaves; ++s) v += red[s][q][l];
-        if constexpr (OUT_BF16) {
-            if (p.C) v += (float)((const __bf16 *)p.C)[(int64_t)m * p.ldc + n];
-            ((__bf16 *)p.D)[(int64_t)m * p.ldd + n] = (__bf16)v;
+            for (int w = 0; w < 8; ++w) v += s[w];
         } else {
-            if (p.C) v += ((const float *)p.C)[(int64_t)m * p.ldc + n];
-            ((float *)p.D)[(int64_t)m * p.ldd + n] = v;
+            for (int w = 0; w < 1 << kwlog; ++w, at += MB * 1024) {
+                float s;
+                asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(s) : "v"(at) : "memory");
+                v += s;
+            }
         }
+        gemv_put(p, split, m, n, v);
     }
 }
 
@@ -130,113 +180,257 @@ __device__ __forceinline__ void gemv_step(const u32x4 (&xf)[MB], uint32_t w, uin
 // (subnormals included).
 __device__ __forceinline__ bool fp16_scale(uint32_t code) { return code >= 104u && code <= 140u; }
 
-// Weight rows 16-byte aligned: each wave's K step of 512 (16 rows of 256
-// bytes) goes straight to LDS in whole rows, sixteen lanes a row, and is
-// read back a word per lane in the MFMA's own order, so that X is read in
-// runs of 64 bytes and a step of 32 K has one scale.  Chunk c of row r sits
-// at chunk c ^ r: the 16 rows of a read fall on all 64 banks.
-template <bool FP16, bool OUT_BF16, int MB>
-__global__ void __launch_bounds__(kGemvWaves * 64) gemv_mxfp4_staged_kernel(GemvArgs p) {
-    __shared__ __attribute__((aligned(16))) char stage[kGemvWaves][4096];
-    __shared__ float red[kGemvWaves][MB * 4][64];
+// W and X rows 16-byte aligned.  What bounds the product besides HBM is the
+// count of vector-memory instructions (a 1 KiB load holds the address unit
+// for about 31 cycles, whatever its lanes ask for), so X is read once per
+// workgroup: a workgroup keeps its K range [k_lo, k_hi) of X in LDS and walks
+// blocks of 16 weight rows (one workgroup per CU).  K ranges that do not
+// cover K (blockIdx.y; X too large for LDS, or too few rows for the CUs) leave
+// fp32 partial sums in the workspace for a second kernel to add in order.
+//
+// Its eight waves share the range in steps of 256 K: KW waves take the steps
+// of one block in turn, 8 / KW blocks at once.  A step's weights (16 rows of
+// 128 bytes) go straight to one of the wave's own R LDS slots in whole rows,
+// eight lanes a row, and are read back a word per lane in the MFMA's own
+// order, in which 32 K have one scale.  Chunk c of row r sits at chunk c ^
+// (r / 2 % 8): the 16 rows of a read fall on all 64 banks; rows of X are 16
+// bytes longer than a multiple of 512 for the same reason.  R - 1 steps are
+// in flight ahead of the one being multiplied, across blocks.
+//
+// SC: groups of 32 with K % 256 == 0 (0) or not (1), of 64 (2), of 128 (3) or
+// wider (4): a step's eight, eight, four, two codes or one of a row.
+constexpr int ring_slots(int MB) { return MB == 1 ? 4 : 2; }
+// LDS bytes a workgroup has for X beside its slots and its waves' sums.
+constexpr int x_bytes(int MB) { return 160 * 1024 - kGemvWaves * 2048 * ring_slots(MB) - 2 * MB * kGemvWaves * 1024; }
+
+template <bool FP16, int MB, int SC>
+__global__ void __launch_bounds__(kGemvWaves * 64, 2) gemv_mxfp4_staged_kernel(GemvArgs p) {
+    constexpr int R = ring_slots(MB);
+    __shared__ __attribute__((aligned(2048))) char ring[kGemvWaves][R][2048];
+    __shared__ float red[2][kGemvWaves][MB * 4][64];
+    extern __shared__ __attribute__((aligned(16))) char xs[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lc = lane & 15, lg = lane >> 4;
-    const int tn = blockIdx.x % p.tiles_n, tm = blockIdx.x / p.tiles_n;
-    const int n0 = tn * 16, m0 = tm * 16 * MB;
-    const int K = p.K;
-    const __amdgpu_buffer_rsrc_t rW = make_rsrc(p.W + (int64_t)n0 * p.ldw_bytes, span_bytes(p.N - n0, K / 2, p.ldw_bytes, 1));
-    char *ring = stage[wave];
-    const int64_t srow = n0 + lc < p.N ? n0 + lc : p.N - 1;
-    const uint8_t *sf = p.SF + srow * p.ldsf;
-    const uint16_t *x[MB];
-    bool xin[MB];
+    const int KW = 1 << p.kwlog, RW = kGemvWaves >> p.kwlog;
+    const int kw = wave & (KW - 1), rw = wave >> p.kwlog;
+    const int groups = (p.tiles_n + RW - 1) / RW;      // groups of RW blocks
+    const int m0 = blockIdx.z * 16 * MB, rows = p.M - m0 < 16 * MB ? p.M - m0 : 16 * MB;
+    const int k_lo = blockIdx.y * p.k_split, k_hi = p.K - k_lo < p.k_split ? p.K : k_lo + p.k_split;
+
+    // ---- X's range into LDS: an instruction moves 512 elements of a row
+    {
+        const __amdgpu_buffer_rsrc_t r = make_rsrc((const uint16_t *)p.X + (int64_t)m0 * p.ldx + k_lo,
+                                                   span_bytes(rows, k_hi - k_lo, p.ldx, 2));
+        const int per_row = (k_hi - k_lo + 511) / 512;
+        for (int m = 0; m < rows; ++m)
+            for (int c = wave; c < per_row; c += kGemvWaves) {
+                const int k = c * 512 + lane * 8;      // (whole vectors: K % 32 == 0)
+                dma_load<16>(r, xs + m * p.x_pitch + c * 1024,
+                             k < k_hi - k_lo ? (uint32_t)(m * p.ldx * 2) + k * 2 : kOOB);
+            }
+    }
+
+    // ---- the step being requested: its group and first K (the wave's rows
+    // are n0 + 16 rows of the group's)
+    int rg = blockIdx.x, rk = k_lo + kw * 256;
+    const uint8_t *wb, *sb;
+    uint32_t wspan, so;
+    auto enter = [&]() __attribute__((always_inline)) {
+        const int n0 = (rg * RW + rw) * 16;
+        const bool in = rg < groups && n0 < p.N;
+        wb = p.W + (in ? (int64_t)n0 * p.ldw_bytes : 0);
+        sb = p.SF + (in ? (int64_t)n0 * p.ldsf : 0);
+        wspan = in ? span_bytes(p.N - n0, p.K / 2, p.ldw_bytes, 1) : 0u;
+        const int last = in ? p.N - 1 - n0 : 0;
+        so = (uint32_t)((lc < last ? lc : last) * p.ldsf);   // (rows past N: never stored)
+    };
+    // eight rows an instruction: lane L writes chunk L % 8 of row 8 i + L / 8
+    // (rows past N lie past the resource, and so does a step past the range)
+    uint32_t wo[2];
+    const int wrow = lane >> 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        wo[i] = (uint32_t)((8 * i + wrow) * p.ldw_bytes) + (((lane & 7) ^ (((8 * i + wrow) >> 1) & 7)) << 4);
+    auto request_w = [&](int s) __attribute__((always_inline)) {
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(wb, rk < k_hi ? wspan : 0u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t o = wo[i] + (uint32_t)(rk / 2);
+            if (SC != 0 && rk / 2 + (((lane & 7) ^ (((8 * i + wrow) >> 1) & 7)) << 4) >= p.K / 2) o = kOOB;
+            dma_load<16>(r, ring[wave][s] + i * 1024, o);
+        }
+    };
+    // The scales of the step in slot S, as loaded (one load, of codes inside the
+    // row): they are looked at later.
+    uint32_t sc[R][2];
+    auto request_scales = [&](uint32_t (&c)[2]) __attribute__((always_inline)) {
+        const uint8_t *sf = sb + so;
+        c[1] = 0;
+        if constexpr (SC <= 1) {
+            const int n = p.K / 32, i = rk / 32;
+            const u32x2 v = ((const Bytes8 *)(sf + (i < n - 8 ? i : n - 8)))->v;
+            c[0] = v[0];
+            c[1] = v[1];
+        } else if constexpr (SC == 2) {
+            const int n = (p.K + 63) / 64, i = rk / 64;
+            c[0] = ((const Bytes4 *)(sf + (i < n - 4 ? i : n - 4)))->v;
+        } else if constexpr (SC == 3) {
+            const int n = (p.K + 127) / 128, i = rk / 128;
+            c[0] = ((const Bytes2 *)(sf + (i < n - 2 ? i : n - 2)))->v;
+        } else {
+            const int last = (p.K - 1) >> p.kshift, i = rk >> p.kshift;
+            c[0] = sf[i < last ? i : last];
+        }
+    };
+    // The step at k's eight codes, byte j of half t for K block 4 t + j, from
+    // its load (of the row's last codes, where the step's own would end past
+    // them: those before the step's drop out, and blocks past K, whose weights
+    // are zeros, get 2^0).
+    auto codes = [&](uint32_t (&c)[2], int k) __attribute__((always_inline)) {
+        constexpr int each = SC <= 1 ? 32 : SC == 2 ? 64 : 128, load = SC <= 1 ? 8 : SC == 2 ? 4 : 2;
+        if constexpr (SC >= 1 && SC <= 3) {
+            const int past = k / each - ((p.K + each - 1) / each - load);
+            if (past > 0) {
+                const uint64_t v = ((uint64_t)c[1] << 32) | c[0];
+                const uint64_t w = (v >> (8 * past)) | (0x7f7f7f7f7f7f7f7full << (8 * (load - past)));
+                c[0] = (uint32_t)w;
+                c[1] = (uint32_t)(w >> 32);
+            }
+        }
+        if constexpr (SC == 2) {
+            c[1] = __builtin_amdgcn_perm(c[0], c[0], 0x03030202u);
+            c[0] = __builtin_amdgcn_perm(c[0], c[0], 0x01010000u);
+        } else if constexpr (SC == 3) {
+            c[1] = __builtin_amdgcn_perm(c[0], c[0], 0x01010101u);
+            c[0] = __builtin_amdgcn_perm(c[0], c[0], 0x00000000u);
+        } else if constexpr (SC == 4) {
+            c[0] = c[1] = __builtin_amdgcn_perm(c[0], c[0], 0x00000000u);
+        }
+    };
+
+    // LDS addresses: this lane's word of chunk 0 of a slot (chunk c at ^ 16 c),
+    // and its eight elements of X's first 32 (rows past M: the last row again,
+    // whose sums are not stored)
+    typedef __attribute__((address_space(3))) char lds_char;
+    const uint32_t w0 = (uint32_t)(uintptr_t)(lds_char *)&ring[wave][0][0] + lc * 128 + ((lc >> 1) << 4) + 4 * lg;
+    uint32_t x0[MB];
 #pragma unroll
     for (int a = 0; a < MB; ++a) {
-        const int m = m0 + 16 * a + lc;
-        xin[a] = m < p.M;
-        x[a] = (const uint16_t *)p.X + (int64_t)(xin[a] ? m : 0) * p.ldx + 8 * lg;
+        const int m = 16 * a + lc < rows ? 16 * a + lc : rows - 1;
+        x0[a] = (uint32_t)(uintptr_t)(lds_char *)xs + m * p.x_pitch + 16 * lg;
     }
-    f32x4 acc[MB];
-#pragma unroll
-    for (int a = 0; a < MB; ++a) acc[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    for (int k0 = wave * 512; k0 < K; k0 += kGemvWaves * 512) {
-        // four rows an instruction: lane L writes chunk L % 16 of row 4 i + L / 16
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = 4 * i + lg, c = lc ^ row;
-            const int kb = k0 / 2 + c * 16;            // (rows past N lie past the resource)
-            dma_load<16>(rW, ring + i * 1024, kb < K / 2 ? (uint32_t)(row * p.ldw_bytes + kb) : kOOB);
+    f32x4 acc[MB];
+    int g = blockIdx.x, k0 = k_lo + kw * 256, b = 0;
+    auto request = [&](auto slot) __attribute__((always_inline)) {
+        constexpr int S = decltype(slot)::value;
+        request_scales(sc[S]);
+        request_w(S);
+        rk += KW * 256;
+        if (rk >= k_hi) {
+            rk = k_lo + kw * 256;
+            rg += gridDim.x;
+            enter();
         }
-        // byte j of sc[t]: the scale of K block 4 t + j
-        uint32_t sc[4];
-        if (p.kshift == 5 && k0 + 512 <= K) {
-            const u32x4 v = ((const Bytes16 *)(sf + k0 / 32))->v;
+    };
+    // One step, of slot S; false after the workgroup's last.
+    auto step = [&](auto slot) __attribute__((always_inline)) {
+        constexpr int S = decltype(slot)::value;
+        request(std::integral_constant<int, (S + R - 1) % R>());
+        if (k0 == k_lo + kw * 256) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) sc[t] = v[t];
-        } else {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                sc[t] = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = k0 + t * 128 + j * 32;
-                    sc[t] |= (k < K ? (uint32_t)sf[k >> p.kshift] : 127u) << (8 * j);
-                }
-            }
+            for (int a = 0; a < MB; ++a) acc[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        bool direct = true;
-        if constexpr (FP16) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) direct = direct && fp16_scale((sc[t] >> (8 * j)) & 0xffu);
-            direct = __all(direct);
-        }
-        u32x4 xf[4][MB];
-        auto load_x = [&](int t, int j) __attribute__((always_inline)) {
-            const int k = k0 + t * 128 + j * 32;
+        // this step's weights landed: only the R - 1 later steps' loads may run
+        wait_vmcnt<(R - 1) * 3>();
+        // (its scales are taken here in any case: left in flight on the way
+        // around the branch, their registers would have the compiler wait for
+        // every load)
+        asm volatile("" : "+v"(sc[S][0]), "+v"(sc[S][1]) : : "memory");
+        if (k0 < k_hi) {                               // (a wave past the range's last step: nothing)
+            // (reads in asm, waited for in their own statement: plain LDS
+            // reads would also wait for the loads into the other slots)
+            uint32_t q[8];
+            u32x4 xf[8][MB];
+            const uint32_t w = w0 + S * 2048;
+            asm volatile(
+                "ds_read_b32 %0, %8\n\tds_read_b32 %1, %9\n\tds_read_b32 %2, %10\n\tds_read_b32 %3, %11\n\t"
+                "ds_read_b32 %4, %12\n\tds_read_b32 %5, %13\n\tds_read_b32 %6, %14\n\tds_read_b32 %7, %15\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(q[0]), "=&v"(q[1]), "=&v"(q[2]), "=&v"(q[3]), "=&v"(q[4]), "=&v"(q[5]), "=&v"(q[6]),
+                  "=&v"(q[7])
+                : "v"(w), "v"(w ^ 16), "v"(w ^ 32), "v"(w ^ 48), "v"(w ^ 64), "v"(w ^ 80), "v"(w ^ 96), "v"(w ^ 112)
+                : "memory");
 #pragma unroll
             for (int a = 0; a < MB; ++a) {
-                xf[j][a] = u32x4{0u, 0u, 0u, 0u};
-                if (xin[a] && k < K) xf[j][a] = ((const Halves8 *)(x[a] + k))->v;
+                const uint32_t x = x0[a] + (uint32_t)(k0 - k_lo) * 2;
+                asm volatile(
+                    "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:64\n\tds_read_b128 %2, %8 offset:128\n\t"
+                    "ds_read_b128 %3, %8 offset:192\n\tds_read_b128 %4, %8 offset:256\n\t"
+                    "ds_read_b128 %5, %8 offset:320\n\tds_read_b128 %6, %8 offset:384\n\t"
+                    "ds_read_b128 %7, %8 offset:448\n\ts_waitcnt lgkmcnt(0)"
+                    : "=&v"(xf[0][a]), "=&v"(xf[1][a]), "=&v"(xf[2][a]), "=&v"(xf[3][a]), "=&v"(xf[4][a]),
+                      "=&v"(xf[5][a]), "=&v"(xf[6][a]), "=&v"(xf[7][a])
+                    : "v"(x)
+                    : "memory");
             }
-        };
+            uint32_t c[2] = {sc[S][0], sc[S][1]};
+            codes(c, k0);
+            bool direct = true;
+            if constexpr (FP16) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) load_x(0, j);
-        wait_vmcnt<0>();
-        asm volatile("" ::: "memory");
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (t > 0) load_x(t, j);
+                for (int j = 0; j < 8; ++j) direct = direct && fp16_scale((c[j / 4] >> (8 * (j % 4))) & 0xffu);
+                direct = __all(direct);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t w = *(const uint32_t *)(ring + lc * 256 + (((4 * t + j) ^ lc) << 4) + 4 * lg);
-                gemv_step<FP16, MB>(xf[j], w, (sc[t] >> (8 * j)) & 0xffu, direct, acc);
-            }
+            for (int j = 0; j < 8; ++j)
+                gemv_step<FP16, MB>(xf[j], q[j], (c[j / 4] >> (8 * (j % 4))) & 0xffu, direct, acc);
         }
-        wait_lgkmcnt0();                               // this step's reads done before the next overwrites it
-        asm volatile("" ::: "memory");
+        k0 += KW * 256;
+        if (k0 < k_hi) return true;
+        k0 = k_lo + kw * 256;
+        if (p.kwlog == 0) {                            // the wave's own block: no join
+#pragma unroll
+            for (int a = 0; a < MB; ++a)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    gemv_put(p, blockIdx.y, m0 + 16 * a + 4 * lg + r, (g * RW + rw) * 16 + lc, acc[a][r]);
+        } else {
+#pragma unroll
+            for (int a = 0; a < MB; ++a)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) red[b][wave][a * 4 + r][lane] = acc[a][r];
+            wait_lgkmcnt0();
+            barrier();                                 // (the other half's readers passed the last one)
+            gemv_join<MB>(red[b], p, p.kwlog, blockIdx.y, m0, g * RW * 16);
+            b ^= 1;
+        }
+        g += gridDim.x;
+        return g < groups;
+    };
+
+    enter();
+    static_for<0, R - 1>([&](auto i) __attribute__((always_inline)) { request(i); });
+    wait_vmcnt<(R - 1) * 3>();            // X landed
+    barrier();
+    if constexpr (R == 4) {
+        while (step(std::integral_constant<int, 0>()) && step(std::integral_constant<int, 1>()) &&
+               step(std::integral_constant<int, 2>()) && step(std::integral_constant<int, 3>())) {
+        }
+    } else {
+        while (step(std::integral_constant<int, 0>()) && step(std::integral_constant<int, 1>())) {
+        }
     }
-#pragma unroll
-    for (int a = 0; a < MB; ++a)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) red[wave][a * 4 + r][lane] = acc[a][r];
-    __syncthreads();
-    gemv_join<OUT_BF16, MB>(red, p, m0, n0);
+    wait_vmcnt<0>();                                   // (requests past the last group: nothing in flight into LDS at the end)
 }
 
 // Weight rows that start at any byte.
-template <bool FP16, bool OUT_BF16, int MB>
+template <bool FP16, int MB>
 __global__ void __launch_bounds__(kGemvWaves * 64) gemv_mxfp4_kernel(GemvArgs p) {
     __shared__ float red[kGemvWaves][MB * 4][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lc = lane & 15, lg = lane >> 4;
-    const int tn = blockIdx.x % p.tiles_n, tm = blockIdx.x / p.tiles_n;
-    const int n0 = tn * 16, m0 = tm * 16 * MB;
+    const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MB;
     const int K = p.K;
     // (rows past N: the last row again, never stored)
     const int64_t wrow = n0 + lc < p.N ? n0 + lc : p.N - 1;
@@ -289,31 +483,105 @@ __global__ void __launch_bounds__(kGemvWaves * 64) gemv_mxfp4_kernel(GemvArgs p)
 #pragma unroll
         for (int r = 0; r < 4; ++r) red[wave][a * 4 + r][lane] = acc[a][r];
     __syncthreads();
-    gemv_join<OUT_BF16, MB>(red, p, m0, n0);
+    gemv_join<MB>(red, p, 3, 0, m0, n0);
 }
 
-template <bool FP16, bool OUT_BF16, int MB>
-hipError_t go_gemv(const GemvArgs &p, unsigned grid, hipStream_t s) {
-    // 16-byte weight rows
-    if (((uintptr_t)p.W | (uintptr_t)p.ldw_bytes) % 16 == 0)
-        hipLaunchKernelGGL((gemv_mxfp4_staged_kernel<FP16, OUT_BF16, MB>), dim3(grid), dim3(kGemvWaves * 64), 0, s, p);
-    else
-        hipLaunchKernelGGL((gemv_mxfp4_kernel<FP16, OUT_BF16, MB>), dim3(grid), dim3(kGemvWaves * 64), 0, s, p);
+struct GemvPlan {
+    bool staged;
+    int mb, splits, k_split, kwlog;
+};
+
+// How a call runs.  K ranges of the staged kernel: multiples of 256 (2048
+// where LDS holds that much of M rows, so that all eight waves have a step of
+// every block), as many as X needs; more where the blocks of rows leave half
+// of the CUs idle, down to ranges of 2048.
+inline GemvPlan plan_gemv(int64_t M, int64_t N, int64_t K, bool aligned, bool workspace) {
+    GemvPlan g;
+    g.mb = M > 16 ? 2 : 1;
+    const int64_t rows = M < 16 * g.mb ? M : 16 * g.mb;
+    int64_t most = (x_bytes(g.mb) / rows - 16) / 2 / 512 * 512;
+    if (most > 2048) most = most / 2048 * 2048;
+    int64_t S = K > 0 ? (K + most - 1) / most : 1;
+    const int64_t tiles = (N + 15) / 16, want = 256 / (tiles < 256 ? tiles : 256);
+    if (S < want && K >= 4096) S = want < K / 2048 ? want : K / 2048;
+    int64_t ks = (K + S - 1) / S;
+    ks = ks > 1024 ? (ks + 2047) / 2048 * 2048 : (ks + 255) / 256 * 256;
+    if (ks > most) ks = most;
+    g.k_split = (int)ks;
+    g.splits = K > 0 ? (int)((K + ks - 1) / ks) : 1;
+    // Waves per block: what gives the busiest wave the fewest steps; among
+    // those, from ranges of 4096 on, the most waves that have four steps of a
+    // block each (together they read longer runs of its rows: 131072 x 8192
+    // for four rows 100 us with eight waves, 113 with one), else the fewest
+    // (one wave needs no join and no barrier: 4096 x 14336 for 16 rows, ranges
+    // of 2048, 13.2 us against 14.9 with two and 16.3 with eight).
+    const int64_t steps = ((ks < K ? ks : K) + 255) / 256;
+    const int64_t tiles_m = (M + 16 * g.mb - 1) / (16 * g.mb);
+    const int64_t per = 256 / (g.splits * tiles_m) > 1 ? 256 / (g.splits * tiles_m) : 1;
+    int64_t best = 0;
+    for (int l = 0; l <= 3; ++l) {
+        const int64_t groups = (tiles + (8 >> l) - 1) / (8 >> l), each = (steps + (1 << l) - 1) >> l;
+        const int64_t busiest = (groups + per - 1) / per * each;
+        if (l == 0 || busiest < best || (busiest == best && steps >= 16 && each >= 4)) {
+            best = busiest;
+            g.kwlog = l;
+        }
+    }
+    // (a step's scales are loaded together: rows hold a whole step)
+    g.staged = aligned && K >= 256 && (g.splits == 1 || workspace);
+    if (!g.staged) g.splits = 1;
+    return g;
+}
+
+template <bool FP16, int MB>
+hipError_t launch_gemv(const GemvPlan &g, GemvArgs &p, hipStream_t s) {
+    const dim3 threads(kGemvWaves * 64);
+    const unsigned tiles_m = (unsigned)((p.M + 16 * MB - 1) / (16 * MB));
+    if (!g.staged) {
+        hipLaunchKernelGGL((gemv_mxfp4_kernel<FP16, MB>), dim3((unsigned)p.tiles_n, tiles_m), threads, 0, s, p);
+        return hipGetLastError();
+    }
+    const int rows = p.M < 16 * MB ? p.M : 16 * MB;
+    const int rw = kGemvWaves >> p.kwlog, groups = (p.tiles_n + rw - 1) / rw;
+    const int span = p.k_split < p.K ? p.k_split : p.K;
+    p.x_pitch = (span + 511) / 512 * 1024 + 16;
+    int per = tg_api::cu_count(s) / (int)(g.splits * tiles_m);
+    if (per <= 0) per = 1;
+    const dim3 grid((unsigned)(groups < per ? groups : per), (unsigned)g.splits, tiles_m);
+    const size_t lds = (size_t)rows * p.x_pitch;
+#define TG_GEMV(sc) hipLaunchKernelGGL((gemv_mxfp4_staged_kernel<FP16, MB, sc>), grid, threads, lds, s, p)
+    switch (p.kshift) {
+    case 5:
+        if (p.K % 256 == 0)
+            TG_GEMV(0);
+        else
+            TG_GEMV(1);
+        break;
+    case 6: TG_GEMV(2); break;
+    case 7: TG_GEMV(3); break;
+    default: TG_GEMV(4); break;
+    }
+#undef TG_GEMV
     return hipGetLastError();
 }
 
-template <bool FP16, bool OUT_BF16>
-hipError_t launch_gemv(const GemvArgs &p, unsigned grid, hipStream_t s) {
-    return p.M > 16 ? go_gemv<FP16, OUT_BF16, 2>(p, grid, s) : go_gemv<FP16, OUT_BF16, 1>(p, grid, s);
+template <bool FP16>
+hipError_t launch_gemv_rows(const GemvPlan &g, GemvArgs &p, hipStream_t s) {
+    return g.mb == 2 ? launch_gemv<FP16, 2>(g, p, s) : launch_gemv<FP16, 1>(g, p, s);
 }
 
 }  // namespace tg
 
 extern "C" {
 
+size_t gemv_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N <= 0 || K <= 0 || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return 0;
+    return splitk_bytes(M, N, tg::plan_gemv(M, N, K, true, true).splits);
+}
+
 gemm_status gemv_mxfp4(int64_t M, int64_t N, int64_t K, int64_t kblock, const void *X, int64_t ldx, int x_type,
                        const void *W, int64_t ldw, const void *SFW, int64_t ldsfw, const void *C, int64_t ldc, void *D,
-                       int64_t ldd, int out_type, hipStream_t stream) {
+                       int64_t ldd, int out_type, void *workspace, size_t workspace_bytes, hipStream_t stream) {
     // (X's 2-byte alignment is checked below: W's rows may start at any byte)
     const Common a{M, N, K, X, ldx, W, ldw, C, ldc, D, ldd, out_type, 1};
     bool none = false;
@@ -327,10 +595,13 @@ gemm_status gemv_mxfp4(int64_t M, int64_t N, int64_t K, int64_t kblock, const vo
         kshift = __builtin_ctzll((uint64_t)kblock);
     }
     if (ldsfw < (K + kblock - 1) / kblock) return GEMM_ERR_BAD_LD;
+    if (ldsfw >= kMaxLdBytes || M > (1 << 20)) return GEMM_ERR_UNSUPPORTED;
     if (K > 0 && !SFW) return GEMM_ERR_NULL_POINTER;
-    if (misaligned(X, 2)) return GEMM_ERR_MISALIGNED;
-    const int64_t tn = (N + 15) / 16, tm = M > 16 ? (M + 31) / 32 : 1;
-    if (tn * tm >= kMaxDim) return GEMM_ERR_UNSUPPORTED;
+    if (misaligned(X, 2) || (uintptr_t)workspace % 256 != 0) return GEMM_ERR_MISALIGNED;
+    const bool aligned = (((uintptr_t)W | (uintptr_t)(ldw / 2) | (uintptr_t)X | (uintptr_t)(ldx * 2)) & 15) == 0;
+    const bool room = workspace && workspace_bytes >= gemv_mxfp4_workspace_bytes(M, N, K) &&
+                      splitk_ldw(N) * 4 < kMaxLdBytes;
+    const tg::GemvPlan g = tg::plan_gemv(M, N, K, aligned, room);
     tg::GemvArgs p;
     p.X = X;
     p.W = (const uint8_t *)W;
@@ -346,15 +617,16 @@ gemm_status gemv_mxfp4(int64_t M, int64_t N, int64_t K, int64_t kblock, const vo
     p.N = (int)N;
     p.K = (int)K;
     p.kshift = kshift;
-    p.tiles_n = (int)tn;
-    const unsigned grid = (unsigned)(tn * tm);
-    const bool b = out_type == GEMM_OUT_BF16;
-    hipError_t e;
-    if (x_type == GEMM_TYPE_FP16)
-        e = b ? tg::launch_gemv<true, true>(p, grid, stream) : tg::launch_gemv<true, false>(p, grid, stream);
-    else
-        e = b ? tg::launch_gemv<false, true>(p, grid, stream) : tg::launch_gemv<false, false>(p, grid, stream);
-    return launched(e);
+    p.tiles_n = (int)((N + 15) / 16);
+    p.out_bf16 = out_type == GEMM_OUT_BF16;
+    p.kwlog = g.kwlog;
+    p.k_split = g.k_split;
+    p.x_pitch = 0;
+    p.ws = g.splits > 1 ? (float *)workspace : nullptr;
+    p.ldws = splitk_ldw(N);
+    st = launched(x_type == GEMM_TYPE_FP16 ? tg::launch_gemv_rows<true>(g, p, stream)
+                                           : tg::launch_gemv_rows<false>(g, p, stream));
+    return st != GEMM_OK || g.splits == 1 ? st : reduce_splits(a, workspace, g.splits, stream);
 }
 
 }  // extern "C"

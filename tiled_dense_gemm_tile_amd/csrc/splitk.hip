@@ -22,7 +22,16 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(SplitReduceArgs a) {
     // partial slices: 16-byte aligned rows (ldw % 4 == 0, 256-byte aligned base)
     const float *w = a.ws + (int64_t)row * a.ldw + col;
     f32x4 s = *(const f32x4 *)w;
-    for (int k = 1; k < a.splits; ++k) s += *(const f32x4 *)(w + (int64_t)k * a.slice);
+    // (four slices' loads in flight; added in order)
+    int k = 1;
+    for (; k + 4 <= a.splits; k += 4) {
+        f32x4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = *(const f32x4 *)(w + (int64_t)(k + i) * a.slice);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s += v[i];
+    }
+    for (; k < a.splits; ++k) s += *(const f32x4 *)(w + (int64_t)k * a.slice);
     const int nv = a.N - col < 4 ? a.N - col : 4;      // columns of this vector inside N
     if (a.C) {
         if constexpr (OUT_BF16) {

@@ -232,13 +232,21 @@ def gemm_wgrad_mxfp8(dY, Q, SF, C=None, out_dtype=None, D=None, workspace=None):
     return D
 
 
-def gemv_mxfp4(X, W, SFW, kblock=32, C=None, out_dtype=None, D=None):
+def gemv_mxfp4_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Workspace bytes with which :func:`gemv_mxfp4` may cut K (0: it would
+    not)."""
+    return _load().gemv_mxfp4_workspace_bytes(M, N, K)
+
+
+def gemv_mxfp4(X, W, SFW, kblock=32, C=None, out_dtype=None, D=None, workspace=None):
     """A few rows times 4-bit weights: D (M, N) = X @ W^T + C, X (M, K)
     bfloat16 or float16, W (N, K/2) bytes of two e2m1 codes and SFW (N,
     ceil(K / kblock)) e8m0 codes, as :func:`gemm_mxfp4` and
     :func:`gemm_mx_kblock` take B and SFB.  X is not quantised.  Made for up
     to 16 rows, right for any number.  ``out_dtype`` float32 (default) or
-    bfloat16; C of that type may be D."""
+    bfloat16; C of that type may be D.  ``workspace``: a device byte tensor,
+    256-byte aligned, of :func:`gemv_mxfp4_workspace_bytes` bytes (allocated
+    per call when not given; a smaller one runs without cutting K)."""
     if X.dim() != 2 or (X.dtype != torch.bfloat16 and X.dtype != torch.float16):
         raise TypeError("X must be a 2-D bfloat16 or float16 tensor")
     dev = _device(X)
@@ -250,5 +258,7 @@ def gemv_mxfp4(X, W, SFW, kblock=32, C=None, out_dtype=None, D=None):
     wp, ldw = _matrix("W", W, (N, K // 2), _E2M1, dev)
     s = _matrix("SFW", SFW, (N, -(-K // kblock)), _E8M0, dev)
     D, out, cd = _product_out((M, N), dev, C, D, out_dtype)
-    _run(_load().gemv_mxfp4, dev, M, N, K, kblock, *x, _TYPES[X.dtype], wp, 2 * ldw, *s, *cd, out)
+    L = _load()
+    workspace, *ws = _workspace(workspace, workspace is None and L.gemv_mxfp4_workspace_bytes(M, N, K), dev)
+    _run(L.gemv_mxfp4, dev, M, N, K, kblock, *x, _TYPES[X.dtype], wp, 2 * ldw, *s, *cd, out, *ws)
     return D
