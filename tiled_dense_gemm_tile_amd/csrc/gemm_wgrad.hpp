@@ -50,6 +50,30 @@ __device__ __forceinline__ void fp8_up(u32x4 q, uint32_t code, u32x4 &lo, u32x4 
     }
 }
 
+// Four columns of D = v + C, at any element alignment.
+template <bool OUT_BF16>
+__device__ __forceinline__ void wgrad_put(f32x4 v, const void *C, int64_t ldc, void *D, int64_t ldd, int m, int n) {
+    struct __attribute__((packed, aligned(4))) F4 {
+        f32x4 v;
+    };
+    struct __attribute__((packed, aligned(2))) H4 {
+        u32x2 v;
+    };
+    if constexpr (OUT_BF16) {
+        if (C) {
+            const u32x2 c = ((const H4 *)((const uint16_t *)C + (int64_t)m * ldc + n))->v;
+            v[0] += __builtin_bit_cast(float, c[0] << 16);
+            v[1] += __builtin_bit_cast(float, c[0] & 0xffff0000u);
+            v[2] += __builtin_bit_cast(float, c[1] << 16);
+            v[3] += __builtin_bit_cast(float, c[1] & 0xffff0000u);
+        }
+        ((H4 *)((uint16_t *)D + (int64_t)m * ldd + n))->v = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    } else {
+        if (C) v += ((const F4 *)((const float *)C + (int64_t)m * ldc + n))->v;
+        ((F4 *)((float *)D + (int64_t)m * ldd + n))->v = v;
+    }
+}
+
 typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
 
 template <bool OUT_BF16>
@@ -150,12 +174,6 @@ __global__ void __launch_bounds__(256) gemm_wgrad_any_kernel(WgradArgs p) {
 
     // Block (i, j) holds its transpose: lane l has row 16 i + l % 16 of the
     // wave's 64 and columns 16 j + 4 (l / 16) .. + 3 (whole vectors, N % 32 == 0).
-    struct __attribute__((packed, aligned(4))) F4 {
-        f32x4 v;
-    };
-    struct __attribute__((packed, aligned(2))) H4 {
-        u32x2 v;
-    };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int m = m0 + wm * 64 + 16 * i + fr;
@@ -164,22 +182,11 @@ __global__ void __launch_bounds__(256) gemm_wgrad_any_kernel(WgradArgs p) {
         for (int j = 0; j < 4; ++j) {
             const int n = n0 + wn * 64 + 16 * j + 4 * fq;
             if (n >= p.N) continue;
-            f32x4 v = acc[i][j];
+            const f32x4 v = acc[i][j];
             if (p.ws) {
                 *(f32x4 *)(p.ws + ((int64_t)split * p.M + m) * p.ldw + n) = v;
-            } else if constexpr (OUT_BF16) {
-                if (p.C) {
-                    const u32x2 c = ((const H4 *)((const uint16_t *)p.C + (int64_t)m * p.ldc + n))->v;
-                    v[0] += __builtin_bit_cast(float, c[0] << 16);
-                    v[1] += __builtin_bit_cast(float, c[0] & 0xffff0000u);
-                    v[2] += __builtin_bit_cast(float, c[1] << 16);
-                    v[3] += __builtin_bit_cast(float, c[1] & 0xffff0000u);
-                }
-                ((H4 *)((uint16_t *)p.D + (int64_t)m * p.ldd + n))->v =
-                    u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
             } else {
-                if (p.C) v += ((const F4 *)((const float *)p.C + (int64_t)m * p.ldc + n))->v;
-                ((F4 *)((float *)p.D + (int64_t)m * p.ldd + n))->v = v;
+                wgrad_put<OUT_BF16>(v, p.C, p.ldc, p.D, p.ldd, m, n);
             }
         }
     }

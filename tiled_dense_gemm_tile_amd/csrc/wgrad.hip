@@ -3,19 +3,49 @@
 #include "../../include/tilegemm_ops.h"
 #include "api.hpp"
 #include "gemm_wgrad.hpp"
+#include "gemm_wgrad_w4.hpp"
 
 using namespace tg_api;
 
 namespace {
 
-// K ranges of a call: as many as fill the GPU's 256 CUs with 128 x 128 tiles
-// two deep, each of at least 1024 rows.
-int wgrad_splits(int64_t M, int64_t N, int64_t K) {
+// How a call runs: the four-wave kernel or the one that takes every call, and
+// the K ranges of its tiles (four-wave: of the tiles past the first `full`).
+struct WgradPlan {
+    bool w4;
+    int splits;
+    int64_t full, rest;
+    size_t bytes;                                      // workspace
+};
+
+constexpr int64_t kCus = 256;
+
+// `rows16`: A and B start their rows on 16 bytes.
+WgradPlan plan_wgrad(int64_t M, int64_t N, int64_t K, bool rows16, bool workspace) {
+    WgradPlan g = {};
+    const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256);
+    g.w4 = rows16 && N >= 256 && K > 0;
+    if (g.w4) {
+        g.full = t256;
+        g.splits = 1;
+        const int64_t rest = t256 % kCus;
+        int64_t s = rest ? kCus / rest : 1;
+        if (K / 512 < s) s = K / 512;
+        if (s >= 2 && workspace) {
+            g.rest = rest;
+            g.full = t256 - rest;
+            g.splits = effective_splits(K, (int)s, 64);
+            g.bytes = (size_t)g.splits * (size_t)rest * 65536 * 4;
+        }
+        return g;
+    }
     const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
-    int64_t s = tiles ? 512 / tiles : 1;
+    int64_t s = tiles ? 2 * kCus / tiles : 1;
     if (K / 1024 < s) s = K / 1024;
     if (s > kMaxSplits) s = kMaxSplits;
-    return s < 2 ? 1 : effective_splits(K, (int)s, 64);
+    g.splits = s < 2 || !workspace ? 1 : effective_splits(K, (int)s, 64);
+    g.bytes = splitk_bytes(M, N, g.splits);
+    return g;
 }
 
 }  // namespace
@@ -24,7 +54,9 @@ extern "C" {
 
 size_t gemm_wgrad_mxfp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0 || K <= 0 || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return 0;
-    return splitk_bytes(M, N, wgrad_splits(M, N, K));
+    // (whichever kernel the operands' alignment admits)
+    const size_t a = plan_wgrad(M, N, K, true, true).bytes, b = plan_wgrad(M, N, K, false, true).bytes;
+    return a > b ? a : b;
 }
 
 gemm_status gemm_wgrad_mxfp8(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *B, int64_t ldb,
@@ -40,8 +72,54 @@ gemm_status gemm_wgrad_mxfp8(int64_t M, int64_t N, int64_t K, const void *A, int
     if (ldsfb < N / 32) return GEMM_ERR_BAD_LD;
     if (K > 0 && !SFB) return GEMM_ERR_NULL_POINTER;
     if (misaligned(A, 2) || (uintptr_t)workspace % 256 != 0) return GEMM_ERR_MISALIGNED;
-    int S = K > 0 ? wgrad_splits(M, N, K) : 1;
-    if (S > 1 && (!workspace || workspace_bytes < splitk_bytes(M, N, S) || splitk_ldw(N) * 4 >= kMaxLdBytes)) S = 1;
+    const bool rows16 = (((uintptr_t)A | (uintptr_t)(lda * 2) | (uintptr_t)B | (uintptr_t)ldb) & 15) == 0;
+    WgradPlan g = plan_wgrad(M, N, K, rows16, true);
+    if (g.splits > 1 &&
+        (!workspace || workspace_bytes < g.bytes || (!g.w4 && splitk_ldw(N) * 4 >= kMaxLdBytes)))
+        g = plan_wgrad(M, N, K, rows16, false);
+    const bool bf16 = out_type == GEMM_OUT_BF16;
+    const int64_t kt = (K + 63) / 64, k_split = (kt + g.splits - 1) / g.splits * 64;
+    if (g.w4) {
+        tg::Wgrad4Args p;
+        p.A = A;
+        p.B = B;
+        p.SF = (const uint8_t *)SFB;
+        p.C = C;
+        p.D = D;
+        p.lda = lda;
+        p.ldb = ldb;
+        p.ldsf = ldsfb;
+        p.ldc = ldc;
+        p.ldd = ldd;
+        p.M = (int)M;
+        p.N = (int)N;
+        p.K = (int)K;
+        p.group_m = 4;
+        p.tiles_m = (int)((M + 255) / 256);
+        p.tiles_n = (int)((N + 255) / 256);
+        const int64_t grid = g.full + g.rest * g.splits;
+        if (grid >= kMaxDim) return GEMM_ERR_UNSUPPORTED;
+        p.full = (int)g.full;
+        p.splits = g.splits;
+        p.k_split = (int)k_split;
+        p.ws = (float *)workspace;
+        const uintptr_t vb = bf16 ? 8 : 16;
+        tg::F16Epi e;
+        e.vec_d = ((uintptr_t)D % vb) == 0 && ldd % 4 == 0;
+        e.vec_c = C && ((uintptr_t)C % vb) == 0 && ldc % 4 == 0;
+        if (bf16)
+            hipLaunchKernelGGL((tg::gemm_wgrad_w4_kernel<true>), dim3((unsigned)grid), dim3(256), 0, stream, p, e);
+        else
+            hipLaunchKernelGGL((tg::gemm_wgrad_w4_kernel<false>), dim3((unsigned)grid), dim3(256), 0, stream, p, e);
+        st = launched(hipGetLastError());
+        if (st != GEMM_OK || g.splits == 1) return st;
+        const dim3 blocks((unsigned)(g.rest * 64));
+        if (bf16)
+            hipLaunchKernelGGL((tg::wgrad_reduce_kernel<true>), blocks, dim3(256), 0, stream, p);
+        else
+            hipLaunchKernelGGL((tg::wgrad_reduce_kernel<false>), blocks, dim3(256), 0, stream, p);
+        return launched(hipGetLastError());
+    }
     tg::WgradArgs p;
     p.A = A;
     p.B = B;
@@ -59,18 +137,17 @@ gemm_status gemm_wgrad_mxfp8(int64_t M, int64_t N, int64_t K, const void *A, int
     p.group_m = 8;
     p.tiles_m = (int)((M + 127) / 128);
     p.tiles_n = (int)((N + 127) / 128);
-    p.ws = S > 1 ? (float *)workspace : nullptr;
+    p.ws = g.splits > 1 ? (float *)workspace : nullptr;
     p.ldw = splitk_ldw(N);
-    const int64_t kt = (K + 63) / 64;
-    p.k_split = (int)((kt + S - 1) / S * 64);
-    const int64_t grid = (int64_t)p.tiles_m * p.tiles_n * S;
+    p.k_split = (int)k_split;
+    const int64_t grid = (int64_t)p.tiles_m * p.tiles_n * g.splits;
     if (grid >= kMaxDim) return GEMM_ERR_UNSUPPORTED;
-    if (out_type == GEMM_OUT_BF16)
+    if (bf16)
         hipLaunchKernelGGL((tg::gemm_wgrad_any_kernel<true>), dim3((unsigned)grid), dim3(256), 0, stream, p);
     else
         hipLaunchKernelGGL((tg::gemm_wgrad_any_kernel<false>), dim3((unsigned)grid), dim3(256), 0, stream, p);
     st = launched(hipGetLastError());
-    return st != GEMM_OK || S == 1 ? st : reduce_splits(a, workspace, S, stream);
+    return st != GEMM_OK || g.splits == 1 ? st : reduce_splits(a, workspace, g.splits, stream);
 }
 
 }  // extern "C"
