@@ -106,8 +106,37 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
     const int K = split < 0 ? p.K : (p.K - k_lo < p.k_split ? p.K - k_lo : p.k_split);
     const int nt = (K + KT - 1) / KT;
 
+    // A K tile's resource: based at its first row, ending with its last row's
+    // last element (A: with the 16-byte block of it -- the range check is per
+    // dword, and the block lies in the same page), moved on by 64 rows a tile.
+    // All loads of a tile share it, and its few scalar instructions are spread
+    // over the MFMAs (each pinned by an empty asm): built for each load, the
+    // resources' ~20 scalar instructions held up the MFMAs around it (1754 us
+    // at 14336 x 4096 x 16384).
+    struct Panel {
+        const char *base;
+        uint32_t span;
+        int rows;                                      // left, from base on
+        __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc() const { return make_rsrc(base, span); }
+        __device__ __forceinline__ void set_span(uint32_t ld_bytes, uint32_t row_bytes, uint32_t round) {
+            const int r = rows < KT ? rows : KT;
+            span = r <= 0 ? 0u : ((uint32_t)(r - 1) * ld_bytes + row_bytes + round) & ~round;
+            asm volatile("" : "+s"(span));
+        }
+        __device__ __forceinline__ void move(int64_t step) {
+            base += step;
+            rows -= KT;
+            asm volatile("" : "+s"(base), "+s"(rows));
+        }
+    };
+
     // ---- A: direct global -> LDS, as gemm_f16_w4t_kernel's AT operand
-    const char *a_base = (const char *)p.A + (int64_t)k_lo * p.lda * 2;
+    Panel pa, pb;
+    pa.base = (const char *)p.A + ((int64_t)k_lo * p.lda + m0) * 2;
+    pa.rows = K;
+    const uint32_t a_row = (uint32_t)(M - m0) * 2, a_ld = (uint32_t)(p.lda * 2);
+    pa.set_span(a_ld, a_row, 15u);
+    const int64_t a_step = (int64_t)KT * p.lda * 2;
     uint32_t a_off[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -115,11 +144,9 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
         const int lchk = ((lane & 31) >> 1) ^ (row & 3) ^ (((row >> 3) & 1) << 2);
         a_off[j] = (uint32_t)((row * p.lda + lchk * 16 + (lane & 1) * 8) * 2);
     }
-    auto dma_a = [&](int t, int j) __attribute__((always_inline)) {
-        const int k0 = t * KT;
-        const uint32_t span = (span_bytes(K - k0, M - m0, p.lda, 2) + 15u) & ~15u;
-        const __amdgpu_buffer_rsrc_t r = make_rsrc(a_base + ((int64_t)k0 * p.lda + m0) * 2, span);
-        dma_load<16>(r, smem + (t & 1) * SLOT + (j * 4 + wave) * 1024, a_off[j]);
+    char *const a_lds = smem + wave * 1024;
+    auto dma_a = [&](__amdgpu_buffer_rsrc_t r, int slot, int j) __attribute__((always_inline)) {
+        dma_load<16>(r, a_lds + slot * SLOT + j * 4096, a_off[j]);
     };
 
     // ---- B: thread t holds row t / 4 of a K tile, columns 16 (t % 4) + 64 j
@@ -129,21 +156,27 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
     const int br = tid >> 2, bt = tid & 3;
     const uint32_t b_off = (uint32_t)(br * p.ldb) + bt * 16;
     const int nb = N / 32, s_at = n0 / 32 < nb - 8 ? n0 / 32 : nb - 8, s_shift = 8 * (n0 / 32 - s_at);
-    const char *b_base = (const char *)p.B + (int64_t)k_lo * p.ldb + n0;
-    const uint8_t *s_base = p.SF + (int64_t)k_lo * p.ldsf + s_at;
+    pb.base = (const char *)p.B + (int64_t)k_lo * p.ldb + n0;
+    pb.rows = K;
+    const uint32_t b_row = (uint32_t)(N - n0), b_ld = (uint32_t)p.ldb;
+    pb.set_span(b_ld, b_row, 0u);
+    const int64_t b_step = (int64_t)KT * p.ldb;
     struct __attribute__((packed, aligned(1))) U64 {
         uint64_t v;
     };
     u32x4 vb[4];
     uint64_t vs;
-    auto load_b = [&](int t, int j) __attribute__((always_inline)) {
-        const int k0 = t * KT;
-        const __amdgpu_buffer_rsrc_t r = make_rsrc(b_base + (int64_t)k0 * p.ldb, span_bytes(K - k0, N - n0, p.ldb, 1));
+    auto load_b = [&](__amdgpu_buffer_rsrc_t r, int j) __attribute__((always_inline)) {
         vb[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b_off + 64 * j, 0, 0));
     };
-    auto load_s = [&](int t) __attribute__((always_inline)) {
-        const int row = t * KT + br < K ? t * KT + br : K - 1;
-        vs = ((const U64 *)(s_base + (int64_t)row * p.ldsf))->v;
+    const uint8_t *s_row = p.SF + (int64_t)k_lo * p.ldsf + s_at + (int64_t)(br < K ? br : K - 1) * p.ldsf;
+    const int64_t s_step = (int64_t)KT * p.ldsf;
+    int s_left = K - 1 - br;                           // rows from s_row's to the last
+    auto load_s = [&]() __attribute__((always_inline)) { vs = ((const U64 *)s_row)->v; };
+    auto next_s = [&]() __attribute__((always_inline)) {
+        // (the row 64 further; past K: the last)
+        s_left -= KT;
+        s_row += s_left >= 0 ? s_step : s_left > -KT ? (int64_t)(s_left + KT) * p.ldsf : 0;
     };
     // Vector j converted, four columns a step; written as two 16-byte halves.
     // (LDS row br, 32-byte chunk bt + 4 j at ^ (br % 4) ^ 4 (br / 8 % 2), the
@@ -160,7 +193,8 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
         sc[1] = (uint32_t)(s >> 32);
     };
     u32x4 half;
-    auto convert = [&](auto step, int slot) __attribute__((always_inline)) {
+    auto convert = [&](auto step, auto slot) __attribute__((always_inline)) {
+        constexpr int at = decltype(slot)::value * SLOT;
         constexpr int j = decltype(step)::value / 4, i = decltype(step)::value % 4;
         const float scale = __builtin_bit_cast(
             float, (j & 1) ? (sc[j / 2] & 0xff0000u) << 7 : (sc[j / 2] & 0xffu) << 23);
@@ -169,11 +203,12 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
         half[2 * (i & 1) + 1] =
             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vb[j][i], scale, true));
         if constexpr (i & 1) {
-            const uint32_t at = b_put[j & 1] + slot * SLOT;
-            if constexpr (i == 1)
-                asm volatile("ds_write_b128 %0, %1 offset:%c2" : : "v"(at), "v"(half), "n"(256 * (j / 2)) : "memory");
-            else
-                asm volatile("ds_write_b128 %0, %1 offset:%c2" : : "v"(at), "v"(half), "n"(256 * (j / 2) + 16) : "memory");
+            const uint32_t put = b_put[j & 1];
+            const u32x4 v = half;
+            asm volatile("ds_write_b128 %0, %1 offset:%c2"
+                         :
+                         : "v"(put), "v"(v), "n"(at + 256 * (j / 2) + 16 * (i / 2))
+                         : "memory");
         }
     };
 
@@ -188,21 +223,22 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
     for (int b = 0; b < TM; ++b) a_mn[b] = mn_base(wm, b);
 #pragma unroll
     for (int b = 0; b < TN; ++b) b_mn[b] = B_BASE + mn_base(wn, b);
-    auto ldfrag_tr = [&](uint32_t a) __attribute__((always_inline)) {
+    auto ldfrag_tr = [&](uint32_t a, auto off) __attribute__((always_inline)) {
         u32x2 lo, hi;
-        asm volatile("ds_read_b64_tr_b16 %0, %1" : "=v"(lo) : "v"(a));
-        asm volatile("ds_read_b64_tr_b16 %0, %1 offset:2048" : "=v"(hi) : "v"(a));
+        asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%c2" : "=v"(lo) : "v"(a), "n"(decltype(off)::value));
+        asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%c2" : "=v"(hi) : "v"(a), "n"(decltype(off)::value + 2048));
         return u32x4{lo[0], lo[1], hi[0], hi[1]};
     };
     f32x4 acc[TM][TN];
     u32x4 fa[2][TM], fb[2][TN];                        // [K step][block]
-    auto read_frag = [&](int t, int st, int k) __attribute__((always_inline)) {
-        const uint32_t o = (t & 1) * SLOT + st * 32 * 512;
+    auto read_frag = [&](auto slot, auto st_, int k) __attribute__((always_inline)) {
+        constexpr int st = decltype(st_)::value;
+        constexpr std::integral_constant<int, decltype(slot)::value * SLOT + st * 32 * 512> off{};
         if (k == 0 || k > TN) {
             const int i = k == 0 ? 0 : k - TN;
-            fa[st][i] = ldfrag_tr(a_mn[i] + o);
+            fa[st][i] = ldfrag_tr(a_mn[i], off);
         } else {
-            fb[st][k - 1] = ldfrag_tr(b_mn[k - 1] + o);
+            fb[st][k - 1] = ldfrag_tr(b_mn[k - 1], off);
         }
     };
     auto mfma = [&](auto zero, int st, int i, int j) __attribute__((always_inline)) {
@@ -219,47 +255,74 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
     // instructions per four MFMAs, a write per eight) and, as its registers
     // fall free, the loads of B(t + 2), which have until the next tile's
     // second half to land.
-    auto tile = [&](auto first, int t) __attribute__((always_inline)) {
-        constexpr int RD = TM + TN;
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
+    // PAR: the K tile's slot.
+    auto tile = [&](auto first, auto par) __attribute__((always_inline)) {
+        constexpr int PAR = decltype(par)::value, RD = TM + TN;
+        constexpr std::integral_constant<int, PAR> cur{};
+        constexpr std::integral_constant<int, PAR ^ 1> nxt{};
+        constexpr std::integral_constant<int, 0> st0{};
+        constexpr std::integral_constant<int, 1> st1{};
+        const __amdgpu_buffer_rsrc_t ra = pa.rsrc();
+        static_for<0, Q>([&](auto qc) __attribute__((always_inline)) {
+            constexpr int q = decltype(qc)::value;
             if constexpr (!decltype(first)::value) mfma(std::false_type(), 1, q / TN, q % TN);
-            if (q * RD % Q == 0 && q * RD / Q < RD) read_frag(t, 0, q * RD / Q);
-            if (q % 8 == 2) dma_a(t + 1, q / 8);
-        }
+            if constexpr (q * RD % Q == 0 && q * RD / Q < RD) read_frag(cur, st0, q * RD / Q);
+            if constexpr (q % 8 == 2) dma_a(ra, PAR ^ 1, q / 8);
+            if constexpr (q == 5 && !decltype(first)::value) pb.move(b_step);
+            if constexpr (q == 7 && !decltype(first)::value) pb.set_span(b_ld, b_row, 0u);
+            if constexpr (q == 61) pa.move(a_step);
+            if constexpr (q == 63) pa.set_span(a_ld, a_row, 15u);
+        });
+        const __amdgpu_buffer_rsrc_t rb = pb.rsrc();
         static_for<0, Q>([&](auto qc) __attribute__((always_inline)) {
             constexpr int q = decltype(qc)::value;
             if constexpr (q % TN == 0) __builtin_amdgcn_s_waitcnt(0xC07F | (wgrad_row_wait(q / TN) << 8));
             mfma(first, 0, q / TN, q % TN);
-            if constexpr (q % 3 == 0 && q / 3 < TM + TN) read_frag(t, 1, q / 3);
+            if constexpr (q % 3 == 0 && q / 3 < TM + TN) read_frag(cur, st1, q / 3);
             if constexpr (q == 1) take_scales();
+            if constexpr (q == 5) load_s();
+            if constexpr (q == 9) next_s();
             if constexpr (q % 4 == 2) {
-                convert(std::integral_constant<int, q / 4>(), (t + 1) & 1);
-                if constexpr (q / 4 % 4 == 3) load_b(t + 2, q / 16);
-                if constexpr (q / 4 == 15) load_s(t + 2);
+                convert(std::integral_constant<int, q / 4>(), nxt);
+                if constexpr (q / 4 % 4 == 3) load_b(rb, q / 16);
             }
         });
-        wait_vmcnt<5>();                               // A(t + 1) landed; B(t + 2) and its scales may still run
+        wait_vmcnt<4>();                               // A(t + 1) landed; B(t + 2) may still run
         wait_lgkmcnt0();
         barrier();
     };
 
     if (nt > 0) {
+        constexpr std::integral_constant<int, 0> even{};
+        constexpr std::integral_constant<int, 1> odd{};
+        auto start_b = [&]() __attribute__((always_inline)) {
+            const __amdgpu_buffer_rsrc_t r = pb.rsrc();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dma_a(0, j);
+            for (int j = 0; j < 4; ++j) load_b(r, j);
+            load_s();
+            next_s();
+            pb.move(b_step);
+            pb.set_span(b_ld, b_row, 0u);
+        };
+        const __amdgpu_buffer_rsrc_t ra = pa.rsrc();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) load_b(0, j);
-        load_s(0);
+        for (int j = 0; j < 8; ++j) dma_a(ra, 0, j);
+        pa.move(a_step);
+        pa.set_span(a_ld, a_row, 15u);
+        start_b();
         take_scales();
-        static_for<0, 16>([&](auto s) __attribute__((always_inline)) { convert(s, 0); });
-#pragma unroll
-        for (int j = 0; j < 4; ++j) load_b(1, j);
-        load_s(1);
-        wait_vmcnt<5>();
+        static_for<0, 16>([&](auto s) __attribute__((always_inline)) { convert(s, even); });
+        start_b();
+        wait_vmcnt<5>();                               // A(0) landed
         wait_lgkmcnt0();
         barrier();
-        tile(std::true_type(), 0);
-        for (int t = 1; t < nt; ++t) tile(std::false_type(), t);
+        tile(std::true_type(), even);
+        int t = 1;
+        for (; t + 1 < nt; t += 2) {
+            tile(std::false_type(), odd);
+            tile(std::false_type(), even);
+        }
+        if (t < nt) tile(std::false_type(), odd);
 #pragma unroll
         for (int q = 0; q < Q; ++q) mfma(std::false_type(), 1, q / TN, q % TN);
         mfma_result_fence<TM, TN>(acc);
