@@ -25,69 +25,106 @@ struct NormBwdArgs {
     bool w_f32;
 };
 
-template <int T, int NT, int VPT>
+// TPR threads per row of a workgroup of NT (64: a wave, NT / 64 rows at once),
+// VPT vectors of 16 bytes per thread.  The next row's vectors are loaded
+// before the current one's reduction where the registers hold both.
+template <int T, int TPR, int NT, int VPT>
 __global__ void __launch_bounds__(NT) rmsnorm_bwd_kernel(NormBwdArgs p) {
     typedef RowVec<T> RV;
-    constexpr int VE = RV::VE;
-    const int t = threadIdx.x, N = p.N;
-    __shared__ float part[2][NT / 64];
+    constexpr int VE = RV::VE, RPB = NT / TPR, WPR = TPR / 64;
+    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR, N = p.N;
+    __shared__ float part[2][RPB][WPR];
     float w[VPT][VE], dw[VPT][VE];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = (i * NT + t) * VE;
+        const int c = (i * TPR + t) * VE;
 #pragma unroll
         for (int u = 0; u < VE; ++u) w[i][u] = dw[i][u] = 0.0f;
         if (c < N) load_weights<T>(p.W, p.w_f32, c, N, w[i]);
     }
-    int slot = 0;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, slot ^= 1) {
-        const float rstd = p.rstd[row];
-        typename RV::V dy[VPT], h[VPT];
-        float m = 0.0f;
+    struct Row {
+        typename RV::V dy[VPT], h[VPT], a[VPT];
+        float rstd;
+    };
+    auto load = [&](int64_t row, Row &r) __attribute__((always_inline)) {
+        r.rstd = 0.0f;
+        if (row < p.rows) r.rstd = p.rstd[row];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (i * NT + t) * VE;
-            dy[i] = h[i] = typename RV::V{};
-            if (c < N) {
-                dy[i] = RV::load((const typename RV::S *)p.dY + row * p.lddy, c, N);
-                h[i] = RV::load((const typename RV::S *)p.H + row * p.ldh, c, N);
+            const int c = (i * TPR + t) * VE;
+            r.dy[i] = r.h[i] = r.a[i] = typename RV::V{};
+            if (row < p.rows && c < N) {
+                r.dy[i] = RV::load((const typename RV::S *)p.dY + row * p.lddy, c, N);
+                r.h[i] = RV::load((const typename RV::S *)p.H + row * p.ldh, c, N);
+                if (p.dH) r.a[i] = RV::load((const typename RV::S *)p.dH + row * p.lddh, c, N);
             }
         }
+    };
+    constexpr bool AHEAD = VPT <= 2;                   // (two rows of four vectors do not fit the registers)
+    Row cur, next;
+    if constexpr (AHEAD) load((int64_t)blockIdx.x * RPB + sub, cur);
+    int slot = 0;
+    for (int64_t first = (int64_t)blockIdx.x * RPB; first < p.rows; first += (int64_t)gridDim.x * RPB, slot ^= 1) {
+        const int64_t row = first + sub;
+        if constexpr (AHEAD)
+            load(row + (int64_t)gridDim.x * RPB, next);
+        else
+            load(row, cur);
+        float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
 #pragma unroll
             for (int u = 0; u < VE; ++u) {
-                const float d = Elem<T>::up(dy[i][u]), f = Elem<T>::up(h[i][u]) * rstd;
+                const float d = Elem<T>::up(cur.dy[i][u]), f = Elem<T>::up(cur.h[i][u]) * cur.rstd;
                 dw[i][u] = fmaf(d, f, dw[i][u]);
                 m = fmaf(d * w[i][u], f, m);
             }
         }
         m = wave_sum(m);
-        if ((t & 63) == 0) part[slot][t >> 6] = m;
-        __syncthreads();                               // (the other slot's readers passed the last one)
-        m = 0.0f;
+        if constexpr (WPR > 1) {
+            if ((t & 63) == 0) part[slot][sub][t >> 6] = m;
+            __syncthreads();                           // (the other slot's readers passed the last one)
+            m = 0.0f;
 #pragma unroll
-        for (int v = 0; v < NT / 64; ++v) m += part[slot][v];
+            for (int v = 0; v < WPR; ++v) m += part[slot][sub][v];
+        }
         m /= (float)N;
+        if (row < p.rows) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = (i * NT + t) * VE;
-            if (c < N) {
-                typename RV::V o, a = {};
-                if (p.dH) a = RV::load((const typename RV::S *)p.dH + row * p.lddh, c, N);
+            for (int i = 0; i < VPT; ++i) {
+                const int c = (i * TPR + t) * VE;
+                if (c < N) {
+                    typename RV::V o;
 #pragma unroll
-                for (int u = 0; u < VE; ++u) {
-                    const float g = Elem<T>::up(dy[i][u]) * w[i][u], f = Elem<T>::up(h[i][u]) * rstd;
-                    o[u] = Elem<T>::down(fmaf(rstd, g - f * m, Elem<T>::up(a[u])));
+                    for (int u = 0; u < VE; ++u) {
+                        const float g = Elem<T>::up(cur.dy[i][u]) * w[i][u], f = Elem<T>::up(cur.h[i][u]) * cur.rstd;
+                        o[u] = Elem<T>::down(fmaf(cur.rstd, g - f * m, Elem<T>::up(cur.a[i][u])));
+                    }
+                    RV::store((typename RV::S *)p.dX + row * p.lddx, c, N, o);
                 }
-                RV::store((typename RV::S *)p.dX + row * p.lddx, c, N, o);
             }
         }
+        if constexpr (AHEAD) cur = next;
     }
-    if (p.part) {
+    if (!p.part) return;
+    // this workgroup's dw: of several rows at once, their shares added in order
+    if constexpr (RPB > 1) {
+        __shared__ float share[RPB][TPR * VPT * VE];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int u = 0; u < VE; ++u) share[sub][(i * TPR + t) * VE + u] = dw[i][u];
+        __syncthreads();
+        for (int c = threadIdx.x; c < N; c += NT) {
+            float v = 0.0f;
+#pragma unroll
+            for (int s = 0; s < RPB; ++s) v += share[s][c];
+            p.part[(int64_t)blockIdx.x * N + c] = v;
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (i * NT + t) * VE;
+            const int c = (i * TPR + t) * VE;
 #pragma unroll
             for (int h = 0; h < VE; h += 4)
                 if (c < N)
@@ -167,8 +204,17 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_reduce_kernel(const float *pa
     const int cl = threadIdx.x & 7, r = threadIdx.x >> 3;
     const int64_t c = (int64_t)blockIdx.x * 32 + cl * 4;
     f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (c < N)
-        for (int g = r; g < G; g += 32) s += RowVec<0>::load(part + (int64_t)g * N, (int)c, N);
+    if (c < N) {
+        int g = r;
+        for (; g + 7 * 32 < G; g += 8 * 32) {          // (eight loads in flight)
+            f32x4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = RowVec<0>::load(part + (int64_t)(g + 32 * i) * N, (int)c, N);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += v[i];
+        }
+        for (; g < G; g += 32) s += RowVec<0>::load(part + (int64_t)g * N, (int)c, N);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) sums[r][cl * 4 + i] = s[i];
     __syncthreads();
@@ -181,7 +227,7 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_reduce_kernel(const float *pa
     }
 }
 
-constexpr int kBwdGroups = 1024;                       // workgroups walking the rows: four per CU
+constexpr int kBwdGroups = 512;                        // workgroups walking the rows: two per CU
 constexpr int kLongGroups = 64;
 
 template <int T>
@@ -189,18 +235,27 @@ hipError_t launch_bwd(const NormBwdArgs &p, float *dW, hipStream_t s) {
     const int nvec = (int)(((int64_t)p.N + kVE<T> - 1) / kVE<T>);
     int G = 0;
     if (p.rows > 0) {
-        G = (int)(p.rows < kBwdGroups ? p.rows : kBwdGroups);
-#define TG_BWD(nt, vpt) hipLaunchKernelGGL((rmsnorm_bwd_kernel<T, nt, vpt>), dim3(G), dim3(nt), 0, s, p)
-        if (nvec <= 256)
-            TG_BWD(256, 1);
-        else if (nvec <= 512)
-            TG_BWD(256, 2);
-        else if (nvec <= 1024)
-            TG_BWD(256, 4);
-        else if (nvec <= 2048)
-            TG_BWD(512, 4);
-        else if (T == 0 && nvec <= 4096) {             // (16-bit rows this long do not fit the registers)
-            if constexpr (T == 0) TG_BWD(1024, 4);
+        // (rows of 16-bit elements past 16384 do not fit the registers)
+#define TG_BWD(tpr, nt, vpt)                                                                                     \
+    {                                                                                                            \
+        const int64_t blocks = (p.rows + (nt) / (tpr) - 1) / ((nt) / (tpr));                                     \
+        G = (int)(blocks < kBwdGroups ? blocks : kBwdGroups);                                                    \
+        hipLaunchKernelGGL((rmsnorm_bwd_kernel<T, tpr, nt, vpt>), dim3(G), dim3(nt), 0, s, p);                   \
+    }
+        if (nvec <= 64) {
+            TG_BWD(64, 512, 1)
+        } else if (nvec <= 128) {
+            TG_BWD(128, 512, 1)
+        } else if (nvec <= 256) {
+            TG_BWD(256, 512, 1)
+        } else if (nvec <= 512) {
+            TG_BWD(512, 512, 1)
+        } else if (nvec <= 1024) {
+            TG_BWD(512, 512, 2)
+        } else if (nvec <= 2048) {
+            TG_BWD(512, 512, 4)
+        } else if (T == 0 && nvec <= 4096) {
+            if constexpr (T == 0) TG_BWD(1024, 1024, 4)
         } else {
             G = (int)(p.rows < kLongGroups ? p.rows : kLongGroups);
             if (p.part) {

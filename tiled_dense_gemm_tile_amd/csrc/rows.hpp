@@ -125,7 +125,7 @@ __device__ __forceinline__ float mx_inverse(uint32_t code) {
 // VE neighbouring lanes: codes and scale of the row's block-scaled form.
 // (Values are at most 448 here, where the conversion neither saturates nor
 // makes a NaN of its own; infinities become the NaN code.)
-template <int VE>
+template <int VE, bool STREAM = false>
 __device__ __forceinline__ void mx_store(const float (&y)[VE], uint8_t *q, uint8_t *sf, int c) {
     uint32_t m = 0;
 #pragma unroll
@@ -148,7 +148,12 @@ __device__ __forceinline__ void mx_store(const float (&y)[VE], uint8_t *q, uint8
         w = __builtin_amdgcn_cvt_pk_fp8_f32(y[i + 2] * inv, y[i + 3] * inv, w, true);
         out.w[i / 4] = (uint32_t)w;
     }
-    *(Words *)(q + c) = out;
+    if constexpr (STREAM) {
+#pragma unroll
+        for (int i = 0; i < VE / 4; ++i) __builtin_nontemporal_store(out.w[i], &((Words *)(q + c))->w[i]);
+    } else {
+        *(Words *)(q + c) = out;
+    }
     if (c % 32 == 0) sf[c / 32] = (uint8_t)code;
 }
 
