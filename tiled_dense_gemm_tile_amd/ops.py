@@ -26,10 +26,10 @@ _NONE = (None, 0)
 
 
 def _run(f, dev, *args):
-    """The C call on torch's current stream of ``dev``, with ``dev`` current
-    (a NULL stream means the current device's)."""
-    stream = torch._C._cuda_getCurrentRawStream(dev.index)
-    if torch.cuda.current_device() == dev.index:
+    """The C call on torch's current stream of GPU ``dev``, with ``dev``
+    current (a NULL stream means the current device's)."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
         status = f(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -39,10 +39,14 @@ def _run(f, dev, *args):
 
 
 def _device(X):
-    dev = X.device
-    if dev.type != "cuda":
+    """Index of the tensor's GPU."""
+    if not X.is_cuda:
         raise ValueError("the tensors must be device tensors")
-    return dev
+    return X.get_device()
+
+
+def _new(shape, dtype, dev):
+    return torch.empty(shape, dtype=dtype, device="cuda:%d" % dev)
 
 
 def _matrix(name, t, shape, dtypes, dev):
@@ -51,8 +55,8 @@ def _matrix(name, t, shape, dtypes, dev):
         raise TypeError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
     if t.shape != shape:
         raise ValueError("%s must be (%d, %d)" % (name, shape[0], shape[1]))
-    if t.device != dev:
-        raise ValueError("%s must be a device tensor on %s" % (name, dev))
+    if t.get_device() != dev or not t.is_cuda:
+        raise ValueError("%s must be a device tensor on cuda:%d" % (name, dev))
     ld, one = t.stride()
     if one != 1 and shape[1] > 1:
         raise ValueError("%s: the last stride must be 1" % name)
@@ -67,8 +71,8 @@ def _vector(name, t, n, dtypes, dev):
         raise TypeError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
     if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError("%s must be a contiguous vector of %d" % (name, n))
-    if t.device != dev:
-        raise ValueError("%s must be a device tensor on %s" % (name, dev))
+    if t.get_device() != dev or not t.is_cuda:
+        raise ValueError("%s must be a device tensor on cuda:%d" % (name, dev))
     return t.data_ptr()
 
 
@@ -84,9 +88,9 @@ def _scaled_out(shape, dev, Q, SF):
     if N % 32:
         raise ValueError("block-scaled rows hold a multiple of 32 elements")
     if Q is None:
-        Q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+        Q = _new(shape, torch.float8_e4m3fn, dev)
     if SF is None:
-        SF = torch.empty((rows, N // 32), dtype=torch.float8_e8m0fnu, device=dev)
+        SF = _new((rows, N // 32), torch.float8_e8m0fnu, dev)
     return Q, SF, _matrix("Q", Q, shape, _E4M3, dev) + _matrix("SF", SF, (rows, N // 32), _E8M0, dev)
 
 
@@ -95,9 +99,9 @@ def _workspace(t, need, dev):
     if t is None:
         if not need:
             return None, None, 0
-        t = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif t.device != dev or not t.is_contiguous():
-        raise ValueError("workspace must be a contiguous device tensor on %s" % dev)
+        t = _new(need, torch.uint8, dev)
+    elif t.get_device() != dev or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous device tensor on cuda:%d" % dev)
     return t, t.data_ptr(), t.numel() * t.element_size()
 
 
@@ -122,10 +126,10 @@ def _norm(f, X, W, eps, residual, H, rstd, shape, code, dev, out):
     if residual is not None:
         r = _matrix("residual", residual, shape, own, dev)
         if H is None:
-            H = torch.empty(shape, dtype=X.dtype, device=dev)
+            H = _new(shape, X.dtype, dev)
     h = _NONE if H is None else _matrix("H", H, shape, own, dev)
     if rstd is None:
-        rstd = torch.empty(shape[0], dtype=torch.float32, device=dev)
+        rstd = _new(shape[0], torch.float32, dev)
     _run(f, dev, *shape, *x, *r, code, w, _TYPES[W.dtype], eps, *h, *out, _vector("rstd", rstd, shape[0], _F32, dev))
     return X if H is None else H, rstd
 
@@ -138,7 +142,7 @@ def rmsnorm(X, W, eps, residual=None, Y=None, H=None, rstd=None):
     Returns (Y, H, rstd), H being X when there is no residual and no H."""
     shape, code, dev = _rows("X", X)
     if Y is None:
-        Y = torch.empty(shape, dtype=X.dtype, device=dev)
+        Y = _new(shape, X.dtype, dev)
     out = _matrix("Y", Y, shape, (X.dtype,), dev)
     return (Y, *_norm(_load().rmsnorm, X, W, eps, residual, H, rstd, shape, code, dev, out))
 
@@ -176,12 +180,12 @@ def rmsnorm_backward(dY, H, W, rstd, dH=None, dX=None, dW=None, workspace=None, 
     s = _vector("rstd", rstd, rows, _F32, dev)
     dh = _NONE if dH is None else _matrix("dH", dH, shape, own, dev)
     if dX is None:
-        dX = torch.empty(shape, dtype=dY.dtype, device=dev)
+        dX = _new(shape, dY.dtype, dev)
     dx = _matrix("dX", dX, shape, own, dev)
     dw, ws = None, (None, 0)
     if weight_grad:
         if dW is None:
-            dW = torch.empty(N, dtype=torch.float32, device=dev)
+            dW = _new(N, torch.float32, dev)
         dw = _vector("dW", dW, N, _F32, dev)
         workspace, *ws = _workspace(workspace, workspace is None and rmsnorm_backward_workspace_bytes(rows, N), dev)
     elif dW is not None:
@@ -197,7 +201,7 @@ def _product_out(shape, dev, C, D, out_dtype):
     elif out_dtype != torch.float32 and out_dtype != torch.bfloat16:
         raise TypeError("out_dtype must be float32 or bfloat16")
     if D is None:
-        D = torch.empty(shape, dtype=out_dtype, device=dev)
+        D = _new(shape, out_dtype, dev)
     c = _NONE if C is None else _matrix("C", C, shape, (out_dtype,), dev)
     return D, OUT_BF16 if out_dtype == torch.bfloat16 else OUT_F32, c + _matrix("D", D, shape, (out_dtype,), dev)
 
