@@ -1,20 +1,20 @@
-// Weight gradient from block-scaled rows, four-wave kernel: 256 x 256 output
-// tiles, K tiles of 64 rows, for 16-byte rows of A and B.
+// Weight gradient from block-scaled rows, four-wave kernel: output tiles of
+// 256 x 256 (T = 8, one workgroup per CU) or 128 x 128 (T = 4, two), K tiles of
+// 64 rows, for 16-byte rows of A and B.
 //
 // The MFMA schedule is the 16-bit four-wave kernel's (gemm_f16_w4.hpp: waves
-// of 128 x 128 in 8 x 8 accumulator blocks, K steps of 32, the second step of
+// of T x T accumulator blocks of 16 x 16, K steps of 32, the second step of
 // a K tile multiplied after the next tile's barrier) with both operands
-// MN-contiguous: a K tile lies in LDS as 64 rows of 256 bf16 and fragments are
+// MN-contiguous: a K tile lies in LDS as 64 rows of 32 T bf16 and fragments are
 // read with ds_read_b64_tr_b16.  A's tile comes by direct global -> LDS loads.
 // B's tile is half as many bytes in memory and takes the registers: each
-// thread loads 64 codes of a row and its scales a K tile ahead, converts them
+// thread loads 8 T codes of a row and its scales a K tile ahead, converts them
 // (one instruction per two, with the scale) between the MFMAs of a tile's
 // second half, and writes them into the slot that the tile before has left.
 // A fragment's eight K-consecutive values have eight different scales, which
 // is why the conversion comes before LDS and not after it.
 //
-// Tiles past the last full round of 256 workgroups (all of them, in a small
-// grid) may be cut along K into `splits` ranges, whose fp32 partial tiles go
+// Tiles past the last full round of workgroups (all of them, in a small grid) may be cut along K into `splits` ranges, whose fp32 partial tiles go
 // to the workspace for a second kernel to add in order.
 #pragma once
 
@@ -37,7 +37,7 @@ struct Wgrad4Args {
     int tiles_m, tiles_n, group_m;
     int full;                                          // tiles multiplied whole: the first `full` of the walk
     int splits, k_split;                               // of the others: ranges, and K per range
-    float *ws;                                         // range s of tile full + i at ws + (s * rest + i) * 65536
+    float *ws;                                         // range s of tile full + i at ws + (s * rest + i) tiles
 };
 
 // Tile `id` of the walk in groups of group_m tile rows.
@@ -57,34 +57,39 @@ __device__ __forceinline__ int xcd_order(int wg, int nwg) {
     return x * q + (x < r ? x : r) + (wg >> 3);
 }
 
+// A half's T * T MFMAs spread B's 2 T conversion steps evenly between them; the
+// step of the second half's fragment reads.
+constexpr int wgrad_convert_every(int T) { return T == 8 ? 4 : 2; }
+constexpr int wgrad_read_every(int T) { return T == 8 ? 3 : 1; }
 // LDS operations outstanding when block row i of a tile's second half needs
 // its first-half fragments (gemm_f16_w4.hpp, tr_row_wait), with the writes of
-// converted B that the half has issued before its MFMA 8 i (two after each
-// 16 MFMAs' fourth conversion: see kConvert below).
-constexpr int wgrad_writes_before(int q) {
+// converted B, one after every second conversion step, that the half has
+// issued before its MFMA T i.
+constexpr int wgrad_writes_before(int T, int q) {
     int n = 0;
-    for (int s = 0; s < 16; ++s)
-        if (s % 2 == 1 && 4 * s + 2 < q) ++n;
+    for (int s = 1; s < 2 * T; s += 2)
+        if (wgrad_convert_every(T) * s + wgrad_convert_every(T) / 2 < q) ++n;
     return n;
 }
-constexpr int wgrad_row_wait(int i) {
-    int n = (7 - i) * 2;
-    const int issued = (8 * i + 2) / 3;
-    for (int m = 0; m < issued && m < 16; ++m) n += 2;
-    n += wgrad_writes_before(8 * i);
+constexpr int wgrad_row_wait(int T, int i) {
+    const int every = wgrad_read_every(T), issued = (T * i + every - 1) / every;
+    const int n = (T - 1 - i) * 2 + 2 * (issued < 2 * T ? issued : 2 * T) + wgrad_writes_before(T, T * i);
     return n > 15 ? 15 : n;
 }
 
-template <bool OUT_BF16>
-__global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi e) {
-    constexpr int TM = 8, TN = 8, BM = 256, BN = 256, KT = 64;
-    constexpr int WTM = 128, WTN = 128, Q = TM * TN;
-    constexpr int SLOT = KT * 512;                     // 64 rows of 256 bf16
+template <bool OUT_BF16, int T>
+__global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi e) {
+    constexpr int TM = T, TN = T, BM = 32 * T, BN = 32 * T, KT = 64;
+    constexpr int WTM = 16 * T, WTN = 16 * T, Q = TM * TN;
+    constexpr int ROWB = BM * 2;                       // an LDS row: 32 T bf16
+    constexpr int SLOT = KT * ROWB;
+    constexpr int LA = SLOT / 4096, NV = T / 2;        // loads per thread and K tile: of A, of B
     constexpr int B_BASE = 2 * SLOT;
     constexpr int RING_BYTES = 4 * SLOT;
     constexpr int EPI_BYTES = 4 * 32 * (WTN + 8) * 4;
-    static_assert(EPI_BYTES <= RING_BYTES && RING_BYTES <= 160 * 1024, "LDS");
-    __shared__ __attribute__((aligned(1024))) char smem[RING_BYTES];
+    constexpr int LDS_BYTES = RING_BYTES > EPI_BYTES ? RING_BYTES : EPI_BYTES;
+    static_assert(LDS_BYTES * (T == 8 ? 1 : 2) <= 160 * 1024, "LDS");
+    __shared__ __attribute__((aligned(1024))) char smem[LDS_BYTES];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -137,11 +142,12 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
     const uint32_t a_row = (uint32_t)(M - m0) * 2, a_ld = (uint32_t)(p.lda * 2);
     pa.set_span(a_ld, a_row, 15u);
     const int64_t a_step = (int64_t)KT * p.lda * 2;
-    uint32_t a_off[8];
+    uint32_t a_off[LA];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int row = 2 * (4 * j + wave) + (lane >> 5);
-        const int lchk = ((lane & 31) >> 1) ^ (row & 3) ^ (((row >> 3) & 1) << 2);
+    for (int j = 0; j < LA; ++j) {
+        constexpr int lanes = ROWB / 16;               // of one row
+        const int row = 64 / lanes * (4 * j + wave) + lane / lanes;
+        const int lchk = ((lane % lanes) >> 1) ^ (row & 3) ^ (((row >> 3) & 1) << 2);
         a_off[j] = (uint32_t)((row * p.lda + lchk * 16 + (lane & 1) * 8) * 2);
     }
     char *const a_lds = smem + wave * 1024;
@@ -150,29 +156,30 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
     };
 
     // ---- B: thread t holds row t / 4 of a K tile, columns 16 (t % 4) + 64 j
-    // .. + 15, and the eight scales of the row's 256 columns (of its last
-    // eight blocks where N ends inside the tile: s_shift bits too far left;
-    // rows past K take the last row's, with codes 0)
+    // .. + 15, and the T scales of the row's columns (of its last T blocks
+    // where N ends inside the tile: s_shift bits too far left; rows past K
+    // take the last row's, with codes 0)
     const int br = tid >> 2, bt = tid & 3;
     const uint32_t b_off = (uint32_t)(br * p.ldb) + bt * 16;
-    const int nb = N / 32, s_at = n0 / 32 < nb - 8 ? n0 / 32 : nb - 8, s_shift = 8 * (n0 / 32 - s_at);
+    const int nb = N / 32, s_at = n0 / 32 < nb - T ? n0 / 32 : nb - T, s_shift = 8 * (n0 / 32 - s_at);
     pb.base = (const char *)p.B + (int64_t)k_lo * p.ldb + n0;
     pb.rows = K;
     const uint32_t b_row = (uint32_t)(N - n0), b_ld = (uint32_t)p.ldb;
     pb.set_span(b_ld, b_row, 0u);
     const int64_t b_step = (int64_t)KT * p.ldb;
-    struct __attribute__((packed, aligned(1))) U64 {
-        uint64_t v;
+    typedef std::conditional_t<T == 8, uint64_t, uint32_t> Scales;
+    struct __attribute__((packed, aligned(1))) PackedScales {
+        Scales v;
     };
-    u32x4 vb[4];
-    uint64_t vs;
+    u32x4 vb[NV];
+    Scales vs;
     auto load_b = [&](__amdgpu_buffer_rsrc_t r, int j) __attribute__((always_inline)) {
         vb[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b_off + 64 * j, 0, 0));
     };
     const uint8_t *s_row = p.SF + (int64_t)k_lo * p.ldsf + s_at + (int64_t)(br < K ? br : K - 1) * p.ldsf;
     const int64_t s_step = (int64_t)KT * p.ldsf;
     int s_left = K - 1 - br;                           // rows from s_row's to the last
-    auto load_s = [&]() __attribute__((always_inline)) { vs = ((const U64 *)s_row)->v; };
+    auto load_s = [&]() __attribute__((always_inline)) { vs = ((const PackedScales *)s_row)->v; };
     auto next_s = [&]() __attribute__((always_inline)) {
         // (the row 64 further; past K: the last)
         s_left -= KT;
@@ -185,12 +192,12 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
     uint32_t b_put[2];
 #pragma unroll
     for (int o = 0; o < 2; ++o)
-        b_put[o] = lds0 + B_BASE + br * 512 + ((bt ^ (br & 3)) + 4 * (o ^ ((br >> 3) & 1))) * 32;
-    uint32_t sc[2];                                    // scales of this thread's vectors 0, 1 and 2, 3, in bytes 0 and 2
+        b_put[o] = lds0 + B_BASE + br * ROWB + ((bt ^ (br & 3)) + 4 * (o ^ ((br >> 3) & 1))) * 32;
+    uint32_t sc[NV / 2];                               // scales of vectors 2 i and 2 i + 1 in bytes 0 and 2
     auto take_scales = [&]() __attribute__((always_inline)) {
-        const uint64_t s = (vs >> s_shift) >> (8 * (bt >> 1));
+        const Scales s = (Scales)(vs >> s_shift) >> (8 * (bt >> 1));
         sc[0] = (uint32_t)s;
-        sc[1] = (uint32_t)(s >> 32);
+        if constexpr (T == 8) sc[1] = (uint32_t)(s >> 32);
     };
     u32x4 half;
     auto convert = [&](auto step, auto slot) __attribute__((always_inline)) {
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
     const int fr = lane & 15, fq = lane >> 4;
     auto mn_base = [&](int wb, int b) __attribute__((always_inline)) {
         const int g = (fr >> 2) ^ ((fq & 1) << 2);
-        return lds0 + (8 * fq + (fr >> 2)) * 512 + (wb * 8 + (b ^ g)) * 32 + (fr & 3) * 8;
+        return lds0 + (8 * fq + (fr >> 2)) * ROWB + ((wb * T + b) ^ g) * 32 + (fr & 3) * 8;
     };
     uint32_t a_mn[TM], b_mn[TN];
 #pragma unroll
@@ -226,14 +233,14 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
     auto ldfrag_tr = [&](uint32_t a, auto off) __attribute__((always_inline)) {
         u32x2 lo, hi;
         asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%c2" : "=v"(lo) : "v"(a), "n"(decltype(off)::value));
-        asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%c2" : "=v"(hi) : "v"(a), "n"(decltype(off)::value + 2048));
+        asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%c2" : "=v"(hi) : "v"(a), "n"(decltype(off)::value + 4 * ROWB));
         return u32x4{lo[0], lo[1], hi[0], hi[1]};
     };
     f32x4 acc[TM][TN];
     u32x4 fa[2][TM], fb[2][TN];                        // [K step][block]
     auto read_frag = [&](auto slot, auto st_, int k) __attribute__((always_inline)) {
         constexpr int st = decltype(st_)::value;
-        constexpr std::integral_constant<int, decltype(slot)::value * SLOT + st * 32 * 512> off{};
+        constexpr std::integral_constant<int, decltype(slot)::value * SLOT + st * 32 * ROWB> off{};
         if (k == 0 || k > TN) {
             const int i = k == 0 ? 0 : k - TN;
             fa[st][i] = ldfrag_tr(a_mn[i], off);
@@ -267,27 +274,28 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
             constexpr int q = decltype(qc)::value;
             if constexpr (!decltype(first)::value) mfma(std::false_type(), 1, q / TN, q % TN);
             if constexpr (q * RD % Q == 0 && q * RD / Q < RD) read_frag(cur, st0, q * RD / Q);
-            if constexpr (q % 8 == 2) dma_a(ra, PAR ^ 1, q / 8);
-            if constexpr (q == 5 && !decltype(first)::value) pb.move(b_step);
-            if constexpr (q == 7 && !decltype(first)::value) pb.set_span(b_ld, b_row, 0u);
-            if constexpr (q == 61) pa.move(a_step);
-            if constexpr (q == 63) pa.set_span(a_ld, a_row, 15u);
+            if constexpr (q % (Q / LA) == (T == 8 ? 2 : 1)) dma_a(ra, PAR ^ 1, q / (Q / LA));
+            if constexpr (q == (T == 8 ? 5 : 3) && !decltype(first)::value) pb.move(b_step);
+            if constexpr (q == (T == 8 ? 7 : 6) && !decltype(first)::value) pb.set_span(b_ld, b_row, 0u);
+            if constexpr (q == Q - 3) pa.move(a_step);
+            if constexpr (q == Q - 1) pa.set_span(a_ld, a_row, 15u);
         });
         const __amdgpu_buffer_rsrc_t rb = pb.rsrc();
         static_for<0, Q>([&](auto qc) __attribute__((always_inline)) {
             constexpr int q = decltype(qc)::value;
-            if constexpr (q % TN == 0) __builtin_amdgcn_s_waitcnt(0xC07F | (wgrad_row_wait(q / TN) << 8));
+            if constexpr (q % TN == 0) __builtin_amdgcn_s_waitcnt(0xC07F | (wgrad_row_wait(T, q / TN) << 8));
             mfma(first, 0, q / TN, q % TN);
-            if constexpr (q % 3 == 0 && q / 3 < TM + TN) read_frag(cur, st1, q / 3);
-            if constexpr (q == 1) take_scales();
-            if constexpr (q == 5) load_s();
-            if constexpr (q == 9) next_s();
-            if constexpr (q % 4 == 2) {
-                convert(std::integral_constant<int, q / 4>(), nxt);
-                if constexpr (q / 4 % 4 == 3) load_b(rb, q / 16);
+            constexpr int re = wgrad_read_every(T), ce = wgrad_convert_every(T);
+            if constexpr (q % re == 0 && q / re < TM + TN) read_frag(cur, st1, q / re);
+            if constexpr (q == (T == 8 ? 1 : 0)) take_scales();
+            if constexpr (q == (T == 8 ? 5 : 2)) load_s();
+            if constexpr (q == (T == 8 ? 9 : 4)) next_s();
+            if constexpr (q % ce == ce / 2) {
+                convert(std::integral_constant<int, q / ce>(), nxt);
+                if constexpr (q / ce % 4 == 3) load_b(rb, q / ce / 4);
             }
         });
-        wait_vmcnt<4>();                               // A(t + 1) landed; B(t + 2) may still run
+        wait_vmcnt<NV>();                              // A(t + 1) landed; B(t + 2) may still run
         wait_lgkmcnt0();
         barrier();
     };
@@ -298,7 +306,7 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
         auto start_b = [&]() __attribute__((always_inline)) {
             const __amdgpu_buffer_rsrc_t r = pb.rsrc();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) load_b(r, j);
+            for (int j = 0; j < NV; ++j) load_b(r, j);
             load_s();
             next_s();
             pb.move(b_step);
@@ -306,14 +314,14 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
         };
         const __amdgpu_buffer_rsrc_t ra = pa.rsrc();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dma_a(ra, 0, j);
+        for (int j = 0; j < LA; ++j) dma_a(ra, 0, j);
         pa.move(a_step);
         pa.set_span(a_ld, a_row, 15u);
         start_b();
         take_scales();
-        static_for<0, 16>([&](auto s) __attribute__((always_inline)) { convert(s, even); });
+        static_for<0, 2 * T>([&](auto s) __attribute__((always_inline)) { convert(s, even); });
         start_b();
-        wait_vmcnt<5>();                               // A(0) landed
+        wait_vmcnt<NV + 1>();                          // A(0) landed
         wait_lgkmcnt0();
         barrier();
         tile(std::true_type(), even);
@@ -325,7 +333,12 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
         if (t < nt) tile(std::false_type(), odd);
 #pragma unroll
         for (int q = 0; q < Q; ++q) mfma(std::false_type(), 1, q / TN, q % TN);
-        mfma_result_fence<TM, TN>(acc);
+        // (the wait states of mfma_result_fence, for either tile)
+        asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 3" : "+a"(acc[0][0]));
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[i][j]));
     } else {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
@@ -339,8 +352,8 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
         epilogue_lds16t<OUT_BF16, TM, TN, WTM, WTN, kStoreStream>(acc, smem, wave, lane, wm, wn, m0, n0, M, N, p.C,
                                                                   p.ldc, p.D, p.ldd, e);
     } else {
-        // a whole partial tile, 256 x 256 (stays cacheable: it is read next)
-        float *out = p.ws + ((int64_t)split * rest + part) * 65536;
+        // a whole partial tile (stays cacheable: it is read next)
+        float *out = p.ws + ((int64_t)split * rest + part) * (BM * BN);
         F16Epi v;
         v.vec_c = false;
         v.vec_d = true;
@@ -350,17 +363,18 @@ __global__ void __launch_bounds__(256) gemm_wgrad_w4_kernel(Wgrad4Args p, F16Epi
 }
 
 // D = the `splits` partial tiles of each cut tile added in order, plus C: four
-// columns a thread, 64 threads a row, four rows a workgroup.
-template <bool OUT_BF16>
+// columns a thread, 1024 elements a workgroup.
+template <bool OUT_BF16, int T>
 __global__ void __launch_bounds__(256) wgrad_reduce_kernel(Wgrad4Args p) {
     const int rest = p.tiles_m * p.tiles_n - p.full;
-    const int part = blockIdx.x >> 6, r = (blockIdx.x & 63) * 4 + (threadIdx.x >> 6), c = (threadIdx.x & 63) * 4;
+    constexpr int BT = 32 * T, per_tile = BT * BT / 1024;
+    const int part = blockIdx.x / per_tile, at = (blockIdx.x % per_tile) * 1024 + threadIdx.x * 4;
     int tm, tn;
     walk_tile(p.full + part, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
-    const int m = tm * 256 + r, n = tn * 256 + c;
+    const int m = tm * BT + at / BT, n = tn * BT + at % BT;
     if (m >= p.M || n >= p.N) return;                  // (N % 32 == 0: whole vectors)
-    const float *w = p.ws + (int64_t)part * 65536 + r * 256 + c;
-    const int64_t slice = (int64_t)rest * 65536;
+    const float *w = p.ws + (int64_t)part * (BT * BT) + at;
+    const int64_t slice = (int64_t)rest * (BT * BT);
     f32x4 s = *(const f32x4 *)w;
     int k = 1;
     for (; k + 4 <= p.splits; k += 4) {

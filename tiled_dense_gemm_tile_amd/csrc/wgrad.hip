@@ -9,11 +9,11 @@ using namespace tg_api;
 
 namespace {
 
-// How a call runs: the four-wave kernel or the one that takes every call, and
-// the K ranges of its tiles (four-wave: of the tiles past the first `full`).
+// How a call runs: the four-wave kernel with T = 8 or 4, or (0) the one that
+// takes every call, and the K ranges of its tiles (four-wave: of the tiles
+// past the first `full`).
 struct WgradPlan {
-    bool w4;
-    int splits;
+    int T, splits;
     int64_t full, rest;
     size_t bytes;                                      // workspace
 };
@@ -23,29 +23,54 @@ constexpr int64_t kCus = 256;
 // `rows16`: A and B start their rows on 16 bytes.
 WgradPlan plan_wgrad(int64_t M, int64_t N, int64_t K, bool rows16, bool workspace) {
     WgradPlan g = {};
-    const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256);
-    g.w4 = rows16 && N >= 256 && K > 0;
-    if (g.w4) {
-        g.full = t256;
-        g.splits = 1;
-        const int64_t rest = t256 % kCus;
-        int64_t s = rest ? kCus / rest : 1;
-        if (K / 512 < s) s = K / 512;
-        if (s >= 2 && workspace) {
-            g.rest = rest;
-            g.full = t256 - rest;
-            g.splits = effective_splits(K, (int)s, 64);
-            g.bytes = (size_t)g.splits * (size_t)rest * 65536 * 4;
-        }
+    const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256), t128 = ((M + 127) / 128) * ((N + 127) / 128);
+    if (rows16 && N >= 128 && K > 0) {
+        auto cut = [&](int T) {                        // T x T blocks a wave: the plan
+            const int64_t tiles = T == 8 ? t256 : t128, round = T == 8 ? kCus : 2 * kCus, rest = tiles % round;
+            int64_t s = rest ? round / rest : 1;
+            // (ranges of 1024 on: at 1024 x 1024 x 1024 12.0 us uncut, 16.6
+            // in two; of 512 for a tile or two: 128 x 128 x 4096 11.0 against 13.9)
+            const int64_t least = tiles < 4 ? 512 : 1024;
+            if (K / least < s) s = K / least;
+            g.T = T;
+            g.full = tiles;
+            g.splits = 1;
+            g.rest = 0;
+            if (s >= 2 && workspace) {
+                g.rest = rest;
+                g.full = tiles - rest;
+                g.splits = effective_splits(K, (int)s, 64);
+            }
+            g.bytes = g.splits > 1 ? (size_t)g.splits * (size_t)g.rest * (size_t)(32 * T * 32 * T) * 4 : 0;
+        };
+        // 256 x 256 tiles for grids of over 144 of them (136: 88 us against 80
+        // with 128 x 128; 168: 89 against 98) and where fewer, cut, leave a
+        // workgroup a long sum (1536 x 1536 x 16384 77 against 89 us); else
+        // four times as many of 128 x 128, two workgroups a CU, with half the
+        // partial sums (1024 x 992 x 8200 31 against 38, 2048 x 2048 x 4096
+        // 45 against 49)
+        if (N >= 256 && (t256 > 144 || (t256 < kCus / 2 && K / (kCus / t256) >= 1536)))
+            cut(8);
+        else
+            cut(4);
         return g;
     }
-    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
-    int64_t s = tiles ? 2 * kCus / tiles : 1;
-    if (K / 1024 < s) s = K / 1024;
+    int64_t s = t128 ? 2 * kCus / t128 : 1;
+    if (K / 256 < s) s = K / 256;
     if (s > kMaxSplits) s = kMaxSplits;
     g.splits = s < 2 || !workspace ? 1 : effective_splits(K, (int)s, 64);
     g.bytes = splitk_bytes(M, N, g.splits);
     return g;
+}
+
+template <bool OUT_BF16, int T>
+hipError_t launch_w4(const tg::Wgrad4Args &p, const tg::F16Epi &e, const WgradPlan &g, hipStream_t s) {
+    hipLaunchKernelGGL((tg::gemm_wgrad_w4_kernel<OUT_BF16, T>), dim3((unsigned)(g.full + g.rest * g.splits)), dim3(256),
+                       0, s, p, e);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess || g.splits == 1) return err;
+    hipLaunchKernelGGL((tg::wgrad_reduce_kernel<OUT_BF16, T>), dim3((unsigned)(g.rest * T * T)), dim3(256), 0, s, p);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -75,11 +100,12 @@ gemm_status gemm_wgrad_mxfp8(int64_t M, int64_t N, int64_t K, const void *A, int
     const bool rows16 = (((uintptr_t)A | (uintptr_t)(lda * 2) | (uintptr_t)B | (uintptr_t)ldb) & 15) == 0;
     WgradPlan g = plan_wgrad(M, N, K, rows16, true);
     if (g.splits > 1 &&
-        (!workspace || workspace_bytes < g.bytes || (!g.w4 && splitk_ldw(N) * 4 >= kMaxLdBytes)))
+        (!workspace || workspace_bytes < g.bytes || (!g.T && splitk_ldw(N) * 4 >= kMaxLdBytes)))
         g = plan_wgrad(M, N, K, rows16, false);
     const bool bf16 = out_type == GEMM_OUT_BF16;
     const int64_t kt = (K + 63) / 64, k_split = (kt + g.splits - 1) / g.splits * 64;
-    if (g.w4) {
+    if (g.T) {
+        const int bt = 32 * g.T;
         tg::Wgrad4Args p;
         p.A = A;
         p.B = B;
@@ -95,8 +121,8 @@ gemm_status gemm_wgrad_mxfp8(int64_t M, int64_t N, int64_t K, const void *A, int
         p.N = (int)N;
         p.K = (int)K;
         p.group_m = 4;
-        p.tiles_m = (int)((M + 255) / 256);
-        p.tiles_n = (int)((N + 255) / 256);
+        p.tiles_m = (int)((M + bt - 1) / bt);
+        p.tiles_n = (int)((N + bt - 1) / bt);
         const int64_t grid = g.full + g.rest * g.splits;
         if (grid >= kMaxDim) return GEMM_ERR_UNSUPPORTED;
         p.full = (int)g.full;
@@ -107,18 +133,9 @@ gemm_status gemm_wgrad_mxfp8(int64_t M, int64_t N, int64_t K, const void *A, int
         tg::F16Epi e;
         e.vec_d = ((uintptr_t)D % vb) == 0 && ldd % 4 == 0;
         e.vec_c = C && ((uintptr_t)C % vb) == 0 && ldc % 4 == 0;
-        if (bf16)
-            hipLaunchKernelGGL((tg::gemm_wgrad_w4_kernel<true>), dim3((unsigned)grid), dim3(256), 0, stream, p, e);
-        else
-            hipLaunchKernelGGL((tg::gemm_wgrad_w4_kernel<false>), dim3((unsigned)grid), dim3(256), 0, stream, p, e);
-        st = launched(hipGetLastError());
-        if (st != GEMM_OK || g.splits == 1) return st;
-        const dim3 blocks((unsigned)(g.rest * 64));
-        if (bf16)
-            hipLaunchKernelGGL((tg::wgrad_reduce_kernel<true>), blocks, dim3(256), 0, stream, p);
-        else
-            hipLaunchKernelGGL((tg::wgrad_reduce_kernel<false>), blocks, dim3(256), 0, stream, p);
-        return launched(hipGetLastError());
+        if (g.T == 8)
+            return launched(bf16 ? launch_w4<true, 8>(p, e, g, stream) : launch_w4<false, 8>(p, e, g, stream));
+        return launched(bf16 ? launch_w4<true, 4>(p, e, g, stream) : launch_w4<false, 4>(p, e, g, stream));
     }
     tg::WgradArgs p;
     p.A = A;
