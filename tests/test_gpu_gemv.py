@@ -72,6 +72,48 @@ def test_random(kind, scales, m):
     assert (np.abs(f64(D) - want) <= 2 * k * ref.U * S).all()   # (x in two parts: twice the terms)
 
 
+# Every path: K ranges (16 rows, 17 rows, few weight rows), blocks per wave and
+# waves per block, more blocks than workgroups, every scale width, K off a step.
+WIDE = [(16, 4100, 6144, 32), (16, 300, 14336, 128), (20, 1000, 4096, 64), (32, 48, 8192, 32), (1, 512, 16384, 32),
+        (3, 9000, 2560, 32), (4, 20000, 1024, 32), (2, 70000, 256, 32), (7, 1111, 4128, 32), (5, 600, 2336, 64),
+        (9, 4096, 3360, 128), (1, 2000, 4000, 256), (6, 333, 20000, 4096), (33, 500, 992, 32)]
+
+
+@pytest.mark.parametrize("kind", XT)
+@pytest.mark.parametrize("case", WIDE, ids=str)
+def test_integers_wide(case, kind):
+    m, n, k, kb = case
+    x, w, sf = case_of(11, m, n, k, kb, kind, 127, 129)
+    W, S = torch.from_numpy(w).to(DEV), torch.from_numpy(sf).to(DEV)
+    want = torch.mm(x.double(), torch.from_numpy(ref.fp4_weights(w, sf, kb)).to(DEV).t().contiguous())
+    assert want.abs().max() < 2 ** 22
+    c = torch.randint(-9, 10, (m, n), device=DEV).float()
+    assert torch.equal(tg.gemv_mxfp4(x, W, S, kblock=kb, C=c).double(), want + c.double())
+    b = tg.gemv_mxfp4(x, W, S, kblock=kb, C=c.bfloat16(), out_dtype=torch.bfloat16)
+    assert torch.equal(b, (want + c.double()).float().bfloat16())
+    # without room for partial sums, and with a workspace whose end is not touched
+    none = torch.empty(0, dtype=torch.uint8, device=DEV)
+    assert torch.equal(tg.gemv_mxfp4(x, W, S, kblock=kb, C=c, workspace=none).double(), want + c.double())
+    need = tg.gemv_mxfp4_workspace_bytes(m, n, k)
+    ws = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device=DEV)
+    D = torch.full((m + 1, n + 7), 5.0, device=DEV)
+    tg.gemv_mxfp4(x, W, S, kblock=kb, C=c, D=D[:m, :n], workspace=ws[:need])
+    assert torch.equal(D[:m, :n].double(), want + c.double()) and (ws[need:] == 0x5A).all()
+    D[:m, :n] = 5
+    assert (D == 5).all()
+
+
+def test_x_in_two_parts_over_the_staged_path():
+    """fp16 X against scales out of fp16's range, K past a step and wide enough for every wave."""
+    for k in (4096, 4128):
+        x, w, sf = case_of(12, 5, 100, k, 32, "fp16", 127, 129)
+        sf[:, 3::7] = 150                              # 2^23
+        wv = ref.fp4_weights(w, sf, 32)
+        want, S = f64(x) @ wv.T, np.abs(f64(x)) @ np.abs(wv).T
+        D = f64(tg.gemv_mxfp4(x, torch.from_numpy(w).to(DEV), torch.from_numpy(sf).to(DEV)))
+        assert (np.abs(D - want) <= 2 * k * ref.U * S).all()
+
+
 def test_fp16_weights_stay_exact_at_the_range_border():
     """Single products at scales around fp16's: subnormal and large weights."""
     for code in (100, 103, 104, 105, 112, 113, 114, 139, 140, 141, 150):

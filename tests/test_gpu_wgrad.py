@@ -69,6 +69,46 @@ def test_integers(case, layout):
     assert np.array_equal(f64(Db), ref.round_to(want + c, "bf16"))
 
 
+# Grids of 256 x 256 tiles: whole, over one round with the rest cut along K, a
+# small grid cut along a long K; the last two rows odd in every size the kernel
+# takes (M in its padded rows, N past a tile, K past a K tile).
+LARGE = [(3208, 3232, 1), (3208, 3232, 64), (3208, 3232, 65), (3200, 3328, 128), (3201, 3232, 200), (4304, 4096, 2080),
+         (1097, 1120, 15500)]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=str)
+@pytest.mark.parametrize("out", OUT)
+def test_integers_large_grids(case, out):
+    m, n, k = case
+    dy, q, sf = integer_case(3, m, n, k)
+    a = strided(dy, torch.bfloat16, -m % 8, 0)          # 16-byte rows
+    b, s = (torch.from_numpy(t).to(DEV) for t in (q, sf))
+    x = torch.from_numpy(ref.dequant(q, sf)).to(DEV)
+    c = torch.randint(-9, 10, (m, n), device=DEV).to(OUT[out])
+    want = torch.mm(a.double().t().contiguous(), x) + c.double()
+    assert want.abs().max() < 2 ** 23                   # halves below 2^23 are fp32 numbers
+    D = tg.gemm_wgrad_mxfp8(a, b, s, C=c, out_dtype=OUT[out])
+    assert torch.equal(D, want.float().to(OUT[out]))
+    assert torch.equal(D, tg.gemm_wgrad_mxfp8(a, b, s, C=c, out_dtype=OUT[out]))
+    uncut = tg.gemm_wgrad_mxfp8(a, b, s, C=c, out_dtype=OUT[out], workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
+    assert torch.equal(D, uncut)
+
+
+def test_large_grid_leaves_its_surroundings():
+    m, n, k = 3208, 3232, 70
+    dy, q, sf = integer_case(4, m, n, k)
+    A = torch.full((k + 64, m + 8), float("nan"), dtype=torch.bfloat16, device=DEV)
+    B = torch.full((k + 64, n + 32), 0x7F, dtype=torch.uint8, device=DEV)
+    S = torch.full((k + 64, n // 32 + 1), 0xFF, dtype=torch.uint8, device=DEV)
+    A[:k, :m], B[:k, :n], S[:k, :n // 32] = (torch.from_numpy(t).to(DEV) for t in (dy, q, sf))
+    D = torch.full((m + 3, n + 12), 5.0, device=DEV)
+    tg.gemm_wgrad_mxfp8(A[:k, :m], B[:k, :n], S[:k, :n // 32], D=D[:m, :n])
+    want = torch.mm(A[:k, :m].double().t().contiguous(), torch.from_numpy(ref.dequant(q, sf)).to(DEV))
+    assert torch.equal(D[:m, :n].double(), want)
+    D[:m, :n] = 5
+    assert (D == 5).all()
+
+
 @pytest.mark.parametrize("case", [(96, 64, 3000), (520, 480, 1111), (256, 256, 8192), (2048, 1024, 600)], ids=str)
 @pytest.mark.parametrize("out", OUT)
 def test_random(case, out):
