@@ -157,9 +157,8 @@ __device__ __forceinline__ void gemv_join(float (&red)[kGemvWaves][MB * 4][64], 
 
 // One MFMA of 32 K: 8 weights (a word of codes) of each lane against its x.
 template <bool FP16, int MB>
-__device__ __forceinline__ void gemv_step(const u32x4 (&xf)[MB], uint32_t w, uint32_t code, bool direct,
+__device__ __forceinline__ void gemv_step(const u32x4 (&xf)[MB], uint32_t w, float scale, bool direct,
                                           f32x4 (&acc)[MB]) {
-    const float scale = __builtin_bit_cast(float, code << 23);
     if (!FP16 || direct) {
         const u32x4 wf = fp4_up<FP16>(w, scale);
 #pragma unroll
@@ -176,9 +175,16 @@ __device__ __forceinline__ void gemv_step(const u32x4 (&xf)[MB], uint32_t w, uin
     }
 }
 
-// fp16 holds a scaled weight exactly when its scale is 2^-23 .. 2^13
-// (subnormals included).
-__device__ __forceinline__ bool fp16_scale(uint32_t code) { return code >= 104u && code <= 140u; }
+// fp16 holds a scaled weight exactly when its scale is 2^-23 (subnormals
+// included) .. 2^13; whether the lowest N codes of c are 104 .. 135, 2^-23 ..
+// 2^8: 24 added to each byte (the top bits apart, so that none carries) leaves
+// exactly those with the bits 100 on top.
+template <int N>
+__device__ __forceinline__ bool fp16_scales(uint32_t c) {
+    const uint32_t v = ((c & 0x7f7f7f7fu) + 0x18181818u) ^ (c & 0x80808080u);
+    constexpr uint32_t bytes = N == 4 ? 0xffffffffu : (1u << (8 * N)) - 1u;
+    return (v & (0xe0e0e0e0u & bytes)) == (0x80808080u & bytes);
+}
 
 // W and X rows 16-byte aligned.  What bounds the product besides HBM is the
 // count of vector-memory instructions (a 1 KiB load holds the address unit
@@ -282,29 +288,20 @@ __global__ void __launch_bounds__(kGemvWaves * 64, 2) gemv_mxfp4_staged_kernel(G
             c[0] = sf[i < last ? i : last];
         }
     };
-    // The step at k's eight codes, byte j of half t for K block 4 t + j, from
-    // its load (of the row's last codes, where the step's own would end past
-    // them: those before the step's drop out, and blocks past K, whose weights
-    // are zeros, get 2^0).
+    // The step at k's codes, from its load (of the row's last codes, where the
+    // step's own would end past them: those before the step's drop out, and
+    // blocks past K, whose weights are zeros, get 2^0): the code of K block j
+    // is byte j / each.
+    constexpr int each = SC <= 1 ? 1 : SC == 2 ? 2 : SC == 3 ? 4 : 8, ncodes = 8 / each;
     auto codes = [&](uint32_t (&c)[2], int k) __attribute__((always_inline)) {
-        constexpr int each = SC <= 1 ? 32 : SC == 2 ? 64 : 128, load = SC <= 1 ? 8 : SC == 2 ? 4 : 2;
         if constexpr (SC >= 1 && SC <= 3) {
-            const int past = k / each - ((p.K + each - 1) / each - load);
+            const int past = k / (32 * each) - ((p.K + 32 * each - 1) / (32 * each) - ncodes);
             if (past > 0) {
                 const uint64_t v = ((uint64_t)c[1] << 32) | c[0];
-                const uint64_t w = (v >> (8 * past)) | (0x7f7f7f7f7f7f7f7full << (8 * (load - past)));
+                const uint64_t w = (v >> (8 * past)) | (0x7f7f7f7f7f7f7f7full << (8 * (ncodes - past)));
                 c[0] = (uint32_t)w;
                 c[1] = (uint32_t)(w >> 32);
             }
-        }
-        if constexpr (SC == 2) {
-            c[1] = __builtin_amdgcn_perm(c[0], c[0], 0x03030202u);
-            c[0] = __builtin_amdgcn_perm(c[0], c[0], 0x01010000u);
-        } else if constexpr (SC == 3) {
-            c[1] = __builtin_amdgcn_perm(c[0], c[0], 0x01010101u);
-            c[0] = __builtin_amdgcn_perm(c[0], c[0], 0x00000000u);
-        } else if constexpr (SC == 4) {
-            c[0] = c[1] = __builtin_amdgcn_perm(c[0], c[0], 0x00000000u);
         }
     };
 
@@ -378,13 +375,16 @@ __global__ void __launch_bounds__(kGemvWaves * 64, 2) gemv_mxfp4_staged_kernel(G
             codes(c, k0);
             bool direct = true;
             if constexpr (FP16) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) direct = direct && fp16_scale((c[j / 4] >> (8 * (j % 4))) & 0xffu);
+                direct = fp16_scales<(ncodes < 4 ? ncodes : 4)>(c[0]);
+                if constexpr (ncodes == 8) direct = direct && fp16_scales<4>(c[1]);
                 direct = __all(direct);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                gemv_step<FP16, MB>(xf[j], q[j], (c[j / 4] >> (8 * (j % 4))) & 0xffu, direct, acc);
+            for (int j = 0; j < 8; ++j) {
+                const int b = j / each;                // byte b % 4 of c[b / 4], as an exponent
+                const uint32_t v = b % 4 == 0 ? c[b / 4] << 23 : b % 4 == 1 ? c[b / 4] << 15 : b % 4 == 2 ? c[b / 4] << 7 : c[b / 4] >> 1;
+                gemv_step<FP16, MB>(xf[j], q[j], __builtin_bit_cast(float, v & 0x7f800000u), direct, acc);
+            }
         }
         k0 += KW * 256;
         if (k0 < k_hi) return true;
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kGemvWaves * 64) gemv_mxfp4_kernel(GemvArgs p)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int64_t k = k0 + t * 128 + lg * 32;
-            const bool direct = !FP16 || __all(fp16_scale(code[t]));
+            const bool direct = !FP16 || __all(fp16_scales<1>(code[t]));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 u32x4 xf[MB];
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kGemvWaves * 64) gemv_mxfp4_kernel(GemvArgs p)
                     xf[a] = u32x4{0u, 0u, 0u, 0u};
                     if (xin[a] && k < K) xf[a] = ((const Halves8 *)(x[a] + k + 8 * j))->v;
                 }
-                gemv_step<FP16, MB>(xf, wq[t][j], code[t], direct, acc);
+                gemv_step<FP16, MB>(xf, wq[t][j], __builtin_bit_cast(float, code[t] << 23), direct, acc);
             }
         }
     }
