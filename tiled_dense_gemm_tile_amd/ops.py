@@ -45,8 +45,11 @@ def _device(X):
     return X.get_device()
 
 
+_GPUS = [torch.device("cuda", i) for i in range(64)]
+
+
 def _new(shape, dtype, dev):
-    return torch.empty(shape, dtype=dtype, device="cuda:%d" % dev)
+    return torch.empty(shape, dtype=dtype, device=_GPUS[dev])
 
 
 def _matrix(name, t, shape, dtypes, dev):
