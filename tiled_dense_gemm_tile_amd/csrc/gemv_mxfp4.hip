@@ -139,8 +139,8 @@ __device__ __forceinline__ void gemv_join(float (&red)[kGemvWaves][MB * 4][64], 
                 "ds_read_b32 %7, %8 offset:%c15\n\ts_waitcnt lgkmcnt(0)"
                 : "=&v"(s[0]), "=&v"(s[1]), "=&v"(s[2]), "=&v"(s[3]), "=&v"(s[4]), "=&v"(s[5]), "=&v"(s[6]),
                   "=&v"(s[7])
-                : "v"(at), "n"(MB * 1024), "n"(MB * 2048), "n"(MB * 3072), "n"(MB * 4096), "n"(MB * 5120),
-                  "n"(MB * 6144), "n"(MB * 7168)
+                : "v"(at), "n"(MB * 1024 * 1), "n"(MB * 1024 * 2), "n"(MB * 1024 * 3), "n"(MB * 1024 * 4),
+                  "n"(MB * 1024 * 5), "n"(MB * 1024 * 6), "n"(MB * 1024 * 7)
                 : "memory");
 #pragma unroll
             for (int w = 0; w < 8; ++w) v += s[w];
@@ -190,7 +190,7 @@ __device__ __forceinline__ bool fp16_scales(uint32_t c) {
 // count of vector-memory instructions (a 1 KiB load holds the address unit
 // for about 31 cycles, whatever its lanes ask for), so X is read once per
 // workgroup: a workgroup keeps its K range [k_lo, k_hi) of X in LDS and walks
-// blocks of 16 weight rows (one workgroup per CU).  K ranges that do not
+// blocks of 16 weight rows (one workgroup per CU, or two).  K ranges that do not
 // cover K (blockIdx.y; X too large for LDS, or too few rows for the CUs) leave
 // fp32 partial sums in the workspace for a second kernel to add in order.
 //
@@ -205,13 +205,18 @@ __device__ __forceinline__ bool fp16_scales(uint32_t c) {
 //
 // SC: groups of 32 with K % 256 == 0 (0) or not (1), of 64 (2), of 128 (3) or
 // wider (4): a step's eight, eight, four, two codes or one of a row.
-constexpr int ring_slots(int MB) { return MB == 1 ? 4 : 2; }
+//
+// R slots: 4; 3 where two workgroups then share a CU's LDS (X of 16 KiB at
+// most: one row of 131072 x 4096 47.8 us against 55.8, of 14336 x 4096 8.5
+// against 9.1, of 4096 x 4096 4.9 against 5.1); 2 with two blocks of 16 rows of
+// X (MB).
 // LDS bytes a workgroup has for X beside its slots and its waves' sums.
-constexpr int x_bytes(int MB) { return 160 * 1024 - kGemvWaves * 2048 * ring_slots(MB) - 2 * MB * kGemvWaves * 1024; }
+constexpr int x_bytes(int MB, int R) {
+    return (R == 3 ? 80 : 160) * 1024 - kGemvWaves * 2048 * R - 2 * MB * kGemvWaves * 1024;
+}
 
-template <bool FP16, int MB, int SC>
-__global__ void __launch_bounds__(kGemvWaves * 64, 2) gemv_mxfp4_staged_kernel(GemvArgs p) {
-    constexpr int R = ring_slots(MB);
+template <bool FP16, int MB, int SC, int R>
+__global__ void __launch_bounds__(kGemvWaves * 64, R == 3 ? 4 : 2) gemv_mxfp4_staged_kernel(GemvArgs p) {
     __shared__ __attribute__((aligned(2048))) char ring[kGemvWaves][R][2048];
     __shared__ float red[2][kGemvWaves][MB * 4][64];
     extern __shared__ __attribute__((aligned(16))) char xs[];
@@ -345,32 +350,6 @@ __global__ void __launch_bounds__(kGemvWaves * 64, 2) gemv_mxfp4_staged_kernel(G
         // every load)
         asm volatile("" : "+v"(sc[S][0]), "+v"(sc[S][1]) : : "memory");
         if (k0 < k_hi) {                               // (a wave past the range's last step: nothing)
-            // (reads in asm, waited for in their own statement: plain LDS
-            // reads would also wait for the loads into the other slots)
-            uint32_t q[8];
-            u32x4 xf[8][MB];
-            const uint32_t w = w0 + S * 2048;
-            asm volatile(
-                "ds_read_b32 %0, %8\n\tds_read_b32 %1, %9\n\tds_read_b32 %2, %10\n\tds_read_b32 %3, %11\n\t"
-                "ds_read_b32 %4, %12\n\tds_read_b32 %5, %13\n\tds_read_b32 %6, %14\n\tds_read_b32 %7, %15\n\t"
-                "s_waitcnt lgkmcnt(0)"
-                : "=&v"(q[0]), "=&v"(q[1]), "=&v"(q[2]), "=&v"(q[3]), "=&v"(q[4]), "=&v"(q[5]), "=&v"(q[6]),
-                  "=&v"(q[7])
-                : "v"(w), "v"(w ^ 16), "v"(w ^ 32), "v"(w ^ 48), "v"(w ^ 64), "v"(w ^ 80), "v"(w ^ 96), "v"(w ^ 112)
-                : "memory");
-#pragma unroll
-            for (int a = 0; a < MB; ++a) {
-                const uint32_t x = x0[a] + (uint32_t)(k0 - k_lo) * 2;
-                asm volatile(
-                    "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:64\n\tds_read_b128 %2, %8 offset:128\n\t"
-                    "ds_read_b128 %3, %8 offset:192\n\tds_read_b128 %4, %8 offset:256\n\t"
-                    "ds_read_b128 %5, %8 offset:320\n\tds_read_b128 %6, %8 offset:384\n\t"
-                    "ds_read_b128 %7, %8 offset:448\n\ts_waitcnt lgkmcnt(0)"
-                    : "=&v"(xf[0][a]), "=&v"(xf[1][a]), "=&v"(xf[2][a]), "=&v"(xf[3][a]), "=&v"(xf[4][a]),
-                      "=&v"(xf[5][a]), "=&v"(xf[6][a]), "=&v"(xf[7][a])
-                    : "v"(x)
-                    : "memory");
-            }
             uint32_t c[2] = {sc[S][0], sc[S][1]};
             codes(c, k0);
             bool direct = true;
@@ -379,11 +358,40 @@ __global__ void __launch_bounds__(kGemvWaves * 64, 2) gemv_mxfp4_staged_kernel(G
                 if constexpr (ncodes == 8) direct = direct && fp16_scales<4>(c[1]);
                 direct = __all(direct);
             }
+            // (reads in asm, waited for in their own statement: plain LDS reads
+            // would also wait for the loads into the other slots; in two halves:
+            // their registers)
+            const uint32_t w = w0 + S * 2048;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int b = j / each;                // byte b % 4 of c[b / 4], as an exponent
-                const uint32_t v = b % 4 == 0 ? c[b / 4] << 23 : b % 4 == 1 ? c[b / 4] << 15 : b % 4 == 2 ? c[b / 4] << 7 : c[b / 4] >> 1;
-                gemv_step<FP16, MB>(xf[j], q[j], __builtin_bit_cast(float, v & 0x7f800000u), direct, acc);
+            for (int h = 0; h < 2; ++h) {
+                uint32_t q[4];
+                u32x4 xf[4][MB];
+                const uint32_t x = (uint32_t)(k0 - k_lo) * 2 + 256 * h;
+                asm volatile(
+                    "ds_read_b32 %0, %8\n\tds_read_b32 %1, %9\n\tds_read_b32 %2, %10\n\tds_read_b32 %3, %11\n\t"
+                    "ds_read_b128 %4, %12\n\tds_read_b128 %5, %12 offset:64\n\tds_read_b128 %6, %12 offset:128\n\t"
+                    "ds_read_b128 %7, %12 offset:192\n\ts_waitcnt lgkmcnt(0)"
+                    : "=&v"(q[0]), "=&v"(q[1]), "=&v"(q[2]), "=&v"(q[3]), "=&v"(xf[0][0]), "=&v"(xf[1][0]),
+                      "=&v"(xf[2][0]), "=&v"(xf[3][0])
+                    : "v"(w ^ (64 * h)), "v"(w ^ (64 * h + 16)), "v"(w ^ (64 * h + 32)), "v"(w ^ (64 * h + 48)),
+                      "v"(x0[0] + x)
+                    : "memory");
+                if constexpr (MB == 2)
+                    asm volatile(
+                        "ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:64\n\tds_read_b128 %2, %4 offset:128\n\t"
+                        "ds_read_b128 %3, %4 offset:192\n\ts_waitcnt lgkmcnt(0)"
+                        : "=&v"(xf[0][MB - 1]), "=&v"(xf[1][MB - 1]), "=&v"(xf[2][MB - 1]), "=&v"(xf[3][MB - 1])
+                        : "v"(x0[MB - 1] + x)
+                        : "memory");
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = 4 * h + i, b = j / each;   // byte b % 4 of c[b / 4], as an exponent
+                    const uint32_t v = b % 4 == 0   ? c[b / 4] << 23
+                                       : b % 4 == 1 ? c[b / 4] << 15
+                                       : b % 4 == 2 ? c[b / 4] << 7
+                                                    : c[b / 4] >> 1;
+                    gemv_step<FP16, MB>(xf[i], q[i], __builtin_bit_cast(float, v & 0x7f800000u), direct, acc);
+                }
             }
         }
         k0 += KW * 256;
@@ -416,6 +424,10 @@ __global__ void __launch_bounds__(kGemvWaves * 64, 2) gemv_mxfp4_staged_kernel(G
     if constexpr (R == 4) {
         while (step(std::integral_constant<int, 0>()) && step(std::integral_constant<int, 1>()) &&
                step(std::integral_constant<int, 2>()) && step(std::integral_constant<int, 3>())) {
+        }
+    } else if constexpr (R == 3) {
+        while (step(std::integral_constant<int, 0>()) && step(std::integral_constant<int, 1>()) &&
+               step(std::integral_constant<int, 2>())) {
         }
     } else {
         while (step(std::integral_constant<int, 0>()) && step(std::integral_constant<int, 1>())) {
@@ -488,7 +500,7 @@ __global__ void __launch_bounds__(kGemvWaves * 64) gemv_mxfp4_kernel(GemvArgs p)
 
 struct GemvPlan {
     bool staged;
-    int mb, splits, k_split, kwlog;
+    int mb, ring, splits, k_split, kwlog;
 };
 
 // How a call runs.  K ranges of the staged kernel: multiples of 256 (2048
@@ -499,7 +511,7 @@ inline GemvPlan plan_gemv(int64_t M, int64_t N, int64_t K, bool aligned, bool wo
     GemvPlan g;
     g.mb = M > 16 ? 2 : 1;
     const int64_t rows = M < 16 * g.mb ? M : 16 * g.mb;
-    int64_t most = (x_bytes(g.mb) / rows - 16) / 2 / 512 * 512;
+    int64_t most = (x_bytes(g.mb, g.mb == 1 ? 4 : 2) / rows - 16) / 2 / 512 * 512;
     if (most > 2048) most = most / 2048 * 2048;
     int64_t S = K > 0 ? (K + most - 1) / most : 1;
     const int64_t tiles = (N + 15) / 16, want = 256 / (tiles < 256 ? tiles : 256);
@@ -517,6 +529,7 @@ inline GemvPlan plan_gemv(int64_t M, int64_t N, int64_t K, bool aligned, bool wo
     // of 2048, 13.2 us against 14.9 with two and 16.3 with eight).
     const int64_t steps = ((ks < K ? ks : K) + 255) / 256;
     const int64_t tiles_m = (M + 16 * g.mb - 1) / (16 * g.mb);
+    g.ring = g.mb == 2 ? 2 : rows * (((ks < K ? ks : K) + 511) / 512 * 1024 + 16) <= x_bytes(1, 3) ? 3 : 4;
     const int64_t per = 256 / (g.splits * tiles_m) > 1 ? 256 / (g.splits * tiles_m) : 1;
     int64_t best = 0;
     for (int l = 0; l <= 3; ++l) {
@@ -533,7 +546,7 @@ inline GemvPlan plan_gemv(int64_t M, int64_t N, int64_t K, bool aligned, bool wo
     return g;
 }
 
-template <bool FP16, int MB>
+template <bool FP16, int MB, int R>
 hipError_t launch_gemv(const GemvPlan &g, GemvArgs &p, hipStream_t s) {
     const dim3 threads(kGemvWaves * 64);
     const unsigned tiles_m = (unsigned)((p.M + 16 * MB - 1) / (16 * MB));
@@ -545,11 +558,11 @@ hipError_t launch_gemv(const GemvPlan &g, GemvArgs &p, hipStream_t s) {
     const int rw = kGemvWaves >> p.kwlog, groups = (p.tiles_n + rw - 1) / rw;
     const int span = p.k_split < p.K ? p.k_split : p.K;
     p.x_pitch = (span + 511) / 512 * 1024 + 16;
-    int per = tg_api::cu_count(s) / (int)(g.splits * tiles_m);
+    int per = tg_api::cu_count(s) * (R == 3 ? 2 : 1) / (int)(g.splits * tiles_m);
     if (per <= 0) per = 1;
     const dim3 grid((unsigned)(groups < per ? groups : per), (unsigned)g.splits, tiles_m);
     const size_t lds = (size_t)rows * p.x_pitch;
-#define TG_GEMV(sc) hipLaunchKernelGGL((gemv_mxfp4_staged_kernel<FP16, MB, sc>), grid, threads, lds, s, p)
+#define TG_GEMV(sc) hipLaunchKernelGGL((gemv_mxfp4_staged_kernel<FP16, MB, sc, R>), grid, threads, lds, s, p)
     switch (p.kshift) {
     case 5:
         if (p.K % 256 == 0)
@@ -567,7 +580,9 @@ hipError_t launch_gemv(const GemvPlan &g, GemvArgs &p, hipStream_t s) {
 
 template <bool FP16>
 hipError_t launch_gemv_rows(const GemvPlan &g, GemvArgs &p, hipStream_t s) {
-    return g.mb == 2 ? launch_gemv<FP16, 2>(g, p, s) : launch_gemv<FP16, 1>(g, p, s);
+    return g.mb == 2     ? launch_gemv<FP16, 2, 2>(g, p, s)
+           : g.ring == 3 ? launch_gemv<FP16, 1, 3>(g, p, s)
+                         : launch_gemv<FP16, 1, 4>(g, p, s);
 }
 
 }  // namespace tg
