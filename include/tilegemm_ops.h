@@ -16,7 +16,8 @@
  * GEMM_OK and GEMM_ERR_HIP leaves every output untouched.  Sizes and
  * leading dimensions count elements; matrices are row-major; pointers are
  * aligned to their element size (GEMM_ERR_MISALIGNED) and need no more than
- * that.  Sizes are below 2^31 (GEMM_ERR_UNSUPPORTED).  Outputs overlap
+ * that.  Sizes are below 2^31, and N of the row operators below 2^28
+ * (GEMM_ERR_UNSUPPORTED).  Outputs overlap
  * neither inputs nor each other unless a call says so.  The same call on
  * the same values gives the same bits.
  *
@@ -67,8 +68,9 @@ gemm_status mxfp8_quantize(int64_t rows, int64_t N, const void *X, int64_t ldx, 
  *     dimension).  Y may be X or R too, unless H is the same.
  *   rstd: `rows` floats, or NULL
  *   eps: finite, >= 0 (GEMM_ERR_UNSUPPORTED otherwise)
- * A row with a NaN or an infinity gives NaN.  rows or N == 0: nothing is
- * enqueued.
+ * A row with a NaN gives NaN.  One with an infinity, or whose sum of squares
+ * exceeds fp32, has rstd 0: NaN at its infinities, zeros elsewhere.  rows or N
+ * == 0: nothing is enqueued.
  */
 gemm_status rmsnorm(int64_t rows, int64_t N, const void *X, int64_t ldx, const void *R, int64_t ldr,
                     int type, const void *W, int w_type, float eps, void *H, int64_t ldh,
@@ -117,11 +119,13 @@ size_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t N);
  * below 2^-117 reach bf16's subnormals, and above 2^119 its end.)
  *   M, N, K < 2^31; N a multiple of 32; lda >= M, ldb >= N, ldsfb >= N/32,
  *   ldd >= N, ldc >= N (C NULL: 0; C == D with ldc == ldd accumulates in
- *   place); out_type as gemm_bf16 (C and D); leading dimensions below 8 MiB.
+ *   place); out_type as gemm_bf16 (C and D); leading dimensions below 8 MiB
+ *   in bytes.
  *   workspace: device memory, 256-byte aligned, or NULL.  With at least
  *     gemm_wgrad_mxfp8_workspace_bytes(M, N, K) bytes, grids too small to fill
  *     the GPU cut K into ranges and sum the fp32 partial products in order; a
  *     smaller one or NULL runs uncut (the same result up to summation order).
+ *     Calls sharing it must be ordered.
  * Scale code 0xFF and e4m3 NaN give NaN in the column's outputs.  K == 0:
  * D = C (or 0).
  */
@@ -148,7 +152,10 @@ size_t gemm_wgrad_mxfp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *     gemv_mxfp4_workspace_bytes(M, N, K) bytes, calls whose X exceeds the
  *     LDS of a compute unit, and those of few rows of W, cut K into ranges
  *     and sum the fp32 partial sums in order; a smaller one or NULL runs
- *     uncut, slower (the same result up to summation order).
+ *     uncut, slower (the same result up to summation order).  Calls sharing it
+ *     must be ordered.
+ * Leading dimensions below 8 MiB in bytes.  Weights beyond bf16's range (4 and
+ * 6 at 2^126, 2 to 6 at 2^127) are infinite.
  * Scale code 0xFF gives NaN in the row's outputs.
  */
 gemm_status gemv_mxfp4(int64_t M, int64_t N, int64_t K, int64_t kblock, const void *X, int64_t ldx, int x_type,

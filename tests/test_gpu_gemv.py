@@ -185,3 +185,46 @@ def test_agrees_with_the_block_scaled_product():
     W, S = torch.from_numpy(w).to(DEV), torch.from_numpy(sf).to(DEV)
     A = tg.gemm_mxfp4(torch.from_numpy(xc).to(DEV), torch.from_numpy(one).to(DEV), W, S)
     assert torch.equal(tg.gemv_mxfp4(X, W, S), A)
+
+
+@pytest.mark.parametrize("kind", XT)
+@pytest.mark.parametrize("case", [(500, 16400, 1056, 32), (2400, 500, 14336, 128)], ids=str)
+def test_rows_in_several_passes(case, kind):
+    """More rows than the partial sums of one pass hold: whole passes and a shorter last one."""
+    m, n, k, kb = case
+    x, w, sf = case_of(13, m, n, k, kb, kind, 127, 129)
+    W, S = torch.from_numpy(w).to(DEV), torch.from_numpy(sf).to(DEV)
+    need = tg.gemv_mxfp4_workspace_bytes(m, n, k)
+    splits = -(-k // 1024)
+    assert 0 < need < splits * m * n * 4 and need <= 64 << 20
+    want = torch.mm(x.double(), torch.from_numpy(ref.fp4_weights(w, sf, kb)).to(DEV).t().contiguous())
+    assert want.abs().max() < 2 ** 22
+    c = torch.randint(-9, 10, (m, n), device=DEV).float()
+    ws = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device=DEV)
+    D = torch.full((m + 1, n + 3), 5.0, device=DEV)
+    D[:m, :n] = c
+    tg.gemv_mxfp4(x, W, S, kblock=kb, C=D[:m, :n], D=D[:m, :n], workspace=ws[:need])
+    assert torch.equal(D[:m, :n].double(), want + c.double()) and (ws[need:] == 0x5A).all()
+    D[:m, :n] = 5
+    assert (D == 5).all()
+    b = tg.gemv_mxfp4(x, W, S, kblock=kb, C=c.bfloat16(), out_dtype=torch.bfloat16)
+    assert torch.equal(b, (want + c.double()).float().bfloat16())
+
+
+@pytest.mark.parametrize("kind", XT)
+@pytest.mark.parametrize("k", [32, 256])
+def test_all_scale_codes(kind, k):
+    """One weight of each row against 1.0: exact from 2^-127 up; infinite past bf16's range."""
+    w = np.full((3, k // 2), 0x21, np.uint8)           # 0.5, 1
+    w[1], w[2] = 0x75, 0                               # 3, 6; zeros
+    x = torch.zeros(2, k, dtype=XT[kind], device=DEV)
+    x[0, 0], x[1, 1] = 1.0, 1.0
+    for code in (0, 1, 2, 9, 103, 104, 135, 136, 245, 252, 253, 254):
+        D = f64(tg.gemv_mxfp4(x, torch.from_numpy(w).to(DEV),
+                              torch.full((3, k // 32), code, dtype=torch.uint8, device=DEV)))
+        s = np.ldexp(1.0, code - 127)
+        assert np.array_equal(D[0, [0, 2]], [0.5 * s, 0]) and np.array_equal(D[1, [0, 2]], [s, 0]), code
+        if code <= 252:
+            assert np.array_equal(D[:, 1], [3 * s, 6 * s]), code
+        else:
+            assert not np.isfinite(D[:, 1]).any(), code

@@ -285,3 +285,55 @@ def test_same_bits_every_call():
         again = tg.rmsnorm_backward(dy, h, w, rstd)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
         assert torch.equal(y, tg.rmsnorm(h, w, EPS)[0])
+
+
+@pytest.mark.parametrize("case", [((4 << 20) + 7, 8, "bf16"), ((2 << 20) + 3, 260, "f32")], ids=str)
+def test_norm_of_more_rows_than_one_launch(case):
+    """2^20 workgroups of four or two rows each, and a few rows more."""
+    rows, n, kind = case
+    x = torch.randn(rows, n, device=DEV, generator=torch.Generator(DEV).manual_seed(40)).to(TYPES[kind])
+    w = rows_of(41, 1, n, "f32")[0].contiguous()
+    y, _, rstd = tg.rmsnorm(x, w, EPS, Y=torch.full_like(x, float("nan")), rstd=torch.full((rows,), -1.0, device=DEV))
+    for a in (0, rows // 2, rows - 4099):
+        want, rs = ref.norm(f64(x[a:a + 4099]), f64(w), EPS)
+        assert (np.abs(f64(rstd[a:a + 4099]) - rs) <= ref.rstd_bound(n) * rs).all()
+        bound = (ref.rstd_bound(n) + 2 * ref.U) * np.abs(want) + 2.0 ** -148
+        assert (np.abs(f64(y[a:a + 4099]) - want) <= bound + ref.HALF[kind] * (np.abs(want) + bound) + ref.TINY[kind]).all()
+    assert (rstd > 0).all() and not torch.isnan(y).any()
+
+
+def test_long_rows_past_the_grid():
+    """More rows than the kernels of long rows have workgroups: each as if alone."""
+    rows, n = 2051, 16388
+    x, dy = (torch.randn(rows, n, device=DEV, generator=torch.Generator(DEV).manual_seed(s)) for s in (42, 43))
+    w = rows_of(44, 1, n, "f32")[0].contiguous()
+    y, _, rstd = tg.rmsnorm(x, w, EPS)
+    dx, dw = tg.rmsnorm_backward(dy, x, w, rstd)
+    for a in (0, 1500, 2047):
+        yb, _, rb = tg.rmsnorm(x[a:a + 4], w, EPS)
+        assert torch.equal(y[a:a + 4], yb) and torch.equal(rstd[a:a + 4], rb)
+        assert torch.equal(dx[a:a + 4], tg.rmsnorm_backward(dy[a:a + 4], x[a:a + 4], w, rb, weight_grad=False)[0])
+    want, rs = ref.norm(f64(x[2040:]), f64(w), EPS)
+    assert (np.abs(f64(rstd[2040:]) - rs) <= ref.rstd_bound(n) * rs).all()
+    u = x.double() * rstd.double()[:, None]
+    adw = (dy.double() * u).abs().sum(0)
+    assert ((dw.double() - (dy.double() * u).sum(0)).abs() <= (rows / 64 + 1 + 64 + 2) * ref.U * adw).all()
+
+
+def test_norm_over_its_input_returns_no_h():
+    x = rows_of(45, 5, 96, "bf16")
+    w = rows_of(46, 1, 96, "bf16")[0].contiguous()
+    y0, h, s0 = tg.rmsnorm(x, w, EPS)
+    assert h is x
+    a = x.clone()
+    y, h, s = tg.rmsnorm(a, w, EPS, Y=a)
+    assert h is None and torch.equal(y, y0) and torch.equal(s, s0) and y.data_ptr() == a.data_ptr()
+
+
+def test_norm_of_infinite_rows():
+    x = rows_of(47, 3, 256, "f32")
+    x[0, 9] = float("inf")
+    x[1] *= 1e20                                       # squares past fp32
+    y, _, rstd = tg.rmsnorm(x, torch.ones(256, device=DEV), EPS)
+    assert rstd[0] == 0 and rstd[1] == 0 and (y[1] == 0).all()
+    assert torch.isnan(y[0, 9]) and (y[0, :9] == 0).all() and (y[0, 10:] == 0).all()

@@ -202,3 +202,18 @@ def test_extreme_scales():
             D = tg.gemm_wgrad_mxfp8(torch.ones(1, 8, dtype=torch.bfloat16, device=DEV),
                                     torch.from_numpy(q[t:t + 1]).to(DEV), torch.from_numpy(sf[t:t + 1]).to(DEV))
             assert (f64(D) == 1.5 * np.ldexp(1.0, int(sf[t, 0]) - 127)).all()
+
+
+@pytest.mark.parametrize("shape", [(1, 32), (64, 32), (1, 128), (64, 256)], ids=str)
+def test_all_scale_codes(shape):
+    """Single products at the ends of the scales, over both kernels: exact where bf16 holds the value."""
+    k, n = shape
+    q = np.zeros((k, n), np.uint8)
+    q[0, 0::4], q[0, 1::4] = 0x3C, 0x08                # 1.5, 2^-6
+    A = torch.zeros(k, 8, dtype=torch.bfloat16, device=DEV)
+    A[0] = 1.0
+    for code in (0, 1, 6, 10, 245, 246, 254):
+        D = f64(tg.gemm_wgrad_mxfp8(A, torch.from_numpy(q).to(DEV),
+                                    torch.full((k, n // 32), code, dtype=torch.uint8, device=DEV)))
+        s = np.ldexp(1.0, code - 127)
+        assert (D[:, 0::4] == 1.5 * s).all() and (D[:, 1::4] == s / 64).all() and (D[:, 2::4] == 0).all(), code

@@ -223,3 +223,26 @@ def test_binding_refuses_host_tensors_and_types():
         tg.gemv_mxfp4(x.float(), torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.uint8))
     with pytest.raises(TypeError):
         tg.gemm_wgrad_mxfp8(x.half(), torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8))
+
+
+def test_limits_of_row_lengths():
+    n = 1 << 28
+    assert quant(N=n, ldx=n, ldq=n, ldsf=n // 32) == UNSUPPORTED
+    for mx in (False, True):
+        assert norm(mx=mx, N=n, ldx=n, ldr=n, ldh=n, ldy=n, ldsf=n // 32) == UNSUPPORTED
+    assert bwd(N=n, lddy=n, ldh=n, lddh=n, lddx=n) == UNSUPPORTED
+    assert tg.rmsnorm_backward_workspace_bytes(4, n) == 0
+
+
+def test_outputs_over_each_other_are_refused():
+    assert quant(q=P) == UNSUPPORTED
+    assert quant(sf=P) == UNSUPPORTED
+    assert quant(q=Q, sf=Q) == UNSUPPORTED
+    assert norm(mx=True, Y=Q + 4096, SF=Q + 4096) == UNSUPPORTED
+
+
+def test_gemv_workspace_is_bounded():
+    """However many rows of X there are: 64 MiB, or 32 rows' partial sums."""
+    for m, n, k in ((1 << 20, 14336, 16384), (4096, 4096, 14336), (1 << 20, 64, 1 << 20)):
+        splits = -(-k // 1024)
+        assert 0 < tg.gemv_mxfp4_workspace_bytes(m, n, k) <= max(64 << 20, splits * 32 * n * 4)

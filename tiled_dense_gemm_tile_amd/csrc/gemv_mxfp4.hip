@@ -507,6 +507,16 @@ struct GemvPlan {
 // where LDS holds that much of M rows, so that all eight waves have a step of
 // every block), as many as X needs; more where the blocks of rows leave half
 // of the CUs idle, down to ranges of 2048.
+//
+// Rows of X a pass of a call in several K ranges takes: its partial sums stay
+// within 64 MiB (or 32 rows').
+inline int64_t gemv_pass(int64_t M, int64_t N, int splits) {
+    if (splits == 1) return M;
+    int64_t rows = ((int64_t)64 << 20) / (splits * tg_api::splitk_ldw(N) * 4) / 32 * 32;
+    if (rows < 32) rows = 32;
+    return M < rows ? M : rows;
+}
+
 inline GemvPlan plan_gemv(int64_t M, int64_t N, int64_t K, bool aligned, bool workspace) {
     GemvPlan g;
     g.mb = M > 16 ? 2 : 1;
@@ -591,7 +601,8 @@ extern "C" {
 
 size_t gemv_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0 || K <= 0 || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return 0;
-    return splitk_bytes(M, N, tg::plan_gemv(M, N, K, true, true).splits);
+    const int splits = tg::plan_gemv(M, N, K, true, true).splits;
+    return splitk_bytes(tg::gemv_pass(M, N, splits), N, splits);
 }
 
 gemm_status gemv_mxfp4(int64_t M, int64_t N, int64_t K, int64_t kblock, const void *X, int64_t ldx, int x_type,
@@ -639,9 +650,20 @@ gemm_status gemv_mxfp4(int64_t M, int64_t N, int64_t K, int64_t kblock, const vo
     p.x_pitch = 0;
     p.ws = g.splits > 1 ? (float *)workspace : nullptr;
     p.ldws = splitk_ldw(N);
-    st = launched(x_type == GEMM_TYPE_FP16 ? tg::launch_gemv_rows<true>(g, p, stream)
-                                           : tg::launch_gemv_rows<false>(g, p, stream));
-    return st != GEMM_OK || g.splits == 1 ? st : reduce_splits(a, workspace, g.splits, stream);
+    const int64_t pass = tg::gemv_pass(M, N, g.splits);
+    for (int64_t m = 0; m < M && st == GEMM_OK; m += pass) {
+        const int os = out_type == GEMM_OUT_BF16 ? 2 : 4;
+        Common part = a;
+        part.M = M - m < pass ? M - m : pass;
+        part.A = p.X = (const char *)X + m * ldx * 2;
+        if (C) part.C = p.C = (const char *)C + m * ldc * os;
+        part.D = p.D = (char *)D + m * ldd * os;
+        p.M = (int)part.M;
+        st = launched(x_type == GEMM_TYPE_FP16 ? tg::launch_gemv_rows<true>(g, p, stream)
+                                               : tg::launch_gemv_rows<false>(g, p, stream));
+        if (st == GEMM_OK && g.splits > 1) st = reduce_splits(part, workspace, g.splits, stream);
+    }
+    return st;
 }
 
 }  // extern "C"

@@ -22,7 +22,7 @@ struct NormArgs {
     uint8_t *SF;
     float *rstd;
     int64_t ldx, ldr, ldh, ldy, ldsf;
-    int64_t rows;
+    int64_t rows, row0;                                // row0: the launch's first row
     int N;
     float eps;
     bool w_f32;
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_kernel(NormArgs
     typedef RowVec<T> RV;
     constexpr int VE = RV::VE, RPB = TPR < 256 ? 256 / TPR : 1;
     const int t = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    const int64_t row = p.row0 + (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
     if (TPR == 64 && row >= p.rows) return;
     const bool in = TPR != 128 || row < p.rows;        // (rows of two waves meet at a barrier)
     const int N = p.N;
@@ -108,10 +108,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_kernel(NormArgs
 // Rows too long for the registers of one workgroup: two passes, the second
 // reading the row again (h from H where it was written, else x + r again).
 template <int T, bool MX>
-__global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs p) {
+__device__ __forceinline__ void rmsnorm_long_row(const NormArgs &p, int64_t row) {
     typedef RowVec<T> RV;
     constexpr int VE = RV::VE;
-    const int64_t row = blockIdx.x;
     const int N = p.N, t = threadIdx.x;
     const typename RV::S *x = (const typename RV::S *)p.X + row * p.ldx;
     const typename RV::S *r = (const typename RV::S *)p.R + row * p.ldr;
@@ -163,6 +162,14 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs p) {
     }
 }
 
+template <int T, bool MX>
+__global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs p) {
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        rmsnorm_long_row<T, MX>(p, row);
+        __syncthreads();                               // (the row's sums in LDS)
+    }
+}
+
 // One vector of one row per thread and step; blocks of 32 elements are
 // independent, so rows need no workgroup of their own.  STREAM: codes are
 // stored past the caches, for results larger than the memory-side cache holds
@@ -186,15 +193,20 @@ __global__ void __launch_bounds__(256)
 }
 
 template <int T, bool MX, int TPR, int VPT>
-hipError_t go(const NormArgs &p, hipStream_t s) {
+hipError_t go(NormArgs &p, hipStream_t s) {
     constexpr int rows = TPR < 256 ? 256 / TPR : 1;
-    hipLaunchKernelGGL((rmsnorm_kernel<T, MX, TPR, VPT>), dim3((unsigned)((p.rows + rows - 1) / rows)),
-                       dim3(TPR < 256 ? 256 : TPR), 0, s, p);
-    return hipGetLastError();
+    hipError_t e = hipSuccess;
+    for (p.row0 = 0; p.row0 < p.rows && e == hipSuccess; p.row0 += kMaxGrid * rows) {
+        const int64_t blocks = (p.rows - p.row0 + rows - 1) / rows;
+        hipLaunchKernelGGL((rmsnorm_kernel<T, MX, TPR, VPT>), dim3((unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid)),
+                           dim3(TPR < 256 ? 256 : TPR), 0, s, p);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 template <int T, bool MX>
-hipError_t launch_norm(const NormArgs &p, hipStream_t s) {
+hipError_t launch_norm(NormArgs &p, hipStream_t s) {
     const int nvec = (int)(((int64_t)p.N + kVE<T> - 1) / kVE<T>);
     // The fewest vectors per thread: a row's loads are all in flight at once
     // either way, and more waves share a row's arithmetic (16384 x 4096 bf16
@@ -207,7 +219,8 @@ hipError_t launch_norm(const NormArgs &p, hipStream_t s) {
     if (nvec <= 1024) return go<T, MX, 256, 4>(p, s);
     if (nvec <= 2048) return go<T, MX, 256, 8>(p, s);
     if (nvec <= 4096) return go<T, MX, 1024, 4>(p, s);
-    hipLaunchKernelGGL((rmsnorm_long_kernel<T, MX>), dim3((unsigned)p.rows), dim3(1024), 0, s, p);
+    hipLaunchKernelGGL((rmsnorm_long_kernel<T, MX>), dim3((unsigned)(p.rows < 2048 ? p.rows : 2048)), dim3(1024),
+                       0, s, p);
     return hipGetLastError();
 }
 
@@ -231,7 +244,7 @@ gemm_status run_norm(bool mx, int64_t rows, int64_t N, const void *X, int64_t ld
         misaligned(W, elem_size(w_type)) || misaligned(rstd, 4))
         return GEMM_ERR_MISALIGNED;
     if ((H && H == Y) || (H == X && ldh != ldx) || (H && H == R && ldh != ldr)) return GEMM_ERR_UNSUPPORTED;
-    if ((Y == X && ldy != ldx) || (Y == R && ldy != ldr) || (mx && (Y == X || Y == R))) return GEMM_ERR_UNSUPPORTED;
+    if ((Y == X && ldy != ldx) || (Y == R && ldy != ldr) || (mx && (Y == X || Y == R || Y == SF))) return GEMM_ERR_UNSUPPORTED;
     tg::NormArgs p;
     p.X = X;
     p.R = R;
@@ -284,6 +297,7 @@ gemm_status mxfp8_quantize(int64_t rows, int64_t N, const void *X, int64_t ldx, 
     if (ldx < N || ldq < N || ldsf < N / 32) return GEMM_ERR_BAD_LD;
     if (!X || !Q || !SF) return GEMM_ERR_NULL_POINTER;
     if (misaligned(X, elem_size(x_type))) return GEMM_ERR_MISALIGNED;
+    if (Q == X || SF == X || SF == Q) return GEMM_ERR_UNSUPPORTED;
     const int ve = x_type == GEMM_TYPE_F32 ? 4 : 8;
     const int nvec = (int)(N / ve);
     const int64_t want = (rows * nvec + 255) / 256;

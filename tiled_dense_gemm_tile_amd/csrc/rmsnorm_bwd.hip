@@ -157,11 +157,10 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_dw_long_kernel(NormBwdArgs p,
 }
 
 template <int T>
-__global__ void __launch_bounds__(1024) rmsnorm_bwd_dx_long_kernel(NormBwdArgs p) {
+__device__ __forceinline__ void rmsnorm_bwd_dx_long_row(const NormBwdArgs &p, int64_t row) {
     typedef RowVec<T> RV;
     constexpr int VE = RV::VE;
     const int t = threadIdx.x, N = p.N;
-    const int64_t row = blockIdx.x;
     const float rstd = p.rstd[row];
     const typename RV::S *dys = (const typename RV::S *)p.dY + row * p.lddy;
     const typename RV::S *hs = (const typename RV::S *)p.H + row * p.ldh;
@@ -193,6 +192,14 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_dx_long_kernel(NormBwdArgs p
             o[u] = Elem<T>::down(fmaf(rstd, g - f * m, Elem<T>::up(a[u])));
         }
         RV::store((typename RV::S *)p.dX + row * p.lddx, (int)c, N, o);
+    }
+}
+
+template <int T>
+__global__ void __launch_bounds__(1024) rmsnorm_bwd_dx_long_kernel(NormBwdArgs p) {
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        rmsnorm_bwd_dx_long_row<T>(p, row);
+        __syncthreads();                               // (the row's sums in LDS)
     }
 }
 
@@ -263,7 +270,8 @@ hipError_t launch_bwd(const NormBwdArgs &p, float *dW, hipStream_t s) {
                 const hipError_t e = hipGetLastError();
                 if (e != hipSuccess) return e;
             }
-            hipLaunchKernelGGL((rmsnorm_bwd_dx_long_kernel<T>), dim3((unsigned)p.rows), dim3(1024), 0, s, p);
+            hipLaunchKernelGGL((rmsnorm_bwd_dx_long_kernel<T>), dim3((unsigned)(p.rows < 2048 ? p.rows : 2048)),
+                               dim3(1024), 0, s, p);
         }
 #undef TG_BWD
         const hipError_t e = hipGetLastError();
@@ -282,7 +290,8 @@ hipError_t launch_bwd(const NormBwdArgs &p, float *dW, hipStream_t s) {
 extern "C" {
 
 size_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t N) {
-    if (rows <= 0 || N <= 0 || rows >= kMaxDim || N >= kMaxDim) return 0;
+    bool none;
+    if (check_rows(rows, N, &none) != GEMM_OK || none) return 0;
     return (size_t)(rows < tg::kBwdGroups ? rows : tg::kBwdGroups) * (size_t)N * 4;
 }
 

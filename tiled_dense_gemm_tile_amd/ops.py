@@ -142,12 +142,14 @@ def rmsnorm(X, W, eps, residual=None, Y=None, H=None, rstd=None):
     type; X itself without a residual): Y = H * W * rstd, rstd = 1 /
     sqrt(mean(H^2) + eps).  W (N,) of X's type or float32.  H may be given as
     X or the residual (in place), and so may Y unless H is the same.
-    Returns (Y, H, rstd), H being X when there is no residual and no H."""
+    Returns (Y, H, rstd), H being X when there is no residual and no H (None
+    where Y has overwritten it)."""
     shape, code, dev = _rows("X", X)
     if Y is None:
         Y = _new(shape, X.dtype, dev)
     out = _matrix("Y", Y, shape, (X.dtype,), dev)
-    return (Y, *_norm(_load().rmsnorm, X, W, eps, residual, H, rstd, shape, code, dev, out))
+    H, rstd = _norm(_load().rmsnorm, X, W, eps, residual, H, rstd, shape, code, dev, out)
+    return Y, None if H is X and out[0] == X.data_ptr() else H, rstd
 
 
 def rmsnorm_mxfp8(X, W, eps, residual=None, Q=None, SF=None, H=None, rstd=None):
