@@ -14,8 +14,9 @@
 // A fragment's eight K-consecutive values have eight different scales, which
 // is why the conversion comes before LDS and not after it.
 //
-// Tiles past the last full round of workgroups (all of them, in a small grid) may be cut along K into `splits` ranges, whose fp32 partial tiles go
-// to the workspace for a second kernel to add in order.
+// Tiles past the last full round of workgroups (all of them, in a small grid)
+// may be cut along K into `splits` ranges, whose fp32 partial tiles go to the
+// workspace for a second kernel to add in order.
 #pragma once
 
 #include <type_traits>
@@ -300,51 +301,45 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
         barrier();
     };
 
-    if (nt > 0) {
-        constexpr std::integral_constant<int, 0> even{};
-        constexpr std::integral_constant<int, 1> odd{};
-        auto start_b = [&]() __attribute__((always_inline)) {
-            const __amdgpu_buffer_rsrc_t r = pb.rsrc();
+    // (every K range holds a row)
+    constexpr std::integral_constant<int, 0> even{};
+    constexpr std::integral_constant<int, 1> odd{};
+    auto start_b = [&]() __attribute__((always_inline)) {
+        const __amdgpu_buffer_rsrc_t r = pb.rsrc();
 #pragma unroll
-            for (int j = 0; j < NV; ++j) load_b(r, j);
-            load_s();
-            next_s();
-            pb.move(b_step);
-            pb.set_span(b_ld, b_row, 0u);
-        };
-        const __amdgpu_buffer_rsrc_t ra = pa.rsrc();
+        for (int j = 0; j < NV; ++j) load_b(r, j);
+        load_s();
+        next_s();
+        pb.move(b_step);
+        pb.set_span(b_ld, b_row, 0u);
+    };
+    const __amdgpu_buffer_rsrc_t ra = pa.rsrc();
 #pragma unroll
-        for (int j = 0; j < LA; ++j) dma_a(ra, 0, j);
-        pa.move(a_step);
-        pa.set_span(a_ld, a_row, 15u);
-        start_b();
-        take_scales();
-        static_for<0, 2 * T>([&](auto s) __attribute__((always_inline)) { convert(s, even); });
-        start_b();
-        wait_vmcnt<NV + 1>();                          // A(0) landed
-        wait_lgkmcnt0();
-        barrier();
-        tile(std::true_type(), even);
-        int t = 1;
-        for (; t + 1 < nt; t += 2) {
-            tile(std::false_type(), odd);
-            tile(std::false_type(), even);
-        }
-        if (t < nt) tile(std::false_type(), odd);
-#pragma unroll
-        for (int q = 0; q < Q; ++q) mfma(std::false_type(), 1, q / TN, q % TN);
-        // (the wait states of mfma_result_fence, for either tile)
-        asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 3" : "+a"(acc[0][0]));
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[i][j]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < LA; ++j) dma_a(ra, 0, j);
+    pa.move(a_step);
+    pa.set_span(a_ld, a_row, 15u);
+    start_b();
+    take_scales();
+    static_for<0, 2 * T>([&](auto s) __attribute__((always_inline)) { convert(s, even); });
+    start_b();
+    wait_vmcnt<NV + 1>();                          // A(0) landed
+    wait_lgkmcnt0();
+    barrier();
+    tile(std::true_type(), even);
+    int t = 1;
+    for (; t + 1 < nt; t += 2) {
+        tile(std::false_type(), odd);
+        tile(std::false_type(), even);
     }
+    if (t < nt) tile(std::false_type(), odd);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) mfma(std::false_type(), 1, q / TN, q % TN);
+    // (the wait states of mfma_result_fence, for either tile)
+    asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 3" : "+a"(acc[0][0]));
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[i][j]));
     wait_vmcnt<0>();
     wait_lgkmcnt0();
     barrier();
