@@ -23,13 +23,15 @@ _E8M0 = (torch.float8_e8m0fnu, torch.uint8)
 _E2M1 = (torch.uint8, torch.float4_e2m1fn_x2)
 _F32 = (torch.float32,)
 _NONE = (None, 0)
+_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _run(f, dev, *args):
     """The C call on torch's current stream of GPU ``dev``, with ``dev``
     current (a NULL stream means the current device's)."""
-    stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch._C._cuda_getDevice() == dev:
+    stream = _current_stream(dev)
+    if _current_device() == dev:
         status = f(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -58,7 +60,7 @@ def _matrix(name, t, shape, dtypes, dev):
         raise TypeError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
     if t.shape != shape:
         raise ValueError("%s must be (%d, %d)" % (name, shape[0], shape[1]))
-    if t.get_device() != dev or not t.is_cuda:
+    if t.get_device() != dev:                          # (-1 of a host tensor)
         raise ValueError("%s must be a device tensor on cuda:%d" % (name, dev))
     ld, one = t.stride()
     if one != 1 and shape[1] > 1:
@@ -74,7 +76,7 @@ def _vector(name, t, n, dtypes, dev):
         raise TypeError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
     if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError("%s must be a contiguous vector of %d" % (name, n))
-    if t.get_device() != dev or not t.is_cuda:
+    if t.get_device() != dev:                          # (-1 of a host tensor)
         raise ValueError("%s must be a device tensor on cuda:%d" % (name, dev))
     return t.data_ptr()
 
@@ -103,7 +105,7 @@ def _workspace(t, need, dev):
         if not need:
             return None, None, 0
         t = _new(need, torch.uint8, dev)
-    elif t.get_device() != dev or not t.is_cuda or not t.is_contiguous():
+    elif t.get_device() != dev or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous device tensor on cuda:%d" % dev)
     return t, t.data_ptr(), t.numel() * t.element_size()
 
