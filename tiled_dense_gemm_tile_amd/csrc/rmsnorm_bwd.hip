@@ -234,7 +234,12 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_reduce_kernel(const float *pa
     }
 }
 
-constexpr int kBwdGroups = 512;                        // workgroups walking the rows: two per CU
+// Workgroups walking the rows: two per CU, or one where a thread has several
+// vectors in flight anyway or the rows are few (fewer partial sums of dw: 1000
+// x 8192 bf16 18.5 against 24.1 us, 4096 x 14336 74 against 81, 1000 x 4096
+// 11.9 against 13.9; 4096 x 4096 28.6 against 26.6, 16384 x 2048 39.5 against
+// 37.2).
+constexpr int kBwdGroups = 512;
 constexpr int kLongGroups = 64;
 
 template <int T>
@@ -246,7 +251,8 @@ hipError_t launch_bwd(const NormBwdArgs &p, float *dW, hipStream_t s) {
 #define TG_BWD(tpr, nt, vpt)                                                                                     \
     {                                                                                                            \
         const int64_t blocks = (p.rows + (nt) / (tpr) - 1) / ((nt) / (tpr));                                     \
-        G = (int)(blocks < kBwdGroups ? blocks : kBwdGroups);                                                    \
+        const int64_t most = (vpt) > 1 || blocks < 2048 ? kBwdGroups / 2 : kBwdGroups;                           \
+        G = (int)(blocks < most ? blocks : most);                                                                \
         hipLaunchKernelGGL((rmsnorm_bwd_kernel<T, tpr, nt, vpt>), dim3(G), dim3(nt), 0, s, p);                   \
     }
         if (nvec <= 64) {
@@ -260,7 +266,11 @@ hipError_t launch_bwd(const NormBwdArgs &p, float *dW, hipStream_t s) {
         } else if (nvec <= 1024) {
             TG_BWD(512, 512, 2)
         } else if (nvec <= 2048) {
-            TG_BWD(512, 512, 4)
+            // (16-bit rows: 1024 threads of two vectors spill)
+            if constexpr (T == 0)
+                TG_BWD(1024, 1024, 2)
+            else
+                TG_BWD(512, 512, 4)
         } else if (T == 0 && nvec <= 4096) {
             if constexpr (T == 0) TG_BWD(1024, 1024, 4)
         } else {
