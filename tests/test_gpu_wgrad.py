@@ -205,15 +205,30 @@ def test_extreme_scales():
 
 
 @pytest.mark.parametrize("shape", [(1, 32), (64, 32), (1, 128), (64, 256)], ids=str)
-def test_all_scale_codes(shape):
+@pytest.mark.parametrize("lda", [8, 9])
+def test_all_scale_codes(shape, lda):
     """Single products at the ends of the scales, over both kernels: exact where bf16 holds the value."""
     k, n = shape
     q = np.zeros((k, n), np.uint8)
     q[0, 0::4], q[0, 1::4] = 0x3C, 0x08                # 1.5, 2^-6
-    A = torch.zeros(k, 8, dtype=torch.bfloat16, device=DEV)
+    A = torch.zeros(k, lda, dtype=torch.bfloat16, device=DEV)[:, :8]
     A[0] = 1.0
     for code in (0, 1, 6, 10, 245, 246, 254):
         D = f64(tg.gemm_wgrad_mxfp8(A, torch.from_numpy(q).to(DEV),
                                     torch.full((k, n // 32), code, dtype=torch.uint8, device=DEV)))
         s = np.ldexp(1.0, code - 127)
         assert (D[:, 0::4] == 1.5 * s).all() and (D[:, 1::4] == s / 64).all() and (D[:, 2::4] == 0).all(), code
+
+
+@pytest.mark.parametrize("case", [(1000, 32, 3001), (4096, 64, 700), (264, 96, 5000), (8, 32, 20000)], ids=str)
+@pytest.mark.parametrize("out", OUT)
+def test_few_columns(case, out):
+    """N below a tile, its scales' rows of one to three bytes and the last one at the end of its storage."""
+    m, n, k = case
+    dy, q, sf = integer_case(61, m, n, k)
+    A, Q = torch.from_numpy(dy.astype(np.float32)).to(DEV).bfloat16(), torch.from_numpy(q).to(DEV)
+    S = torch.from_numpy(sf).to(DEV)
+    want = dy.astype(np.float64).T @ ref.dequant(q, sf)
+    assert np.abs(want).max() < 2 ** 23                 # halves below 2^23 are fp32 numbers
+    D = tg.gemm_wgrad_mxfp8(A, Q, S, out_dtype=OUT[out])
+    assert np.array_equal(f64(D), want if out == "f32" else ref.round_to(want, "bf16"))

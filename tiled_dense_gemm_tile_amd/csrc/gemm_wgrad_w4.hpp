@@ -19,8 +19,6 @@
 // workspace for a second kernel to add in order.
 #pragma once
 
-#include <type_traits>
-
 #include "common.hpp"
 #include "gemm_f16_w4.hpp"
 #include "gemm_wgrad.hpp"
@@ -157,30 +155,40 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
     };
 
     // ---- B: thread t holds row t / 4 of a K tile, columns 16 (t % 4) + 64 j
-    // .. + 15, and the T scales of the row's columns (of its last T blocks
-    // where N ends inside the tile: s_shift bits too far left; rows past K
-    // take the last row's, with codes 0)
+    // .. + 15, and their scales: T = 8: the tile's eight in one load (the row's
+    // last eight where N ends inside the tile: s_shift bits too far left); T =
+    // 4: its own two, of blocks inside the row.  (Rows past K take the last
+    // row's, with codes 0.)
     const int br = tid >> 2, bt = tid & 3;
     const uint32_t b_off = (uint32_t)(br * p.ldb) + bt * 16;
-    const int nb = N / 32, s_at = n0 / 32 < nb - T ? n0 / 32 : nb - T, s_shift = 8 * (n0 / 32 - s_at);
+    const int nb = N / 32, s_at = T == 4 ? 0 : n0 / 32 < nb - 8 ? n0 / 32 : nb - 8, s_shift = 8 * (n0 / 32 - s_at);
+    const int s_b0 = n0 / 32 + (bt >> 1), s_b[2] = {s_b0 < nb ? s_b0 : nb - 1, s_b0 + 2 < nb ? s_b0 + 2 : nb - 1};
     pb.base = (const char *)p.B + (int64_t)k_lo * p.ldb + n0;
     pb.rows = K;
     const uint32_t b_row = (uint32_t)(N - n0), b_ld = (uint32_t)p.ldb;
     pb.set_span(b_ld, b_row, 0u);
     const int64_t b_step = (int64_t)KT * p.ldb;
-    typedef std::conditional_t<T == 8, uint64_t, uint32_t> Scales;
     struct __attribute__((packed, aligned(1))) PackedScales {
-        Scales v;
+        uint64_t v;
     };
     u32x4 vb[NV];
-    Scales vs;
+    uint64_t vs;                                       // T == 8
+    uint32_t vs2[2];                                   // T == 4
+    constexpr int NS = T == 8 ? 1 : 2;                 // loads of scales
     auto load_b = [&](__amdgpu_buffer_rsrc_t r, int j) __attribute__((always_inline)) {
         vb[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b_off + 64 * j, 0, 0));
     };
     const uint8_t *s_row = p.SF + (int64_t)k_lo * p.ldsf + s_at + (int64_t)(br < K ? br : K - 1) * p.ldsf;
     const int64_t s_step = (int64_t)KT * p.ldsf;
     int s_left = K - 1 - br;                           // rows from s_row's to the last
-    auto load_s = [&]() __attribute__((always_inline)) { vs = ((const PackedScales *)s_row)->v; };
+    auto load_s = [&]() __attribute__((always_inline)) {
+        if constexpr (T == 8) {
+            vs = ((const PackedScales *)s_row)->v;
+        } else {
+            vs2[0] = s_row[s_b[0]];
+            vs2[1] = s_row[s_b[1]];
+        }
+    };
     auto next_s = [&]() __attribute__((always_inline)) {
         // (the row 64 further; past K: the last)
         s_left -= KT;
@@ -196,9 +204,13 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
         b_put[o] = lds0 + B_BASE + br * ROWB + ((bt ^ (br & 3)) + 4 * (o ^ ((br >> 3) & 1))) * 32;
     uint32_t sc[NV / 2];                               // scales of vectors 2 i and 2 i + 1 in bytes 0 and 2
     auto take_scales = [&]() __attribute__((always_inline)) {
-        const Scales s = (Scales)(vs >> s_shift) >> (8 * (bt >> 1));
-        sc[0] = (uint32_t)s;
-        if constexpr (T == 8) sc[1] = (uint32_t)(s >> 32);
+        if constexpr (T == 8) {
+            const uint64_t s = (vs >> s_shift) >> (8 * (bt >> 1));
+            sc[0] = (uint32_t)s;
+            sc[1] = (uint32_t)(s >> 32);
+        } else {
+            sc[0] = vs2[0] | vs2[1] << 16;
+        }
     };
     u32x4 half;
     auto convert = [&](auto step, auto slot) __attribute__((always_inline)) {
@@ -322,7 +334,7 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
     take_scales();
     static_for<0, 2 * T>([&](auto s) __attribute__((always_inline)) { convert(s, even); });
     start_b();
-    wait_vmcnt<NV + 1>();                          // A(0) landed
+    wait_vmcnt<NV + NS>();                         // A(0) landed
     wait_lgkmcnt0();
     barrier();
     tile(std::true_type(), even);

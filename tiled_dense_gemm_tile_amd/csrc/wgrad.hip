@@ -24,7 +24,7 @@ constexpr int64_t kCus = 256;
 WgradPlan plan_wgrad(int64_t M, int64_t N, int64_t K, bool rows16, bool workspace) {
     WgradPlan g = {};
     const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256), t128 = ((M + 127) / 128) * ((N + 127) / 128);
-    if (rows16 && N >= 128 && K > 0) {
+    if (rows16 && K > 0) {
         auto cut = [&](int T) {                        // T x T blocks a wave: the plan
             const int64_t tiles = T == 8 ? t256 : t128, round = T == 8 ? kCus : 2 * kCus, rest = tiles % round;
             int64_t s = rest ? round / rest : 1;
