@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
     constexpr int LDS_BYTES = RING_BYTES > EPI_BYTES ? RING_BYTES : EPI_BYTES;
     static_assert(LDS_BYTES * (T == 8 ? 1 : 2) <= 160 * 1024, "LDS");
     __shared__ __attribute__((aligned(1024))) char smem[LDS_BYTES];
+    __shared__ __attribute__((aligned(1024))) char unread[4096];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -232,6 +233,24 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
         }
     };
 
+    // ---- C's tile, which the epilogue reads: brought near the CU while the
+    // matrix units are busy, a KiB a wave and K tile, into LDS that nothing
+    // reads (aligned 16-byte blocks, down from its elements; past the tile, or
+    // without C: no access)
+    constexpr int OS = OUT_BF16 ? 2 : 4, CL = BN * OS / 16;   // blocks of a tile row
+    const bool has_c = p.C && split < 0;
+    const uintptr_t c_at = has_c ? (uintptr_t)p.C + ((int64_t)m0 * p.ldc + n0) * OS : 0;
+    const uint32_t c_lead = (uint32_t)(c_at & 15);
+    const __amdgpu_buffer_rsrc_t rc =
+        make_rsrc((const void *)(c_at - c_lead),
+                  has_c ? c_lead + span_bytes(M - m0 < BM ? M - m0 : BM, N - n0 < BN ? N - n0 : BN, p.ldc, OS) : 0u);
+    uint32_t c_off = (uint32_t)((wave * 64 + lane) / CL * p.ldc * OS) + (lane % CL) * 16;
+    const uint32_t c_step = (uint32_t)(256 / CL * p.ldc * OS);
+    auto touch_c = [&]() __attribute__((always_inline)) {
+        dma_load<16>(rc, unread + wave * 1024, (c_lead + c_off) & ~15u);
+        c_off = c_off + c_step < 0x7fffffffu ? c_off + c_step : 0x7fffffffu;
+    };
+
     // ---- fragments: transposing reads (gemm_f16_w4t_kernel, MN-contiguous)
     const int fr = lane & 15, fq = lane >> 4;
     auto mn_base = [&](int wb, int b) __attribute__((always_inline)) {
@@ -308,7 +327,8 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
                 if constexpr (q / ce % 4 == 3) load_b(rb, q / ce / 4);
             }
         });
-        wait_vmcnt<NV>();                              // A(t + 1) landed; B(t + 2) may still run
+        touch_c();
+        wait_vmcnt<NV + 1>();                          // A(t + 1) landed; B(t + 2) and the touch of C may still run
         wait_lgkmcnt0();
         barrier();
     };
