@@ -123,8 +123,10 @@ size_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t N);
  *   in bytes.
  *   workspace: device memory, 256-byte aligned, or NULL.  With at least
  *     gemm_wgrad_mxfp8_workspace_bytes(M, N, K) bytes, grids too small to fill
- *     the GPU cut K into ranges and sum the fp32 partial products in order; a
- *     smaller one or NULL runs uncut (the same result up to summation order).
+ *     the GPU cut K into ranges and sum the fp32 partial products in order, and
+ *     A whose rows do not start on 16 bytes is copied first where M is no
+ *     multiple of 8 and the product large; a smaller one or NULL runs without
+ *     (the same result up to summation order).
  *     Calls sharing it must be ordered.
  * Scale code 0xFF and e4m3 NaN give NaN in the column's outputs.  K == 0:
  * D = C (or 0).

@@ -232,3 +232,27 @@ def test_few_columns(case, out):
     assert np.abs(want).max() < 2 ** 23                 # halves below 2^23 are fp32 numbers
     D = tg.gemm_wgrad_mxfp8(A, Q, S, out_dtype=OUT[out])
     assert np.array_equal(f64(D), want if out == "f32" else ref.round_to(want, "bf16"))
+
+
+@pytest.mark.parametrize("case", [(1097, 1120, 1700), (4091, 512, 1001), (257, 4096, 2049)], ids=str)
+def test_rows_moved_to_16_bytes(case):
+    """M that packed rows do not keep on 16 bytes, sizes that copy A into the workspace; and without room for it."""
+    m, n, k = case
+    dy, q, sf = integer_case(62, m, n, k)
+    store = torch.full((k * m + 9,), float("nan"), dtype=torch.bfloat16, device=DEV)
+    a = store[1:1 + k * m].view(k, m)                   # NaN on both sides
+    a.copy_(torch.from_numpy(dy).to(DEV))
+    Q, S = torch.from_numpy(q).to(DEV), torch.from_numpy(sf).to(DEV)
+    c = torch.randint(-9, 10, (m, n), device=DEV).float()
+    want = torch.mm(a.double().t().contiguous(), torch.from_numpy(ref.dequant(q, sf)).to(DEV)) + c.double()
+    assert want.abs().max() < 2 ** 23
+    need = tg.gemm_wgrad_mxfp8_workspace_bytes(m, n, k)
+    assert need >= k * m * 2
+    ws = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device=DEV)
+    D = torch.full((m + 1, n + 3), 5.0, device=DEV)
+    tg.gemm_wgrad_mxfp8(a, Q, S, C=c, D=D[:m, :n], workspace=ws[:need])
+    assert torch.equal(D[:m, :n].double(), want) and (ws[need:] == 0x5A).all()
+    D[:m, :n] = 5
+    assert (D == 5).all()
+    for short in (need - 1, 0):
+        assert torch.equal(tg.gemm_wgrad_mxfp8(a, Q, S, C=c, workspace=ws[:short]).double(), want)

@@ -74,6 +74,16 @@ __device__ __forceinline__ void wgrad_put(f32x4 v, const void *C, int64_t ldc, v
     }
 }
 
+// A with its rows moved to 16-byte boundaries, for the four-wave kernel: a
+// workgroup copies 2048 columns of a row.
+__global__ void __launch_bounds__(256)
+    wgrad_align_kernel(const void *A, int64_t lda, void *out, int64_t ldo, int K, int M) {
+    const int c = (blockIdx.x * 256 + threadIdx.x) * 8;
+    if (c >= M) return;
+    for (int64_t k = blockIdx.y; k < K; k += gridDim.y)   // (out: whole vectors, ldo >= c + 8)
+        *(RowVec<1>::V *)((__bf16 *)out + k * ldo + c) = RowVec<1>::load((const __bf16 *)A + k * lda, c, M);
+}
+
 typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
 
 template <bool OUT_BF16>

@@ -214,8 +214,8 @@ def _product_out(shape, dev, C, D, out_dtype):
 
 
 def gemm_wgrad_mxfp8_workspace_bytes(M: int, N: int, K: int) -> int:
-    """Workspace bytes with which :func:`gemm_wgrad_mxfp8` may cut K (0: it
-    would not)."""
+    """Workspace bytes with which :func:`gemm_wgrad_mxfp8` may cut K or copy A
+    (0: it would not)."""
     return _load().gemm_wgrad_mxfp8_workspace_bytes(M, N, K)
 
 
@@ -226,7 +226,8 @@ def gemm_wgrad_mxfp8(dY, Q, SF, C=None, out_dtype=None, D=None, workspace=None):
     (default) or bfloat16, C of that type; C may be D (gradient
     accumulation).  ``workspace``: a device byte tensor, 256-byte aligned, of
     :func:`gemm_wgrad_mxfp8_workspace_bytes` bytes (allocated per call when
-    not given; a smaller one runs without cutting K)."""
+    not given; a smaller one runs without cutting K or moving dY's rows to 16
+    bytes)."""
     if dY.dtype != torch.bfloat16 or dY.dim() != 2:
         raise TypeError("dY must be a 2-D bfloat16 tensor")
     if Q.dim() != 2 or Q.shape[1] % 32:
