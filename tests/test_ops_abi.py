@@ -161,8 +161,11 @@ def test_wgrad_workspace_bytes():
     assert tg.gemm_wgrad_mxfp8_workspace_bytes(64, -32, 64) == 0
     assert tg.gemm_wgrad_mxfp8_workspace_bytes(64, 64, 64) == 0
     assert tg.gemm_wgrad_mxfp8_workspace_bytes(8192, 8192, 65536) == 0
-    b = tg.gemm_wgrad_mxfp8_workspace_bytes(100, 96, 65536)
-    assert b > 0 and b % (100 * 96 * 4) == 0
+    # the partial sums of one round of tiles, however long K is
+    assert 0 < tg.gemm_wgrad_mxfp8_workspace_bytes(104, 96, 65536) <= 512 * 128 * 128 * 4
+    assert 0 < tg.gemm_wgrad_mxfp8_workspace_bytes(100, 96, 1 << 30) <= 512 * 128 * 128 * 4
+    # rows off 16 bytes, a large product: a copy of A too
+    assert tg.gemm_wgrad_mxfp8_workspace_bytes(8191, 8192, 65536) == 65536 * 8192 * 2
 
 
 def gemv(M=2, N=64, K=64, kb=32, X=P, ldx=64, xt=BF16, W=P + (1 << 20), ldw=64, SF=P + (2 << 20), ldsf=2, C=None,
