@@ -82,14 +82,18 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
     constexpr int WTM = 16 * T, WTN = 16 * T, Q = TM * TN;
     constexpr int ROWB = BM * 2;                       // an LDS row: 32 T bf16
     constexpr int SLOT = KT * ROWB;
-    constexpr int LA = SLOT / 4096, NV = T / 2;        // loads per thread and K tile: of A, of B
-    constexpr int B_BASE = 2 * SLOT;
-    constexpr int RING_BYTES = 4 * SLOT;
+    // loads per thread and K tile: of A, of B, of B's scales, of C
+    constexpr int LA = SLOT / 4096, NV = T / 2, NS = T == 8 ? 1 : 2, NC = T == 8 ? 1 : 0;
+    // LDS slots of A and register sets of B: a K tile of T = 4 takes less time
+    // than a load, so A comes two tiles ahead and B three
+    constexpr int DA = T == 8 ? 2 : 3, DB = T == 8 ? 1 : 2, UNROLL = T == 8 ? 2 : 6;
+    constexpr int B_BASE = DA * SLOT;
+    constexpr int RING_BYTES = (DA + 2) * SLOT;
     constexpr int EPI_BYTES = 4 * 32 * (WTN + 8) * 4;
-    constexpr int LDS_BYTES = RING_BYTES > EPI_BYTES ? RING_BYTES : EPI_BYTES;
+    static_assert(RING_BYTES >= EPI_BYTES, "LDS");
+    constexpr int LDS_BYTES = RING_BYTES + NC * 4096;
     static_assert(LDS_BYTES * (T == 8 ? 1 : 2) <= 160 * 1024, "LDS");
     __shared__ __attribute__((aligned(1024))) char smem[LDS_BYTES];
-    __shared__ __attribute__((aligned(1024))) char unread[4096];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -172,22 +176,21 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
     struct __attribute__((packed, aligned(1))) PackedScales {
         uint64_t v;
     };
-    u32x4 vb[NV];
+    u32x4 vb[DB][NV];
     uint64_t vs;                                       // T == 8
-    uint32_t vs2[2];                                   // T == 4
-    constexpr int NS = T == 8 ? 1 : 2;                 // loads of scales
-    auto load_b = [&](__amdgpu_buffer_rsrc_t r, int j) __attribute__((always_inline)) {
-        vb[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b_off + 64 * j, 0, 0));
+    uint32_t vs2[DB][2];                               // T == 4
+    auto load_b = [&](__amdgpu_buffer_rsrc_t r, int set, int j) __attribute__((always_inline)) {
+        vb[set][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b_off + 64 * j, 0, 0));
     };
     const uint8_t *s_row = p.SF + (int64_t)k_lo * p.ldsf + s_at + (int64_t)(br < K ? br : K - 1) * p.ldsf;
     const int64_t s_step = (int64_t)KT * p.ldsf;
     int s_left = K - 1 - br;                           // rows from s_row's to the last
-    auto load_s = [&]() __attribute__((always_inline)) {
+    auto load_s = [&](int set) __attribute__((always_inline)) {
         if constexpr (T == 8) {
             vs = ((const PackedScales *)s_row)->v;
         } else {
-            vs2[0] = s_row[s_b[0]];
-            vs2[1] = s_row[s_b[1]];
+            vs2[set][0] = s_row[s_b[0]];
+            vs2[set][1] = s_row[s_b[1]];
         }
     };
     auto next_s = [&]() __attribute__((always_inline)) {
@@ -204,25 +207,25 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
     for (int o = 0; o < 2; ++o)
         b_put[o] = lds0 + B_BASE + br * ROWB + ((bt ^ (br & 3)) + 4 * (o ^ ((br >> 3) & 1))) * 32;
     uint32_t sc[NV / 2];                               // scales of vectors 2 i and 2 i + 1 in bytes 0 and 2
-    auto take_scales = [&]() __attribute__((always_inline)) {
+    auto take_scales = [&](int set) __attribute__((always_inline)) {
         if constexpr (T == 8) {
             const uint64_t s = (vs >> s_shift) >> (8 * (bt >> 1));
             sc[0] = (uint32_t)s;
             sc[1] = (uint32_t)(s >> 32);
         } else {
-            sc[0] = vs2[0] | vs2[1] << 16;
+            sc[0] = vs2[set][0] | vs2[set][1] << 16;
         }
     };
     u32x4 half;
-    auto convert = [&](auto step, auto slot) __attribute__((always_inline)) {
+    auto convert = [&](auto step, auto slot, int set) __attribute__((always_inline)) {
         constexpr int at = decltype(slot)::value * SLOT;
         constexpr int j = decltype(step)::value / 4, i = decltype(step)::value % 4;
         const float scale = __builtin_bit_cast(
             float, (j & 1) ? (sc[j / 2] & 0xff0000u) << 7 : (sc[j / 2] & 0xffu) << 23);
         half[2 * (i & 1)] =
-            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vb[j][i], scale, false));
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vb[set][j][i], scale, false));
         half[2 * (i & 1) + 1] =
-            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vb[j][i], scale, true));
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vb[set][j][i], scale, true));
         if constexpr (i & 1) {
             const uint32_t put = b_put[j & 1];
             const u32x4 v = half;
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
     uint32_t c_off = (uint32_t)((wave * 64 + lane) / CL * p.ldc * OS) + (lane % CL) * 16;
     const uint32_t c_step = (uint32_t)(256 / CL * p.ldc * OS);
     auto touch_c = [&]() __attribute__((always_inline)) {
-        dma_load<16>(rc, unread + wave * 1024, (c_lead + c_off) & ~15u);
+        dma_load<16>(rc, smem + RING_BYTES + wave * 1024, (c_lead + c_off) & ~15u);
         c_off = c_off + c_step < 0x7fffffffu ? c_off + c_step : 0x7fffffffu;
     };
 
@@ -270,14 +273,16 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
     };
     f32x4 acc[TM][TN];
     u32x4 fa[2][TM], fb[2][TN];                        // [K step][block]
-    auto read_frag = [&](auto slot, auto st_, int k) __attribute__((always_inline)) {
-        constexpr int st = decltype(st_)::value;
-        constexpr std::integral_constant<int, decltype(slot)::value * SLOT + st * 32 * ROWB> off{};
+    // of K tile I % UNROLL
+    auto read_frag = [&](auto index, auto st_, int k) __attribute__((always_inline)) {
+        constexpr int I = decltype(index)::value, st = decltype(st_)::value;
+        constexpr std::integral_constant<int, I % DA * SLOT + st * 32 * ROWB> a_at{};
+        constexpr std::integral_constant<int, I % 2 * SLOT + st * 32 * ROWB> b_at{};
         if (k == 0 || k > TN) {
             const int i = k == 0 ? 0 : k - TN;
-            fa[st][i] = ldfrag_tr(a_mn[i], off);
+            fa[st][i] = ldfrag_tr(a_mn[i], a_at);
         } else {
-            fb[st][k - 1] = ldfrag_tr(b_mn[k - 1], off);
+            fb[st][k - 1] = ldfrag_tr(b_mn[k - 1], b_at);
         }
     };
     auto mfma = [&](auto zero, int st, int i, int j) __attribute__((always_inline)) {
@@ -288,25 +293,23 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    // One K tile.  First half: step 1 of tile t - 1, with the reads of tile t
-    // step 0 and the loads of A(t + 1).  Second half: step 0 of tile t, with
-    // the reads of step 1, the conversion of B(t + 1) (a step of two
-    // instructions per four MFMAs, a write per eight) and, as its registers
-    // fall free, the loads of B(t + 2), which have until the next tile's
-    // second half to land.
-    // PAR: the K tile's slot.
-    auto tile = [&](auto first, auto par) __attribute__((always_inline)) {
-        constexpr int PAR = decltype(par)::value, RD = TM + TN;
-        constexpr std::integral_constant<int, PAR> cur{};
-        constexpr std::integral_constant<int, PAR ^ 1> nxt{};
+    // K tile t, I = t % UNROLL.  First half: step 1 of tile t - 1, with the
+    // reads of tile t step 0 and the loads of A(t + DA - 1).  Second half: step
+    // 0 of tile t, with the reads of step 1, the conversion of B(t + 1) (a step
+    // of two instructions per four or two MFMAs, a write per two steps) and, as
+    // its registers fall free, the loads of B(t + 1 + DB), which have until
+    // DB tiles later's second half to land.
+    auto tile = [&](auto first, auto index) __attribute__((always_inline)) {
+        constexpr int I = decltype(index)::value, SET = (I + 1) % DB, RD = TM + TN;
+        constexpr std::integral_constant<int, (I + 1) % 2> b_nxt{};
         constexpr std::integral_constant<int, 0> st0{};
         constexpr std::integral_constant<int, 1> st1{};
         const __amdgpu_buffer_rsrc_t ra = pa.rsrc();
         static_for<0, Q>([&](auto qc) __attribute__((always_inline)) {
             constexpr int q = decltype(qc)::value;
             if constexpr (!decltype(first)::value) mfma(std::false_type(), 1, q / TN, q % TN);
-            if constexpr (q * RD % Q == 0 && q * RD / Q < RD) read_frag(cur, st0, q * RD / Q);
-            if constexpr (q % (Q / LA) == (T == 8 ? 2 : 1)) dma_a(ra, PAR ^ 1, q / (Q / LA));
+            if constexpr (q * RD % Q == 0 && q * RD / Q < RD) read_frag(index, st0, q * RD / Q);
+            if constexpr (q % (Q / LA) == (T == 8 ? 2 : 1)) dma_a(ra, (I + DA - 1) % DA, q / (Q / LA));
             if constexpr (q == (T == 8 ? 5 : 3) && !decltype(first)::value) pb.move(b_step);
             if constexpr (q == (T == 8 ? 7 : 6) && !decltype(first)::value) pb.set_span(b_ld, b_row, 0u);
             if constexpr (q == Q - 3) pa.move(a_step);
@@ -318,52 +321,60 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
             if constexpr (q % TN == 0) __builtin_amdgcn_s_waitcnt(0xC07F | (wgrad_row_wait(T, q / TN) << 8));
             mfma(first, 0, q / TN, q % TN);
             constexpr int re = wgrad_read_every(T), ce = wgrad_convert_every(T);
-            if constexpr (q % re == 0 && q / re < TM + TN) read_frag(cur, st1, q / re);
-            if constexpr (q == (T == 8 ? 1 : 0)) take_scales();
-            if constexpr (q == (T == 8 ? 5 : 2)) load_s();
+            if constexpr (q % re == 0 && q / re < TM + TN) read_frag(index, st1, q / re);
+            if constexpr (q == (T == 8 ? 1 : 0)) take_scales(SET);
+            if constexpr (q == (T == 8 ? 5 : 2)) load_s(SET);
             if constexpr (q == (T == 8 ? 9 : 4)) next_s();
             if constexpr (q % ce == ce / 2) {
-                convert(std::integral_constant<int, q / ce>(), nxt);
-                if constexpr (q / ce % 4 == 3) load_b(rb, q / ce / 4);
+                convert(std::integral_constant<int, q / ce>(), b_nxt, SET);
+                if constexpr (q / ce % 4 == 3) load_b(rb, SET, q / ce / 4);
             }
         });
-        touch_c();
-        wait_vmcnt<NV + 1>();                          // A(t + 1) landed; B(t + 2) and the touch of C may still run
+        if constexpr (NC) touch_c();
+        wait_vmcnt<(DA - 1) * (NV + NS + NC) + (DA - 2) * LA>();   // A(t + 1) landed; what came after it may still run
         wait_lgkmcnt0();
         barrier();
     };
 
     // (every K range holds a row)
-    constexpr std::integral_constant<int, 0> even{};
-    constexpr std::integral_constant<int, 1> odd{};
-    auto start_b = [&]() __attribute__((always_inline)) {
+    auto start_b = [&](int set) __attribute__((always_inline)) {
         const __amdgpu_buffer_rsrc_t r = pb.rsrc();
 #pragma unroll
-        for (int j = 0; j < NV; ++j) load_b(r, j);
-        load_s();
+        for (int j = 0; j < NV; ++j) load_b(r, set, j);
+        load_s(set);
         next_s();
         pb.move(b_step);
         pb.set_span(b_ld, b_row, 0u);
     };
-    const __amdgpu_buffer_rsrc_t ra = pa.rsrc();
+    auto start_a = [&](int slot) __attribute__((always_inline)) {
+        const __amdgpu_buffer_rsrc_t r = pa.rsrc();
 #pragma unroll
-    for (int j = 0; j < LA; ++j) dma_a(ra, 0, j);
-    pa.move(a_step);
-    pa.set_span(a_ld, a_row, 15u);
-    start_b();
-    take_scales();
-    static_for<0, 2 * T>([&](auto s) __attribute__((always_inline)) { convert(s, even); });
-    start_b();
-    wait_vmcnt<NV + NS>();                         // A(0) landed
+        for (int j = 0; j < LA; ++j) dma_a(r, slot, j);
+        pa.move(a_step);
+        pa.set_span(a_ld, a_row, 15u);
+    };
+    start_a(0);
+    start_b(0);
+    if constexpr (DA == 3) start_a(1);
+    if constexpr (DB == 2) start_b(1);
+    take_scales(0);
+    static_for<0, 2 * T>([&](auto s) __attribute__((always_inline)) {
+        convert(s, std::integral_constant<int, 0>(), 0);
+    });
+    start_b(0);
+    wait_vmcnt<(DA - 2) * LA + DB * (NV + NS)>();      // A(0) landed
     wait_lgkmcnt0();
     barrier();
-    tile(std::true_type(), even);
+    tile(std::true_type(), std::integral_constant<int, 0>());
     int t = 1;
-    for (; t + 1 < nt; t += 2) {
-        tile(std::false_type(), odd);
-        tile(std::false_type(), even);
-    }
-    if (t < nt) tile(std::false_type(), odd);
+    for (; t + UNROLL <= nt; t += UNROLL)
+        static_for<0, UNROLL>([&](auto i) __attribute__((always_inline)) {
+            tile(std::false_type(), std::integral_constant<int, (decltype(i)::value + 1) % UNROLL>());
+        });
+    static_for<0, UNROLL - 1>([&](auto i) __attribute__((always_inline)) {
+        if (t + decltype(i)::value < nt)
+            tile(std::false_type(), std::integral_constant<int, decltype(i)::value + 1>());
+    });
 #pragma unroll
     for (int q = 0; q < Q; ++q) mfma(std::false_type(), 1, q / TN, q % TN);
     // (the wait states of mfma_result_fence, for either tile)

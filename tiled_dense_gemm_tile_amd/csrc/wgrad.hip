@@ -5,6 +5,8 @@
 #include "gemm_wgrad.hpp"
 #include "gemm_wgrad_w4.hpp"
 
+#include <math.h>
+
 using namespace tg_api;
 
 namespace {
@@ -28,10 +30,18 @@ WgradPlan plan_wgrad(int64_t M, int64_t N, int64_t K, bool rows16, bool workspac
         auto cut = [&](int T) {                        // T x T blocks a wave: the plan
             const int64_t tiles = T == 8 ? t256 : t128, round = T == 8 ? kCus : 2 * kCus, rest = tiles % round;
             int64_t s = rest ? round / rest : 1;
-            // (ranges of 1024 on: at 1024 x 1024 x 1024 12.0 us uncut, 16.6
-            // in two; of 512 for a tile or two: 128 x 128 x 4096 11.0 against 13.9)
-            const int64_t least = tiles < 4 ? 512 : 1024;
+            // Ranges of 1024 on; of 256 on with 128 x 128 tiles, of which
+            // one's K tile takes about as long as the writing and reading of
+            // a tenth of a partial sum: the least of K tiles / s and 10 s rest
+            // tiles (1024 x 1024 x 1024 14.3 us uncut, 16.4 in two, 20.8 in four;
+            // 512 x 512 x 8192 21.0 in eight, 23.3 in sixteen; 16 x 1920 x
+            // 1382 16.8, 11.9 in two, 9.9 in five).
+            const int64_t least = T == 8 ? 1024 : 256;
             if (K / least < s) s = K / least;
+            if (T == 4 && rest) {
+                const int64_t best = (int64_t)(sqrt(10.0 * (double)((K + 63) / 64) / (double)rest) + 0.3);
+                if (best < s) s = best;
+            }
             g.T = T;
             g.full = tiles;
             g.splits = 1;
