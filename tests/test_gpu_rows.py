@@ -337,3 +337,29 @@ def test_norm_of_infinite_rows():
     y, _, rstd = tg.rmsnorm(x, torch.ones(256, device=DEV), EPS)
     assert rstd[0] == 0 and rstd[1] == 0 and (y[1] == 0).all()
     assert torch.isnan(y[0, 9]) and (y[0, :9] == 0).all() and (y[0, 10:] == 0).all()
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("base", [0, 504, 2040, 4096, 8192])
+def test_every_row_end(kind, base):
+    """Rows that end at every element of a vector, forward and backward, in surroundings that stay as they are."""
+    w = rows_of(50, 1, base + 9, "f32")[0].contiguous()
+    for n in range(base + 1, base + 9):
+        x, r, dy = (rows_of(s, 5, n, kind, 3, 1) for s in (51, 52, 53))
+        big = torch.full((7, n + 5), 7.0, dtype=TYPES[kind], device=DEV)
+        y, h, rstd = tg.rmsnorm(x, w[:n], EPS, residual=r, Y=big[1:6, 2:n + 2])
+        want, rs = ref.norm(f64(h), f64(w[:n]), EPS)
+        s = f64(x) + f64(r)
+        assert (np.abs(f64(h) - s) <= (ref.HALF[kind] + (ref.U if kind != "f32" else 0)) * np.abs(s) + ref.TINY[kind]).all()
+        assert (np.abs(f64(rstd) - rs) <= ref.rstd_bound(n) * rs).all()
+        bound = (ref.rstd_bound(n) + 2 * ref.U) * np.abs(want) + 2.0 ** -148
+        assert (np.abs(f64(y) - want) <= bound + ref.HALF[kind] * (np.abs(want) + bound) + ref.TINY[kind]).all()
+        big[1:6, 2:n + 2] = 7
+        assert (big == 7).all()
+        dx, dw = tg.rmsnorm_backward(dy, h, w[:n], rstd, dH=x, dX=big[1:6, 2:n + 2])
+        want, wdw, ag, au, adw = ref.norm_backward(f64(dy), f64(h), f64(w[:n]), f64(rstd), f64(x))
+        bound = 4 * ref.U * ag + (n / 64 + 32 + 9) * ref.U * au + 2 * ref.U * np.abs(want)
+        assert (np.abs(f64(dx) - want) <= bound + ref.HALF[kind] * (np.abs(want) + bound) + ref.TINY[kind]).all()
+        assert (np.abs(f64(dw) - wdw) <= (1 + 1 + 64 + 2) * ref.U * adw).all()
+        big[1:6, 2:n + 2] = 7
+        assert (big == 7).all()

@@ -48,19 +48,24 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_kernel(NormArgs
     for (int i = 0; i < VPT; ++i) {
         const int c = (i * TPR + t) * VE;
         h[i] = typename RV::V{};
-        if (in && c < N) h[i] = RV::load(x, c, N);
+        if (in && c < N) h[i] = RV::load_raw(x, c, N);
     }
     if (p.R) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (i * TPR + t) * VE;
             if (in && c < N) {
-                const typename RV::V v = RV::load(r, c, N);
+                const typename RV::V v = RV::load_raw(r, c, N);
 #pragma unroll
                 for (int u = 0; u < VE; ++u)
                     h[i][u] = Elem<T>::down(Elem<T>::up(h[i][u]) + Elem<T>::up(v[u]));
             }
         }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = (i * TPR + t) * VE;
+        if (c < N) h[i] = RV::settle(h[i], c, N);
     }
     float ss = 0.0f;
 #pragma unroll
@@ -217,7 +222,7 @@ hipError_t launch_norm(NormArgs &p, hipStream_t s) {
     if (nvec <= 256) return go<T, MX, 256, 1>(p, s);
     if (nvec <= 512) return go<T, MX, 256, 2>(p, s);
     if (nvec <= 1024) return go<T, MX, 256, 4>(p, s);
-    if (nvec <= 2048) return go<T, MX, 256, 8>(p, s);
+    if (nvec <= 2048) return go<T, MX, 512, 4>(p, s);
     if (nvec <= 4096) return go<T, MX, 1024, 4>(p, s);
     hipLaunchKernelGGL((rmsnorm_long_kernel<T, MX>), dim3((unsigned)(p.rows < 2048 ? p.rows : 2048)), dim3(1024),
                        0, s, p);

@@ -42,9 +42,15 @@ __global__ void __launch_bounds__(NT) rmsnorm_bwd_kernel(NormBwdArgs p) {
         for (int u = 0; u < VE; ++u) w[i][u] = dw[i][u] = 0.0f;
         if (c < N) load_weights<T>(p.W, p.w_f32, c, N, w[i]);
     }
+    constexpr bool AHEAD = VPT <= 2;                   // (two rows of four vectors do not fit the registers)
     struct Row {
         typename RV::V dy[VPT], h[VPT], a[VPT];
         float rstd;
+    };
+    // (loaded ahead: settled when used; at once, but element by element, where
+    // the registers are short)
+    auto get = [&](const typename RV::S *row, int c) __attribute__((always_inline)) {
+        return AHEAD ? RV::load_raw(row, c, N) : RV::load_each(row, c, N);
     };
     auto load = [&](int64_t row, Row &r) __attribute__((always_inline)) {
         r.rstd = 0.0f;
@@ -54,13 +60,12 @@ __global__ void __launch_bounds__(NT) rmsnorm_bwd_kernel(NormBwdArgs p) {
             const int c = (i * TPR + t) * VE;
             r.dy[i] = r.h[i] = r.a[i] = typename RV::V{};
             if (row < p.rows && c < N) {
-                r.dy[i] = RV::load((const typename RV::S *)p.dY + row * p.lddy, c, N);
-                r.h[i] = RV::load((const typename RV::S *)p.H + row * p.ldh, c, N);
-                if (p.dH) r.a[i] = RV::load((const typename RV::S *)p.dH + row * p.lddh, c, N);
+                r.dy[i] = get((const typename RV::S *)p.dY + row * p.lddy, c);
+                r.h[i] = get((const typename RV::S *)p.H + row * p.ldh, c);
+                if (p.dH) r.a[i] = get((const typename RV::S *)p.dH + row * p.lddh, c);
             }
         }
     };
-    constexpr bool AHEAD = VPT <= 2;                   // (two rows of four vectors do not fit the registers)
     Row cur, next;
     if constexpr (AHEAD) load((int64_t)blockIdx.x * RPB + sub, cur);
     int slot = 0;
@@ -73,6 +78,12 @@ __global__ void __launch_bounds__(NT) rmsnorm_bwd_kernel(NormBwdArgs p) {
         float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
+            const int c = (i * TPR + t) * VE;
+            if (AHEAD && c < N && c + VE > N) {        // the row's last vector
+                cur.dy[i] = RV::settle(cur.dy[i], c, N);
+                cur.h[i] = RV::settle(cur.h[i], c, N);
+                cur.a[i] = RV::settle(cur.a[i], c, N);
+            }
 #pragma unroll
             for (int u = 0; u < VE; ++u) {
                 const float d = Elem<T>::up(cur.dy[i][u]), f = Elem<T>::up(cur.h[i][u]) * cur.rstd;
@@ -100,7 +111,11 @@ __global__ void __launch_bounds__(NT) rmsnorm_bwd_kernel(NormBwdArgs p) {
                         const float g = Elem<T>::up(cur.dy[i][u]) * w[i][u], f = Elem<T>::up(cur.h[i][u]) * cur.rstd;
                         o[u] = Elem<T>::down(fmaf(cur.rstd, g - f * m, Elem<T>::up(cur.a[i][u])));
                     }
-                    RV::store((typename RV::S *)p.dX + row * p.lddx, c, N, o);
+                    typename RV::S *dx = (typename RV::S *)p.dX + row * p.lddx;
+                    if constexpr (AHEAD)
+                        RV::store(dx, c, N, o);
+                    else
+                        RV::store_each(dx, c, N, o);
                 }
             }
         }

@@ -41,8 +41,9 @@ struct RowVec {
     struct __attribute__((packed, aligned(sizeof(S)))) U {
         V v;
     };
-    // elements [c, c + VE) of a row of n; past the end: zeros
-    static __device__ __forceinline__ V load(const void *row, int c, int n) {
+    // As load below, the row's last vector element by element: the fewest
+    // registers.
+    static __device__ __forceinline__ V load_each(const void *row, int c, int n) {
         const S *p = (const S *)row + c;
         if (c + VE <= n) return ((const U *)p)->v;
         V v = {};
@@ -50,7 +51,33 @@ struct RowVec {
             if (c + i < n) v[i] = p[i];
         return v;
     }
-    static __device__ __forceinline__ void store(void *row, int c, int n, V v) {
+    // Elements [c, c + VE) of a row of n, 0 <= c; past the end: zeros.  The row's
+    // last vector is loaded from the row's end and moved down in registers, in
+    // two parts: load_raw has no branch and no wait (but in rows shorter than a
+    // vector), so that several can be in flight, and settle moves.
+    static __device__ __forceinline__ V load_raw(const void *row, int c, int n) {
+        if (n < VE) return load_each(row, c, n);
+        return ((const U *)((const S *)row + (c + VE <= n ? c : n - VE)))->v;
+    }
+    static __device__ __forceinline__ V settle(V v, int c, int n) {
+        const int past = c + VE - n;
+        if (past <= 0 || n < VE) return v;
+        return down(v, past);
+    }
+    static __device__ __forceinline__ V load(const void *row, int c, int n) {
+        return settle(load_raw(row, c, n), c, n);
+    }
+    // element i + by in the place of element i, zeros on top
+    static __device__ __forceinline__ V down(V v, int by) {
+        typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+        const u64x2 u = __builtin_bit_cast(u64x2, v);
+        const uint32_t bits = 8 * sizeof(S) * (uint32_t)by;    // >= 16
+        u64x2 o;
+        o[0] = bits < 64 ? (u[0] >> bits) | (u[1] << (64 - bits)) : bits < 128 ? u[1] >> (bits - 64) : 0;
+        o[1] = bits < 64 ? u[1] >> bits : 0;
+        return __builtin_bit_cast(V, o);
+    }
+    static __device__ __forceinline__ void store_each(void *row, int c, int n, V v) {
         S *p = (S *)row + c;
         if (c + VE <= n) {
             ((U *)p)->v = v;
@@ -58,6 +85,27 @@ struct RowVec {
         }
         for (int i = 0; i < VE; ++i)
             if (c + i < n) p[i] = v[i];
+    }
+    // (the row's end in at most three stores)
+    static __device__ __forceinline__ void store(void *row, int c, int n, V v) {
+        S *p = (S *)row + c;
+        if (c + VE <= n) {
+            ((U *)p)->v = v;
+            return;
+        }
+        int left = n - c;
+#pragma unroll
+        for (int h = VE / 2; h > 0; h /= 2) {
+            if (left < h) continue;
+            struct __attribute__((packed, aligned(sizeof(S)))) Part {
+                S s[VE];
+            };
+#pragma unroll
+            for (int i = 0; i < h; ++i) ((Part *)p)->s[i] = v[i];
+            p += h;
+            left -= h;
+            v = down(v, h);
+        }
     }
 };
 
