@@ -8,7 +8,10 @@
 // transposing LDS read.  B's codes become bf16 on the way into LDS, where 16
 // consecutive columns of a row share one scale (a fragment's eight values
 // have eight scales); e4m3 * 2^e is exact in bf16.  Rows may start at any
-// element: loads are 16-byte vectors of element alignment.
+// element: loads are 16-byte vectors of element alignment.  Bound by the wait
+// for each K tile's loads, one tile ahead (4090 x 4096 x 4100 315 us, 436
+// TFLOP/s): large calls whose rows start off 16 bytes copy A and run the
+// four-wave kernel.
 #pragma once
 
 #include "common.hpp"

@@ -1,15 +1,18 @@
-// C ABI and kernel of gemv_mxfp4 (include/tilegemm_ops.h): a few 16-bit rows
+// C ABI and kernels of gemv_mxfp4 (include/tilegemm_ops.h): a few 16-bit rows
 // times 4-bit weights with group scales.
 //
 // Bound by the reading of W (half a byte per weight; 2 M flops per weight).
-// A workgroup takes 16 weight rows and its waves share K, so that a matrix
-// of a few thousand rows still spreads over the whole GPU; each wave runs
-// 16x16x32 MFMAs with X as the row operand (its M rows padded to 16) and the
-// weights, converted to 16 bits with their scale by one instruction per two,
-// as the column operand.  A lane's 16 bytes of a weight row are one whole
-// 32-element block with one scale: K is permuted inside a step of 128 so
-// that lane group g holds block g, and X is read with the same permutation.
-// The waves' sums are joined through LDS in wave order.
+// The products run on 16x16x32 MFMAs with X as the row operand (its M rows
+// padded to 16) and 16 weight rows, converted to 16 bits with their scale by
+// one instruction per two, as the column operand; every product is exact
+// (weights beyond fp16's range go to bf16, and fp16 X in two bf16 parts), the
+// sums fp32.  Waves that share a block of weight rows along K join their sums
+// through LDS in wave order; K ranges of several workgroups go through a
+// workspace and are added in range order.
+//
+// One row of 131072 x 4096 47.8 us (5.6 TB/s of W), of 14336 x 4096 8.5 us, of
+// which an empty launch is 2.7; four rows of 131072 x 8192 100 us (5.7 TB/s);
+// 16 rows of 4096 x 14336 12.3 us and 2 for the ranges' sums.
 #include "api.hpp"
 #include "pipeline.hpp"
 #include "rows.hpp"
@@ -436,7 +439,11 @@ __global__ void __launch_bounds__(kGemvWaves * 64, R == 3 ? 4 : 2) gemv_mxfp4_st
     wait_vmcnt<0>();                                   // (requests past the last group: nothing in flight into LDS at the end)
 }
 
-// Weight rows that start at any byte.
+// Weight rows that start at any byte, K below a step, and calls without room
+// for their ranges' sums.  A workgroup takes 16 weight rows and its waves share
+// K; a lane's 16 bytes of a weight row are one whole 32-element block with one
+// scale: K is permuted inside a step of 128 so that lane group g holds block
+// g, and X is read with the same permutation.
 template <bool FP16, int MB>
 __global__ void __launch_bounds__(kGemvWaves * 64) gemv_mxfp4_kernel(GemvArgs p) {
     __shared__ float red[kGemvWaves][MB * 4][64];

@@ -6,7 +6,9 @@
 // per thread, so a row needs one reduction (mean(g * u)) and a thread's share
 // of dw stays in registers over all its rows.  Each workgroup's dw goes to
 // the workspace and a second kernel adds those partial sums in order: no
-// atomics, the same bits on every call.  Bound by the HBM rate.
+// atomics, the same bits on every call.  Bound by the HBM rate: 16384 x 4096
+// bf16 with dh 102 us, 5.3 TB/s (97 and 5 for the two kernels); 1001 x 4100
+// fp32 14 us.
 #include "rows.hpp"
 #include "rows_api.hpp"
 
