@@ -151,9 +151,10 @@ size_t gemm_wgrad_mxfp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   ldx, ldw >= K; ldsfw >= ceil(K / kblock); C NULL: 0; C == D with
  *   ldc == ldd accumulates in place.
  *   workspace: device memory, 256-byte aligned, or NULL.  With at least
- *     gemv_mxfp4_workspace_bytes(M, N, K) bytes, calls whose X exceeds the
- *     LDS of a compute unit, and those of few rows of W, cut K into ranges
- *     and sum the fp32 partial sums in order; a smaller one or NULL runs
+ *     gemv_mxfp4_workspace_bytes(M, N, K) bytes (at most 64 MiB or 32 rows'
+ *     partial sums), calls whose X exceeds the LDS of a compute unit, and
+ *     those of few rows of W, cut K into ranges and sum the fp32 partial
+ *     sums in order; a smaller one or NULL runs
  *     uncut, slower (the same result up to summation order).  Calls sharing it
  *     must be ordered.
  * Leading dimensions below 8 MiB in bytes.  Weights beyond bf16's range (4 and

@@ -328,6 +328,8 @@ def test_norm_over_its_input_returns_no_h():
     a = x.clone()
     y, h, s = tg.rmsnorm(a, w, EPS, Y=a)
     assert h is None and torch.equal(y, y0) and torch.equal(s, s0) and y.data_ptr() == a.data_ptr()
+    e = torch.zeros(0, 96, dtype=torch.bfloat16, device=DEV)
+    assert tg.rmsnorm(e, w, EPS)[1] is e
 
 
 def test_norm_of_infinite_rows():

@@ -508,13 +508,9 @@ __global__ void __launch_bounds__(kGemvWaves * 64) gemv_mxfp4_kernel(GemvArgs p)
 struct GemvPlan {
     bool staged;
     int mb, ring, splits, k_split, kwlog;
+    int64_t busiest;                                   // steps of the busiest wave
 };
 
-// How a call runs.  K ranges of the staged kernel: multiples of 256 (2048
-// where LDS holds that much of M rows, so that all eight waves have a step of
-// every block), as many as X needs; more where the blocks of rows leave half
-// of the CUs idle, down to ranges of 2048.
-//
 // Rows of X a pass of a call in several K ranges takes: its partial sums stay
 // within 64 MiB (or 32 rows').
 inline int64_t gemv_pass(int64_t M, int64_t N, int splits) {
@@ -524,11 +520,45 @@ inline int64_t gemv_pass(int64_t M, int64_t N, int splits) {
     return M < rows ? M : rows;
 }
 
-inline GemvPlan plan_gemv(int64_t M, int64_t N, int64_t K, bool aligned, bool workspace) {
+// The staged kernel with K ranges of ks.  Waves per block: what gives the
+// busiest wave the fewest steps; among those, from ranges of 4096 on, the most
+// waves that have four steps of a block each (together they read longer runs
+// of its rows: 131072 x 8192 for four rows 100 us with eight waves, 113 with
+// one), else the fewest (one wave needs no join and no barrier: 4096 x 14336
+// for 16 rows, ranges of 2048, 13.2 us against 14.9 with two and 16.3 with
+// eight).
+inline GemvPlan plan_ranges(int64_t M, int64_t N, int64_t K, int64_t ks) {
     GemvPlan g;
+    g.staged = true;
     g.mb = M > 16 ? 2 : 1;
-    const int64_t rows = M < 16 * g.mb ? M : 16 * g.mb;
-    int64_t most = (x_bytes(g.mb, g.mb == 1 ? 4 : 2) / rows - 16) / 2 / 512 * 512;
+    g.k_split = (int)ks;
+    g.splits = K > 0 ? (int)((K + ks - 1) / ks) : 1;
+    const int64_t rows = M < 16 * g.mb ? M : 16 * g.mb, range = ks < K ? ks : K, steps = (range + 255) / 256;
+    g.ring = g.mb == 2 ? 2 : rows * ((range + 511) / 512 * 1024 + 16) <= x_bytes(1, 3) ? 3 : 4;
+    const int64_t tiles = (N + 15) / 16, tiles_m = (M + 16 * g.mb - 1) / (16 * g.mb);
+    const int64_t per = 256 / (g.splits * tiles_m) > 1 ? 256 / (g.splits * tiles_m) : 1;
+    g.busiest = 0;
+    for (int l = 0; l <= 3; ++l) {
+        const int64_t groups = (tiles + (8 >> l) - 1) / (8 >> l), each = (steps + (1 << l) - 1) >> l;
+        const int64_t busiest = (groups + per - 1) / per * each;
+        if (l == 0 || busiest < g.busiest || (busiest == g.busiest && steps >= 16 && each >= 4)) {
+            g.busiest = busiest;
+            g.kwlog = l;
+        }
+    }
+    return g;
+}
+
+// How a call runs.  K ranges of the staged kernel: multiples of 256 (2048
+// where LDS holds that much of M rows, so that all eight waves have a step of
+// every block), as many as X needs; more where the blocks of rows leave half
+// of the CUs idle, down to ranges of 2048; up to a quarter (and eight) more
+// where the busiest wave then has fewer steps (8192 x 28672 for 16 rows 32.3 us
+// against 39.0, 70000 x 8192 for two 54.8 against 58.8).
+inline GemvPlan plan_gemv(int64_t M, int64_t N, int64_t K, bool aligned, bool workspace) {
+    const int mb = M > 16 ? 2 : 1;
+    const int64_t rows = M < 16 * mb ? M : 16 * mb;
+    int64_t most = (x_bytes(mb, mb == 1 ? 4 : 2) / rows - 16) / 2 / 512 * 512;
     if (most > 2048) most = most / 2048 * 2048;
     int64_t S = K > 0 ? (K + most - 1) / most : 1;
     const int64_t tiles = (N + 15) / 16, want = 256 / (tiles < 256 ? tiles : 256);
@@ -536,26 +566,11 @@ inline GemvPlan plan_gemv(int64_t M, int64_t N, int64_t K, bool aligned, bool wo
     int64_t ks = (K + S - 1) / S;
     ks = ks > 1024 ? (ks + 2047) / 2048 * 2048 : (ks + 255) / 256 * 256;
     if (ks > most) ks = most;
-    g.k_split = (int)ks;
-    g.splits = K > 0 ? (int)((K + ks - 1) / ks) : 1;
-    // Waves per block: what gives the busiest wave the fewest steps; among
-    // those, from ranges of 4096 on, the most waves that have four steps of a
-    // block each (together they read longer runs of its rows: 131072 x 8192
-    // for four rows 100 us with eight waves, 113 with one), else the fewest
-    // (one wave needs no join and no barrier: 4096 x 14336 for 16 rows, ranges
-    // of 2048, 13.2 us against 14.9 with two and 16.3 with eight).
-    const int64_t steps = ((ks < K ? ks : K) + 255) / 256;
-    const int64_t tiles_m = (M + 16 * g.mb - 1) / (16 * g.mb);
-    g.ring = g.mb == 2 ? 2 : rows * (((ks < K ? ks : K) + 511) / 512 * 1024 + 16) <= x_bytes(1, 3) ? 3 : 4;
-    const int64_t per = 256 / (g.splits * tiles_m) > 1 ? 256 / (g.splits * tiles_m) : 1;
-    int64_t best = 0;
-    for (int l = 0; l <= 3; ++l) {
-        const int64_t groups = (tiles + (8 >> l) - 1) / (8 >> l), each = (steps + (1 << l) - 1) >> l;
-        const int64_t busiest = (groups + per - 1) / per * each;
-        if (l == 0 || busiest < best || (busiest == best && steps >= 16 && each >= 4)) {
-            best = busiest;
-            g.kwlog = l;
-        }
+    GemvPlan g = plan_ranges(M, N, K, ks);
+    const int64_t base = g.splits;
+    for (int64_t s = base + 1; base > 1 && 4 * s <= 5 * S + 3 && s <= base + 8; ++s) {
+        const GemvPlan o = plan_ranges(M, N, K, ((K + s - 1) / s + 255) / 256 * 256);
+        if (o.busiest < g.busiest) g = o;
     }
     // (a step's scales are loaded together: rows hold a whole step)
     g.staged = aligned && K >= 256 && (g.splits == 1 || workspace);

@@ -151,7 +151,7 @@ def rmsnorm(X, W, eps, residual=None, Y=None, H=None, rstd=None):
         Y = _new(shape, X.dtype, dev)
     out = _matrix("Y", Y, shape, (X.dtype,), dev)
     H, rstd = _norm(_load().rmsnorm, X, W, eps, residual, H, rstd, shape, code, dev, out)
-    return Y, None if H is X and out[0] == X.data_ptr() else H, rstd
+    return Y, None if H is X and out[0] == X.data_ptr() and X.numel() else H, rstd
 
 
 def rmsnorm_mxfp8(X, W, eps, residual=None, Q=None, SF=None, H=None, rstd=None):
