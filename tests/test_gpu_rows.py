@@ -320,6 +320,17 @@ def test_long_rows_past_the_grid():
     assert ((dw.double() - (dy.double() * u).sum(0)).abs() <= (rows / 64 + 1 + 64 + 2) * ref.U * adw).all()
 
 
+@pytest.mark.parametrize("n", [32, 1024, 4096, 8192, 14336])
+@pytest.mark.parametrize("residual", [False, True])
+def test_a_row_does_not_depend_on_its_batch(n, residual):
+    x, r = rows_of(48, 3000, n, "bf16"), rows_of(49, 3000, n, "bf16")
+    w = torch.ones(n, dtype=torch.bfloat16, device=DEV)
+    y, h, rstd = tg.rmsnorm(x, w, EPS, residual=r if residual else None)
+    for a, b in ((0, 1), (2999, 3000), (700, 733)):
+        ya, ha, sa = tg.rmsnorm(x[a:b], w, EPS, residual=r[a:b] if residual else None)
+        assert torch.equal(ya, y[a:b]) and torch.equal(ha, h[a:b]) and torch.equal(sa, rstd[a:b])
+
+
 def test_norm_over_its_input_returns_no_h():
     x = rows_of(45, 5, 96, "bf16")
     w = rows_of(46, 1, 96, "bf16")[0].contiguous()

@@ -7,8 +7,8 @@
 // before the sum because that stored h is what the backward pass and the next
 // layer read; y is formed as (h * w) * rstd -- for 16-bit h and w the first
 // product is exact -- and rounded once.  16384 x 4096 bf16 with residual to
-// block-scaled rows 84 us (5.6 TB/s), one row 2.8 us (an empty launch: 2.7);
-// 16384 x 14336 bf16 quantised 126 us (5.6 TB/s).
+// block-scaled rows 82 us (5.8 TB/s), one row 2.7 us (hardly more than an empty
+// launch); 16384 x 14336 bf16 quantised 125 us (5.7 TB/s).
 #include <math.h>
 
 #include "rows.hpp"
@@ -217,16 +217,16 @@ hipError_t launch_norm(NormArgs &p, hipStream_t s) {
     const int nvec = (int)(((int64_t)p.N + kVE<T> - 1) / kVE<T>);
     // The fewest vectors per thread: a row's loads are all in flight at once
     // either way, and more waves share a row's arithmetic (16384 x 4096 bf16
-    // with residual to mxfp8: 84 us, 5.6 TB/s, with 256 threads of two
-    // vectors or 512 of one; 107 us with a wave of eight).
+    // with residual to mxfp8: 84 us with 256 threads of two vectors, 82 with
+    // 512 of one; 107 with a wave of eight).
     if (nvec <= 64) return go<T, MX, 64, 1>(p, s);
     if (nvec <= 128) return go<T, MX, 128, 1>(p, s);
     if (nvec <= 256) return go<T, MX, 256, 1>(p, s);
     // 512 threads where three quarters of them have work (8192 x 8192 bf16 84.7
     // against 91.4, one row 3.3 against 4.4; 16384 x 2304 59.9 against 52.1)
-    // and two loads each, or the rows are few (16384 x 3968 without residual
-    // 44.0 against 35.2, one row of 4096 2.7 against 3.2).
-    if (nvec <= 384 || (nvec <= 512 && !p.R && p.rows >= 2048)) return go<T, MX, 256, 2>(p, s);
+    // and two loads each (16384 x 3968 without residual 44.0 against 35.2).  The
+    // count of rows plays no part: a row's bits do not depend on its batch.
+    if (nvec <= 384 || (nvec <= 512 && !p.R)) return go<T, MX, 256, 2>(p, s);
     if (nvec <= 512) return go<T, MX, 512, 1>(p, s);
     if (nvec <= 768) return go<T, MX, 256, 4>(p, s);
     if (nvec <= 1024) return go<T, MX, 512, 2>(p, s);
