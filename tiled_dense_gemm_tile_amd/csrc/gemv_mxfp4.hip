@@ -11,7 +11,7 @@
 // workspace and are added in range order.
 //
 // One row of 131072 x 4096 47.8 us (5.6 TB/s of W), of 14336 x 4096 8.5 us, of
-// which an empty launch is 2.7; four rows of 131072 x 8192 100 us (5.7 TB/s);
+// which an empty launch is 1.6; four rows of 131072 x 8192 100 us (5.7 TB/s);
 // 16 rows of 4096 x 14336 12.3 us and 2 for the ranges' sums.
 #include "api.hpp"
 #include "pipeline.hpp"
