@@ -211,15 +211,16 @@ __device__ __forceinline__ bool fp16_scales(uint32_t c) {
 //
 // R slots: 4; 3 where two workgroups then share a CU's LDS (X of 16 KiB at
 // most: one row of 131072 x 4096 47.8 us against 55.8, of 14336 x 4096 8.5
-// against 9.1, of 4096 x 4096 4.9 against 5.1); 2 with two blocks of 16 rows of
-// X (MB).
+// against 9.1, of 4096 x 4096 4.9 against 5.1), and with two blocks of 16 rows
+// of X (MB; with two slots 20 rows of 28672 x 8192 42.7 against 38.4).
+constexpr bool pair(int MB, int R) { return MB == 1 && R == 3; }   // two workgroups per CU
 // LDS bytes a workgroup has for X beside its slots and its waves' sums.
 constexpr int x_bytes(int MB, int R) {
-    return (R == 3 ? 80 : 160) * 1024 - kGemvWaves * 2048 * R - 2 * MB * kGemvWaves * 1024;
+    return (pair(MB, R) ? 80 : 160) * 1024 - kGemvWaves * 2048 * R - 2 * MB * kGemvWaves * 1024;
 }
 
 template <bool FP16, int MB, int SC, int R>
-__global__ void __launch_bounds__(kGemvWaves * 64, R == 3 ? 4 : 2) gemv_mxfp4_staged_kernel(GemvArgs p) {
+__global__ void __launch_bounds__(kGemvWaves * 64, pair(MB, R) ? 4 : 2) gemv_mxfp4_staged_kernel(GemvArgs p) {
     __shared__ __attribute__((aligned(2048))) char ring[kGemvWaves][R][2048];
     __shared__ float red[2][kGemvWaves][MB * 4][64];
     extern __shared__ __attribute__((aligned(16))) char xs[];
@@ -428,12 +429,9 @@ __global__ void __launch_bounds__(kGemvWaves * 64, R == 3 ? 4 : 2) gemv_mxfp4_st
         while (step(std::integral_constant<int, 0>()) && step(std::integral_constant<int, 1>()) &&
                step(std::integral_constant<int, 2>()) && step(std::integral_constant<int, 3>())) {
         }
-    } else if constexpr (R == 3) {
+    } else {
         while (step(std::integral_constant<int, 0>()) && step(std::integral_constant<int, 1>()) &&
                step(std::integral_constant<int, 2>())) {
-        }
-    } else {
-        while (step(std::integral_constant<int, 0>()) && step(std::integral_constant<int, 1>())) {
         }
     }
     wait_vmcnt<0>();                                   // (requests past the last group: nothing in flight into LDS at the end)
@@ -534,7 +532,7 @@ inline GemvPlan plan_ranges(int64_t M, int64_t N, int64_t K, int64_t ks) {
     g.k_split = (int)ks;
     g.splits = K > 0 ? (int)((K + ks - 1) / ks) : 1;
     const int64_t rows = M < 16 * g.mb ? M : 16 * g.mb, range = ks < K ? ks : K, steps = (range + 255) / 256;
-    g.ring = g.mb == 2 ? 2 : rows * ((range + 511) / 512 * 1024 + 16) <= x_bytes(1, 3) ? 3 : 4;
+    g.ring = g.mb == 2 ? 3 : rows * ((range + 511) / 512 * 1024 + 16) <= x_bytes(1, 3) ? 3 : 4;
     const int64_t tiles = (N + 15) / 16, tiles_m = (M + 16 * g.mb - 1) / (16 * g.mb);
     const int64_t per = 256 / (g.splits * tiles_m) > 1 ? 256 / (g.splits * tiles_m) : 1;
     g.busiest = 0;
@@ -558,7 +556,7 @@ inline GemvPlan plan_ranges(int64_t M, int64_t N, int64_t K, int64_t ks) {
 inline GemvPlan plan_gemv(int64_t M, int64_t N, int64_t K, bool aligned, bool workspace) {
     const int mb = M > 16 ? 2 : 1;
     const int64_t rows = M < 16 * mb ? M : 16 * mb;
-    int64_t most = (x_bytes(mb, mb == 1 ? 4 : 2) / rows - 16) / 2 / 512 * 512;
+    int64_t most = (x_bytes(mb, mb == 1 ? 4 : 3) / rows - 16) / 2 / 512 * 512;
     if (most > 2048) most = most / 2048 * 2048;
     int64_t S = K > 0 ? (K + most - 1) / most : 1;
     const int64_t tiles = (N + 15) / 16, want = 256 / (tiles < 256 ? tiles : 256);
@@ -590,7 +588,7 @@ hipError_t launch_gemv(const GemvPlan &g, GemvArgs &p, hipStream_t s) {
     const int rw = kGemvWaves >> p.kwlog, groups = (p.tiles_n + rw - 1) / rw;
     const int span = p.k_split < p.K ? p.k_split : p.K;
     p.x_pitch = (span + 511) / 512 * 1024 + 16;
-    int per = tg_api::cu_count(s) * (R == 3 ? 2 : 1) / (int)(g.splits * tiles_m);
+    int per = tg_api::cu_count(s) * (pair(MB, R) ? 2 : 1) / (int)(g.splits * tiles_m);
     if (per <= 0) per = 1;
     const dim3 grid((unsigned)(groups < per ? groups : per), (unsigned)g.splits, tiles_m);
     const size_t lds = (size_t)rows * p.x_pitch;
@@ -612,7 +610,7 @@ hipError_t launch_gemv(const GemvPlan &g, GemvArgs &p, hipStream_t s) {
 
 template <bool FP16>
 hipError_t launch_gemv_rows(const GemvPlan &g, GemvArgs &p, hipStream_t s) {
-    return g.mb == 2     ? launch_gemv<FP16, 2, 2>(g, p, s)
+    return g.mb == 2     ? launch_gemv<FP16, 2, 3>(g, p, s)
            : g.ring == 3 ? launch_gemv<FP16, 1, 3>(g, p, s)
                          : launch_gemv<FP16, 1, 4>(g, p, s);
 }

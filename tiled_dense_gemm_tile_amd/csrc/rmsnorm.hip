@@ -7,7 +7,8 @@
 // before the sum because that stored h is what the backward pass and the next
 // layer read; y is formed as (h * w) * rstd -- for 16-bit h and w the first
 // product is exact -- and rounded once.  16384 x 4096 bf16 with residual to
-// block-scaled rows 82 us (5.8 TB/s), one row 2.7 us (an empty launch: 1.6); 16384 x 14336 bf16 quantised 125 us (5.7 TB/s).
+// block-scaled rows 82 us (5.8 TB/s), one row 2.7 us (an empty launch: 1.6);
+// 16384 x 14336 bf16 quantised 125 us (5.7 TB/s).
 #include <math.h>
 
 #include "rows.hpp"
