@@ -256,3 +256,18 @@ def test_rows_moved_to_16_bytes(case):
     assert (D == 5).all()
     for short in (need - 1, 0):
         assert torch.equal(tg.gemm_wgrad_mxfp8(a, Q, S, C=c, workspace=ws[:short]).double(), want)
+
+
+@pytest.mark.parametrize("tiles", range(1, 15))
+@pytest.mark.parametrize("shape", [(128, 128), (3328, 3328)], ids=["128x128 tiles", "256x256 tiles"])
+def test_every_count_of_k_tiles(shape, tiles):
+    """One K range of 1 to 14 K tiles: each way through the unrolled loop and its rest."""
+    (m, n), k = shape, 64 * tiles
+    g = torch.Generator(DEV).manual_seed(tiles)
+    dy = torch.randint(-4, 5, (k, m), device=DEV, generator=g).bfloat16()
+    q = torch.from_numpy(INT_CODES).to(DEV)[torch.randint(0, 9, (k, n), device=DEV, generator=g)]
+    sf = torch.randint(126, 129, (k, n // 32), device=DEV, generator=g).to(torch.uint8)
+    x = q.view(torch.float8_e4m3fn).double() * torch.exp2(sf.double() - 127).repeat_interleave(32, 1)
+    want = dy.double().t().contiguous() @ x             # multiples of 1/2 below 2^15
+    assert torch.equal(tg.gemm_wgrad_mxfp8(dy, q, sf, workspace=torch.empty(0, dtype=torch.uint8, device=DEV)).double(),
+                       want)

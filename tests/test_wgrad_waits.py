@@ -1,0 +1,117 @@
+"""The waits of the four-wave weight-gradient kernel, checked in the gfx950
+assembly of its source (CPU only: compiled, never run).
+
+A K tile ends with s_waitcnt vmcnt(n) and a barrier, after which A's next
+tile is read from LDS.  n counts on what the tiles issue after that tile's
+loads: were a load left out of one copy of the unrolled loop, n would be too
+many and the tile could be read before it has landed.  Here every path through
+the kernel is followed with the queue of outstanding vector-memory operations
+(they return in order), of which a wait leaves the youngest n; only the waits
+right before the barriers are counted, so that the others, which come and go
+with the compiler's choices, carry nothing."""
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+from tiled_dense_gemm_tile_amd import build as B
+
+pytestmark = pytest.mark.skipif(shutil.which(B.HIPCC) is None and not os.path.exists(B.HIPCC),
+                                reason="hipcc not available")
+
+KERNEL = "gemm_wgrad_w4_kernelILb%dELi%dE"
+# per tile size: A's loads a K tile and wave, K tiles from their issue to their use
+A_LOADS, AHEAD = {8: 8, 4: 4}, {8: 1, 4: 2}
+
+
+@pytest.fixture(scope="module")
+def assembly(tmp_path_factory):
+    out = str(tmp_path_factory.mktemp("asm") / "wgrad.s")
+    subprocess.run([B.HIPCC] + B.FLAGS + ["-S", "--cuda-device-only", os.path.join(B.CSRC, "wgrad.hip"), "-o", out],
+                   check=True, capture_output=True)
+    return open(out).read()
+
+
+def blocks_of(text, name):
+    """Basic blocks of a kernel: {label: (instructions, labels that follow)}, the first one's label."""
+    body = re.search(r"^(\w*%s\w*):.*?^\.Lfunc_end" % re.escape(name), text, re.M | re.S).group(0)
+    blocks, label, first, fresh = {}, "entry", "entry", 0
+    ins, ended = [], False
+
+    def close(nxt, falls):
+        blocks[label][1].extend([nxt] if falls else [])
+
+    blocks[label] = (ins, [])
+    for line in body.splitlines()[1:]:
+        line = line.split(";")[0].strip()
+        m = re.match(r"(\.LBB\w+):$", line)
+        if m:
+            close(m.group(1), not ended)
+            label, ins, ended = m.group(1), [], False
+            blocks[label] = (ins, [])
+        elif line and not line.startswith("."):
+            op = line.split()[0]
+            ins.append(line)
+            if op.startswith("s_cbranch"):
+                blocks[label][1].append(line.split()[-1])
+                fresh += 1
+                close("after%d" % fresh, True)
+                label, ins, ended = "after%d" % fresh, [], False
+                blocks[label] = (ins, [])
+            elif op == "s_branch":
+                blocks[label][1].append(line.split()[-1])
+                ended = True
+            elif op == "s_endpgm":
+                ended = True
+    return blocks, first
+
+
+VMEM = re.compile(r"(buffer|global|flat|scratch)_(load|store|atomic)")
+
+
+def walk(text, name, loads, ahead, visit):
+    """Follows every path; `visit(queue)` at each barrier, with the queue after its wait.  An entry of the queue is
+    the number of barriers until it has to have landed (0: any time)."""
+    blocks, first = blocks_of(text, name)
+    # (block, queue, barriers passed up to one, direct loads since the last one)
+    todo, seen, barriers = [(first, (), 0, 0)], set(), 0
+    while todo:
+        state = todo.pop()
+        if state in seen:
+            continue
+        seen.add(state)
+        assert len(seen) < 200000
+        label, queue, passed, direct = state
+        ins, after = blocks[label]
+        for i, line in enumerate(ins):
+            if VMEM.match(line):
+                due = 0
+                if line.endswith(" lds"):
+                    if passed:
+                        due = ahead if direct < loads else 0
+                    else:                              # the first tiles, before the first barrier
+                        due = direct // loads + 1 if direct < loads * ahead else 0
+                    direct += 1
+                queue += (due,)
+                queue = queue[-64:]
+            elif line.startswith("s_barrier"):
+                n = re.search(r"vmcnt\((\d+)\)", ins[i - 1]) if i else None
+                if n:
+                    queue = queue[len(queue) - int(n.group(1)):] if int(n.group(1)) < len(queue) else queue
+                visit(queue)
+                barriers += 1
+                queue = tuple(max(d - 1, 0) for d in queue)
+                passed, direct = 1, 0
+        todo.extend((b, queue, passed, direct) for b in after)
+    return barriers
+
+
+@pytest.mark.parametrize("tile", [8, 4])
+@pytest.mark.parametrize("bf16", [0, 1])
+def test_a_tile_has_landed_before_it_is_read(assembly, tile, bf16):
+    def visit(queue):
+        assert 1 not in queue, "A's next tile may still be on its way behind this barrier"
+
+    assert walk(assembly, KERNEL % (bf16, tile), A_LOADS[tile], AHEAD[tile], visit) > 3

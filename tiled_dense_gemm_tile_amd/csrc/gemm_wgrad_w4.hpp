@@ -390,6 +390,16 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[i][j]));
+    // (the last tiles' loads of B and its scales, which nobody multiplies: used
+    // here, so that every tile issues them -- left out of a tile, as a load
+    // without a use is, they would be missing from its wait's count)
+#pragma unroll
+    for (int d = 0; d < DB; ++d) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) asm volatile("" : : "v"(vb[d][j]));
+        if constexpr (T == 4) asm volatile("" : : "v"(vs2[d][0]), "v"(vs2[d][1]));
+    }
+    if constexpr (T == 8) asm volatile("" : : "v"(vs));
     wait_vmcnt<0>();
     wait_lgkmcnt0();
     barrier();
