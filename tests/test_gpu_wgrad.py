@@ -271,3 +271,17 @@ def test_every_count_of_k_tiles(shape, tiles):
     want = dy.double().t().contiguous() @ x             # multiples of 1/2 below 2^15
     assert torch.equal(tg.gemm_wgrad_mxfp8(dy, q, sf, workspace=torch.empty(0, dtype=torch.uint8, device=DEV)).double(),
                        want)
+
+
+@pytest.mark.parametrize("k", [1, 2, 3, 4, 7, 64, 70])
+@pytest.mark.parametrize("n", [32, 64, 96, 128, 160, 224, 288])
+@pytest.mark.parametrize("pad", [0, 1, 3])
+def test_scales_amid_nan_codes(n, k, pad):
+    """Scales whose neighbours in memory are NaN codes, before, between and behind their rows."""
+    m = 48
+    dy, q, sf = integer_case(3, m, n, k)
+    s = torch.full((7 + k * (n // 32 + pad) + 9,), 0xFF, dtype=torch.uint8, device=DEV)
+    v = s[7:7 + k * (n // 32 + pad)].view(k, n // 32 + pad)[:, :n // 32]
+    v.copy_(torch.from_numpy(sf).to(DEV))
+    d = tg.gemm_wgrad_mxfp8(torch.from_numpy(dy).to(DEV).bfloat16(), torch.from_numpy(q).to(DEV), v)
+    assert np.array_equal(f64(d), dy.astype(np.float64).T @ ref.dequant(q, sf))

@@ -71,19 +71,26 @@ def blocks_of(text, name):
 VMEM = re.compile(r"(buffer|global|flat|scratch)_(load|store|atomic)")
 
 
+def count_of(line):
+    """The vector-memory count of a wait (63: none)."""
+    m = re.search(r"vmcnt\((\d+)\)", line)
+    return int(m.group(1)) if m else 63
+
+
 def walk(text, name, loads, ahead, visit):
-    """Follows every path; `visit(queue)` at each barrier, with the queue after its wait.  An entry of the queue is
-    the number of barriers until it has to have landed (0: any time)."""
+    """Follows every path; `visit(nth, queue, wait, least)` at each barrier, with the queue after its wait, that wait's
+    count and the least count of the waits since the barrier before.  An entry of the queue is the number of barriers until
+    it has to have landed (0: any time); nth counts the barriers up to two."""
     blocks, first = blocks_of(text, name)
-    # (block, queue, barriers passed up to one, direct loads since the last one)
-    todo, seen, barriers = [(first, (), 0, 0)], set(), 0
+    # (block, queue, barriers passed up to two, direct loads since the last one, least count since it)
+    todo, seen, barriers = [(first, (), 0, 0, 63)], set(), 0
     while todo:
         state = todo.pop()
         if state in seen:
             continue
         seen.add(state)
         assert len(seen) < 200000
-        label, queue, passed, direct = state
+        label, queue, passed, direct, least = state
         ins, after = blocks[label]
         for i, line in enumerate(ins):
             if VMEM.match(line):
@@ -96,22 +103,41 @@ def walk(text, name, loads, ahead, visit):
                     direct += 1
                 queue += (due,)
                 queue = queue[-64:]
+            elif line.startswith("s_waitcnt") and "vmcnt" in line and not ins[i + 1:i + 2] == ["s_barrier"]:
+                least = min(least, count_of(line))
             elif line.startswith("s_barrier"):
-                n = re.search(r"vmcnt\((\d+)\)", ins[i - 1]) if i else None
-                if n:
-                    queue = queue[len(queue) - int(n.group(1)):] if int(n.group(1)) < len(queue) else queue
-                visit(queue)
+                n = count_of(ins[i - 1]) if i else 63
+                if n < len(queue):
+                    queue = queue[len(queue) - n:]
+                visit(passed, queue, n, least)
                 barriers += 1
                 queue = tuple(max(d - 1, 0) for d in queue)
-                passed, direct = 1, 0
-        todo.extend((b, queue, passed, direct) for b in after)
+                passed, direct, least = min(passed + 1, 2), 0, 63
+        todo.extend((b, queue, passed, direct, least) for b in after)
     return barriers
 
 
 @pytest.mark.parametrize("tile", [8, 4])
 @pytest.mark.parametrize("bf16", [0, 1])
 def test_a_tile_has_landed_before_it_is_read(assembly, tile, bf16):
-    def visit(queue):
+    def visit(nth, queue, wait, least):
         assert 1 not in queue, "A's next tile may still be on its way behind this barrier"
 
     assert walk(assembly, KERNEL % (bf16, tile), A_LOADS[tile], AHEAD[tile], visit) > 3
+
+
+@pytest.mark.parametrize("tile", [8, 4])
+@pytest.mark.parametrize("bf16", [0, 1])
+def test_no_wait_inside_a_tile_is_longer_than_its_last(assembly, tile, bf16):
+    """The loads of tiles ahead stay in flight through a tile: the compiler's own waits, for B's codes and scales, ask
+    for no more than the wait at its end."""
+    found = []
+
+    def visit(nth, queue, wait, least):
+        # (the first tile waits for codes loaded right before it; no count, or none left: behind the last tile)
+        if nth == 2 and 0 < wait < 63:
+            found.append(wait)
+            assert least >= wait
+
+    walk(assembly, KERNEL % (bf16, tile), A_LOADS[tile], AHEAD[tile], visit)
+    assert found

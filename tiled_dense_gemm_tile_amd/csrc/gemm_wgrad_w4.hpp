@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
     constexpr int ROWB = BM * 2;                       // an LDS row: 32 T bf16
     constexpr int SLOT = KT * ROWB;
     // loads per thread and K tile: of A, of B, of B's scales, of C
-    constexpr int LA = SLOT / 4096, NV = T / 2, NS = T == 8 ? 1 : 2, NC = T == 8 ? 1 : 0;
+    constexpr int LA = SLOT / 4096, NV = T / 2, NS = 1, NC = T == 8 ? 1 : 0;
     // LDS slots of A and register sets of B: a K tile of T = 4 takes less time
     // than a load, so A comes two tiles ahead and B three
     constexpr int DA = T == 8 ? 2 : 3, DB = T == 8 ? 1 : 2, UNROLL = T == 8 ? 2 : 6;
@@ -167,25 +167,28 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
     };
 
     // ---- B: thread t holds row t / 4 of a K tile, columns 16 (t % 4) + 64 j
-    // .. + 15, and their scales: T = 8: the tile's eight in one load (the row's
+    // .. + 15, and their scales, the tile's in one load: T = 8: eight (the row's
     // last eight where N ends inside the tile: s_shift bits too far left); T =
-    // 4: its own two, of blocks inside the row.  (Rows past K take the last
-    // row's, with codes 0.)
+    // 4: four, with what follows the row where N ends inside the tile, and the
+    // matrix's last four where those would end past it.  (One load of 32 bits:
+    // bytes kept across the loop are masked on arrival, and the wait for that
+    // drained the loads of the tiles ahead.  Rows past K take the last row's,
+    // with codes 0.)
     const int br = tid >> 2, bt = tid & 3;
     const uint32_t b_off = (uint32_t)(br * p.ldb) + bt * 16;
-    const int nb = N / 32, s_at = T == 4 ? 0 : n0 / 32 < nb - 8 ? n0 / 32 : nb - 8, s_shift = 8 * (n0 / 32 - s_at);
-    const int s_b0 = n0 / 32 + (bt >> 1), s_b[2] = {s_b0 < nb ? s_b0 : nb - 1, s_b0 + 2 < nb ? s_b0 + 2 : nb - 1};
+    const int nb = N / 32, s_at = T == 4 || n0 / 32 < nb - 8 ? n0 / 32 : nb - 8, s_shift = 8 * (n0 / 32 - s_at);
+    const uint8_t *const s_end = p.SF + (int64_t)(p.K - 1) * p.ldsf + nb - 4;   // (T == 4: not before SF, wgrad.hip)
     pb.base = (const char *)p.B + (int64_t)k_lo * p.ldb + n0;
     pb.rows = K;
     const uint32_t b_row = (uint32_t)(N - n0), b_ld = (uint32_t)p.ldb;
     pb.set_span(b_ld, b_row, 0u);
     const int64_t b_step = (int64_t)KT * p.ldb;
     struct __attribute__((packed, aligned(1))) PackedScales {
-        uint64_t v;
+        typename std::conditional<T == 8, uint64_t, uint32_t>::type v;
     };
     u32x4 vb[DB][NV];
     uint64_t vs;                                       // T == 8
-    uint32_t vs2[DB][2];                               // T == 4
+    uint32_t vs4[DB], vs4_shift[DB];                   // T == 4: the scales, and the bits to this thread's first
     auto load_b = [&](__amdgpu_buffer_rsrc_t r, int set, int j) __attribute__((always_inline)) {
         vb[set][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b_off + 64 * j, 0, 0));
     };
@@ -196,8 +199,9 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
         if constexpr (T == 8) {
             vs = ((const PackedScales *)s_row)->v;
         } else {
-            vs2[set][0] = s_row[s_b[0]];
-            vs2[set][1] = s_row[s_b[1]];
+            const uint8_t *at = s_row < s_end ? s_row : s_end;
+            vs4[set] = ((const PackedScales *)at)->v;
+            vs4_shift[set] = 8 * ((uint32_t)(s_row - at) + (bt >> 1));
         }
     };
     auto next_s = [&]() __attribute__((always_inline)) {
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
             sc[0] = (uint32_t)s;
             sc[1] = (uint32_t)(s >> 32);
         } else {
-            sc[0] = vs2[set][0] | vs2[set][1] << 16;
+            sc[0] = vs4[set] >> (vs4_shift[set] & 31);   // (32: of columns past N)
         }
     };
     u32x4 half;
@@ -378,10 +382,17 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
         static_for<0, UNROLL>([&](auto i) __attribute__((always_inline)) {
             tile(std::false_type(), std::integral_constant<int, (decltype(i)::value + 1) % UNROLL>());
         });
-    static_for<0, UNROLL - 1>([&](auto i) __attribute__((always_inline)) {
-        if (t + decltype(i)::value < nt)
-            tile(std::false_type(), std::integral_constant<int, decltype(i)::value + 1>());
-    });
+    // (the rest nested, each copy only behind the one before: side by side, the
+    // compiler waits as if a copy could be left out)
+    auto more = [&](auto self, auto i) __attribute__((always_inline)) {
+        constexpr int n = decltype(i)::value;
+        if constexpr (n < UNROLL) {
+            if (t++ >= nt) return;
+            tile(std::false_type(), i);
+            self(self, std::integral_constant<int, n + 1>());
+        }
+    };
+    more(more, std::integral_constant<int, 1>());
 #pragma unroll
     for (int q = 0; q < Q; ++q) mfma(std::false_type(), 1, q / TN, q % TN);
     // (the wait states of mfma_result_fence, for either tile)
@@ -397,7 +408,7 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
     for (int d = 0; d < DB; ++d) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) asm volatile("" : : "v"(vb[d][j]));
-        if constexpr (T == 4) asm volatile("" : : "v"(vs2[d][0]), "v"(vs2[d][1]));
+        if constexpr (T == 4) asm volatile("" : : "v"(vs4[d]));
     }
     if constexpr (T == 8) asm volatile("" : : "v"(vs));
     wait_vmcnt<0>();

@@ -22,7 +22,7 @@ struct WgradPlan {
 
 constexpr int64_t kCus = 256;
 
-// `rows16`: A and B start their rows on 16 bytes.
+// `rows16`: A and B start their rows on 16 bytes (and SFB holds four scales).
 WgradPlan plan_wgrad(int64_t M, int64_t N, int64_t K, bool rows16, bool workspace) {
     WgradPlan g = {};
     const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256), t128 = ((M + 127) / 128) * ((N + 127) / 128);
@@ -117,8 +117,10 @@ gemm_status gemm_wgrad_mxfp8(int64_t M, int64_t N, int64_t K, const void *A, int
     if (ldsfb < N / 32) return GEMM_ERR_BAD_LD;
     if (K > 0 && !SFB) return GEMM_ERR_NULL_POINTER;
     if (misaligned(A, 2) || (uintptr_t)workspace % 256 != 0) return GEMM_ERR_MISALIGNED;
-    bool rows16 = (((uintptr_t)A | (uintptr_t)(lda * 2) | (uintptr_t)B | (uintptr_t)ldb) & 15) == 0;
-    if (const size_t copy = rows16 || (((uintptr_t)B | (uintptr_t)ldb) & 15) ? 0 : wgrad_copy_bytes(M, N, K)) {
+    // (the four-wave kernel loads four scales at once: SFB holds as many)
+    const bool b16 = (((uintptr_t)B | (uintptr_t)ldb) & 15) == 0 && (K - 1) * ldsfb + N / 32 >= 4;
+    bool rows16 = b16 && (((uintptr_t)A | (uintptr_t)(lda * 2)) & 15) == 0;
+    if (const size_t copy = rows16 || !b16 ? 0 : wgrad_copy_bytes(M, N, K)) {
         // (behind the partial sums, which are a multiple of 16 KiB)
         const size_t at = plan_wgrad(M, N, K, true, true).bytes;
         if (workspace && workspace_bytes >= at + copy) {
