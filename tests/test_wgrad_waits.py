@@ -141,3 +141,15 @@ def test_no_wait_inside_a_tile_is_longer_than_its_last(assembly, tile, bf16):
 
     walk(assembly, KERNEL % (bf16, tile), A_LOADS[tile], AHEAD[tile], visit)
     assert found
+
+
+def test_k_tiles_up_to_the_largest_k(tmp_path):
+    """The count of K tiles at the ends of K's range, by the compiler (an overflow is an error there)."""
+    src = tmp_path / "count.hip"
+    src.write_text('#include "gemm_wgrad_w4.hpp"\n' + "".join(
+        "static_assert(tg::k_tiles(%d, 64) == %d);\n" % (k, -(-k // 64))
+        for k in (1, 63, 64, 65, 8200, 2 ** 31 - 65, 2 ** 31 - 64, 2 ** 31 - 63, 2 ** 31 - 1)))
+    subprocess.run([B.HIPCC] + B.FLAGS + ["-I" + B.CSRC, "--cuda-host-only", "-fsyntax-only", str(src)], check=True,
+                   capture_output=True)
+    text = open(os.path.join(B.CSRC, "gemm_wgrad_w4.hpp")).read()
+    assert text.count("k_tiles(K, KT)") == 1 and "K + KT" not in text

@@ -63,6 +63,10 @@ __device__ __forceinline__ int xcd_order(int wg, int nwg) {
     return x * q + (x < r ? x : r) + (wg >> 3);
 }
 
+// K tiles of `kt` rows that hold K >= 1, of any 32-bit K: K + kt - 1 would pass
+// 2^31 at its end.
+constexpr int k_tiles(int K, int kt) { return (K - 1) / kt + 1; }
+
 // A half's T * T MFMAs spread B's 2 T conversion steps evenly between them; the
 // step of the second half's fragment reads.
 constexpr int wgrad_convert_every(int T) { return T == 8 ? 4 : 2; }
@@ -120,7 +124,7 @@ __global__ void __launch_bounds__(256, T == 8 ? 1 : 2) gemm_wgrad_w4_kernel(Wgra
     const int M = p.M, N = p.N;
     const int k_lo = split > 0 ? split * p.k_split : 0;
     const int K = split < 0 ? p.K : (p.K - k_lo < p.k_split ? p.K - k_lo : p.k_split);
-    const int nt = (K + KT - 1) / KT;
+    const int nt = k_tiles(K, KT);
 
     // A K tile's resource: based at its first row, ending with its last row's
     // last element (A: with the 16-byte block of it -- the range check is per
