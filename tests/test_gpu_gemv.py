@@ -228,3 +228,29 @@ def test_all_scale_codes(kind, k):
             assert np.array_equal(D[:, 1], [3 * s, 6 * s]), code
         else:
             assert not np.isfinite(D[:, 1]).any(), code
+
+
+@pytest.mark.parametrize("kind", XT)
+@pytest.mark.parametrize("k", [32, 256])
+@pytest.mark.parametrize("m", [1, 20])
+def test_weights_past_bf16_are_infinite(kind, k, m):
+    """Non-zero x against one weight at or past 2^128 and zeros: an infinity of the product's sign, with x that bf16
+    holds and x that it does not; the largest finite weights of the same scales stay exact."""
+    x = torch.tensor([1.0, 0.1, -3.1416, 2.0 ** -10] * (k // 4), device=DEV).to(XT[kind]).repeat(m, 1)
+    for code, over, finite in ((253, (4, 6), 3), (254, (2, 3, 4, 6), 1.5)):
+        codes = [list(ref.E2M1).index(v) for v in over]
+        rows = [(c ^ s, at) for c in codes for s in (0, 8) for at in range(4)]
+        w = np.zeros((len(rows) + 4, k // 2), np.uint8)
+        for i, (c, at) in enumerate(rows):
+            w[i, at // 2] = c << (4 * (at % 2))
+        for at in range(4):
+            w[len(rows) + at, at // 2] = list(ref.E2M1).index(finite) << (4 * (at % 2))
+        S = torch.full((len(w), k // 32), code, dtype=torch.uint8, device=DEV)
+        D = f64(tg.gemv_mxfp4(x, torch.from_numpy(w).to(DEV), S))
+        xv = f64(x)
+        for i, (c, at) in enumerate(rows):
+            assert (D[:, i] == np.sign(xv[:, at]) * (np.inf if c < 8 else -np.inf)).all(), (code, c, at)
+        # (in fp32: 3.1416 * 1.5 * 2^127 is past its range)
+        with np.errstate(over="ignore"):
+            want = (xv[:, :4] * finite * np.ldexp(1.0, code - 127)).astype(np.float32).astype(np.float64)
+        assert np.array_equal(D[:, len(rows):], want), code

@@ -168,12 +168,22 @@ __device__ __forceinline__ void gemv_step(const u32x4 (&xf)[MB], uint32_t w, flo
         for (int a = 0; a < MB; ++a) acc[a] = mfma16<FP16>(xf[a], wf, acc[a]);
     } else {
         const u32x4 wf = fp4_up<false>(w, scale);
+        // (weights past bf16's range meet hi alone: x that bf16 holds has lo = 0,
+        // and 0 * infinity would be a NaN beside hi's infinity)
+        u32x4 wl = wf;
+        if (__any(scale >= 0x1p126f)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if ((wl[i] & 0x7f80u) == 0x7f80u) wl[i] &= 0xffff0000u;
+                if ((wl[i] & 0x7f800000u) == 0x7f800000u) wl[i] &= 0xffffu;
+            }
+        }
 #pragma unroll
         for (int a = 0; a < MB; ++a) {
             u32x4 hi, lo;
             split_f16(xf[a], hi, lo);
             acc[a] = mfma16<false>(hi, wf, acc[a]);
-            acc[a] = mfma16<false>(lo, wf, acc[a]);
+            acc[a] = mfma16<false>(lo, wl, acc[a]);
         }
     }
 }
