@@ -151,3 +151,26 @@ def test_calls_on_another_stream():
     s.synchronize()
     assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8))
     assert torch.equal(dW, tg.gemm_wgrad_mxfp8(rand(92, 700, 64), want[0], want[1]))
+
+
+def test_the_last_token_of_a_long_batch_of_one():
+    """x[:, -1] is one row whose stride is the whole batch: as good as a packed row."""
+    n, m = 4096, 96
+    x = rand(30, 1, 2100, n)
+    last, row = x[:, -1], x[0, -1:].clone()
+    assert last.stride(0) * 2 >= 8 << 20
+    w = rand(31, n, scale=0.1) + 1
+    W = torch.randint(0, 256, (m, n // 2), device=DEV, generator=torch.Generator(DEV).manual_seed(32)).to(torch.uint8)
+    S = torch.full((m, n // 32), 120, dtype=torch.uint8, device=DEV)
+    assert torch.equal(tg.gemv_mxfp4(last, W, S), tg.gemv_mxfp4(row, W, S))
+    q, sf = tg.mxfp8_quantize(last)
+    for a, b in zip((q, sf), tg.mxfp8_quantize(row)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert torch.equal(tg.gemm_wgrad_mxfp8(last, q, sf), tg.gemm_wgrad_mxfp8(row, q, sf))
+    y = tg.rmsnorm(row, w, EPS)[0]
+    out = torch.zeros_like(x)
+    tg.rmsnorm(last, w, EPS, Y=out[:, -1])              # and so for results
+    assert torch.equal(out[:, -1], y) and (out[:, :-1] == 0).all()
+    D = torch.zeros(1, 40000, m, device=DEV)
+    tg.gemv_mxfp4(row, W, S, D=D[:, -1])
+    assert torch.equal(D[:, -1], tg.gemv_mxfp4(row, W, S)) and (D[:, :-1] == 0).all()

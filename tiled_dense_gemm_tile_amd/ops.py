@@ -23,6 +23,7 @@ _E8M0 = (torch.float8_e8m0fnu, torch.uint8)
 _E2M1 = (torch.uint8, torch.float4_e2m1fn_x2)
 _F32 = (torch.float32,)
 _NONE = (None, 0)
+_LD_LIMIT = 1 << 21                                    # elements of 4 bytes: the products' rows are below 8 MiB
 _current_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -65,7 +66,7 @@ def _matrix(name, t, shape, dtypes, dev):
     ld, one = t.stride()
     if one != 1 and shape[1] > 1:
         raise ValueError("%s: the last stride must be 1" % name)
-    if shape[0] <= 1 and ld < shape[1]:
+    if shape[0] <= 1 and not shape[1] <= ld < _LD_LIMIT:  # (of one row any will do: x[:, -1] of a long batch of one)
         ld = shape[1]
     return t.data_ptr(), ld
 
