@@ -157,8 +157,9 @@ size_t gemm_wgrad_mxfp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *     sums in order; a smaller one or NULL runs
  *     uncut, slower (the same result up to summation order).  Calls sharing it
  *     must be ordered.
- * Leading dimensions below 8 MiB in bytes.  Weights beyond bf16's range (4 and
- * 6 at 2^126, 2 to 6 at 2^127) are infinite.
+ * Leading dimensions below 8 MiB in bytes (ldd's holds N below 2^21 with fp32
+ * results and 2^22 with bf16 ones), ldsfw below 2^23.  Weights beyond bf16's
+ * range (4 and 6 at 2^126, 2 to 6 at 2^127) are infinite.
  * Scale code 0xFF gives NaN in the row's outputs.
  */
 gemm_status gemv_mxfp4(int64_t M, int64_t N, int64_t K, int64_t kblock, const void *X, int64_t ldx, int x_type,

@@ -249,3 +249,12 @@ def test_gemv_workspace_is_bounded():
     for m, n, k in ((1 << 20, 14336, 16384), (4096, 4096, 14336), (1 << 20, 64, 1 << 20)):
         splits = -(-k // 1024)
         assert 0 < tg.gemv_mxfp4_workspace_bytes(m, n, k) <= max(64 << 20, splits * 32 * n * 4)
+
+
+@pytest.mark.parametrize("out,n", [(F32, 1 << 21), (1, 1 << 22)], ids=["f32", "bf16"])
+def test_gemv_refuses_more_columns_than_a_row_of_d_holds(out, n):
+    """N is bounded by ldd's limit of 8 MiB, far below what one launch counts (2^32 threads, 512 for 16 columns)."""
+    assert n // 16 * 512 < 1 << 32
+    for big in (n, 1 << 27, (1 << 31) - 1):
+        assert gemv(M=1, N=big, K=32, ldx=32, ldw=32, ldsf=1, ldd=big, out=out) == UNSUPPORTED
+        assert gemv(M=1, N=big, K=32, ldx=32, ldw=32, ldsf=1, ldd=n - 1, out=out) == BAD_LD

@@ -214,7 +214,13 @@ __device__ __forceinline__ bool fp16_scales(uint32_t c) {
 // order, in which 32 K have one scale.  Chunk c of row r sits at chunk c ^
 // (r / 2 % 8): the 16 rows of a read fall on all 64 banks; rows of X are 16
 // bytes longer than a multiple of 512 for the same reason.  R - 1 steps are
-// in flight ahead of the one being multiplied, across blocks.
+// requested ahead of the one being multiplied, across blocks.  Two things
+// shorten that: once a turn of the ring the compiler waits for all but the
+// newest one or two steps, and with C a block's end waits for C's elements and
+// so for every step requested before them (131072 x 8192 for four rows, fp32 C
+// and D: 100.6 us against 95.7 without C, of which 0.4 are C's bytes; all
+// elements requested before the first is used made the compiler wait in calls
+// without C too, 120.7).
 //
 // SC: groups of 32 with K % 256 == 0 (0) or not (1), of 64 (2), of 128 (3) or
 // wider (4): a step's eight, eight, four, two codes or one of a row.
@@ -534,7 +540,11 @@ inline int64_t gemv_pass(int64_t M, int64_t N, int splits) {
 // of its rows: 131072 x 8192 for four rows 100 us with eight waves, 113 with
 // one), else the fewest (one wave needs no join and no barrier: 4096 x 14336
 // for 16 rows, ranges of 2048, 13.2 us against 14.9 with two and 16.3 with
-// eight).
+// eight).  The count is of CUs, one workgroup each, also where two share a CU:
+// they share its loads, and with 512 workgroups in the count the choice was
+// slower in most calls it changed (one row of 8192 x 4096 6.1 against 6.8 us,
+// of 12288 x 4096 7.9 against 8.5, of 20480 x 512 4.3 against 6.0; 28672 x 2048
+// 9.3 against 8.8).
 inline GemvPlan plan_ranges(int64_t M, int64_t N, int64_t K, int64_t ks) {
     GemvPlan g;
     g.staged = true;
