@@ -376,3 +376,30 @@ def test_every_row_end(kind, base):
         assert (np.abs(f64(dw) - wdw) <= (1 + 1 + 64 + 2) * ref.U * adw).all()
         big[1:6, 2:n + 2] = 7
         assert (big == 7).all()
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_codes_off_the_64_bit_result_lie_on_its_borders(kind):
+    """Where rmsnorm_mxfp8's code is not that of the 64-bit y, y lies within fp32's error of the border between the
+    two codes; a scale differs only where the block's maximum lies as near to 448 steps of it.  The same bits every
+    call."""
+    rows, n = 2048, 4096
+    x, r = rows_of(50, rows, n, kind), rows_of(51, rows, n, kind)
+    w = rows_of(52, 1, n, kind)[0].contiguous()
+    q, sf, h, rstd = tg.rmsnorm_mxfp8(x, w, EPS, residual=r)
+    for _ in range(3):
+        for a, b in zip((q, sf, h, rstd), tg.rmsnorm_mxfp8(x, w, EPS, residual=r)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    y, _ = ref.norm(f64(h), f64(w), EPS)
+    slack = ref.rstd_bound(n) + 2 * ref.U               # relative: rstd's error and the products' two roundings
+    want, code = ref.quantize(y)
+    same = u8(sf) == code
+    top = np.abs(y).reshape(rows, -1, 32).max(axis=2)[~same]
+    border = 448 * np.ldexp(1.0, np.minimum(u8(sf), code).astype(np.int64)[~same] - 127)
+    assert (np.abs(top - border) <= slack * top).all()
+    got = ref.e4m3(u8(q))
+    off = (got != want) & np.repeat(same, 32, axis=1)
+    v = (y / np.repeat(np.ldexp(1.0, code.astype(np.int64) - 127), 32, axis=1))[off]
+    # (slack of v beside the border, which is at most (1 + slack) |v|)
+    assert (np.abs(v - (got[off] + want[off]) / 2) <= slack * np.abs(v)).all()
+    assert off.sum() < off.size // 100 and (~same).sum() < same.size // 100
