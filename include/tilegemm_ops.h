@@ -69,8 +69,9 @@ gemm_status mxfp8_quantize(int64_t rows, int64_t N, const void *X, int64_t ldx, 
  *   rstd: `rows` floats, or NULL
  *   eps: finite, >= 0 (GEMM_ERR_UNSUPPORTED otherwise)
  * A row with a NaN gives NaN.  One with an infinity, or whose sum of squares
- * exceeds fp32, has rstd 0: NaN at its infinities, zeros elsewhere.  rows or N
- * == 0: nothing is enqueued.
+ * exceeds fp32, has rstd 0: NaN at its infinities, zeros elsewhere.  With eps 0
+ * a row of zeros, or whose sum of squares is below fp32, has an infinite rstd:
+ * NaN at its zeros, infinities elsewhere.  rows or N == 0: nothing is enqueued.
  */
 gemm_status rmsnorm(int64_t rows, int64_t N, const void *X, int64_t ldx, const void *R, int64_t ldr,
                     int type, const void *W, int w_type, float eps, void *H, int64_t ldh,

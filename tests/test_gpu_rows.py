@@ -403,3 +403,20 @@ def test_codes_off_the_64_bit_result_lie_on_its_borders(kind):
     # (slack of v beside the border, which is at most (1 + slack) |v|)
     assert (np.abs(v - (got[off] + want[off]) / 2) <= slack * np.abs(v)).all()
     assert off.sum() < off.size // 100 and (~same).sum() < same.size // 100
+
+
+def test_rows_without_a_norm():
+    """eps 0: a row of zeros and one whose squares are below fp32; with any eps: one whose squares are past it."""
+    x = torch.zeros(4, 96, device=DEV)
+    x[1, ::2] = -2.0 ** -100
+    x[2], x[3] = 2.0 ** 80, 1.0
+    w = torch.full((96,), 2.0, device=DEV)
+    y, _, rstd = tg.rmsnorm(x, w, 0.0)
+    assert torch.isinf(rstd[:2]).all() and rstd[2] == 0 and rstd[3] == 1
+    assert torch.isnan(y[0]).all() and torch.isnan(y[1, 1::2]).all() and (y[1, ::2] == -float("inf")).all()
+    assert (y[2] == 0).all() and (y[3] == 2).all()
+    q, _, _, _ = tg.rmsnorm_mxfp8(x, w, 0.0)
+    v = ref.e4m3(u8(q))
+    assert np.isnan(v[:2]).all() and (v[2] == 0).all() and (v[3] != 0).all()
+    y, _, _ = tg.rmsnorm(x, w, EPS)
+    assert (y[0] == 0).all() and (y[2] == 0).all() and torch.isfinite(y).all()
