@@ -17,9 +17,11 @@
 // T = 8 is bound by the MFMAs and the instructions issued between them: 14336
 // x 4096 x 16384 1.40 ms, 1375 TFLOP/s (8192^3 in bf16 on the plain product's
 // kernels: 1494); 4096 x 4096 x 4100 with fp32 C 128 us, of which about 30 are
-// the epilogue's C and D, all tiles being of one round.  T = 4 is bound by LDS
-// (64 KiB of fragment reads for 512 cycles of MFMAs a K tile and workgroup) and
-// in small grids by the ranges' sums: 1024 x 992 x 8200 28 us.
+// the epilogue's C and D, all tiles being of one round.  T = 4 is bound by what
+// its waves wait for: small grids put one workgroup, a wave a SIMD, on most
+// CUs.  1024 x 992 x 8200 28 us, 25.6 of them here, in which the MFMAs are busy
+// for 33 % of the cycles and LDS for 35 %; 31 % of a wave's time goes to waits
+// for loads, LDS and barriers, 22 % to instructions that cannot issue yet.
 //
 // Tiles past the last full round of workgroups (all of them, in a small grid)
 // may be cut along K into `splits` ranges, whose fp32 partial tiles go to the

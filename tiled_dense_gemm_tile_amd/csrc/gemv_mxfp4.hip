@@ -539,8 +539,8 @@ inline int64_t gemv_pass(int64_t M, int64_t N, int splits) {
 // waves that have four steps of a block each (together they read longer runs
 // of its rows: 131072 x 8192 for four rows 100 us with eight waves, 113 with
 // one), else the fewest (one wave needs no join and no barrier: 4096 x 14336
-// for 16 rows, ranges of 2048, 13.2 us against 14.9 with two and 16.3 with
-// eight).  The count is of CUs, one workgroup each, also where two share a CU:
+// for 16 rows, eight ranges of 1792, 12.4 us against 14.1 with two and 15.9
+// with eight).  The count is of CUs, one workgroup each, also where two share a CU:
 // they share its loads, and with 512 workgroups in the count the choice was
 // slower in most calls it changed (one row of 8192 x 4096 6.1 against 6.8 us,
 // of 12288 x 4096 7.9 against 8.5, of 20480 x 512 4.3 against 6.0; 28672 x 2048

@@ -56,7 +56,7 @@ WgradPlan plan_wgrad(int64_t M, int64_t N, int64_t K, bool rows16, bool workspac
         // 256 x 256 tiles for grids of over 144 of them (136: 88 us against 80
         // with 128 x 128; 168: 89 against 98) and where fewer, cut, leave a
         // workgroup a long sum (1536 x 1536 x 16384 77 against 89 us); else
-        // four times as many of 128 x 128, two workgroups a CU, with half the
+        // four times as many of 128 x 128, up to two workgroups a CU, with half the
         // partial sums (1024 x 992 x 8200 31 against 38, 2048 x 2048 x 4096
         // 45 against 49)
         if (N >= 256 && (t256 > 144 || (t256 < kCus / 2 && K / (kCus / t256) >= 1536)))
