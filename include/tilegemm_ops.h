@@ -59,8 +59,9 @@ gemm_status mxfp8_quantize(int64_t rows, int64_t N, const void *X, int64_t ldx, 
  * rmsnorm -- root-mean-square norm of each row, after the residual's addition:
  *     h = x + r  (rounded to `type`; h = x without R)
  *     rstd = 1 / sqrt(sum_n h[n]^2 / N + eps)       y[n] = h[n] * w[n] * rstd
- * with sums and products in fp32 and y rounded once.  y is the norm of the
- * rounded h, the row that the next layer and rmsnorm_backward read.
+ * with the sum and rstd in fp64, products in fp32 (by the rounded rstd) and y
+ * rounded once.  y is the norm of the rounded h, the row that the next layer and
+ * rmsnorm_backward read.
  *   X, R (NULL: no residual), H, Y: rows x N of `type`, ldx, ldr, ldh, ldy >= N
  *   W: N elements of w_type, which is `type` or GEMM_TYPE_F32
  *     (GEMM_ERR_UNSUPPORTED otherwise)
@@ -70,8 +71,8 @@ gemm_status mxfp8_quantize(int64_t rows, int64_t N, const void *X, int64_t ldx, 
  *   eps: finite, >= 0 (GEMM_ERR_UNSUPPORTED otherwise)
  * A row with a NaN gives NaN.  One with an infinity, or whose sum of squares
  * exceeds fp32, has rstd 0: NaN at its infinities, zeros elsewhere.  With eps 0
- * a row of zeros, or whose sum of squares is below fp32, has an infinite rstd:
- * NaN at its zeros, infinities elsewhere.  rows or N == 0: nothing is enqueued.
+ * a row of zeros has an infinite rstd and gives NaN.  rows or N == 0: nothing is
+ * enqueued.
  */
 gemm_status rmsnorm(int64_t rows, int64_t N, const void *X, int64_t ldx, const void *R, int64_t ldr,
                     int type, const void *W, int w_type, float eps, void *H, int64_t ldh,
@@ -79,7 +80,8 @@ gemm_status rmsnorm(int64_t rows, int64_t N, const void *X, int64_t ldx, const v
 
 /*
  * rmsnorm_mxfp8 -- rmsnorm with y given out as block-scaled rows (quantised
- * from the fp32 y, without a rounding to `type` between): the A and SFA of
+ * from y as it is before any rounding: codes and scales that the roundings of
+ * fp32 could change are taken in fp64): the A and SFA of
  * gemm_mxfp8, and the 8-bit copy that gemm_wgrad_mxfp8 reads in the backward
  * pass.  N a multiple of 32.  Everything else as rmsnorm.
  */

@@ -379,44 +379,76 @@ def test_every_row_end(kind, base):
 
 
 @pytest.mark.parametrize("kind", TYPES)
-def test_codes_off_the_64_bit_result_lie_on_its_borders(kind):
-    """Where rmsnorm_mxfp8's code is not that of the 64-bit y, y lies within fp32's error of the border between the
-    two codes; a scale differs only where the block's maximum lies as near to 448 steps of it.  The same bits every
-    call."""
-    rows, n = 2048, 4096
+@pytest.mark.parametrize("case", [(2048, 4096), (5000, 96), (3001, 512), (4097, 1024), (1500, 2304), (700, 8192),
+                                  (500, 14336), (301, 40032)], ids=str)
+def test_codes_of_the_norm_are_those_of_the_64_bit_result(kind, case):
+    """rmsnorm_mxfp8 takes what fp32's roundings could change in 64 bits: codes and scales equal those of the 64-bit
+    y, whose own error of 2^-45 lies a million times nearer to a border than any of these values.  The same bits
+    every call."""
+    rows, n = case
     x, r = rows_of(50, rows, n, kind), rows_of(51, rows, n, kind)
-    w = rows_of(52, 1, n, kind)[0].contiguous()
+    w = rows_of(52, 1, n, kind if n % 3 else "f32")[0].contiguous()
     q, sf, h, rstd = tg.rmsnorm_mxfp8(x, w, EPS, residual=r)
     for _ in range(3):
         for a, b in zip((q, sf, h, rstd), tg.rmsnorm_mxfp8(x, w, EPS, residual=r)):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
-    y, _ = ref.norm(f64(h), f64(w), EPS)
-    slack = ref.rstd_bound(n) + 2 * ref.U               # relative: rstd's error and the products' two roundings
+    y, rs = ref.norm(f64(h), f64(w), EPS)
     want, code = ref.quantize(y)
-    same = u8(sf) == code
-    top = np.abs(y).reshape(rows, -1, 32).max(axis=2)[~same]
-    border = 448 * np.ldexp(1.0, np.minimum(u8(sf), code).astype(np.int64)[~same] - 127)
-    assert (np.abs(top - border) <= slack * top).all()
-    got = ref.e4m3(u8(q))
-    off = (got != want) & np.repeat(same, 32, axis=1)
-    v = (y / np.repeat(np.ldexp(1.0, code.astype(np.int64) - 127), 32, axis=1))[off]
-    # (slack of v beside the border, which is at most (1 + slack) |v|)
-    assert (np.abs(v - (got[off] + want[off]) / 2) <= slack * np.abs(v)).all()
-    assert off.sum() < off.size // 100 and (~same).sum() < same.size // 100
+    assert np.array_equal(u8(sf), code) and np.array_equal(ref.e4m3(u8(q)), want)
+    assert (np.abs(f64(rstd) - rs) <= ref.U * rs).all()
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("h", [1.0, 0.25])
+def test_norm_codes_on_and_beside_the_borders(kind, h):
+    """Rows of one magnitude and eps 0: y is +-w itself.  Weights in the middle of two neighbouring codes (to even),
+    and one fp32 step to either side; block maxima at 448 steps of a scale and beside it."""
+    codes = np.arange(0, 127)
+    mid = (ref.e4m3(codes[:-1].astype(np.uint8)) + ref.e4m3(codes[1:].astype(np.uint8))) / 2
+    rng = np.random.default_rng(53)
+    rows = []
+    for k in range(40):
+        b = rng.permutation(mid)[:31 * 4].reshape(4, 31)
+        b = np.concatenate((b, np.full((4, 1), 448.0)), axis=1)
+        rows.append((b * 2.0 ** rng.integers(-30, 30)).reshape(-1))
+    w = np.concatenate(rows).astype(np.float32)
+    step = rng.integers(-1, 2, w.shape)
+    w = np.where(step > 0, np.nextafter(w, np.float32(np.inf)), np.where(step < 0, np.nextafter(w, np.float32(0)), w))
+    n = w.size
+    sign = rng.choice([-1.0, 1.0], size=(3, n))
+    x = torch.from_numpy(sign * h).to(DEV).to(TYPES[kind])
+    q, sf, _, rstd = tg.rmsnorm_mxfp8(x, torch.from_numpy(w).to(DEV), 0.0)
+    assert (rstd == 1 / h).all()
+    want, code = ref.quantize(sign * w.astype(np.float64))
+    assert np.array_equal(u8(sf), code) and np.array_equal(ref.e4m3(u8(q)), want)
 
 
 def test_rows_without_a_norm():
-    """eps 0: a row of zeros and one whose squares are below fp32; with any eps: one whose squares are past it."""
+    """eps 0: a row of zeros, one of small values; with any eps: one whose sum of squares is past fp32."""
     x = torch.zeros(4, 96, device=DEV)
     x[1, ::2] = -2.0 ** -100
     x[2], x[3] = 2.0 ** 80, 1.0
     w = torch.full((96,), 2.0, device=DEV)
     y, _, rstd = tg.rmsnorm(x, w, 0.0)
-    assert torch.isinf(rstd[:2]).all() and rstd[2] == 0 and rstd[3] == 1
-    assert torch.isnan(y[0]).all() and torch.isnan(y[1, 1::2]).all() and (y[1, ::2] == -float("inf")).all()
-    assert (y[2] == 0).all() and (y[3] == 2).all()
-    q, _, _, _ = tg.rmsnorm_mxfp8(x, w, 0.0)
-    v = ref.e4m3(u8(q))
-    assert np.isnan(v[:2]).all() and (v[2] == 0).all() and (v[3] != 0).all()
+    assert torch.isinf(rstd[0]) and rstd[2] == 0 and rstd[3] == 1
+    assert torch.isnan(y[0]).all() and (y[1, 1::2] == 0).all() and (y[2] == 0).all() and (y[3] == 2).all()
+    assert (np.abs(f64(y[1, ::2]) + 8 ** 0.5) <= 3 * ref.U * 8 ** 0.5).all()
+    q, sf, _, _ = tg.rmsnorm_mxfp8(x, w, 0.0)
+    v = ref.dequant(u8(q), u8(sf))
+    assert np.isnan(v[0]).all() and (v[2] == 0).all() and (v[3] == 2).all()
+    assert (np.abs(v[1, ::2] + 8 ** 0.5) <= 2.0 ** -4 * 8 ** 0.5).all() and (v[1, 1::2] == 0).all()
     y, _, _ = tg.rmsnorm(x, w, EPS)
     assert (y[0] == 0).all() and (y[2] == 0).all() and torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_norm_codes_beside_weights_that_are_not_finite(kind):
+    """NaN codes at them, and block scales as if they were zero."""
+    x = rows_of(54, 5, 256, kind)
+    w = rows_of(55, 1, 256, "f32")[0].contiguous()
+    w[3], w[40], w[200] = float("inf"), float("nan"), -float("inf")
+    q, sf, h, _ = tg.rmsnorm_mxfp8(x, w, EPS)
+    y, _ = ref.norm(f64(h), f64(w), EPS)
+    want, code = ref.quantize(y)
+    assert np.array_equal(u8(sf), code) and np.array_equal(ref.e4m3(u8(q)), want, equal_nan=True)
+    assert np.isnan(want).sum() == 15

@@ -3,10 +3,14 @@
 //
 // One pass: a row's elements stay in registers between the sum of squares
 // and the output, so every element is read and written once and the bound is
-// the HBM rate.  Sums and products are fp32; h is rounded to the row type
-// before the sum because that stored h is what the backward pass and the next
-// layer read; y is formed as (h * w) * rstd -- for 16-bit h and w the first
-// product is exact -- and rounded once.  16384 x 4096 bf16 with residual to
+// the HBM rate.  h is rounded to the row type before the sum because that
+// stored h is what the backward pass and the next layer read.  The sum and
+// rstd are fp64; y is formed in fp32 as (h * w) * rstd -- for 16-bit h and w
+// the first product is exact -- and rounded once.  Codes of block-scaled rows
+// are those of the y before any rounding: one code that fp32 tips over a
+// border is off by up to an eighth of its value, and some thirty of 16384 x
+// 4096 were, for 0.3 us where rows are few (256 x 4096 3.5 against 3.7 us) and
+// nothing where they are many.  16384 x 4096 bf16 with residual to
 // block-scaled rows 82 us (5.8 TB/s), one row 2.7 us (an empty launch: 1.6);
 // 16384 x 14336 bf16 quantised 125 us (5.7 TB/s).
 #include <math.h>
@@ -26,9 +30,98 @@ struct NormArgs {
     int64_t ldx, ldr, ldh, ldy, ldsf;
     int64_t rows, row0;                                // row0: the launch's first row
     int N;
-    float eps;
+    double eps, inv_n;
     bool w_f32;
 };
+
+// 1 / sqrt(ss / N + eps) to about 2^-46: the hardware's estimate and a Newton
+// step.  A sum past fp32 gives 0.
+__device__ __forceinline__ double row_rstd(const NormArgs &p, double ss) {
+    const double x = __builtin_fma(ss, p.inv_n, p.eps);
+    if (ss > 0x1.fffffep127) return 0.0;
+    const double r = __builtin_amdgcn_rsq(x);
+    return x > 0.0 ? __builtin_fma(0.5 * r, __builtin_fma(-x * r, r, 1.0), r) : r;
+}
+
+// VE elements of a normed row as block-scaled ones.  In fp32 y is off by 3 of
+// its half steps of 2^-24 (rstd and two products rounded), so codes and scales
+// that 8 of them up or down do not change are those of the exact y.  Where
+// they do -- in one wave of some 200 -- the wave takes them from y in 64 bits,
+// which also settles blocks with an infinity.
+template <int T>
+__device__ __forceinline__ void norm_mx_store(const typename RowVec<T>::V &h, const float (&w)[kVE<T>], double rstd,
+                                              uint8_t *q, uint8_t *sf, int c) {
+    constexpr int VE = kVE<T>;
+    constexpr float UP = 1.0f + 0x1p-21f, DOWN = 1.0f - 0x1p-21f;
+    const float rstd32 = (float)rstd;
+    float y[VE], m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+        y[i] = Elem<T>::up(h[i]) * w[i] * rstd32;
+        m = __builtin_fmaxf(m, __builtin_fabsf(y[i]));
+    }
+    auto join = [](auto &v, auto other) __attribute__((always_inline)) { v = v > other ? v : other; };
+    uint32_t mb = __builtin_bit_cast(uint32_t, m);
+    join(mb, dpp<kXor1>(mb));
+    join(mb, dpp<kXor2>(mb));
+    if constexpr (VE == 4) join(mb, dpp<kMirror8>(mb));
+    m = __builtin_bit_cast(float, mb);
+    uint32_t code = mx_code(__builtin_bit_cast(uint32_t, m * UP));
+    const float inv = mx_inverse(code);
+    struct __attribute__((packed, aligned(1))) Words {
+        uint32_t w[VE / 4];
+    } out;
+    bool near = code != mx_code(__builtin_bit_cast(uint32_t, m * DOWN)) || !(m < __builtin_inff());
+#pragma unroll
+    for (int i = 0; i < VE; i += 4) {
+        uint32_t o[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float by = inv * (k ? DOWN : UP);
+            int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[i] * by, y[i + 1] * by, 0, false);
+            o[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[i + 2] * by, y[i + 3] * by, v, true);
+        }
+        out.w[i / 4] = o[0];
+        near = near || o[0] != o[1];
+    }
+    if (__any(near)) {
+        // (h anew: 64-bit forms kept from the sum of squares on would not fit the registers)
+        u32x4 hb = __builtin_bit_cast(u32x4, h);
+        asm volatile("" : "+v"(hb));
+        const typename RowVec<T>::V hv = __builtin_bit_cast(typename RowVec<T>::V, hb);
+        auto exact = [&](int i) __attribute__((always_inline)) { return (double)Elem<T>::up(hv[i]) * (double)w[i] * rstd; };
+        double top = 0.0;
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+            const double a = __builtin_fabs(exact(i));
+            if (a < 0x1.ffffffp127) join(top, a);     // (what fp32 holds; no NaN)
+        }
+        join(top, dpp64<kXor1>(top));
+        join(top, dpp64<kXor2>(top));
+        if constexpr (VE == 4) join(top, dpp64<kMirror8>(top));
+        // mx_code of a double: the exponent field is e + 8 + 1023
+        const uint32_t f = (uint32_t)((__builtin_bit_cast(uint64_t, top) + ((1ull << 50) - 1)) >> 52);
+        code = f > 904u ? f - 904u : 0u;
+        const double by = __builtin_bit_cast(double, (uint64_t)(1150u - code) << 52);
+        float v[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+            // (cut to 24 bits with the last one telling of what was cut, which
+            // the rounding to a code then sees)
+            const double d = exact(i);
+            uint64_t b = __builtin_bit_cast(uint64_t, d * by);
+            b = (b & ~0x1fffffffull) | ((b & 0x1fffffffull) ? 1ull << 29 : 0);
+            v[i] = __builtin_fabs(d) < 0x1.ffffffp127 ? (float)__builtin_bit_cast(double, b) : __builtin_nanf("");
+        }
+#pragma unroll
+        for (int i = 0; i < VE; i += 4) {
+            int o = __builtin_amdgcn_cvt_pk_fp8_f32(v[i], v[i + 1], 0, false);
+            out.w[i / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[i + 2], v[i + 3], o, true);
+        }
+    }
+    *(Words *)(q + c) = out;
+    if (c % 32 == 0) sf[c / 32] = (uint8_t)code;
+}
 
 // TPR threads per row (64 or 128: four or two rows per workgroup of 256; 256
 // or 1024: the workgroup), VPT vectors of 16 bytes per thread: N <= TPR * VPT *
@@ -50,62 +143,61 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_kernel(NormArgs
     for (int i = 0; i < VPT; ++i) {
         const int c = (i * TPR + t) * VE;
         h[i] = typename RV::V{};
-        if (in && c < N) h[i] = RV::load_raw(x, c, N);
+        if (in && c < N) h[i] = MX ? RV::load_whole(x, c) : RV::load_raw(x, c, N);
     }
     if (p.R) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (i * TPR + t) * VE;
             if (in && c < N) {
-                const typename RV::V v = RV::load_raw(r, c, N);
+                const typename RV::V v = MX ? RV::load_whole(r, c) : RV::load_raw(r, c, N);
 #pragma unroll
                 for (int u = 0; u < VE; ++u)
                     h[i][u] = Elem<T>::down(Elem<T>::up(h[i][u]) + Elem<T>::up(v[u]));
             }
         }
     }
+    if constexpr (!MX) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = (i * TPR + t) * VE;
-        if (c < N) h[i] = RV::settle(h[i], c, N);
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (i * TPR + t) * VE;
+            if (c < N) h[i] = RV::settle(h[i], c, N);
+        }
     }
-    float ss = 0.0f;
+    double ss = 0.0;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        float s = 0.0f;
+    for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int u = 0; u < VE; ++u) {
-            const float f = Elem<T>::up(h[i][u]);
-            s = fmaf(f, f, s);
+            const double f = (double)Elem<T>::up(h[i][u]);
+            ss = __builtin_fma(f, f, ss);
         }
-        ss += s;
-    }
-    ss = wave_sum(ss);
+    ss = wave_sum64(ss);
     if constexpr (TPR > 64) {
-        __shared__ float part[RPB][TPR / 64];
+        __shared__ double part[RPB][TPR / 64];
         if ((t & 63) == 0) part[threadIdx.x / TPR][t >> 6] = ss;
         __syncthreads();
-        ss = 0.0f;
+        ss = 0.0;
 #pragma unroll
         for (int w = 0; w < TPR / 64; ++w) ss += part[threadIdx.x / TPR][w];
     }
-    const float rstd = 1.0f / sqrtf(ss / (float)N + p.eps);
-    if (in && p.rstd && t == 0) p.rstd[row] = rstd;
+    const double rstd = row_rstd(p, ss);
+    if (in && p.rstd && t == 0) p.rstd[row] = (float)rstd;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (i * TPR + t) * VE;
         if (in && c < N) {
-            if (p.H) RV::store((typename RV::S *)p.H + row * p.ldh, c, N, h[i]);
-            float w[VE], y[VE];
-            load_weights<T>(p.W, p.w_f32, c, N, w);
-#pragma unroll
-            for (int u = 0; u < VE; ++u) y[u] = Elem<T>::up(h[i][u]) * w[u] * rstd;
+            float w[VE];
             if constexpr (MX) {
-                mx_store<VE>(y, (uint8_t *)p.Y + row * p.ldy, p.SF + row * p.ldsf, c);
+                if (p.H) RV::store_whole((typename RV::S *)p.H + row * p.ldh, c, h[i]);
+                load_weights<T, true>(p.W, p.w_f32, c, N, w);
+                norm_mx_store<T>(h[i], w, rstd, (uint8_t *)p.Y + row * p.ldy, p.SF + row * p.ldsf, c);
             } else {
+                if (p.H) RV::store((typename RV::S *)p.H + row * p.ldh, c, N, h[i]);
+                load_weights<T>(p.W, p.w_f32, c, N, w);
                 typename RV::V o;
 #pragma unroll
-                for (int u = 0; u < VE; ++u) o[u] = Elem<T>::down(y[u]);
+                for (int u = 0; u < VE; ++u) o[u] = Elem<T>::down(Elem<T>::up(h[i][u]) * w[u] * (float)rstd);
                 RV::store((typename RV::S *)p.Y + row * p.ldy, c, N, o);
             }
         }
@@ -131,39 +223,35 @@ __device__ __forceinline__ void rmsnorm_long_row(const NormArgs &p, int64_t row)
         }
         return h;
     };
-    float ss = 0.0f;
+    double ss = 0.0;
     for (int64_t c = (int64_t)t * VE; c < N; c += 1024 * VE) {
         const typename RV::V h = sum_at(c);
-        float s = 0.0f;
 #pragma unroll
         for (int u = 0; u < VE; ++u) {
-            const float f = Elem<T>::up(h[u]);
-            s = fmaf(f, f, s);
+            const double f = (double)Elem<T>::up(h[u]);
+            ss = __builtin_fma(f, f, ss);
         }
-        ss += s;
         if (p.H) RV::store(hs, (int)c, N, h);
     }
-    __shared__ float part[16];
-    ss = wave_sum(ss);
+    __shared__ double part[16];
+    ss = wave_sum64(ss);
     if ((t & 63) == 0) part[t >> 6] = ss;
     __syncthreads();
-    ss = 0.0f;
+    ss = 0.0;
 #pragma unroll
     for (int w = 0; w < 16; ++w) ss += part[w];
-    const float rstd = 1.0f / sqrtf(ss / (float)N + p.eps);
-    if (p.rstd && t == 0) p.rstd[row] = rstd;
+    const double rstd = row_rstd(p, ss);
+    if (p.rstd && t == 0) p.rstd[row] = (float)rstd;
     for (int64_t c = (int64_t)t * VE; c < N; c += 1024 * VE) {
         const typename RV::V h = p.H ? RV::load(hs, (int)c, N) : sum_at(c);   // this thread's own stores
-        float w[VE], y[VE];
+        float w[VE];
         load_weights<T>(p.W, p.w_f32, (int)c, N, w);
-#pragma unroll
-        for (int u = 0; u < VE; ++u) y[u] = Elem<T>::up(h[u]) * w[u] * rstd;
         if constexpr (MX) {
-            mx_store<VE>(y, (uint8_t *)p.Y + row * p.ldy, p.SF + row * p.ldsf, (int)c);
+            norm_mx_store<T>(h, w, rstd, (uint8_t *)p.Y + row * p.ldy, p.SF + row * p.ldsf, (int)c);
         } else {
             typename RV::V o;
 #pragma unroll
-            for (int u = 0; u < VE; ++u) o[u] = Elem<T>::down(y[u]);
+            for (int u = 0; u < VE; ++u) o[u] = Elem<T>::down(Elem<T>::up(h[u]) * w[u] * (float)rstd);
             RV::store((typename RV::S *)p.Y + row * p.ldy, (int)c, N, o);
         }
     }
@@ -274,6 +362,7 @@ gemm_status run_norm(bool mx, int64_t rows, int64_t N, const void *X, int64_t ld
     p.rows = rows;
     p.N = (int)N;
     p.eps = eps;
+    p.inv_n = 1.0 / (double)N;
     p.w_f32 = w_type == GEMM_TYPE_F32;
     hipError_t e;
     switch (type) {

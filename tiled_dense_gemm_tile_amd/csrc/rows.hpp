@@ -67,6 +67,9 @@ struct RowVec {
     static __device__ __forceinline__ V load(const void *row, int c, int n) {
         return settle(load_raw(row, c, n), c, n);
     }
+    // (of rows of whole vectors)
+    static __device__ __forceinline__ V load_whole(const void *row, int c) { return ((const U *)((const S *)row + c))->v; }
+    static __device__ __forceinline__ void store_whole(void *row, int c, V v) { ((U *)((S *)row + c))->v = v; }
     // element i + by in the place of element i, zeros on top
     static __device__ __forceinline__ V down(V v, int by) {
         typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
@@ -109,21 +112,21 @@ struct RowVec {
     }
 };
 
-// VE weights as fp32: of the row's type, or fp32.
-template <int T>
+// VE weights as fp32: of the row's type, or fp32 (WHOLE: rows of whole vectors).
+template <int T, bool WHOLE = false>
 __device__ __forceinline__ void load_weights(const void *w, bool w_f32, int c, int n, float (&out)[kVE<T>]) {
     if constexpr (T != 0) {
         if (w_f32) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const f32x4 v = RowVec<0>::load(w, c + 4 * h, n);
+                const f32x4 v = WHOLE ? RowVec<0>::load_whole(w, c + 4 * h) : RowVec<0>::load(w, c + 4 * h, n);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) out[4 * h + i] = v[i];
             }
             return;
         }
     }
-    const auto v = RowVec<T>::load(w, c, n);
+    const auto v = WHOLE ? RowVec<T>::load_whole(w, c) : RowVec<T>::load(w, c, n);
 #pragma unroll
     for (int i = 0; i < kVE<T>; ++i) out[i] = Elem<T>::up(v[i]);
 }
@@ -144,6 +147,30 @@ __device__ __forceinline__ float wave_sum(float v) {
     v += __builtin_bit_cast(float, dpp<kMirror16>(__builtin_bit_cast(uint32_t, v)));
     v += __shfl_xor(v, 16);
     v += __shfl_xor(v, 32);
+    return v;
+}
+
+// 64-bit values of another lane: any, and one at the other end of an exchange
+// inside 16 lanes.
+__device__ __forceinline__ double shfl_xor64(double v, int by) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __shfl_xor((uint32_t)u, by), hi = __shfl_xor((uint32_t)(u >> 32), by);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, ((uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32) | dpp<CTRL>((uint32_t)u));
+}
+
+// As wave_sum, of 64-bit values.
+__device__ __forceinline__ double wave_sum64(double v) {
+    v += dpp64<kXor1>(v);
+    v += dpp64<kXor2>(v);
+    v += dpp64<kMirror8>(v);
+    v += dpp64<kMirror16>(v);
+    v += shfl_xor64(v, 16);
+    v += shfl_xor64(v, 32);
     return v;
 }
 
