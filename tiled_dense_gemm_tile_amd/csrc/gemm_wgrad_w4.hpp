@@ -19,7 +19,7 @@
 // kernels: 1494); 4096 x 4096 x 4100 with fp32 C 128 us, of which about 30 are
 // the epilogue's C and D, all tiles being of one round.  T = 4 is bound by what
 // its waves wait for: small grids put one workgroup, a wave a SIMD, on most
-// CUs.  1024 x 992 x 8200 28 us, 25.6 of them here, in which the MFMAs are busy
+// CUs.  1024 x 992 x 8200 28 us, 25 of them here, in which the MFMAs are busy
 // for 33 % of the cycles and LDS for 35 %; 31 % of a wave's time goes to waits
 // for loads, LDS and barriers, 22 % to instructions that cannot issue yet.
 //
