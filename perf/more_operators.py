@@ -201,8 +201,9 @@ def _glubwd(s):
 
 def _quant(s):
     x = s["x"].float()
-    scale = (x.abs().amax(1) / 127).clamp_min(2.0 ** -126)
-    # (in 64 bits: the nearest of two codes is a matter of the last bit at a border)
+    # (in 64 bits: the nearest of two codes is a matter of the last bit at a border, and torch divides fp32 by a
+    # plain number as a product with its rounded inverse)
+    scale = (x.abs().amax(1).double() / 127).float().clamp_min(2.0 ** -126)
     return torch.round(x.double() / scale.double()[:, None]).to(torch.int8), scale
 
 
