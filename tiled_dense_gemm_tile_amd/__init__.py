@@ -15,8 +15,10 @@ Tensor conventions (same as the C ABI):
 
 The operators around the block-scaled products (``include/tilegemm_ops.h``:
 ``mxfp8_quantize``, ``rmsnorm``, ``rmsnorm_mxfp8``, ``rmsnorm_backward``,
-``gemm_wgrad_mxfp8``, ``gemv_mxfp4``) are bound in :mod:`.ops` and exported
-here.
+``gemm_wgrad_mxfp8``, ``gemv_mxfp4``) are bound in :mod:`.ops`, those of a
+feed-forward layer's linear parts (``include/tilegemm_layers.h``: ``gemm_glu``,
+``gemm_glu_backward``, ``int8_quantize``, ``gemm_int8``, ``grad_norm``,
+``clip_grads``) in :mod:`.layers`, and all exported here.
 """
 from __future__ import annotations
 
@@ -27,7 +29,9 @@ import threading
 __all__ = ["gemm_bf16", "gemm_fp16", "gemm_bf16_splitk", "gemm_fp16_splitk", "splitk_workspace_bytes",
            "gemm_mxfp8", "gemm_mxfp4", "gemm_mxfp6", "gemm_mxfp8_splitk", "gemm_mxfp4_splitk", "gemm_mxfp6_splitk", "raw", "GemmError", "LibraryMissing",
            "library_path", "STATUS", "mxfp8_quantize", "rmsnorm", "rmsnorm_mxfp8", "rmsnorm_backward",
-           "rmsnorm_backward_workspace_bytes", "gemm_wgrad_mxfp8", "gemm_wgrad_mxfp8_workspace_bytes", "gemv_mxfp4", "gemv_mxfp4_workspace_bytes"]
+           "rmsnorm_backward_workspace_bytes", "gemm_wgrad_mxfp8", "gemm_wgrad_mxfp8_workspace_bytes", "gemv_mxfp4", "gemv_mxfp4_workspace_bytes",
+           "gemm_glu", "gemm_glu_backward", "gemm_glu_backward_workspace_bytes", "int8_quantize", "gemm_int8",
+           "grad_norm", "clip_grads", "grad_workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libtilegemm.so")
@@ -129,6 +133,7 @@ def _load():
             L.gemm_last_hip_error.restype = ci
             L.gemm_last_hip_error.argtypes = []
             _declare_ops(L)
+            _declare_layers(L)
             _lib = L
     return _lib
 
@@ -152,6 +157,26 @@ def _declare_ops(L):
     L.gemm_wgrad_mxfp8_workspace_bytes.argtypes = [i64, i64, i64]
     L.gemv_mxfp4_workspace_bytes.restype = sz
     L.gemv_mxfp4_workspace_bytes.argtypes = [i64, i64, i64]
+
+
+def _declare_layers(L):
+    """Signatures of include/tilegemm_layers.h."""
+    i64, vp, ci, sz, f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+    m = [vp, i64]                                      # a matrix and its leading dimension
+    size = [i64, i64, i64]
+    for name, args in (
+            ("gemm_glu", size + m * 3 + [ci, ci] + m * 3 + [vp]),
+            ("gemm_glu_backward", size + m * 6 + [ci, ci] + m * 5 + [ci, vp, sz, vp]),
+            ("int8_quantize", [i64, i64] + m + [ci] + m + [vp, vp]),
+            ("gemm_int8", size + (m + [vp]) * 2 + m * 2 + [ci, vp]),
+            ("grad_norm", [i64, vp, vp, vp, vp, vp, sz, vp]),
+            ("grad_clip", [i64, vp, vp, vp, vp, f32, vp, vp, vp, sz, vp])):
+        f = getattr(L, name)
+        f.restype, f.argtypes = ci, args
+    L.gemm_glu_backward_workspace_bytes.restype = sz
+    L.gemm_glu_backward_workspace_bytes.argtypes = size
+    L.grad_workspace_bytes.restype = sz
+    L.grad_workspace_bytes.argtypes = [i64]
 
 
 class _Raw:
@@ -687,14 +712,19 @@ def gemm_mxfp6_splitk(A, SFA, B, SFB, C=None, out_dtype=None, D=None, fmt="e2m3"
     return _mx6("gemm_mxfp6_splitk", A, SFA, B, SFB, C, out_dtype, D, fmt, (splits, workspace))
 
 
-# The functions of ops.py, which needs torch at import, load with their first use.
+# The functions of ops.py and layers.py, which need torch at import, load with their first use.
 _OPS = ("mxfp8_quantize", "rmsnorm", "rmsnorm_mxfp8", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes",
         "gemm_wgrad_mxfp8", "gemm_wgrad_mxfp8_workspace_bytes", "gemv_mxfp4", "gemv_mxfp4_workspace_bytes")
+_LAYERS = ("gemm_glu", "gemm_glu_backward", "gemm_glu_backward_workspace_bytes", "int8_quantize", "gemm_int8",
+           "grad_norm", "clip_grads", "grad_workspace_bytes")
 
 
 def __getattr__(name):
-    if name not in _OPS:
+    if name in _OPS:
+        from . import ops as where
+    elif name in _LAYERS:
+        from . import layers as where
+    else:
         raise AttributeError("module %r has no attribute %r" % (__name__, name))
-    from . import ops
-    f = globals()[name] = getattr(ops, name)
+    f = globals()[name] = getattr(where, name)
     return f

@@ -1,0 +1,43 @@
+// C ABI of gemm_glu (include/tilegemm_layers.h): checks and launch.
+#include "prod_api.hpp"
+
+using namespace tg_api;
+
+extern "C" gemm_status gemm_glu(int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx, const void *Wg,
+                                int64_t ldwg, const void *Wu, int64_t ldwu, int type, int act, void *H, int64_t ldh,
+                                void *G, int64_t ldg, void *U, int64_t ldu, hipStream_t stream) {
+    if (M < 0 || F < 0 || K < 0) return GEMM_ERR_INVALID_SIZE;
+    if (M >= kMaxDim || F >= kMaxDim || K >= kMaxDim || !type16(type) || !known_act(act)) return GEMM_ERR_UNSUPPORTED;
+    if (M == 0 || F == 0) return GEMM_OK;
+    if (ldx < K || ldwg < K || ldwu < K || ldh < F || (G && ldg < F) || (U && ldu < F)) return GEMM_ERR_BAD_LD;
+    if (!H || (K > 0 && (!X || !Wg || !Wu))) return GEMM_ERR_NULL_POINTER;
+    if (misaligned(X, 2) || misaligned(Wg, 2) || misaligned(Wu, 2) || misaligned(H, 2) || misaligned(G, 2) ||
+        misaligned(U, 2))
+        return GEMM_ERR_MISALIGNED;
+    for (int64_t ld : {ldx, ldwg, ldwu, ldh, G ? ldg : 0, U ? ldu : 0})
+        if (ld * 2 >= kMaxLdBytes) return GEMM_ERR_UNSUPPORTED;
+    struct Out {
+        void *p;
+        int64_t ld;
+    } out[3] = {{H, ldh}, {G, ldg}, {U, ldu}};
+    for (int i = 0; i < 3; ++i) {
+        const int64_t b = matrix_bytes(M, F, out[i].ld, 2);
+        if (K > 0 && (overlap(out[i].p, b, X, matrix_bytes(M, K, ldx, 2)) ||
+                      overlap(out[i].p, b, Wg, matrix_bytes(F, K, ldwg, 2)) ||
+                      overlap(out[i].p, b, Wu, matrix_bytes(F, K, ldwu, 2))))
+            return GEMM_ERR_UNSUPPORTED;
+    }
+    if ((G && G == H) || (U && U == H) || (G && G == U)) return GEMM_ERR_UNSUPPORTED;
+    tg::ProdArgs p = {};
+    p.A = X;
+    p.B = Wg;
+    p.B1 = Wu;
+    p.lda = ldx * 2;
+    p.ldb = ldwg * 2;
+    p.ldb1 = ldwu * 2;
+    p.M = (int)M;
+    p.N = (int)F;
+    p.KB = (int)(K * 2);
+    if (type == GEMM_TYPE_BF16) return launched(tg::launch_glu<1>(p, {H, G, U, ldh, ldg, ldu, act}, stream));
+    return launched(tg::launch_glu<2>(p, {H, G, U, ldh, ldg, ldu, act}, stream));
+}

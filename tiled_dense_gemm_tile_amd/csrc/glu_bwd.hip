@@ -1,0 +1,286 @@
+// gemm_glu_backward (include/tilegemm_layers.h): checks, the kernel that makes
+// the products' operands, launches.
+//
+// Three of the backward pass's four products sum along rows of what they are
+// given (dg^T X over tokens, dg Wg over features), so their operands would be
+// read across K.  One kernel lays all of them along K in the workspace, rows
+// padded to whole K tiles with zeros: dg | du next to each other as M rows (A
+// of the input gradient) and transposed as 2 F' rows (A of the weight
+// gradients), X and Wg | Wu transposed.  Both products then run the aligned
+// kernels, whatever the caller's sizes and strides, and the activation's
+// derivative is computed once.  F' is F in whole tiles of 64, M' likewise.
+#include "prod_api.hpp"
+
+using namespace tg_api;
+
+namespace tg {
+
+constexpr int kCopyTile = 64;
+
+struct GluBwdArgs {
+    const void *dH, *G, *U, *X, *Wg, *Wu;
+    int64_t lddh, ldg, ldu, ldx, ldwg, ldwu;
+    uint16_t *dgu, *dgut, *xt, *wt;                    // (dgu, wt NULL: no input gradient; dgut, xt NULL: no weights')
+    int M, F, K, Fp, Mp, act;
+    int tm, tf, tk;                                    // tiles of 64 along M, F, K
+};
+
+// 64 x 64 elements in LDS, rows of 64 plus two: a column's reads by 64 lanes
+// (8 rows apart, eight columns) fall on distinct banks but for pairs.
+constexpr int kCopyPitch = kCopyTile + 2;
+
+// A thread's 8 elements of a row (tile row r, elements c ..) into LDS.
+__device__ __forceinline__ void tile_put(uint16_t *lds, int r, int c, const uint16_t (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) *(uint32_t *)(lds + r * kCopyPitch + c + i) = v[i] | (uint32_t)v[i + 1] << 16;
+}
+// 8 rows' elements of column c, from row r on, as 16 bytes.
+__device__ __forceinline__ u32x4 tile_column(const uint16_t *lds, int r, int c) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = lds[(r + 2 * i) * kCopyPitch + c] | (uint32_t)lds[(r + 2 * i + 1) * kCopyPitch + c] << 16;
+    return v;
+}
+
+template <int T>
+__global__ void __launch_bounds__(256) glu_bwd_operands_kernel(GluBwdArgs p) {
+    typedef RowVec<T> R;
+    __shared__ __attribute__((aligned(16))) uint16_t lds[2][kCopyTile * kCopyPitch];
+    const int tid = threadIdx.x;
+    const int r0 = tid >> 3, c = (tid & 7) * 8;        // rows r0 and r0 + 32, elements c .. c + 7
+    int w = blockIdx.x;
+    // dg and du of 64 rows and 64 features
+    const int n_act = p.tm * p.tf;
+    if (w < n_act) {
+        const int m0 = w / p.tf * kCopyTile, f0 = w % p.tf * kCopyTile;
+        with_act(p.act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int m = m0 + r0 + 32 * h, f = f0 + c;
+                uint16_t dg[8] = {}, du[8] = {};
+                if (m < p.M && f < p.F) {
+                    const typename R::V dh = R::load((const uint16_t *)p.dH + m * p.lddh, f, p.F);
+                    const typename R::V g = R::load((const uint16_t *)p.G + m * p.ldg, f, p.F);
+                    const typename R::V u = R::load((const uint16_t *)p.U + m * p.ldu, f, p.F);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float value, slope;
+                        const float d = Elem<T>::up(dh[i]);
+                        act_both<decltype(a)::value>(Elem<T>::up(g[i]), value, slope);
+                        if (f + i < p.F) {
+                            dg[i] = __builtin_bit_cast(uint16_t, Elem<T>::down(d * Elem<T>::up(u[i]) * slope));
+                            du[i] = __builtin_bit_cast(uint16_t, Elem<T>::down(d * value));
+                        }
+                    }
+                }
+                if (p.dgu && m < p.M) {
+                    uint16_t *row = p.dgu + (int64_t)m * 2 * p.Fp;
+                    *(u32x4 *)(row + f) = __builtin_bit_cast(u32x4, dg);
+                    *(u32x4 *)(row + p.Fp + f) = __builtin_bit_cast(u32x4, du);
+                }
+                tile_put(lds[0], r0 + 32 * h, c, dg);
+                tile_put(lds[1], r0 + 32 * h, c, du);
+            }
+        });
+        if (!p.dgut) return;
+        __syncthreads();
+        // feature f's tokens m0 + 8 k ..: 512 pieces of 16 bytes each
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int f = r0 + 32 * h, m = c;
+            *(u32x4 *)(p.dgut + (int64_t)(f0 + f) * p.Mp + m0 + m) = tile_column(lds[0], m, f);
+            *(u32x4 *)(p.dgut + (int64_t)(p.Fp + f0 + f) * p.Mp + m0 + m) = tile_column(lds[1], m, f);
+        }
+        return;
+    }
+    // a transposed copy: `rows` x K elements into K rows
+    w -= n_act;
+    const uint16_t *src;
+    uint16_t *dst;
+    int64_t lds_, ldd;
+    int rows;
+    const int n_x = p.xt ? p.tm * p.tk : 0;
+    if (w < n_x) {
+        src = (const uint16_t *)p.X, lds_ = p.ldx, rows = p.M, dst = p.xt, ldd = p.Mp;
+    } else {
+        w -= n_x;
+        const int n_w = p.tf * p.tk;
+        const bool up = w >= n_w;
+        if (up) w -= n_w;
+        src = (const uint16_t *)(up ? p.Wu : p.Wg), lds_ = up ? p.ldwu : p.ldwg, rows = p.F;
+        dst = p.wt + (up ? p.Fp : 0), ldd = 2 * (int64_t)p.Fp;
+    }
+    const int a0 = w / p.tk * kCopyTile, k0 = w % p.tk * kCopyTile;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = a0 + r0 + 32 * h, k = k0 + c;
+        typename R::V v = {};
+        if (r < rows && k < p.K) v = R::load(src + r * lds_, k, p.K);
+        const u32x4 e = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *(uint32_t *)(lds[0] + (r0 + 32 * h) * kCopyPitch + c + 2 * i) = e[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int k = r0 + 32 * h, r = c;
+        if (k0 + k < p.K) *(u32x4 *)(dst + (int64_t)(k0 + k) * ldd + a0 + r) = tile_column(lds[0], r, k);
+    }
+}
+
+}  // namespace tg
+
+namespace {
+
+int64_t padded(int64_t n) { return (n + tg::kCopyTile - 1) / tg::kCopyTile * tg::kCopyTile; }
+int64_t part(int64_t elements) { return (elements * 2 + 255) / 256 * 256; }
+
+template <int T, int OT>
+gemm_status weight_products(const tg::GluBwdArgs &a, const tg::PlainEpi<OT> &e, hipStream_t s) {
+    tg::ProdArgs p = {};
+    p.A = a.dgut;
+    p.B = a.xt;
+    p.lda = p.ldb = (int64_t)a.Mp * 2;
+    p.M = 2 * a.Fp;
+    p.N = a.K;
+    p.KB = a.Mp * 2;
+    return launched(tg::launch_plain<T, OT>(p, e, s));
+}
+
+template <int T>
+gemm_status run(const tg::GluBwdArgs &a, void *dX, int64_t lddx, const void *Cg, int64_t ldcg, const void *Cu,
+                int64_t ldcu, void *dWg, int64_t lddwg, void *dWu, int64_t lddwu, bool f32, hipStream_t s) {
+    const int64_t n_act = (int64_t)a.tm * a.tf, n_x = a.xt ? (int64_t)a.tm * a.tk : 0,
+                  n_w = a.wt ? 2 * (int64_t)a.tf * a.tk : 0;
+    const int64_t grid = n_act + n_x + n_w;
+    if (grid > 0) {
+        hipLaunchKernelGGL(tg::glu_bwd_operands_kernel<T>, dim3((unsigned)grid), dim3(256), 0, s, a);
+        gemm_status st = launched(hipGetLastError());
+        if (st != GEMM_OK) return st;
+    }
+    if (dX && a.M > 0) {
+        tg::ProdArgs p = {};
+        p.A = a.dgu;
+        p.B = a.wt;
+        p.lda = p.ldb = (int64_t)a.Fp * 4;
+        p.M = a.M;
+        p.N = a.K;
+        p.KB = a.Fp * 4;
+        gemm_status st = launched(tg::launch_plain<T, T>(
+            p, {{nullptr, nullptr}, {dX, nullptr}, {0, 0}, {lddx, 0}, 0x7fffffff, a.M}, s));
+        if (st != GEMM_OK) return st;
+    }
+    if (!dWg) return GEMM_OK;
+    if (f32)
+        return weight_products<T, 0>(a, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F}, s);
+    return weight_products<T, T>(a, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F}, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gemm_glu_backward_workspace_bytes(int64_t M, int64_t F, int64_t K) {
+    if (M < 0 || F <= 0 || K <= 0 || M >= (int64_t)1 << 21 || F >= (int64_t)1 << 20 || K >= kMaxDim) return 0;
+    const int64_t Fp = padded(F), Mp = padded(M);
+    return (size_t)(part(M * 2 * Fp) + part(2 * Fp * Mp) + part(K * Mp) + part(K * 2 * Fp));
+}
+
+gemm_status gemm_glu_backward(int64_t M, int64_t F, int64_t K, const void *dH, int64_t lddh, const void *G,
+                              int64_t ldg, const void *U, int64_t ldu, const void *X, int64_t ldx, const void *Wg,
+                              int64_t ldwg, const void *Wu, int64_t ldwu, int type, int act, void *dX, int64_t lddx,
+                              const void *Cg, int64_t ldcg, const void *Cu, int64_t ldcu, void *dWg, int64_t lddwg,
+                              void *dWu, int64_t lddwu, int grad_type, void *workspace, size_t workspace_bytes,
+                              hipStream_t stream) {
+    if (M < 0 || F < 0 || K < 0) return GEMM_ERR_INVALID_SIZE;
+    if (M >= (int64_t)1 << 21 || F >= (int64_t)1 << 20 || K >= kMaxDim || !type16(type) || !known_act(act) ||
+        (grad_type != type && grad_type != GEMM_TYPE_F32))
+        return GEMM_ERR_UNSUPPORTED;
+    if ((dWg != nullptr) != (dWu != nullptr) || (Cg != nullptr) != (Cu != nullptr) || (Cg && !dWg))
+        return GEMM_ERR_NULL_POINTER;
+    const bool dx = dX && M > 0, dw = dWg && F > 0;
+    if (K == 0 || (!dx && !dw)) return GEMM_OK;
+    const int gs = elem_size(grad_type);
+    if (M > 0 && F > 0 && (lddh < F || ldg < F || ldu < F)) return GEMM_ERR_BAD_LD;
+    if ((dx && (lddx < K || (F > 0 && (ldwg < K || ldwu < K)))) ||
+        (dw && ((M > 0 && ldx < K) || lddwg < K || lddwu < K || (Cg && (ldcg < K || ldcu < K)))))
+        return GEMM_ERR_BAD_LD;
+    if (M > 0 && F > 0 && (!dH || !G || !U || (dx && (!Wg || !Wu)) || (dw && !X))) return GEMM_ERR_NULL_POINTER;
+    for (const void *q : {dH, G, U, X, Wg, Wu, (const void *)dX})
+        if (misaligned(q, 2)) return GEMM_ERR_MISALIGNED;
+    for (const void *q : {Cg, Cu, (const void *)dWg, (const void *)dWu})
+        if (misaligned(q, gs)) return GEMM_ERR_MISALIGNED;
+    for (int64_t ld : {lddh, ldg, ldu, dw ? ldx : 0, dx ? ldwg : 0, dx ? ldwu : 0, dx ? lddx : 0})
+        if (ld * 2 >= kMaxLdBytes) return GEMM_ERR_UNSUPPORTED;
+    for (int64_t ld : {dw ? lddwg : 0, dw ? lddwu : 0, Cg ? ldcg : 0, Cg ? ldcu : 0})
+        if (ld * gs >= kMaxLdBytes) return GEMM_ERR_UNSUPPORTED;
+    // (K is a row of the weights, so below 8 MiB too)
+    const int64_t mf = M > 0 && F > 0;
+    struct Piece {
+        const void *p;
+        int64_t bytes;
+    };
+    const Piece in[] = {{dH, mf ? matrix_bytes(M, F, lddh, 2) : 0}, {G, mf ? matrix_bytes(M, F, ldg, 2) : 0},
+                        {U, mf ? matrix_bytes(M, F, ldu, 2) : 0},   {dw && M > 0 ? X : nullptr, matrix_bytes(M, K, ldx, 2)},
+                        {dx && F > 0 ? Wg : nullptr, matrix_bytes(F, K, ldwg, 2)},
+                        {dx && F > 0 ? Wu : nullptr, matrix_bytes(F, K, ldwu, 2)}};
+    const Piece out[] = {{dx ? dX : nullptr, matrix_bytes(M, K, lddx, 2)},
+                         {dw ? dWg : nullptr, matrix_bytes(F, K, lddwg, gs)},
+                         {dw ? dWu : nullptr, matrix_bytes(F, K, lddwu, gs)}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Piece &q : in)
+            if (q.bytes > 0 && overlap(out[i].p, out[i].bytes, q.p, q.bytes)) return GEMM_ERR_UNSUPPORTED;
+        for (int j = 0; j < i; ++j)
+            // (the halves of one tensor may lie row by row next to each other)
+            if (out[i].p == out[j].p && out[i].p) return GEMM_ERR_UNSUPPORTED;
+    }
+    const Piece c[] = {{dw ? Cg : nullptr, matrix_bytes(F, K, ldcg, gs)}, {dw ? Cu : nullptr, matrix_bytes(F, K, ldcu, gs)}};
+    if (dw && ((Cg == dWg && Cg && ldcg != lddwg) || (Cu == dWu && Cu && ldcu != lddwu) || (Cg && (Cg == dWu || Cu == dWg))))
+        return GEMM_ERR_UNSUPPORTED;
+    for (int i = 0; i < 2; ++i)
+        if ((c[i].p != out[1 + i].p && overlap(c[i].p, c[i].bytes, out[1 + i].p, out[1 + i].bytes)) ||
+            overlap(c[i].p, c[i].bytes, out[0].p, out[0].bytes))
+            return GEMM_ERR_UNSUPPORTED;
+    if (F == 0) {                                      // (a product without a sum: zeros)
+        tg::GluBwdArgs a = {};
+        a.M = (int)M;
+        a.K = (int)K;
+        return type == GEMM_TYPE_BF16 ? run<1>(a, dX, lddx, 0, 0, 0, 0, 0, 0, 0, 0, false, stream)
+                                      : run<2>(a, dX, lddx, 0, 0, 0, 0, 0, 0, 0, 0, false, stream);
+    }
+    if (!workspace || workspace_bytes < gemm_glu_backward_workspace_bytes(M, F, K)) return GEMM_ERR_WORKSPACE;
+    if ((uintptr_t)workspace % 256 != 0) return GEMM_ERR_MISALIGNED;
+    tg::GluBwdArgs a = {};
+    a.M = (int)M;
+    a.F = (int)F;
+    a.K = (int)K;
+    a.Fp = (int)padded(F);
+    a.Mp = (int)padded(M);
+    a.act = act;
+    a.tm = a.Mp / tg::kCopyTile;
+    a.tf = a.Fp / tg::kCopyTile;
+    a.tk = (int)(padded(K) / tg::kCopyTile);
+    a.dH = dH, a.lddh = lddh;
+    a.G = G, a.ldg = ldg;
+    a.U = U, a.ldu = ldu;
+    a.X = X, a.ldx = ldx;
+    a.Wg = Wg, a.ldwg = ldwg;
+    a.Wu = Wu, a.ldwu = ldwu;
+    if (((int64_t)a.tm * a.tf + (int64_t)(a.tm + 2 * a.tf) * a.tk) >= (int64_t)1 << 24) return GEMM_ERR_UNSUPPORTED;
+    char *ws = (char *)workspace;
+    if (dx) a.dgu = (uint16_t *)ws;
+    ws += part(M * 2 * a.Fp);
+    if (dw) a.dgut = (uint16_t *)ws;
+    ws += part(2 * (int64_t)a.Fp * a.Mp);
+    if (dw) a.xt = (uint16_t *)ws;
+    ws += part(K * a.Mp);
+    if (dx) a.wt = (uint16_t *)ws;
+    if (type == GEMM_TYPE_BF16)
+        return run<1>(a, dx ? dX : nullptr, lddx, Cg, ldcg, Cu, ldcu, dw ? dWg : nullptr, lddwg, dWu, lddwu,
+                      grad_type == GEMM_TYPE_F32, stream);
+    return run<2>(a, dx ? dX : nullptr, lddx, Cg, ldcg, Cu, ldcu, dw ? dWg : nullptr, lddwg, dWu, lddwu,
+                  grad_type == GEMM_TYPE_F32, stream);
+}
+
+}  // extern "C"

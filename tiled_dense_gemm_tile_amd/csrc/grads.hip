@@ -1,0 +1,273 @@
+// grad_norm and grad_clip (include/tilegemm_layers.h): the sum of all
+// gradients' squares, and their scaling.
+//
+// Bound by memory: one read for the sum, one read and write for the scaling,
+// and by the launches where gradients are few.  A launch takes up to 128
+// tensors in its arguments (so that nothing is copied to the GPU and a captured
+// graph holds what it needs), cut into chunks of 8192 elements that a fixed
+// number of workgroups walks; each keeps its sum in fp64 and writes one partial
+// sum.  The scaling's workgroups add the partial sums for themselves, which
+// costs less than a launch between the two, and walk the chunks from the last
+// to the first: the last ones read are still in the caches.
+#include "rows_api.hpp"
+#include "rows.hpp"
+
+#include "../../include/tilegemm_layers.h"
+
+using namespace tg_api;
+
+namespace tg {
+
+constexpr int kGradTable = 128, kGradChunk = 8192, kGradGroups = 2048;
+
+struct GradTable {
+    const void *src[kGradTable];
+    void *dst[kGradTable];
+    int64_t n[kGradTable];
+    uint32_t first[kGradTable + 1];                    // first chunk of each tensor; [count]: all chunks
+    uint8_t type[kGradTable];
+    int count;
+};
+static_assert(sizeof(GradTable) <= 3800, "kernel arguments");
+
+// The tensor whose chunk c is.
+__device__ __forceinline__ int grad_tensor(const GradTable &t, uint32_t c) {
+    int lo = 0, hi = t.count;                          // first[lo] <= c < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (t.first[mid] <= c) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// f(vector, where, end) for each 16-byte vector of a chunk that is this
+// thread's: a whole chunk's loads are all in flight at once, a tensor's last
+// chunk goes vector by vector.
+template <int T, class F>
+__device__ __forceinline__ void grad_vectors(const void *src, int64_t begin, int64_t n, F &&f) {
+    typedef RowVec<T> R;
+    const typename R::S *p = (const typename R::S *)src + begin;
+    constexpr int VE = R::VE, NV = kGradChunk / 256 / VE;
+    if (n - begin >= kGradChunk) {
+        typename R::V v[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) v[k] = R::load_whole(p, (k * 256 + (int)threadIdx.x) * VE);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) f(v[k], (k * 256 + (int)threadIdx.x) * VE, kGradChunk);
+    } else {
+        const int len = (int)(n - begin);
+#pragma unroll 1
+        for (int c = (int)threadIdx.x * VE; c < len; c += 256 * VE) f(R::load_each(p, c, len), c, len);
+    }
+}
+
+__device__ __forceinline__ double group_sum(double v, double *lds) {
+    v = wave_sum64(v);
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return lds[0] + lds[1] + lds[2] + lds[3];
+}
+
+__global__ void __launch_bounds__(256) grad_squares_kernel(GradTable t, double *part) {
+    __shared__ double lds[4];
+    double s = 0.0;
+    const uint32_t chunks = t.first[t.count];
+    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int i = __builtin_amdgcn_readfirstlane(grad_tensor(t, c));
+        const int64_t begin = (int64_t)(c - t.first[i]) * kGradChunk;
+        auto add = [&](auto type) __attribute__((always_inline)) {
+            constexpr int T = decltype(type)::value;
+            grad_vectors<T>(t.src[i], begin, t.n[i], [&](auto v, int, int) __attribute__((always_inline)) {
+#pragma unroll
+                for (int k = 0; k < kVE<T>; ++k) {
+                    const double d = (double)Elem<T>::up(v[k]);
+                    s += d * d;
+                }
+            });
+        };
+        switch (t.type[i]) {
+        case 0: add(std::integral_constant<int, 0>()); break;
+        case 1: add(std::integral_constant<int, 1>()); break;
+        default: add(std::integral_constant<int, 2>()); break;
+        }
+    }
+    s = group_sum(s, lds);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+// The norm from the partial sums, by one workgroup.
+__device__ __forceinline__ float grad_total(const double *part, int parts, double *lds) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < parts; i += 256) s += part[i];
+    return (float)sqrt(group_sum(s, lds));
+}
+
+__global__ void __launch_bounds__(256) grad_norm_kernel(const double *part, int parts, float *norm) {
+    __shared__ double lds[4];
+    const float v = grad_total(part, parts, lds);
+    if (threadIdx.x == 0) *norm = v;
+}
+
+__global__ void __launch_bounds__(256) grad_scale_kernel(GradTable t, const double *part, int parts,
+                                                         const float *given, float max_norm, float *norm) {
+    __shared__ double lds[4];
+    const float v = given ? *given : grad_total(part, parts, lds);
+    if (norm && norm != given && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+    float by = max_norm / (v + 1e-6f);
+    by = by > 1.0f ? 1.0f : by;                        // (a NaN stays one)
+    const uint32_t chunks = t.first[t.count];
+    for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+        const uint32_t c = chunks - 1 - k;
+        const int i = __builtin_amdgcn_readfirstlane(grad_tensor(t, c));
+        if (by == 1.0f && t.src[i] == t.dst[i]) continue;
+        const int64_t begin = (int64_t)(c - t.first[i]) * kGradChunk;
+        auto scale = [&](auto type) __attribute__((always_inline)) {
+            constexpr int T = decltype(type)::value;
+            typedef RowVec<T> R;
+            typename R::S *to = (typename R::S *)t.dst[i] + begin;
+            grad_vectors<T>(t.src[i], begin, t.n[i], [&](auto x, int at, int len) __attribute__((always_inline)) {
+                typename R::V o;
+#pragma unroll
+                for (int j = 0; j < kVE<T>; ++j) o[j] = Elem<T>::down(Elem<T>::up(x[j]) * by);
+                R::store(to, at, len, o);
+            });
+        };
+        switch (t.type[i]) {
+        case 0: scale(std::integral_constant<int, 0>()); break;
+        case 1: scale(std::integral_constant<int, 1>()); break;
+        default: scale(std::integral_constant<int, 2>()); break;
+        }
+    }
+}
+
+}  // namespace tg
+
+namespace {
+
+constexpr int64_t kMostGrads = (int64_t)1 << 20, kMostElements = (int64_t)1 << 40;
+
+gemm_status check_grads(int64_t n, const void *const *src, void *const *dst, const int64_t *sizes, const int *types) {
+    if (n < 0) return GEMM_ERR_INVALID_SIZE;
+    if (n >= kMostGrads) return GEMM_ERR_UNSUPPORTED;
+    if (n > 0 && (!src || !sizes || !types)) return GEMM_ERR_NULL_POINTER;
+    int64_t all = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (sizes[i] < 0) return GEMM_ERR_INVALID_SIZE;
+        if (sizes[i] >= kMostElements || !elem_type(types[i])) return GEMM_ERR_UNSUPPORTED;
+        if (sizes[i] == 0) continue;
+        if (!src[i] || (dst && !dst[i])) return GEMM_ERR_NULL_POINTER;
+        if (misaligned(src[i], elem_size(types[i])) || (dst && misaligned(dst[i], elem_size(types[i]))))
+            return GEMM_ERR_MISALIGNED;
+        all += sizes[i];
+        if (all >= kMostElements) return GEMM_ERR_UNSUPPORTED;
+    }
+    return GEMM_OK;
+}
+
+// Tensors [at, next) in one launch's table; a tensor of more chunks than a
+// launch counts in 32 bits takes none (sizes below 2^40 have 2^27).
+int64_t fill(tg::GradTable &t, int64_t at, int64_t n, const void *const *src, void *const *dst, const int64_t *sizes,
+             const int *types) {
+    t.count = 0;
+    t.first[0] = 0;
+    for (; at < n && t.count < tg::kGradTable; ++at) {
+        if (sizes[at] == 0) continue;
+        const int c = t.count++;
+        t.src[c] = src[at];
+        t.dst[c] = dst ? dst[at] : const_cast<void *>(src[at]);
+        t.n[c] = sizes[at];
+        t.type[c] = (uint8_t)types[at];
+        t.first[c + 1] = t.first[c] + (uint32_t)((sizes[at] + tg::kGradChunk - 1) / tg::kGradChunk);
+    }
+    return at;
+}
+
+unsigned groups(const tg::GradTable &t) {
+    const uint32_t c = t.first[t.count];
+    return c < (uint32_t)tg::kGradGroups ? c : tg::kGradGroups;
+}
+
+// Partial sums of all tensors; *parts: how many.
+gemm_status squares(int64_t n, const void *const *src, const int64_t *sizes, const int *types, double *part,
+                    int *parts, hipStream_t s) {
+    tg::GradTable t;
+    *parts = 0;
+    for (int64_t at = 0; at < n;) {
+        at = fill(t, at, n, src, nullptr, sizes, types);
+        if (t.count == 0) break;
+        const unsigned g = groups(t);
+        hipLaunchKernelGGL(tg::grad_squares_kernel, dim3(g), dim3(256), 0, s, t, part + *parts);
+        const gemm_status st = launched(hipGetLastError());
+        if (st != GEMM_OK) return st;
+        *parts += (int)g;
+    }
+    return GEMM_OK;
+}
+
+gemm_status check_room(int64_t n, const void *ws, size_t bytes) {
+    if (!ws || bytes < grad_workspace_bytes(n)) return GEMM_ERR_WORKSPACE;
+    return (uintptr_t)ws % 256 != 0 ? GEMM_ERR_MISALIGNED : GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t grad_workspace_bytes(int64_t n) {
+    if (n < 0 || n >= kMostGrads) return 0;
+    return (size_t)((n + tg::kGradTable - 1) / tg::kGradTable + 1) * tg::kGradGroups * sizeof(double);
+}
+
+gemm_status grad_norm(int64_t n, const void *const *grads, const int64_t *sizes, const int *types, float *norm,
+                      void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    gemm_status st = check_grads(n, grads, nullptr, sizes, types);
+    if (st != GEMM_OK) return st;
+    if (!norm) return GEMM_ERR_NULL_POINTER;
+    if (misaligned(norm, 4)) return GEMM_ERR_MISALIGNED;
+    if ((st = check_room(n, workspace, workspace_bytes)) != GEMM_OK) return st;
+    int parts;
+    if ((st = squares(n, grads, sizes, types, (double *)workspace, &parts, stream)) != GEMM_OK) return st;
+    hipLaunchKernelGGL(tg::grad_norm_kernel, dim3(1), dim3(256), 0, stream, (const double *)workspace, parts, norm);
+    return launched(hipGetLastError());
+}
+
+gemm_status grad_clip(int64_t n, const void *const *grads, void *const *out, const int64_t *sizes, const int *types,
+                      float max_norm, const float *given, float *norm, void *workspace, size_t workspace_bytes,
+                      hipStream_t stream) {
+    gemm_status st = check_grads(n, grads, out, sizes, types);
+    if (st != GEMM_OK) return st;
+    if (!(max_norm >= 0.0f)) return GEMM_ERR_UNSUPPORTED;
+    if (!given && !norm) return GEMM_ERR_NULL_POINTER;
+    if (misaligned(given, 4) || misaligned(norm, 4)) return GEMM_ERR_MISALIGNED;
+    int parts = 0;
+    if (!given) {
+        if ((st = check_room(n, workspace, workspace_bytes)) != GEMM_OK) return st;
+        if ((st = squares(n, grads, sizes, types, (double *)workspace, &parts, stream)) != GEMM_OK) return st;
+    }
+    // the tables again, the last first
+    int64_t starts[kMostGrads / tg::kGradTable + 1];
+    int tables = 0;
+    tg::GradTable t;
+    for (int64_t at = 0; at < n;) {
+        const int64_t next = fill(t, at, n, grads, out, sizes, types);
+        if (t.count == 0) break;
+        starts[tables++] = at;
+        at = next;
+    }
+    if (tables == 0) {                                 // (no elements: the norm alone)
+        t.count = 0;
+        t.first[0] = 0;
+        hipLaunchKernelGGL(tg::grad_scale_kernel, dim3(1), dim3(256), 0, stream, t, (const double *)workspace, parts,
+                           given, max_norm, norm);
+        return launched(hipGetLastError());
+    }
+    for (int k = tables - 1; k >= 0; --k) {
+        fill(t, starts[k], n, grads, out, sizes, types);
+        hipLaunchKernelGGL(tg::grad_scale_kernel, dim3(groups(t)), dim3(256), 0, stream, t, (const double *)workspace,
+                           parts, given, max_norm, k == 0 ? norm : nullptr);
+        if ((st = launched(hipGetLastError())) != GEMM_OK) return st;
+    }
+    return GEMM_OK;
+}
+
+}  // extern "C"

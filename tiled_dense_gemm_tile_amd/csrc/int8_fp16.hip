@@ -1,0 +1,8 @@
+// Products of 8-bit integers, fp16 results.
+#include "prod_api.hpp"
+#include "prod_launch.hpp"
+
+template <>
+hipError_t tg::launch_int8<2>(const ProdArgs &p, const Int8Epi<2> &e, hipStream_t s) {
+    return launch_prod<kI8, false>(p, e, s);
+}

@@ -1,0 +1,149 @@
+// Products in BM x BN tiles of one workgroup of four waves (2 x 2), for grids
+// too small for 256 x 256 tiles and for operands at any alignment.
+//
+// K tiles of 128 bytes; LDS rows of 128 bytes, 16-byte chunk c of row r at
+// chunk c ^ (r & 7) (free of bank conflicts for the 16-row fragment reads).
+//   * Aligned operands (rows on 16 bytes, whole 16-byte chunks): S slots a
+//     K tile, filled by direct global->LDS loads S - 1 tiles ahead; one barrier
+//     a tile, the loads of S - 2 tiles in flight across it.
+//   * ANY: the same chunks through registers (a 16-byte global load serves any
+//     element alignment), a tile ahead; a row's last chunk is assembled from
+//     elements.  Two slots.
+#pragma once
+
+#include "prod.hpp"
+
+namespace tg {
+
+template <int T, int BM, int BN, int S, bool PAIR, bool ANY, class Epi>
+__global__ void __launch_bounds__(256) prod_mid_kernel(ProdArgs p, Epi e) {
+    constexpr int WTM = BM / 2, WTN = BN / 2, TM = WTM / 16, TN = WTN / 16;
+    constexpr int LA = BM / 32, LB = BN / 32;          // load instructions of a wave a tile
+    constexpr int SLOT_A = BM * 128, SLOT_B = BN * 128, B_BASE = S * SLOT_A;
+    constexpr int W = PAIR ? WTN / 2 : WTN;            // result columns of a wave
+    constexpr int RING = S * (SLOT_A + SLOT_B), STAGE = 16 * kStagePitch<W> * 4;
+    static_assert(!ANY || S == 2, "ANY: two slots");
+    static_assert(RING >= 4 * STAGE && RING <= 160 * 1024, "LDS");
+    static_assert((S - 2) * (LA + LB) < 64, "vmcnt");
+
+    __shared__ __attribute__((aligned(1024))) char smem[RING];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    int tmi, tni;
+    tile_order(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
+    const int m0 = tmi * BM, n0 = tni * (PAIR ? BN / 2 : BN);
+    const int KB = p.KB, nt = (KB + 127) / 128;
+
+    // Load instruction j of a wave: A rows 32 j + 8 wave + lane / 8; B the
+    // same, or (PAIR) rows 16 j + 8 (wave % 2) + lane / 8 of the wave's half.
+    // Lane l writes chunk l % 8 and fetches chunk (l % 8) ^ (l / 8).
+    const bool up = PAIR && wave >= 2;
+    const char *A = (const char *)p.A + (int64_t)m0 * p.lda;
+    const int64_t ldb = up ? p.ldb1 : p.ldb;
+    const char *B = (const char *)(up ? p.B1 : p.B) + (int64_t)n0 * ldb;
+    const int arow = 8 * wave + (lane >> 3), brow = PAIR ? 8 * (wave & 1) + (lane >> 3) : arow;
+    constexpr int BSTEP = PAIR ? 16 : 32;
+    const int kc = ((lane & 7) ^ (lane >> 3)) * 16;    // byte of the tile this lane fetches
+
+    const __amdgpu_buffer_rsrc_t rA = make_rsrc(A, span_bytes(p.M - m0, KB, p.lda, 1));
+    const __amdgpu_buffer_rsrc_t rB = make_rsrc(B, span_bytes(p.N - n0, KB, ldb, 1));
+    auto dma = [&](__amdgpu_buffer_rsrc_t r, char *d, uint32_t voff, int soff) __attribute__((always_inline)) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)d, 16, voff, soff, 0, 0);
+    };
+    const uint32_t aoff = (uint32_t)(arow * p.lda) + kc, boff = (uint32_t)(brow * ldb) + kc;
+    // (chunks past K read as zeros from an offset beyond the resource, and so
+    // do all of a tile past the last, which keeps the count of loads in flight)
+    auto fetch = [&](int t, int slot) __attribute__((always_inline)) {
+        const int k0 = t * 128;
+        const bool in = k0 + kc < KB;
+        const uint32_t va = in ? aoff + k0 : kOOB, vb = in ? boff + k0 : kOOB;
+#pragma unroll
+        for (int j = 0; j < LA; ++j)
+            dma(rA, smem + slot * SLOT_A + (4 * j + wave) * 1024, va, (int)(32 * j * p.lda));
+#pragma unroll
+        for (int j = 0; j < LB; ++j)
+            dma(rB, smem + B_BASE + slot * SLOT_B + (4 * j + wave) * 1024, vb, (int)(BSTEP * j * ldb));
+    };
+    u32x4 ra[ANY ? LA : 1], rb[ANY ? LB : 1];
+    auto read_any = [&](int t) __attribute__((always_inline)) {
+        const int kb = t * 128 + kc;
+#pragma unroll
+        for (int j = 0; j < LA; ++j) {
+            ra[j] = u32x4{0u, 0u, 0u, 0u};
+            if (m0 + arow + 32 * j < p.M && kb < KB) ra[j] = load_chunk<T>(A + (int64_t)(arow + 32 * j) * p.lda, kb, KB);
+        }
+#pragma unroll
+        for (int j = 0; j < LB; ++j) {
+            rb[j] = u32x4{0u, 0u, 0u, 0u};
+            if (n0 + brow + BSTEP * j < p.N && kb < KB)
+                rb[j] = load_chunk<T>(B + (int64_t)(brow + BSTEP * j) * ldb, kb, KB);
+        }
+    };
+    auto write_any = [&](int slot) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < LA; ++j) *(u32x4 *)(smem + slot * SLOT_A + (4 * j + wave) * 1024 + lane * 16) = ra[j];
+#pragma unroll
+        for (int j = 0; j < LB; ++j)
+            *(u32x4 *)(smem + B_BASE + slot * SLOT_B + (4 * j + wave) * 1024 + lane * 16) = rb[j];
+    };
+
+    const int fr = lane & 15, fq = lane >> 4;
+    f32x4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto compute = [&](int slot) __attribute__((always_inline)) {
+        const char *sa = smem + slot * SLOT_A + (wm * WTM + fr) * 128;
+        const char *sb = smem + B_BASE + slot * SLOT_B + (wn * WTN + fr) * 128;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            const int c = ((4 * st + fq) ^ swz16(fr)) << 4;
+            u32x4 fa[TM], fb[TN];
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fa[i] = *(const u32x4 *)(sa + i * 16 * 128 + c);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fb[j] = *(const u32x4 *)(sb + j * 16 * 128 + c);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = prod_mfma<T>(fb[j], fa[i], acc[i][j]);
+        }
+    };
+
+    if constexpr (ANY) {
+        if (nt > 0) {
+            read_any(0);
+            write_any(0);
+            wait_lgkmcnt0();
+            barrier();
+        }
+        for (int t = 0; t < nt; ++t) {
+            if (t + 1 < nt) read_any(t + 1);
+            compute(t & 1);
+            if (t + 1 < nt) write_any((t + 1) & 1);    // (read last before the barrier that opened tile t)
+            wait_lgkmcnt0();
+            barrier();
+        }
+    } else if (nt > 0) {
+#pragma unroll
+        for (int t = 0; t < S - 1; ++t) fetch(t, t);
+        int slot = 0, next = S - 1;
+        for (int t = 0; t < nt; ++t) {
+            wait_vmcnt<(S - 2) * (LA + LB)>();         // tile t landed
+            barrier();                                 // for every wave; and tile t - 1's slot is free
+            fetch(t + S - 1, next);
+            compute(slot);
+            wait_lgkmcnt0();
+            next = slot;
+            slot = slot + 1 == S ? 0 : slot + 1;
+        }
+        wait_vmcnt<0>();                               // no load still writes a slot
+        barrier();
+    }
+    e.template block<TM, TN, false>(acc, (float *)(smem + wave * STAGE), lane, m0 + wm * WTM, n0 + wn * W, p.M, p.N);
+}
+
+}  // namespace tg
