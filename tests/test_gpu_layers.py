@@ -415,3 +415,34 @@ def test_norm_does_not_depend_on_addresses():
     grads = some_grads(5, [70000, 33, 8192 * 5 + 1])
     again = [torch.cat([g.new_zeros(3), g])[3:] for g in grads]
     assert torch.equal(tg.grad_norm(grads), tg.grad_norm(again))
+
+
+# ---- grids of 256 x 256 tiles -------------------------------------------------------
+
+# just over half the GPU's workgroups, one round and a ragged second, three rounds; one K tile, an odd and an even number
+BIG = [(2048, 2040, 64), (2050, 2049, 200), (4100, 2300, 72), (4352, 2176, 328), (8000, 3400, 48)]
+
+
+@pytest.mark.parametrize("m,f,k", BIG)
+@pytest.mark.parametrize("dtype", [BF, FP], ids=KIND.get)
+def test_glu_large_grids(m, f, k, dtype):
+    x, wg, wu = rand(1, m, k, dtype=dtype), rand(2, f, k, dtype=dtype, scale=k ** -0.5), rand(3, f, k, dtype=dtype, scale=k ** -0.5)
+    check_glu(x, wg, wu, "silu")
+    out = [padded(torch.zeros(m, f, dtype=dtype, device=DEV), f + 1 + i, 7.0) for i in range(3)]
+    check_glu(x, wg, wu, "relu", H=out[0], G=out[1], U=out[2])
+    for o in out:
+        whole = o.as_strided((m + 1, o.stride(0)), (o.stride(0), 1))
+        assert bool((whole[:, f:] == 7).all()) and bool((whole[m] == 7).all())
+
+
+@pytest.mark.parametrize("m,n,k", [(2048, 4090, 128), (2050, 4098, 400), (4100, 4700, 144), (8000, 7000, 96)])
+@pytest.mark.parametrize("out", [F32, BF, FP], ids=KIND.get)
+def test_int8_large_grids(m, n, k, out):
+    check_int8(m, n, k, out)
+    check_int8(m, n, k, out, "matrix", pads=(16, 32, 3))
+
+
+@pytest.mark.parametrize("m,f,k", [(4000, 300, 3000), (600, 2100, 2100), (257, 4100, 2049)])
+@pytest.mark.parametrize("dtype,grad", [(BF, BF), (BF, F32), (FP, FP)])
+def test_glu_backward_large_grids(m, f, k, dtype, grad):
+    check_backward(m, f, k, dtype, grad=grad, acc=True)

@@ -3,6 +3,7 @@
 
 #include "prod_mid.hpp"
 #include "prod_rows.hpp"
+#include "prod_w4.hpp"
 
 namespace tg {
 
@@ -21,8 +22,19 @@ inline bool prod_aligned(const ProdArgs &p) {
     return p.KB % 16 == 0 && on16(p.A, p.lda, p.M) && on16(p.B, p.ldb, p.N) && (!p.B1 || on16(p.B1, p.ldb1, p.N));
 }
 
+// 256 x 256 tiles: from half a wave of them on.
+template <int T, bool PAIR, class Epi>
+bool launch_prod_w4(ProdArgs p, const Epi &e, hipStream_t s) {
+    const unsigned tiles = prod_tiles(p, 256, PAIR ? 128 : 256), cus = 256;
+    if (tiles < cus / 2 || p.KB == 0) return false;
+    hipLaunchKernelGGL((prod_w4_kernel<T, PAIR, Epi>), dim3(tiles < cus ? tiles : cus), dim3(256), 0, s, p, e);
+    return true;
+}
+
 template <int T, bool PAIR, bool ANY, class Epi>
 hipError_t launch_prod_mid(ProdArgs p, const Epi &e, hipStream_t s) {
+    if constexpr (!ANY)
+        if (launch_prod_w4<T, PAIR>(p, e, s)) return hipGetLastError();
     const int64_t t128 = ((p.M + 127) / 128) * (int64_t)((p.N + (PAIR ? 63 : 127)) / (PAIR ? 64 : 128));
     if (t128 >= 200) {
         const unsigned grid = prod_tiles(p, 128, PAIR ? 64 : 128);

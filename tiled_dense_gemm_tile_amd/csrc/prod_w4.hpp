@@ -1,0 +1,167 @@
+// Products in 256 x 256 tiles (PAIR: 256 rows and 128 gated columns), for
+// grids that fill the GPU: one persistent workgroup per CU of four waves, each
+// with a 128 x 128 quadrant as 8 x 8 blocks of 16 x 16 accumulators in AGPRs.
+//
+// K tiles of 128 bytes in two LDS slots an operand.  A wave issues 128 MFMAs a
+// K tile in two steps of 64 bytes; the second step of tile t - 1 runs after the
+// barrier that opens tile t, so that the matrix pipe does not drain there:
+//   after barrier t:  64 MFMAs of tile t - 1 step 1, between them the fragment
+//                     reads of tile t step 0 and the loads of tile t + 1
+//                     64 MFMAs of tile t step 0, between them the reads of
+//                     tile t step 1
+//                     wait for the loads; barrier t + 1
+// After a tile's last K step the next tile's first loads are issued, into the
+// slots K tile 0 always uses, and then the finished tile's results are staged
+// and stored from the other slots.
+#pragma once
+
+#include "gemm_f16_w4.hpp"                             // mfma_result_fence
+#include "prod.hpp"
+
+namespace tg {
+
+// acc = a.b + acc, or a.b, in place in AGPRs.
+template <int T, bool ZERO>
+__device__ __forceinline__ void prod_mfma_agpr(f32x4 &acc, const u32x4 &a, const u32x4 &b) {
+#define TG_PROD_MFMA(op)                                                                         \
+    if constexpr (ZERO)                                                                          \
+        asm volatile(op " %0, %1, %2, 0" : "=a"(acc) : "v"(a), "v"(b));                          \
+    else                                                                                         \
+        asm volatile(op " %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b))
+    if constexpr (T == kI8) {
+        TG_PROD_MFMA("v_mfma_i32_16x16x64_i8");
+    } else if constexpr (T == 2) {
+        TG_PROD_MFMA("v_mfma_f32_16x16x32_f16");
+    } else {
+        TG_PROD_MFMA("v_mfma_f32_16x16x32_bf16");
+    }
+#undef TG_PROD_MFMA
+}
+
+// (operand rows on 16 bytes, KB > 0 a multiple of 16)
+template <int T, bool PAIR, class Epi>
+__global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
+    constexpr int TM = 8, TN = 8, Q = TM * TN, SLOT = 256 * 128, B_BASE = 2 * SLOT;
+    constexpr int BN = PAIR ? 128 : 256;               // result columns of a tile
+    constexpr int W = BN / 2, STAGE = 16 * kStagePitch<W> * 4;
+    static_assert(2 * STAGE <= SLOT, "staging areas");
+    __shared__ __attribute__((aligned(1024))) char smem[4 * SLOT];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    int vt = blockIdx.x, tmi, tni;
+    tile_order(vt, p.tiles_m * p.tiles_n, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
+    int m0 = tmi * 256, n0 = tni * BN;
+    const int KB = p.KB, nt = (KB + 127) / 128;
+
+    // Load instruction j of a wave: A rows 32 j + 8 wave + lane / 8, B the same
+    // or (PAIR) rows 16 j + 8 (wave % 2) + lane / 8 of the wave's half.  Lane l
+    // writes chunk l % 8 and fetches chunk (l % 8) ^ (l / 8); the K offset goes
+    // with the lane's offset (beyond the resource for a chunk past K, which
+    // then reads as zeros), 32 or 16 rows with the scalar one.
+    const bool up = PAIR && wave >= 2;
+    const int64_t ldb = up ? p.ldb1 : p.ldb;
+    const int kc = ((lane & 7) ^ (lane >> 3)) * 16;
+    const uint32_t aoff = (uint32_t)((8 * wave + (lane >> 3)) * p.lda) + kc;
+    const uint32_t boff = (uint32_t)(((PAIR ? 8 * (wave & 1) : 8 * wave) + (lane >> 3)) * ldb) + kc;
+    const int astep = (int)(32 * p.lda), bstep = (int)((PAIR ? 16 : 32) * ldb);
+    __amdgpu_buffer_rsrc_t rA, rB;
+    auto resources = [&](const ProdArgs &a) __attribute__((always_inline)) {
+        const int64_t lb = up ? a.ldb1 : a.ldb;
+        rA = make_rsrc((const char *)a.A + (int64_t)m0 * a.lda, span_bytes(a.M - m0, a.KB, a.lda, 1));
+        rB = make_rsrc((const char *)(up ? a.B1 : a.B) + (int64_t)n0 * lb, span_bytes(a.N - n0, a.KB, lb, 1));
+    };
+    resources(p);
+    auto dma = [&](__amdgpu_buffer_rsrc_t r, int lds, uint32_t voff, int soff) __attribute__((always_inline)) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(smem + lds), 16, voff,
+                                                 soff, 0, 0);
+    };
+    auto fetch_a = [&](int t, int j) __attribute__((always_inline)) {
+        const uint32_t v = t * 128 + kc < KB ? aoff + t * 128 : kOOB;
+        dma(rA, (t & 1) * SLOT + (4 * j + wave) * 1024, v, j * astep);
+    };
+    auto fetch_b = [&](int t, int j) __attribute__((always_inline)) {
+        const uint32_t v = t * 128 + kc < KB ? boff + t * 128 : kOOB;
+        dma(rB, B_BASE + (t & 1) * SLOT + (4 * j + wave) * 1024, v, j * bstep);
+    };
+
+    const int fr = lane & 15, fq = lane >> 4, fswz = swz16(fr);
+    const int a_read = (wm * 128 + fr) * 128, b_read = B_BASE + (wn * 128 + fr) * 128;
+    f32x4 acc[TM][TN];
+    u32x4 fa[2][TM], fb[2][TN];                        // [step][block]
+    // fragment read k of step st of tile t, in the order the MFMAs use them: A
+    // block 0, B blocks 0 .. 7, A blocks 1 .. 7
+    auto read_frag = [&](int t, int st, int k) __attribute__((always_inline)) {
+        const int c = (t & 1) * SLOT + (((4 * st + fq) ^ fswz) << 4);
+        if (k == 0 || k > TN) {
+            const int i = k == 0 ? 0 : k - TN;
+            fa[st][i] = *(const u32x4 *)(smem + a_read + i * 16 * 128 + c);
+        } else {
+            fb[st][k - 1] = *(const u32x4 *)(smem + b_read + (k - 1) * 16 * 128 + c);
+        }
+    };
+    auto mfma = [&](auto zero, int st, int i, int j) __attribute__((always_inline)) {
+        prod_mfma_agpr<T, decltype(zero)::value>(acc[i][j], fb[st][j], fa[st][i]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // One K tile; FIRST: none before it (accumulators start from zero).
+    auto tile = [&](auto first, int t) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            if constexpr (!decltype(first)::value) mfma(std::false_type(), 1, q / TN, q % TN);
+            if (q % 4 == 0) read_frag(t, 0, q / 4);
+            if (q % 8 == 2) fetch_a(t + 1, q / 8);
+            if (q % 8 == 6) fetch_b(t + 1, q / 8);
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            mfma(first, 0, q / TN, q % TN);
+            if (q % 3 == 0 && q / 3 < TM + TN) read_frag(t, 1, q / 3);
+        }
+        wait_vmcnt<0>();                               // tile t + 1 landed
+        wait_lgkmcnt0();
+        barrier();
+    };
+
+#pragma unroll
+    for (int j = 0; j < 8; ++j) fetch_a(0, j);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) fetch_b(0, j);
+    wait_vmcnt<0>();
+    barrier();
+    float *stage = (float *)(smem + (wave < 2 ? SLOT : B_BASE + SLOT) + (wave & 1) * STAGE);
+    while (true) {
+        tile(std::true_type(), 0);
+        for (int t = 1; t < nt; ++t) tile(std::false_type(), t);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) mfma(std::false_type(), 1, q / TN, q % TN);
+        mfma_result_fence<TM, TN>(acc);
+        // (every wave is past its last barrier, so past all reads of the slots;
+        // the loads of the tile past the end have landed there)
+        const ProdArgs r = kernel_arg0_reloaded<ProdArgs>();
+        const int dm0 = m0, dn0 = n0, ntl = r.tiles_m * r.tiles_n;
+        vt += gridDim.x;
+        const bool more = vt < ntl;
+        if (more) {
+            tile_order(vt, ntl, r.tiles_m, r.tiles_n, r.group_m, tmi, tni);
+            m0 = tmi * 256;
+            n0 = tni * BN;
+            resources(r);
+            int wv = wave;                             // (their LDS addresses are computed here, not held)
+            asm volatile("" : "+s"(wv));
+            const uint32_t va = kc < KB ? aoff : kOOB, vb = kc < KB ? boff : kOOB;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dma(rA, (4 * j + wv) * 1024, va, j * astep);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dma(rB, B_BASE + (4 * j + wv) * 1024, vb, j * bstep);
+        }
+        e.template block<TM, TN, true>(acc, stage, lane, dm0 + wm * 128, dn0 + wn * W, r.M, r.N);
+        if (!more) break;
+        wait_vmcnt<0>();
+        wait_lgkmcnt0();
+        barrier();
+    }
+}
+
+}  // namespace tg
