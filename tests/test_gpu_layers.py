@@ -446,3 +446,29 @@ def test_int8_large_grids(m, n, k, out):
 @pytest.mark.parametrize("dtype,grad", [(BF, BF), (BF, F32), (FP, FP)])
 def test_glu_backward_large_grids(m, f, k, dtype, grad):
     check_backward(m, f, k, dtype, grad=grad, acc=True)
+
+
+# ---- every tile size --------------------------------------------------------------
+
+# (rows, columns) that reach each kernel by the count of tiles: few rows, 32 x 32 / 32 x 64, 64 x 64 in one and two
+# groups, 64 x 128, 128 x 128 in two and one, at even sizes and at odd ones
+TILES = [(9, 13000), (24, 9000), (33, 100), (70, 2000), (100, 4100), (64, 9000), (250, 4000), (500, 4030), (900, 4090), (1100, 6000)]
+
+
+@pytest.mark.parametrize("m,n", TILES)
+@pytest.mark.parametrize("k", [384, 1040, 203])
+def test_int8_tiles(m, n, k):
+    check_int8(m, n, k, BF)
+    check_int8(m, n, k, F32, "matrix", pads=(16 - k % 16, 16 - k % 16, 0))
+
+
+@pytest.mark.parametrize("m,f", [(m, n // 2) for m, n in TILES])
+@pytest.mark.parametrize("k", [72, 520, 203])
+def test_glu_tiles(m, f, k):
+    x, wg, wu = rand(1, m, k), rand(2, f, k, scale=k ** -0.5), rand(3, f, k, scale=k ** -0.5)
+    check_glu(x, wg, wu, "silu")
+
+
+@pytest.mark.parametrize("m,k", [(33, 100), (70, 2000), (100, 4100), (250, 4000), (500, 4030), (900, 4090)])
+def test_glu_backward_tiles(m, k):
+    check_backward(m, 150, k, BF)

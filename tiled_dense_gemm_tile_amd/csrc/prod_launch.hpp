@@ -22,49 +22,89 @@ inline bool prod_aligned(const ProdArgs &p) {
     return p.KB % 16 == 0 && on16(p.A, p.lda, p.M) && on16(p.B, p.ldb, p.N) && (!p.B1 || on16(p.B1, p.ldb1, p.N));
 }
 
-// 256 x 256 tiles: from half a wave of them on.
-template <int T, bool PAIR, class Epi>
-bool launch_prod_w4(ProdArgs p, const Epi &e, hipStream_t s) {
-    const unsigned tiles = prod_tiles(p, 256, PAIR ? 128 : 256), cus = 256;
-    if (tiles < cus / 2 || p.KB == 0) return false;
-    hipLaunchKernelGGL((prod_w4_kernel<T, PAIR, Epi>), dim3(tiles < cus ? tiles : cus), dim3(256), 0, s, p, e);
-    return true;
+inline int64_t tiles_of(const ProdArgs &p, int bm, int bn) {
+    return ((p.M + bm - 1) / bm) * (int64_t)((p.N + bn - 1) / bn);
 }
 
-template <int T, bool PAIR, bool ANY, class Epi>
-hipError_t launch_prod_mid(ProdArgs p, const Epi &e, hipStream_t s) {
-    if constexpr (!ANY)
-        if (launch_prod_w4<T, PAIR>(p, e, s)) return hipGetLastError();
-    const int64_t t128 = ((p.M + 127) / 128) * (int64_t)((p.N + (PAIR ? 63 : 127)) / (PAIR ? 64 : 128));
-    if (t128 >= 200) {
-        const unsigned grid = prod_tiles(p, 128, PAIR ? 64 : 128);
-        hipLaunchKernelGGL((prod_mid_kernel<T, 128, 128, ANY ? 2 : 4, PAIR, ANY, Epi>), dim3(grid), dim3(256), 0, s, p, e);
-    } else {
-        const unsigned grid = prod_tiles(p, 64, PAIR ? 32 : 64);
-        hipLaunchKernelGGL((prod_mid_kernel<T, 64, 64, ANY ? 2 : 4, PAIR, ANY, Epi>), dim3(grid), dim3(256), 0, s, p, e);
-    }
+template <int T, int BM, int BN, int S, int KS, bool PAIR, bool ANY, class Epi>
+hipError_t go_mid(ProdArgs p, const Epi &e, hipStream_t s) {
+    const unsigned grid = prod_tiles(p, BM, PAIR ? BN / 2 : BN);
+    hipLaunchKernelGGL((prod_mid_kernel<T, BM, BN, ANY ? 2 : S, KS, PAIR, ANY, Epi>), dim3(grid), dim3(256 * KS), 0, s, p,
+                       e);
     return hipGetLastError();
+}
+
+template <int T, bool PAIR, class Epi>
+hipError_t go_w4(ProdArgs p, const Epi &e, hipStream_t s) {
+    const unsigned tiles = prod_tiles(p, 256, PAIR ? 128 : 256), cus = 256;
+    hipLaunchKernelGGL((prod_w4_kernel<T, PAIR, Epi>), dim3(tiles < cus ? tiles : cus), dim3(256), 0, s, p, e);
+    return hipGetLastError();
+}
+
+// Tiles by how many of them there are (a K tile's loads bound a workgroup, 31
+// to 44 bytes a clock and CU, until all CUs have work; times in us, weights
+// that no cache holds, int8 M x N x K or the gated block's M x F x K in bf16).
+template <int T, bool PAIR, bool ANY, class Epi>
+hipError_t launch_prod_tiles(const ProdArgs &p, const Epi &e, hipStream_t s) {
+    constexpr int D = PAIR ? 2 : 1;                    // a tile's columns of B for one of the results
+    const int64_t t64 = tiles_of(p, 64, 64 / D), t128 = tiles_of(p, 128, 128 / D);
+    if constexpr (!ANY) {
+        // 256 x 256: one round of up to 256 tiles takes as long as 630 of the
+        // 128 x 128 tiles, of which 512 run at once (gated 512 x 14336 x 4096,
+        // 224 tiles: 88 against 125; 256 x 14336 x 4096, 112: 90 against 66)
+        const int64_t rounds = (tiles_of(p, 256, 256 / D) + 255) / 256;
+        if (t128 > 512 && (rounds == 1 || t128 >= 630 * rounds) && p.KB > 0) return go_w4<T, PAIR>(p, e, s);
+    }
+    // few tiles: small ones, K cut over the waves (int8 64 x 4096 x 14336: 32 x
+    // 32 over four groups 20.7, 64 x 64 over two 37.7, over one 37.4; 128 x 4096
+    // x 4096: 32 x 64 10.2, 64 x 64 12.6; gated 64 x 4096 x 4096 22.1 and 25.7)
+    if constexpr (!PAIR)
+        if (t64 <= 64) return go_mid<T, 32, 32, 3, 4, PAIR, ANY>(p, e, s);
+    if (t64 <= 128) return go_mid<T, 32, 64, 4, 2, PAIR, ANY>(p, e, s);
+    // (rows for one 64-row tile only: larger ones would be part empty.  int8 48
+    // x 65536 x 4096: 59.5, 128 x 128 72.7)
+    if (p.M <= 64) return go_mid<T, 64, 64, 4, 1, PAIR, ANY>(p, e, s);
+    // gated 256 x 2048 x 2048: 9.4, over one group 11.0, 64 x 128 11.7
+    if (t64 <= 256) return go_mid<T, 64, 64, 4, 2, PAIR, ANY>(p, e, s);
+    if constexpr (ANY) {
+        if (t64 <= 512) return go_mid<T, 64, 64, 2, 1, PAIR, ANY>(p, e, s);
+    } else {
+        // int8 512 x 4096 x 4096: 15.0; 64 x 64 18.1, 128 x 128 21.1
+        if (t64 <= 512) return go_mid<T, 64, 128, 3, 2, PAIR, ANY>(p, e, s);
+        // int8 1000 x 4096 x 4096: 23.5, over one group 28.7, 64 x 64 32.1;
+        // gated 128 x 14336 x 4096 41 and 47
+        if (t128 <= 256) return go_mid<T, 128, 128, 2, 2, PAIR, ANY>(p, e, s);
+    }
+    // two workgroups a CU (gated 1024 x 2736 x 1008: 19.2; four slots and one
+    // workgroup 29.3, 64 x 64 28.4)
+    return go_mid<T, 128, 128, 2, 1, PAIR, ANY>(p, e, s);
 }
 
 // Products whose operands lie aligned (the library's own copies).
 template <int T, class Epi>
 hipError_t launch_prod_aligned(const ProdArgs &p, const Epi &e, hipStream_t s) {
-    return launch_prod_mid<T, false, false, Epi>(p, e, s);
+    return launch_prod_tiles<T, false, false, Epi>(p, e, s);
+}
+
+template <int T, int MB, bool PAIR, class Epi>
+hipError_t go_rows(const ProdArgs &p, const Epi &e, hipStream_t s) {
+    hipLaunchKernelGGL((prod_rows_kernel<T, MB, PAIR, Epi>), dim3((unsigned)((p.N + 15) / 16)), dim3(512), 0, s, p, e);
+    return hipGetLastError();
 }
 
 // Any operands.
 template <int T, bool PAIR, class Epi>
-hipError_t launch_prod(ProdArgs p, const Epi &e, hipStream_t s) {
-    if (p.M <= 32) {
-        const unsigned grid = (unsigned)((p.N + 15) / 16);
-        if (p.M <= 16)
-            hipLaunchKernelGGL((prod_rows_kernel<T, 1, PAIR, Epi>), dim3(grid), dim3(512), 0, s, p, e);
-        else
-            hipLaunchKernelGGL((prod_rows_kernel<T, 2, PAIR, Epi>), dim3(grid), dim3(512), 0, s, p, e);
-        return hipGetLastError();
-    }
-    if (prod_aligned(p)) return launch_prod_mid<T, PAIR, false, Epi>(p, e, s);
-    return launch_prod_mid<T, PAIR, true, Epi>(p, e, s);
+hipError_t launch_prod(const ProdArgs &p, const Epi &e, hipStream_t s) {
+    // A few rows (every workgroup of prod_rows reads all of A, which from nine
+    // rows on costs more than a tile's detour through LDS where the tiles fill
+    // the GPU: int8 1 x 65536 x 4096 49 us against 57, 16 rows 63 against 58, 1 x
+    // 4096 x 4096 5.4 against 7.5, 32 x 14336 x 4096 24 against 16; gated 1 x
+    // 4096 x 4096 15.0 against 17.8, 32 rows 21.0 against 22.3)
+    const int64_t t64 = tiles_of(p, 64, PAIR ? 32 : 64);
+    if (p.M <= 8 || (p.M <= 16 && t64 < 200)) return go_rows<T, 1, PAIR>(p, e, s);
+    if (p.M <= 32 && t64 <= 128) return go_rows<T, 2, PAIR>(p, e, s);
+    if (prod_aligned(p)) return launch_prod_tiles<T, PAIR, false, Epi>(p, e, s);
+    return launch_prod_tiles<T, PAIR, true, Epi>(p, e, s);
 }
 
 }  // namespace tg

@@ -1,5 +1,10 @@
-// Products in BM x BN tiles of one workgroup of four waves (2 x 2), for grids
-// too small for 256 x 256 tiles and for operands at any alignment.
+// Products in BM x BN tiles of one workgroup, for grids too small for 256 x 256
+// tiles and for operands at any alignment.
+//
+// KS groups of four waves (2 x 2 over the tile) take every KS-th K tile each,
+// in LDS slots of their own; their sums meet in LDS at the end and are added in
+// order.  Where tiles are fewer than the GPU can hold, that cuts the K loop's
+// length and has KS times the loads in flight.
 //
 // K tiles of 128 bytes; LDS rows of 128 bytes, 16-byte chunk c of row r at
 // chunk c ^ (r & 7) (free of bank conflicts for the 16-row fragment reads).
@@ -15,26 +20,30 @@
 
 namespace tg {
 
-template <int T, int BM, int BN, int S, bool PAIR, bool ANY, class Epi>
-__global__ void __launch_bounds__(256) prod_mid_kernel(ProdArgs p, Epi e) {
+template <int T, int BM, int BN, int S, int KS, bool PAIR, bool ANY, class Epi>
+__global__ void __launch_bounds__(256 * KS) prod_mid_kernel(ProdArgs p, Epi e) {
     constexpr int WTM = BM / 2, WTN = BN / 2, TM = WTM / 16, TN = WTN / 16;
     constexpr int LA = BM / 32, LB = BN / 32;          // load instructions of a wave a tile
     constexpr int SLOT_A = BM * 128, SLOT_B = BN * 128, B_BASE = S * SLOT_A;
+    constexpr int GROUP = S * (SLOT_A + SLOT_B);       // LDS of a group
     constexpr int W = PAIR ? WTN / 2 : WTN;            // result columns of a wave
-    constexpr int RING = S * (SLOT_A + SLOT_B), STAGE = 16 * kStagePitch<W> * 4;
+    constexpr int RING = KS * GROUP, STAGE = 16 * kStagePitch<W> * 4;
+    constexpr int SUMS = TM * TN * 1024;               // a wave's accumulators
     static_assert(!ANY || S == 2, "ANY: two slots");
-    static_assert(RING >= 4 * STAGE && RING <= 160 * 1024, "LDS");
+    static_assert(RING >= 4 * STAGE && RING >= (KS - 1) * 4 * SUMS + 4 * STAGE && RING <= 160 * 1024, "LDS");
     static_assert((S - 2) * (LA + LB) < 64, "vmcnt");
 
-    __shared__ __attribute__((aligned(1024))) char smem[RING];
+    __shared__ __attribute__((aligned(1024))) char lds[RING];
 
     const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int group = KS > 1 ? __builtin_amdgcn_readfirstlane(tid >> 8) : 0;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
+    char *const smem = lds + group * GROUP;
     const int wm = wave >> 1, wn = wave & 1;
     int tmi, tni;
     tile_order(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
     const int m0 = tmi * BM, n0 = tni * (PAIR ? BN / 2 : BN);
-    const int KB = p.KB, nt = (KB + 127) / 128;
+    const int KB = p.KB, nt = (KB + 128 * KS - 1) / (128 * KS);    // K tiles of a group: tile t is K tile KS t + group
 
     // Load instruction j of a wave: A rows 32 j + 8 wave + lane / 8; B the
     // same, or (PAIR) rows 16 j + 8 (wave % 2) + lane / 8 of the wave's half.
@@ -56,7 +65,7 @@ __global__ void __launch_bounds__(256) prod_mid_kernel(ProdArgs p, Epi e) {
     // (chunks past K read as zeros from an offset beyond the resource, and so
     // do all of a tile past the last, which keeps the count of loads in flight)
     auto fetch = [&](int t, int slot) __attribute__((always_inline)) {
-        const int k0 = t * 128;
+        const int k0 = (KS * t + group) * 128;
         const bool in = k0 + kc < KB;
         const uint32_t va = in ? aoff + k0 : kOOB, vb = in ? boff + k0 : kOOB;
 #pragma unroll
@@ -68,7 +77,7 @@ __global__ void __launch_bounds__(256) prod_mid_kernel(ProdArgs p, Epi e) {
     };
     u32x4 ra[ANY ? LA : 1], rb[ANY ? LB : 1];
     auto read_any = [&](int t) __attribute__((always_inline)) {
-        const int kb = t * 128 + kc;
+        const int kb = (KS * t + group) * 128 + kc;
 #pragma unroll
         for (int j = 0; j < LA; ++j) {
             ra[j] = u32x4{0u, 0u, 0u, 0u};
@@ -143,7 +152,33 @@ __global__ void __launch_bounds__(256) prod_mid_kernel(ProdArgs p, Epi e) {
         wait_vmcnt<0>();                               // no load still writes a slot
         barrier();
     }
-    e.template block<TM, TN, false>(acc, (float *)(smem + wave * STAGE), lane, m0 + wm * WTM, n0 + wn * W, p.M, p.N);
+    if constexpr (KS > 1) {
+        // (every wave is past the last reads of the slots)
+        if (group > 0) {
+            float *sums = (float *)(lds + ((group - 1) * 4 + wave) * SUMS) + lane * 4;
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) *(f32x4 *)(sums + (i * TN + j) * 256) = acc[i][j];
+        }
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int k = 1; k < KS; ++k)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const f32x4 v = *(const f32x4 *)((float *)(lds + ((k - 1) * 4 + wave) * SUMS) + lane * 4 + (i * TN + j) * 256);
+                    if constexpr (T == kI8)
+                        acc[i][j] = __builtin_bit_cast(f32x4, __builtin_bit_cast(i32x4, acc[i][j]) + __builtin_bit_cast(i32x4, v));
+                    else
+                        acc[i][j] += v;
+                }
+        stage_fence();
+    }
+    e.template block<TM, TN, false>(acc, (float *)(KS > 1 ? lds + (KS - 1) * 4 * SUMS + wave * STAGE : lds + wave * STAGE),
+                                    lane, m0 + wm * WTM, n0 + wn * W, p.M, p.N);
 }
 
 }  // namespace tg
