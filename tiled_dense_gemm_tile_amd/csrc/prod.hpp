@@ -53,20 +53,46 @@ __device__ __forceinline__ f32x4 prod_mfma(u32x4 a, u32x4 b, f32x4 c) {
 
 // 16 bytes of an operand row from byte kb on, at any element alignment; zeros
 // past the row's kbytes.
+template <int T> using ProdElem = typename std::conditional<T == kI8, uint8_t, uint16_t>::type;
 template <int T>
-__device__ __forceinline__ u32x4 load_chunk(const char *row, int kb, int kbytes) {
-    typedef typename std::conditional<T == kI8, uint8_t, uint16_t>::type E;
-    struct __attribute__((packed, aligned(sizeof(E)))) U {
+__device__ __forceinline__ u32x4 load_chunk_whole(const char *at) {
+    struct __attribute__((packed, aligned(sizeof(ProdElem<T>)))) U {
         u32x4 v;
     };
-    if (kb + 16 <= kbytes) return ((const U *)(row + kb))->v;
-    u32x4 v = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 16 / (int)sizeof(E); ++i) {
-        const int at = kb + i * (int)sizeof(E);
-        if (at < kbytes) v[i * sizeof(E) / 4] |= (uint32_t)*(const E *)(row + at) << (8 * (i * sizeof(E) % 4));
+    return ((const U *)at)->v;
+}
+// Rows of 16 bytes on, in two parts: chunk_raw has no branch and no wait, so
+// that several can be in flight; it loads the row's last 16 bytes where the
+// chunk would pass the row's end, and chunk_settle moves them down.
+template <int T>
+__device__ __forceinline__ u32x4 chunk_raw(const char *row, int kb, int kbytes) {
+    return load_chunk_whole<T>(row + (kb + 16 <= kbytes ? kb : kbytes - 16));
+}
+__device__ __forceinline__ u32x4 chunk_settle(u32x4 v, int kb, int kbytes) {
+    typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+    const int past = kb + 16 - kbytes;                 // bytes of the chunk past the row's end
+    if (past <= 0) return v;
+    const u64x2 u = __builtin_bit_cast(u64x2, v);
+    const uint32_t bits = 8u * (uint32_t)(past < 16 ? past : 16);
+    u64x2 o;
+    o[0] = bits < 64 ? (u[0] >> bits) | (u[1] << (64 - bits)) : bits < 128 ? u[1] >> (bits - 64) : 0;
+    o[1] = bits < 64 ? u[1] >> bits : 0;
+    return __builtin_bit_cast(u32x4, o);
+}
+template <int T>
+__device__ __forceinline__ u32x4 load_chunk(const char *row, int kb, int kbytes) {
+    if (kbytes >= 16) return chunk_settle(chunk_raw<T>(row, kb, kbytes), kb, kbytes);
+    typedef ProdElem<T> E;
+    uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+    for (int at = kb; at < kbytes; at += (int)sizeof(E)) {
+        const uint64_t e = *(const E *)(row + at);
+        if (at - kb < 8)
+            lo |= e << (8 * (at - kb));
+        else
+            hi |= e << (8 * (at - kb - 8));
     }
-    return v;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
 // ---- results ------------------------------------------------------------------

@@ -12,8 +12,9 @@
 //     K tile, filled by direct global->LDS loads S - 1 tiles ahead; one barrier
 //     a tile, the loads of S - 2 tiles in flight across it.
 //   * ANY: the same chunks through registers (a 16-byte global load serves any
-//     element alignment), a tile ahead; a row's last chunk is assembled from
-//     elements.  Two slots.
+//     element alignment), PD tiles ahead of the slot they are written to; the
+//     chunk at a row's end is loaded whole from there and moved down in
+//     registers.  Two slots.
 #pragma once
 
 #include "prod.hpp"
@@ -75,27 +76,38 @@ __global__ void __launch_bounds__(256 * KS) prod_mid_kernel(ProdArgs p, Epi e) {
         for (int j = 0; j < LB; ++j)
             dma(rB, smem + B_BASE + slot * SLOT_B + (4 * j + wave) * 1024, vb, (int)(BSTEP * j * ldb));
     };
-    u32x4 ra[ANY ? LA : 1], rb[ANY ? LB : 1];
-    auto read_any = [&](int t) __attribute__((always_inline)) {
-        const int kb = (KS * t + group) * 128 + kc;
+    // (rows past the end are read as the last one: their results are not stored)
+    constexpr int PD = !ANY ? 1 : LA + LB <= 4 ? 4 : 2;
+    u32x4 ra[PD][ANY ? LA : 1], rb[PD][ANY ? LB : 1];
+    const char *pa[ANY ? LA : 1], *pb[ANY ? LB : 1];
+    if constexpr (ANY) {
 #pragma unroll
-        for (int j = 0; j < LA; ++j) {
-            ra[j] = u32x4{0u, 0u, 0u, 0u};
-            if (m0 + arow + 32 * j < p.M && kb < KB) ra[j] = load_chunk<T>(A + (int64_t)(arow + 32 * j) * p.lda, kb, KB);
-        }
-#pragma unroll
-        for (int j = 0; j < LB; ++j) {
-            rb[j] = u32x4{0u, 0u, 0u, 0u};
-            if (n0 + brow + BSTEP * j < p.N && kb < KB)
-                rb[j] = load_chunk<T>(B + (int64_t)(brow + BSTEP * j) * ldb, kb, KB);
-        }
-    };
-    auto write_any = [&](int slot) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < LA; ++j) *(u32x4 *)(smem + slot * SLOT_A + (4 * j + wave) * 1024 + lane * 16) = ra[j];
+        for (int j = 0; j < LA; ++j)
+            pa[j] = A + (int64_t)(arow + 32 * j < p.M - m0 ? arow + 32 * j : p.M - 1 - m0) * p.lda;
 #pragma unroll
         for (int j = 0; j < LB; ++j)
-            *(u32x4 *)(smem + B_BASE + slot * SLOT_B + (4 * j + wave) * 1024 + lane * 16) = rb[j];
+            pb[j] = B + (int64_t)(brow + BSTEP * j < p.N - n0 ? brow + BSTEP * j : p.N - 1 - n0) * ldb;
+    }
+    auto read_any = [&](int t, int d) __attribute__((always_inline)) {
+        const int kb = (KS * t + group) * 128 + kc;
+#pragma unroll
+        for (int j = 0; j < LA; ++j) ra[d][j] = chunk_raw<T>(pa[j], kb, KB);
+#pragma unroll
+        for (int j = 0; j < LB; ++j) rb[d][j] = chunk_raw<T>(pb[j], kb, KB);
+    };
+    auto write_any = [&](int t, int d) __attribute__((always_inline)) {
+        const int slot = t & 1, k0 = (KS * t + group) * 128;
+        if (KB >= 16 && k0 + 128 > KB) {
+#pragma unroll
+            for (int j = 0; j < LA; ++j) ra[d][j] = chunk_settle(ra[d][j], k0 + kc, KB);
+#pragma unroll
+            for (int j = 0; j < LB; ++j) rb[d][j] = chunk_settle(rb[d][j], k0 + kc, KB);
+        }
+#pragma unroll
+        for (int j = 0; j < LA; ++j) *(u32x4 *)(smem + slot * SLOT_A + (4 * j + wave) * 1024 + lane * 16) = ra[d][j];
+#pragma unroll
+        for (int j = 0; j < LB; ++j)
+            *(u32x4 *)(smem + B_BASE + slot * SLOT_B + (4 * j + wave) * 1024 + lane * 16) = rb[d][j];
     };
 
     const int fr = lane & 15, fq = lane >> 4;
@@ -123,16 +135,37 @@ __global__ void __launch_bounds__(256 * KS) prod_mid_kernel(ProdArgs p, Epi e) {
     };
 
     if constexpr (ANY) {
-        if (nt > 0) {
-            read_any(0);
-            write_any(0);
+        // tile t's chunks are in registers t % PD until they are written to slot
+        // t % 2, before the barrier that opens it; that slot's last reads were
+        // before the barrier that opened tile t - 1
+        auto step = [&](int t, auto d) __attribute__((always_inline)) {
+            constexpr int D = decltype(d)::value;
+            write_any(t, D);
+            read_any(t + PD, D);                       // (past K: the rows' ends, settled to zeros)
             wait_lgkmcnt0();
             barrier();
-        }
-        for (int t = 0; t < nt; ++t) {
-            if (t + 1 < nt) read_any(t + 1);
             compute(t & 1);
-            if (t + 1 < nt) write_any((t + 1) & 1);    // (read last before the barrier that opened tile t)
+        };
+        if (KB >= 16) {
+            static_for<0, PD>([&](auto d) { read_any(decltype(d)::value, decltype(d)::value); });
+            int t = 0;
+            for (; t + PD <= nt; t += PD)
+                static_for<0, PD>([&](auto d) __attribute__((always_inline)) { step(t + decltype(d)::value, d); });
+            static_for<0, PD - 1>([&](auto d) __attribute__((always_inline)) {
+                if (t + decltype(d)::value < nt) step(t + decltype(d)::value, d);
+            });
+            wait_lgkmcnt0();
+            barrier();
+        } else if (KB > 0) {                           // rows shorter than a chunk: one tile
+            const int kb = group * 128 + kc;
+#pragma unroll
+            for (int j = 0; j < LA; ++j) ra[0][j] = load_chunk<T>(pa[j], kb, KB);
+#pragma unroll
+            for (int j = 0; j < LB; ++j) rb[0][j] = load_chunk<T>(pb[j], kb, KB);
+            write_any(0, 0);
+            wait_lgkmcnt0();
+            barrier();
+            compute(0);
             wait_lgkmcnt0();
             barrier();
         }

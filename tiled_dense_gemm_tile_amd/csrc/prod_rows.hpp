@@ -37,10 +37,6 @@ __global__ void __launch_bounds__(512) prod_rows_kernel(ProdArgs p, Epi e) {
         const int m = 16 * b + r < p.M ? 16 * b + r : p.M - 1;
         x[b] = (const char *)p.A + (int64_t)m * p.lda;
     }
-    typedef typename std::conditional<T == kI8, uint8_t, uint16_t>::type E;
-    struct __attribute__((packed, aligned(sizeof(E)))) U {
-        u32x4 v;
-    };
     f32x4 acc[MB][RB];
 #pragma unroll
     for (int b = 0; b < MB; ++b)
@@ -53,9 +49,9 @@ __global__ void __launch_bounds__(512) prod_rows_kernel(ProdArgs p, Epi e) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
 #pragma unroll
-            for (int c = 0; c < RB; ++c) wf[buf][c][s] = ((const U *)(w[c] + kb + 64 * s))->v;
+            for (int c = 0; c < RB; ++c) wf[buf][c][s] = load_chunk_whole<T>(w[c] + kb + 64 * s);
 #pragma unroll
-            for (int b = 0; b < MB; ++b) xf[buf][b][s] = ((const U *)(x[b] + kb + 64 * s))->v;
+            for (int b = 0; b < MB; ++b) xf[buf][b][s] = load_chunk_whole<T>(x[b] + kb + 64 * s);
         }
     };
     auto multiply = [&](int buf) __attribute__((always_inline)) {

@@ -175,21 +175,29 @@ def _dense(t):
 
 
 def _gradients(name, grads):
-    """(device, addresses, sizes, types) of a list of tensors, the arrays that
-    the C calls read."""
+    """(device, whether all are contiguous, addresses, sizes, types) of a list
+    of tensors: the arrays that the C calls read."""
     if not grads:
         raise ValueError("no %s" % name)
     dev = _device(grads[0])
-    for t in grads:
-        if t.get_device() != dev:                      # (-1 of a host tensor)
-            raise ValueError("%s must be device tensors on cuda:%d" % (name, dev))
-        if not _dense(t):
-            raise ValueError("%s must each fill one piece of memory" % name)
+    if {t.get_device() for t in grads} != {dev}:       # (-1 of a host tensor)
+        raise ValueError("%s must be device tensors on cuda:%d" % (name, dev))
+    whole = all([t.is_contiguous() for t in grads])
+    if not whole and not all([_dense(t) for t in grads]):
+        raise ValueError("%s must each fill one piece of memory" % name)
     try:
         types = array("i", [_TYPES[t.dtype] for t in grads])
     except KeyError:
         raise TypeError("%s must be float32, bfloat16 or float16 tensors" % name) from None
-    return dev, array("q", [t.data_ptr() for t in grads]), array("q", [t.numel() for t in grads]), types
+    return dev, whole, array("q", [t.data_ptr() for t in grads]), array("q", [t.numel() for t in grads]), types
+
+
+def _twice(at, sizes):
+    """Whether two tensors with elements start at the same address."""
+    if len(set(at)) == len(at):
+        return False
+    at = [a for a, n in zip(at, sizes) if n]
+    return len(set(at)) != len(at)
 
 
 def _at(a):
@@ -210,7 +218,7 @@ def grad_norm(grads, norm=None, workspace=None):
     :func:`grad_workspace_bytes` bytes, 256-byte aligned (allocated per call
     when not given)."""
     grads = list(grads)
-    dev, at, sizes, types = _gradients("gradients", grads)
+    dev, _, at, sizes, types = _gradients("gradients", grads)
     norm, to = _norm_out(norm, dev)
     workspace, *ws = _workspace(workspace, workspace is None and grad_workspace_bytes(len(grads)), dev)
     _run(_load().grad_norm, dev, len(grads), _at(at), _at(sizes), _at(types), to, *ws)
@@ -231,26 +239,27 @@ def _scalar(name, t, dev):
 
 def clip_grads(grads, max_norm, out=None, norm=None, given=None, workspace=None):
     """Every gradient times min(1, max_norm / (norm + 1e-6)), in place or into
-    ``out`` (tensors of the same shapes, types and strides).  The norm is that
+    ``out`` (tensors of the same sizes and types, contiguous where the
+    gradients are, else of the same strides).  The norm is that
     of :func:`grad_norm`, computed here, or ``given``: one float32 on the GPU,
     such as a norm whose square the ranks have summed.  Returns the norm
     (``given`` where it was).  No two gradients may share memory."""
     grads = list(grads)
-    dev, at, sizes, types = _gradients("gradients", grads)
-    if len(set(at)) != len(at) and len({a for a, n in zip(at, sizes) if n}) != sum(n > 0 for n in sizes):
+    dev, whole, at, sizes, types = _gradients("gradients", grads)
+    if _twice(at, sizes):
         raise ValueError("the same gradient is given twice")
     to = at
     if out is not None:
         out = list(out)
-        for t, o in zip(grads, out):
-            if o.shape != t.shape or o.dtype != t.dtype or (o.stride() != t.stride() and t.numel() > 1):
-                raise ValueError("out must have the gradients' shapes, types and strides")
         if len(out) != len(grads):
             raise ValueError("out must hold one tensor for each gradient")
-        odev, to, _, _ = _gradients("out", out)
+        odev, owhole, to, osizes, otypes = _gradients("out", out)
         if odev != dev:
             raise ValueError("out must be device tensors on cuda:%d" % dev)
-        if len(set(to)) != len(to) and len({a for a, n in zip(to, sizes) if n}) != sum(n > 0 for n in sizes):
+        if otypes != types or osizes != sizes or (not (whole and owhole) and any(
+                [o.shape != t.shape or (o.stride() != t.stride() and t.numel() > 1) for t, o in zip(grads, out)])):
+            raise ValueError("out must have the gradients' sizes and types, and strides where those are not contiguous")
+        if _twice(to, sizes):
             raise ValueError("the same result is given twice")
     if given is None:
         norm, into = _norm_out(norm, dev)
