@@ -120,8 +120,8 @@ def test_glu_backward_workspace_bytes():
     assert tg.gemm_glu_backward_workspace_bytes(4, 0, 32) == 0
     assert tg.gemm_glu_backward_workspace_bytes(-1, 64, 32) == 0
     assert tg.gemm_glu_backward_workspace_bytes(1 << 21, 64, 32) == 0
-    # dg | du, both transposed, X and the weights transposed, tiles of 64
-    assert tg.gemm_glu_backward_workspace_bytes(100, 70, 32) == 2 * (100 * 256 + 256 * 128 + 32 * 128 + 32 * 256)
+    # dg | du, both transposed, X and the weights transposed: tiles of 64, rows of an odd multiple of 256 bytes
+    assert tg.gemm_glu_backward_workspace_bytes(100, 70, 32) == 2 * (100 * 384 + 256 * 128 + 32 * 128 + 32 * 384)
 
 
 def quant(rows=4, N=64, X=P, ldx=64, t=BF16, q=Q, ldq=64, s=Q + MB):

@@ -32,6 +32,7 @@ struct ProdArgs {
     int64_t lda, ldb, ldb1;                            // bytes
     int M, N, KB;                                      // results' rows and columns; bytes of an operand row
     int tiles_m, tiles_n, group_m;
+    int run;                                           // prod_w4: tiles it computes; prod_mid, QUARTERS: the first it does not
 };
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));

@@ -34,10 +34,17 @@ hipError_t go_mid(ProdArgs p, const Epi &e, hipStream_t s) {
     return hipGetLastError();
 }
 
+// 256 x 256 tiles in whole rounds of one a CU; what is left of up to half a
+// round in 128 x 128 tiles (four times as many: gated 8256 features).
 template <int T, bool PAIR, class Epi>
 hipError_t go_w4(ProdArgs p, const Epi &e, hipStream_t s) {
-    const unsigned tiles = prod_tiles(p, 256, PAIR ? 128 : 256), cus = 256;
+    const unsigned tiles = prod_tiles(p, 256, PAIR ? 128 : 256), cus = 256, rest = tiles % cus;
+    const bool cut = tiles > cus && rest > 0 && rest <= cus / 2;
+    p.run = (int)(cut ? tiles - rest : tiles);
     hipLaunchKernelGGL((prod_w4_kernel<T, PAIR, Epi>), dim3(tiles < cus ? tiles : cus), dim3(256), 0, s, p, e);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess || !cut) return err;
+    hipLaunchKernelGGL((prod_mid_kernel<T, 128, 128, 2, 2, PAIR, false, Epi, true>), dim3(4 * rest), dim3(512), 0, s, p, e);
     return hipGetLastError();
 }
 
@@ -49,11 +56,10 @@ hipError_t launch_prod_tiles(const ProdArgs &p, const Epi &e, hipStream_t s) {
     constexpr int D = PAIR ? 2 : 1;                    // a tile's columns of B for one of the results
     const int64_t t64 = tiles_of(p, 64, 64 / D), t128 = tiles_of(p, 128, 128 / D);
     if constexpr (!ANY) {
-        // 256 x 256: one round of up to 256 tiles takes as long as 630 of the
-        // 128 x 128 tiles, of which 512 run at once (gated 512 x 14336 x 4096,
-        // 224 tiles: 88 against 125; 256 x 14336 x 4096, 112: 90 against 66)
-        const int64_t rounds = (tiles_of(p, 256, 256 / D) + 255) / 256;
-        if (t128 > 512 && (rounds == 1 || t128 >= 630 * rounds) && p.KB > 0) return go_w4<T, PAIR>(p, e, s);
+        // 256 x 256: more 128 x 128 tiles than run at once, two a CU (gated 512 x
+        // 14336 x 4096, 224 tiles: 88 against 125; 256 x 14336 x 4096, 112 tiles:
+        // 90 against 66)
+        if (t128 > 512 && p.KB > 0) return go_w4<T, PAIR>(p, e, s);
     }
     // few tiles: small ones, K cut over the waves (int8 64 x 4096 x 14336: 32 x
     // 32 over four groups 20.7, 64 x 64 over two 37.7, over one 37.4; 128 x 4096

@@ -21,7 +21,9 @@
 
 namespace tg {
 
-template <int T, int BM, int BN, int S, int KS, bool PAIR, bool ANY, class Epi>
+// QUARTERS: the tiles are the quarters of those 256 x 256 tiles (in prod_w4's
+// order) that fill no round of workgroups.
+template <int T, int BM, int BN, int S, int KS, bool PAIR, bool ANY, class Epi, bool QUARTERS = false>
 __global__ void __launch_bounds__(256 * KS) prod_mid_kernel(ProdArgs p, Epi e) {
     constexpr int WTM = BM / 2, WTN = BN / 2, TM = WTM / 16, TN = WTN / 16;
     constexpr int LA = BM / 32, LB = BN / 32;          // load instructions of a wave a tile
@@ -42,8 +44,16 @@ __global__ void __launch_bounds__(256 * KS) prod_mid_kernel(ProdArgs p, Epi e) {
     char *const smem = lds + group * GROUP;
     const int wm = wave >> 1, wn = wave & 1;
     int tmi, tni;
-    tile_order(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
+    if constexpr (QUARTERS) {
+        static_assert(BM == 128 && BN == 128, "quarters");
+        const int q = blockIdx.x & 3;
+        tile_order(p.run + (blockIdx.x >> 2), p.tiles_m * p.tiles_n, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
+        tmi = 2 * tmi + (q >> 1), tni = 2 * tni + (q & 1);
+    } else {
+        tile_order(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
+    }
     const int m0 = tmi * BM, n0 = tni * (PAIR ? BN / 2 : BN);
+    if (QUARTERS && (m0 >= p.M || n0 >= p.N)) return;  // (past the matrix's edge)
     const int KB = p.KB, nt = (KB + 128 * KS - 1) / (128 * KS);    // K tiles of a group: tile t is K tile KS t + group
 
     // Load instruction j of a wave: A rows 32 j + 8 wave + lane / 8; B the

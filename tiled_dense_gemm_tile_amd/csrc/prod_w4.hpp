@@ -140,11 +140,11 @@ __global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
         // (every wave is past its last barrier, so past all reads of the slots;
         // the loads of the tile past the end have landed there)
         const ProdArgs r = kernel_arg0_reloaded<ProdArgs>();
-        const int dm0 = m0, dn0 = n0, ntl = r.tiles_m * r.tiles_n;
+        const int dm0 = m0, dn0 = n0;
         vt += gridDim.x;
-        const bool more = vt < ntl;
+        const bool more = vt < r.run;
         if (more) {
-            tile_order(vt, ntl, r.tiles_m, r.tiles_n, r.group_m, tmi, tni);
+            tile_order(vt, r.tiles_m * r.tiles_n, r.tiles_m, r.tiles_n, r.group_m, tmi, tni);
             m0 = tmi * 256;
             n0 = tni * BN;
             resources(r);
