@@ -77,12 +77,19 @@ __global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(smem + lds), 16, voff,
                                                  soff, 0, 0);
     };
+    const int k_first = (int)(blockIdx.x & 7) * nt / 8 * 128;
+    auto koff = [&](int t) __attribute__((always_inline)) {
+        const int k = t * 128 + k_first;
+        return t >= nt ? 0x40000000 : k >= nt * 128 ? k - nt * 128 : k;
+    };
     auto fetch_a = [&](int t, int j) __attribute__((always_inline)) {
-        const uint32_t v = t * 128 + kc < KB ? aoff + t * 128 : kOOB;
+        const int k0 = koff(t);
+        const uint32_t v = k0 + kc < KB ? aoff + k0 : kOOB;
         dma(rA, (t & 1) * SLOT + (4 * j + wave) * 1024, v, j * astep);
     };
     auto fetch_b = [&](int t, int j) __attribute__((always_inline)) {
-        const uint32_t v = t * 128 + kc < KB ? boff + t * 128 : kOOB;
+        const int k0 = koff(t);
+        const uint32_t v = k0 + kc < KB ? boff + k0 : kOOB;
         dma(rB, B_BASE + (t & 1) * SLOT + (4 * j + wave) * 1024, v, j * bstep);
     };
 
@@ -150,7 +157,8 @@ __global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
             resources(r);
             int wv = wave;                             // (their LDS addresses are computed here, not held)
             asm volatile("" : "+s"(wv));
-            const uint32_t va = kc < KB ? aoff : kOOB, vb = kc < KB ? boff : kOOB;
+            const int k0 = koff(0);
+            const uint32_t va = k0 + kc < KB ? aoff + k0 : kOOB, vb = k0 + kc < KB ? boff + k0 : kOOB;
 #pragma unroll
             for (int j = 0; j < 8; ++j) dma(rA, (4 * j + wv) * 1024, va, j * astep);
 #pragma unroll
