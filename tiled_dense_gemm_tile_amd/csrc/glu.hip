@@ -38,6 +38,7 @@ extern "C" gemm_status gemm_glu(int64_t M, int64_t F, int64_t K, const void *X, 
     p.M = (int)M;
     p.N = (int)F;
     p.KB = (int)(K * 2);
-    if (type == GEMM_TYPE_BF16) return launched(tg::launch_glu<1>(p, {H, G, U, ldh, ldg, ldu, act}, stream));
-    return launched(tg::launch_glu<2>(p, {H, G, U, ldh, ldg, ldu, act}, stream));
+    const bool vec = tg::emit_whole(H, ldh, F, 2) && (!G || tg::emit_whole(G, ldg, F, 2)) && (!U || tg::emit_whole(U, ldu, F, 2));
+    if (type == GEMM_TYPE_BF16) return launched(tg::launch_glu<1>(p, {H, G, U, ldh, ldg, ldu, act, vec}, stream));
+    return launched(tg::launch_glu<2>(p, {H, G, U, ldh, ldg, ldu, act, vec}, stream));
 }

@@ -174,13 +174,15 @@ gemm_status run(const tg::GluBwdArgs &a, void *dX, int64_t lddx, const void *Cg,
         p.N = a.K;
         p.KB = a.Fp * 4;
         gemm_status st = launched(tg::launch_plain<T, T>(
-            p, {{nullptr, nullptr}, {dX, nullptr}, {0, 0}, {lddx, 0}, 0x7fffffff, a.M}, s));
+            p, {{nullptr, nullptr}, {dX, nullptr}, {0, 0}, {lddx, 0}, 0x7fffffff, a.M, tg::emit_whole(dX, lddx, a.K, 2)}, s));
         if (st != GEMM_OK) return st;
     }
     if (!dWg) return GEMM_OK;
+    const int gs = f32 ? 4 : 2;
+    const bool vec = tg::emit_whole(dWg, lddwg, a.K, gs) && tg::emit_whole(dWu, lddwu, a.K, gs);
     if (f32)
-        return weight_products<T, 0>(a, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F}, s);
-    return weight_products<T, T>(a, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F}, s);
+        return weight_products<T, 0>(a, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F, vec}, s);
+    return weight_products<T, T>(a, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F, vec}, s);
 }
 
 }  // namespace

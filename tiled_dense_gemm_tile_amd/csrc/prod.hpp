@@ -115,20 +115,29 @@ __device__ __forceinline__ f32x4 acc_value(const f32x4 &a) {
 // Floats between two rows of a wave's staged block of W columns: four banks.
 template <int W> constexpr int kStagePitch = W + 4;
 
+// Store instructions of a lane for 16 staged rows of W columns.
+template <int OT, int W> constexpr int kEmitStores = 16 / (64 / (W / kVE<OT>) < 16 ? 64 / (W / kVE<OT>) : 16);
+
 // 16 staged rows of W fp32 values as rows row0 .. of D (element type OT), plus
 // C's: whole 16-byte pieces of a row at any element alignment (C: NULL or the
-// same type; ldc 0: one row for all).
-template <int OT, int W>
+// same type; ldc 0: one row for all).  VEC: D's rows start on 16 bytes and hold
+// whole pieces; the stores are then always issued, kEmitStores of them (past
+// the matrix: beyond the resource), and stream past the caches.
+template <int OT, int W, bool VEC>
 __device__ __forceinline__ void emit_rows(const float *stage, int lane, int row0, int col0, int M, int N, void *D,
                                           int64_t ldd, const void *C, int64_t ldc) {
     typedef RowVec<OT> R;
+    typedef typename R::S S;
     constexpr int VE = R::VE, LPR = W / VE, RPI = 64 / LPR;
     const int lr0 = lane / LPR, c = (lane % LPR) * VE, col = col0 + c;
-    if (col >= N) return;
+    static_assert(!VEC || RPI <= 16, "whole instructions");
+    const __amdgpu_buffer_rsrc_t rD =
+        make_rsrc((S *)D + (int64_t)row0 * ldd, VEC ? span_bytes(M - row0 < 16 ? M - row0 : 16, N, ldd, sizeof(S)) : 0u);
+    if (!VEC && col >= N) return;
 #pragma unroll
-    for (int q = 0; q < (RPI < 16 ? 16 / RPI : 1); ++q) {
+    for (int q = 0; q < kEmitStores<OT, W>; ++q) {
         const int lr = q * RPI + lr0, row = row0 + lr;
-        if ((RPI > 16 && lr >= 16) || row >= M) continue;
+        if (!VEC && ((RPI > 16 && lr >= 16) || row >= M)) continue;
         float v[VE];
 #pragma unroll
         for (int h = 0; h < VE; h += 4) {
@@ -136,16 +145,27 @@ __device__ __forceinline__ void emit_rows(const float *stage, int lane, int row0
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[h + r] = t[r];
         }
-        typename R::V o;
-        if (C) {
-            const typename R::V a = R::load((const typename R::S *)C + (int64_t)row * ldc, col, N);
+        const bool in = row < M && col < N;
+        if (C && (!VEC || in)) {
+            const typename R::V a = R::load((const S *)C + (int64_t)row * ldc, col, N);
 #pragma unroll
             for (int i = 0; i < VE; ++i) v[i] += Elem<OT>::up(a[i]);
         }
+        typename R::V o;
 #pragma unroll
         for (int i = 0; i < VE; ++i) o[i] = Elem<OT>::down(v[i]);
-        R::store((typename R::S *)D + (int64_t)row * ldd, col, N, o);
+        if constexpr (VEC)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), rD,
+                                                   in ? (uint32_t)(lr * ldd + col) * (uint32_t)sizeof(S) : kOOB, 0,
+                                                   kStoreStream);
+        else
+            R::store((S *)D + (int64_t)row * ldd, col, N, o);
     }
+}
+
+// Whether D allows that.
+inline bool emit_whole(const void *D, int64_t ldd, int64_t N, int size) {
+    return (uintptr_t)D % 16 == 0 && ldd * size % 16 == 0 && N * size % 16 == 0;
 }
 
 __device__ __forceinline__ void stage_fence() {
@@ -162,8 +182,10 @@ struct Int8Epi {
     const void *C;
     void *D;
     int64_t ldc, ldd;
+    bool vec;                                          // emit_whole
+    template <int TM, int TN> static constexpr int stores() { return TM * kEmitStores<OT, TN * 16> < 63 ? TM * kEmitStores<OT, TN * 16> : 63; }
 
-    template <int TM, int TN, bool AGPR>
+    template <int TM, int TN, bool AGPR, bool VEC>
     __device__ __forceinline__ void block(const f32x4 (&acc)[TM][TN], float *stage, int lane, int row0, int col0, int M,
                                           int N) const {
         constexpr int W = TN * 16;
@@ -190,7 +212,7 @@ struct Int8Epi {
                 *(f32x4 *)(stage + fr * kStagePitch<W> + 16 * j + 4 * fq) = v;
             }
             stage_fence();
-            emit_rows<OT, W>(stage, lane, row0 + 16 * i, col0, M, N, D, ldd, C, ldc);
+            emit_rows<OT, W, VEC>(stage, lane, row0 + 16 * i, col0, M, N, D, ldd, C, ldc);
             stage_fence();
         }
     }
@@ -266,8 +288,10 @@ struct GluEpi {
     void *H, *G, *U;
     int64_t ldh, ldg, ldu;
     int act;
+    bool vec;
+    template <int TM, int TN> static constexpr int stores() { return TM * kEmitStores<OT, TN * 8>; }    // (H alone)
 
-    template <int TM, int TN, bool AGPR>
+    template <int TM, int TN, bool AGPR, bool VEC>
     __device__ __forceinline__ void block(const f32x4 (&acc)[TM][TN], float *stage, int lane, int row0, int col0, int M,
                                           int N) const {
         constexpr int W = TN * 8;
@@ -285,7 +309,7 @@ struct GluEpi {
 #pragma unroll
                 for (int j = 0; j < TN / 2; ++j) *(f32x4 *)(stage + fr * kStagePitch<W> + 16 * j + 4 * fq) = v[j];
                 stage_fence();
-                emit_rows<OT, W>(stage, lane, row0 + 16 * i, col0, M, N, D, ldd, nullptr, 0);
+                emit_rows<OT, W, VEC>(stage, lane, row0 + 16 * i, col0, M, N, D, ldd, nullptr, 0);
                 stage_fence();
             };
             if (G) put(g, G, ldg);
@@ -318,8 +342,10 @@ struct PlainEpi {
     void *D[2];
     int64_t ldc[2], ldd[2];
     int split, rows;
+    bool vec;
+    template <int TM, int TN> static constexpr int stores() { return TM * kEmitStores<OT, TN * 16> < 63 ? TM * kEmitStores<OT, TN * 16> : 63; }
 
-    template <int TM, int TN, bool AGPR>
+    template <int TM, int TN, bool AGPR, bool VEC>
     __device__ __forceinline__ void block(const f32x4 (&acc)[TM][TN], float *stage, int lane, int row0, int col0, int M,
                                           int N) const {
         constexpr int W = TN * 16;
@@ -333,7 +359,7 @@ struct PlainEpi {
             stage_fence();
             // (split is a multiple of 16: the 16 rows lie on one side)
             const int r0 = row0 + 16 * i, h = r0 >= split ? 1 : 0;
-            emit_rows<OT, W>(stage, lane, h ? r0 - split : r0, col0, rows, N, h ? D[1] : D[0], h ? ldd[1] : ldd[0],
+            emit_rows<OT, W, VEC>(stage, lane, h ? r0 - split : r0, col0, rows, N, h ? D[1] : D[0], h ? ldd[1] : ldd[0],
                              h ? C[1] : C[0], h ? ldc[1] : ldc[0]);
             stage_fence();
         }

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(256 * KS) prod_mid_kernel(ProdArgs p, Epi e) {
                 }
         stage_fence();
     }
-    e.template block<TM, TN, false>(acc, (float *)(KS > 1 ? lds + (KS - 1) * 4 * SUMS + wave * STAGE : lds + wave * STAGE),
+    e.template block<TM, TN, false, false>(acc, (float *)(KS > 1 ? lds + (KS - 1) * 4 * SUMS + wave * STAGE : lds + wave * STAGE),
                                     lane, m0 + wm * WTM, n0 + wn * W, p.M, p.N);
 }
 
