@@ -472,3 +472,24 @@ def test_glu_tiles(m, f, k):
 @pytest.mark.parametrize("m,k", [(33, 100), (70, 2000), (100, 4100), (250, 4000), (500, 4030), (900, 4090)])
 def test_glu_backward_tiles(m, k):
     check_backward(m, 150, k, BF)
+
+
+# both products of the backward pass in one launch of 256 x 256 tiles: evenly divided, one of them with fewer tiles than
+# workgroups, sums of very different lengths, and without one of the products
+@pytest.mark.parametrize("m,f,k", [(2100, 2100, 2050), (2048, 1024, 2560), (300, 6000, 2300), (6000, 200, 3100), (4200, 1000, 1500)])
+@pytest.mark.parametrize("dtype,grad", [(BF, BF), (FP, F32)])
+def test_glu_backward_one_launch(m, f, k, dtype, grad):
+    check_backward(m, f, k, dtype, grad=grad, acc=True)
+
+
+def test_glu_backward_parts_of_large_grids():
+    """Each gradient alone is the same as both, up to the order of its sums."""
+    m, f, k = 2100, 2100, 2050
+    a = [rand(i, m, f) for i in range(3)] + [rand(3, m, k), rand(4, f, k, scale=0.05), rand(5, f, k, scale=0.05)]
+    both = tg.gemm_glu_backward(*a, grad_dtype=F32)
+    want, bound = ref.glu_backward(*a, "silu")
+    dx, _, _ = tg.gemm_glu_backward(*a, weight_grad=False)
+    _, dwg, dwu = tg.gemm_glu_backward(*a, input_grad=False, grad_dtype=F32)
+    for got, w, b in zip((dx, dwg, dwu), want, bound):
+        within(got, w, half(w, b, got.dtype))
+    assert torch.equal(both[0], tg.gemm_glu_backward(*a, grad_dtype=F32)[0])

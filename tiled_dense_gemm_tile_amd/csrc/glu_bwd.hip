@@ -142,16 +142,27 @@ int64_t padded(int64_t n) { return (n + tg::kCopyTile - 1) / tg::kCopyTile * tg:
 int64_t pitch(int64_t n) { return n + (256 + 128 - n % 256) % 256; }
 int64_t part(int64_t elements) { return (elements * 2 + 255) / 256 * 256; }
 
+// The products: the input gradient where dX is given, the weights' where e.D is.
 template <int T, int OT>
-gemm_status weight_products(const tg::GluBwdArgs &a, const tg::PlainEpi<OT> &e, hipStream_t s) {
-    tg::ProdArgs p = {};
-    p.A = a.dgut;
-    p.B = a.xt;
-    p.lda = p.ldb = (int64_t)a.ldm * 2;
-    p.M = 2 * a.Fp;
-    p.N = a.K;
-    p.KB = a.Mp * 2;
-    return launched(tg::launch_plain<T, OT>(p, e, s));
+gemm_status products(const tg::GluBwdArgs &a, void *dX, int64_t lddx, const tg::PlainEpi<OT> &e, hipStream_t s) {
+    tg::ProdArgs x = {}, w = {};
+    x.A = a.dgu;
+    x.B = a.wt;
+    x.lda = x.ldb = (int64_t)a.ldf * 2;
+    x.M = a.M;
+    x.N = a.K;
+    x.KB = a.Fp * 4;
+    w.A = a.dgut;
+    w.B = a.xt;
+    w.lda = w.ldb = (int64_t)a.ldm * 2;
+    w.M = 2 * a.Fp;
+    w.N = a.K;
+    w.KB = a.Mp * 2;
+    const tg::PlainEpi<T> ex{{nullptr, nullptr}, {dX, nullptr}, {0, 0}, {lddx, 0}, 0x7fffffff, a.M,
+                             tg::emit_whole(dX, lddx, a.K, 2)};
+    if (!e.D[0]) return launched(tg::launch_plain<T, T>(x, ex, s));
+    if (!dX) return launched(tg::launch_plain<T, OT>(w, e, s));
+    return launched(tg::launch_plain_two<T, OT>(x, ex, w, e, s));
 }
 
 template <int T>
@@ -165,24 +176,13 @@ gemm_status run(const tg::GluBwdArgs &a, void *dX, int64_t lddx, const void *Cg,
         gemm_status st = launched(hipGetLastError());
         if (st != GEMM_OK) return st;
     }
-    if (dX && a.M > 0) {
-        tg::ProdArgs p = {};
-        p.A = a.dgu;
-        p.B = a.wt;
-        p.lda = p.ldb = (int64_t)a.ldf * 2;
-        p.M = a.M;
-        p.N = a.K;
-        p.KB = a.Fp * 4;
-        gemm_status st = launched(tg::launch_plain<T, T>(
-            p, {{nullptr, nullptr}, {dX, nullptr}, {0, 0}, {lddx, 0}, 0x7fffffff, a.M, tg::emit_whole(dX, lddx, a.K, 2)}, s));
-        if (st != GEMM_OK) return st;
-    }
-    if (!dWg) return GEMM_OK;
+    if (a.M == 0) dX = nullptr;
+    if (!dX && !dWg) return GEMM_OK;
     const int gs = f32 ? 4 : 2;
     const bool vec = tg::emit_whole(dWg, lddwg, a.K, gs) && tg::emit_whole(dWu, lddwu, a.K, gs);
     if (f32)
-        return weight_products<T, 0>(a, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F, vec}, s);
-    return weight_products<T, T>(a, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F, vec}, s);
+        return products<T, 0>(a, dX, lddx, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F, vec}, s);
+    return products<T, T>(a, dX, lddx, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F, vec}, s);
 }
 
 }  // namespace

@@ -2,11 +2,15 @@
 #include "prod_api.hpp"
 #include "prod_launch.hpp"
 
-template <>
-hipError_t tg::launch_plain<2, 0>(const ProdArgs &p, const PlainEpi<0> &e, hipStream_t s) {
-    return launch_prod_aligned<2>(p, e, s);
-}
-template <>
-hipError_t tg::launch_plain<2, 2>(const ProdArgs &p, const PlainEpi<2> &e, hipStream_t s) {
-    return launch_prod_aligned<2>(p, e, s);
-}
+#define TG_PLAIN(OT)                                                                                           \
+    template <>                                                                                                \
+    hipError_t tg::launch_plain<2, OT>(const ProdArgs &p, const PlainEpi<OT> &e, hipStream_t s) {              \
+        return launch_prod_aligned<2>(p, e, s);                                                                \
+    }                                                                                                          \
+    template <>                                                                                                \
+    hipError_t tg::launch_plain_two<2, OT>(const ProdArgs &p0, const PlainEpi<2> &e0, const ProdArgs &p1,      \
+                                           const PlainEpi<OT> &e1, hipStream_t s) {                            \
+        return launch_prod_two<2>(p0, e0, p1, e1, s);                                                          \
+    }
+TG_PLAIN(0)
+TG_PLAIN(2)

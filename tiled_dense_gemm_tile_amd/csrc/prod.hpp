@@ -35,6 +35,12 @@ struct ProdArgs {
     int run;                                           // prod_w4: tiles it computes; prod_mid, QUARTERS: the first it does not
 };
 
+// Two products in one launch.
+struct ProdPair {
+    ProdArgs p[2];
+    int split;                                         // a multiple of 8, so that workgroups keep their XCD
+};
+
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 // acc + a.b; the sums of 8-bit integers are int32, carried in the same bits.

@@ -41,10 +41,16 @@ hipError_t go_w4(ProdArgs p, const Epi &e, hipStream_t s) {
     const unsigned tiles = prod_tiles(p, 256, PAIR ? 128 : 256), cus = 256, rest = tiles % cus;
     const bool cut = tiles > cus && rest > 0 && rest <= cus / 2;
     p.run = (int)(cut ? tiles - rest : tiles);
-    hipLaunchKernelGGL((prod_w4_kernel<T, PAIR, Epi>), dim3(tiles < cus ? tiles : cus), dim3(256), 0, s, p, e);
+    hipLaunchKernelGGL((prod_w4_kernel<T, PAIR, !PAIR && T != kI8, Epi>), dim3(tiles < cus ? tiles : cus), dim3(256), 0, s, p, e);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || !cut) return err;
-    hipLaunchKernelGGL((prod_mid_kernel<T, 128, 128, 2, 2, PAIR, false, Epi, true>), dim3(4 * rest), dim3(512), 0, s, p, e);
+    // (one a CU; more of them two a CU)
+    if (rest <= cus / 4)
+        hipLaunchKernelGGL((prod_mid_kernel<T, 128, 128, 2, 2, PAIR, false, Epi, true>), dim3(4 * rest), dim3(512), 0, s,
+                           p, e);
+    else
+        hipLaunchKernelGGL((prod_mid_kernel<T, 128, 128, 2, 1, PAIR, false, Epi, true>), dim3(4 * rest), dim3(256), 0, s,
+                           p, e);
     return hipGetLastError();
 }
 
@@ -90,6 +96,51 @@ hipError_t launch_prod_tiles(const ProdArgs &p, const Epi &e, hipStream_t s) {
 template <int T, class Epi>
 hipError_t launch_prod_aligned(const ProdArgs &p, const Epi &e, hipStream_t s) {
     return launch_prod_tiles<T, false, false, Epi>(p, e, s);
+}
+
+template <int T, int BM, int BN, int S, int KS, class Epi0, class Epi1>
+hipError_t go_mid_two(ProdPair q, const Epi0 &e0, const Epi1 &e1, hipStream_t s) {
+    q.split = (int)(prod_tiles(q.p[0], BM, BN) + 7) / 8 * 8;
+    const unsigned grid = (unsigned)q.split + prod_tiles(q.p[1], BM, BN);
+    hipLaunchKernelGGL((prod_mid_two_kernel<T, BM, BN, S, KS, Epi0, Epi1>), dim3(grid), dim3(256 * KS), 0, s, q, e0, e1);
+    return hipGetLastError();
+}
+
+// Two such products in one launch, which leaves no CU idle between them or in
+// the last round of the first.
+template <int T, class Epi0, class Epi1>
+hipError_t launch_prod_two(const ProdArgs &p0, const Epi0 &e0, const ProdArgs &p1, const Epi1 &e1, hipStream_t s) {
+    ProdPair q;
+    q.p[0] = p0;
+    q.p[1] = p1;
+    const int64_t k0 = (p0.KB + 127) / 128, k1 = (p1.KB + 127) / 128;
+    const int64_t a128 = tiles_of(p0, 128, 128), b128 = tiles_of(p1, 128, 128);
+    // 256 x 256 tiles: the workgroups are divided so that the later of the two
+    // ends soonest, in K tiles of 1.4 us; 128 x 128: two a CU, 1.1 us
+    const int64_t a256 = tiles_of(p0, 256, 256), b256 = tiles_of(p1, 256, 256);
+    int64_t best = INT64_MAX;
+    for (int n = 8; n < 256; n += 8) {
+        const int64_t x = (a256 + n - 1) / n * k0, y = (b256 + 255 - n) / (256 - n) * k1, end = x > y ? x : y;
+        if (end < best) best = end, q.split = n;
+    }
+    const int64_t t128 = a128 + b128, longest = k0 > k1 ? k0 : k1;
+    const int64_t mid = t128 <= 512 ? longest : (a128 * k0 + b128 * k1) / 512 + longest / 2;
+    if (t128 > 256 && best * 14 <= mid * 11 && k0 > 0 && k1 > 0) {
+        prod_tiles(q.p[0], 256, 256);
+        prod_tiles(q.p[1], 256, 256);
+        q.p[0].run = (int)a256;
+        q.p[1].run = (int)b256;
+        hipLaunchKernelGGL((prod_w4_two_kernel<T, Epi0, Epi1>), dim3(256), dim3(256), 0, s, q, e0, e1);
+        return hipGetLastError();
+    }
+    // smaller tiles as launch_prod_tiles takes them
+    const int64_t t64 = tiles_of(p0, 64, 64) + tiles_of(p1, 64, 64);
+    if (t64 <= 64) return go_mid_two<T, 32, 32, 3, 4>(q, e0, e1, s);
+    if (t64 <= 128) return go_mid_two<T, 32, 64, 4, 2>(q, e0, e1, s);
+    if (t64 <= 256) return go_mid_two<T, 64, 64, 4, 2>(q, e0, e1, s);
+    if (t64 <= 512) return go_mid_two<T, 64, 128, 3, 2>(q, e0, e1, s);
+    if (t128 <= 256) return go_mid_two<T, 128, 128, 2, 2>(q, e0, e1, s);
+    return go_mid_two<T, 128, 128, 2, 1>(q, e0, e1, s);
 }
 
 template <int T, int MB, bool PAIR, class Epi>

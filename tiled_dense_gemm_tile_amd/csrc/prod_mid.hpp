@@ -21,10 +21,11 @@
 
 namespace tg {
 
-// QUARTERS: the tiles are the quarters of those 256 x 256 tiles (in prod_w4's
-// order) that fill no round of workgroups.
-template <int T, int BM, int BN, int S, int KS, bool PAIR, bool ANY, class Epi, bool QUARTERS = false>
-__global__ void __launch_bounds__(256 * KS) prod_mid_kernel(ProdArgs p, Epi e) {
+template <int BM, int BN, int S, int KS> constexpr int kMidLds = KS * S * (BM + BN) * 128;
+
+// Tile (tmi, tni); emit(acc, stage, lane, row0, col0) stores a wave's results.
+template <int T, int BM, int BN, int S, int KS, bool PAIR, bool ANY, class Emit>
+__device__ __forceinline__ void prod_mid_body(const ProdArgs &p, int tmi, int tni, char *lds, Emit &&emit) {
     constexpr int WTM = BM / 2, WTN = BN / 2, TM = WTM / 16, TN = WTN / 16;
     constexpr int LA = BM / 32, LB = BN / 32;          // load instructions of a wave a tile
     constexpr int SLOT_A = BM * 128, SLOT_B = BN * 128, B_BASE = S * SLOT_A;
@@ -36,24 +37,12 @@ __global__ void __launch_bounds__(256 * KS) prod_mid_kernel(ProdArgs p, Epi e) {
     static_assert(RING >= 4 * STAGE && RING >= (KS - 1) * 4 * SUMS + 4 * STAGE && RING <= 160 * 1024, "LDS");
     static_assert((S - 2) * (LA + LB) < 64, "vmcnt");
 
-    __shared__ __attribute__((aligned(1024))) char lds[RING];
-
     const int tid = threadIdx.x, lane = tid & 63;
     const int group = KS > 1 ? __builtin_amdgcn_readfirstlane(tid >> 8) : 0;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
     char *const smem = lds + group * GROUP;
     const int wm = wave >> 1, wn = wave & 1;
-    int tmi, tni;
-    if constexpr (QUARTERS) {
-        static_assert(BM == 128 && BN == 128, "quarters");
-        const int q = blockIdx.x & 3;
-        tile_order(p.run + (blockIdx.x >> 2), p.tiles_m * p.tiles_n, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
-        tmi = 2 * tmi + (q >> 1), tni = 2 * tni + (q & 1);
-    } else {
-        tile_order(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
-    }
     const int m0 = tmi * BM, n0 = tni * (PAIR ? BN / 2 : BN);
-    if (QUARTERS && (m0 >= p.M || n0 >= p.N)) return;  // (past the matrix's edge)
     const int KB = p.KB, nt = (KB + 128 * KS - 1) / (128 * KS);    // K tiles of a group: tile t is K tile KS t + group
 
     // Load instruction j of a wave: A rows 32 j + 8 wave + lane / 8; B the
@@ -220,8 +209,54 @@ __global__ void __launch_bounds__(256 * KS) prod_mid_kernel(ProdArgs p, Epi e) {
                 }
         stage_fence();
     }
-    e.template block<TM, TN, false, false>(acc, (float *)(KS > 1 ? lds + (KS - 1) * 4 * SUMS + wave * STAGE : lds + wave * STAGE),
-                                    lane, m0 + wm * WTM, n0 + wn * W, p.M, p.N);
+    emit(acc, (float *)(KS > 1 ? lds + (KS - 1) * 4 * SUMS + wave * STAGE : lds + wave * STAGE), lane, m0 + wm * WTM,
+         n0 + wn * W);
+}
+
+template <class Epi, int TM, int TN>
+__device__ __forceinline__ void emit_vgpr(const Epi &e, const ProdArgs &p, const f32x4 (&acc)[TM][TN], float *stage,
+                                          int lane, int row0, int col0) {
+    e.template block<TM, TN, false, false>(acc, stage, lane, row0, col0, p.M, p.N);
+}
+
+// QUARTERS: the tiles are the quarters of those 256 x 256 tiles (in prod_w4's
+// order) that fill no round of workgroups.
+template <int T, int BM, int BN, int S, int KS, bool PAIR, bool ANY, class Epi, bool QUARTERS = false>
+__global__ void __launch_bounds__(256 * KS) prod_mid_kernel(ProdArgs p, Epi e) {
+    __shared__ __attribute__((aligned(1024))) char lds[kMidLds<BM, BN, S, KS>];
+    int tmi, tni;
+    if constexpr (QUARTERS) {
+        static_assert(BM == 128 && BN == 128, "quarters");
+        const int q = blockIdx.x & 3;
+        tile_order(p.run + (blockIdx.x >> 2), p.tiles_m * p.tiles_n, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
+        tmi = 2 * tmi + (q >> 1), tni = 2 * tni + (q & 1);
+        if (tmi * BM >= p.M || tni * (PAIR ? BN / 2 : BN) >= p.N) return;    // (past the matrix's edge)
+    } else {
+        tile_order(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
+    }
+    prod_mid_body<T, BM, BN, S, KS, PAIR, ANY>(
+        p, tmi, tni, lds, [&](const auto &acc, float *stage, int lane, int row0, int col0)
+                              __attribute__((always_inline)) { emit_vgpr(e, p, acc, stage, lane, row0, col0); });
+}
+
+// Two products in one launch: workgroups below q.split run the first one's
+// tiles.
+template <int T, int BM, int BN, int S, int KS, class Epi0, class Epi1>
+__global__ void __launch_bounds__(256 * KS) prod_mid_two_kernel(ProdPair q, Epi0 e0, Epi1 e1) {
+    __shared__ __attribute__((aligned(1024))) char lds[kMidLds<BM, BN, S, KS>];
+    const bool second = (int)blockIdx.x >= q.split;
+    const ProdArgs p = second ? q.p[1] : q.p[0];
+    const int wg = second ? blockIdx.x - q.split : blockIdx.x, tiles = p.tiles_m * p.tiles_n;
+    if (wg >= tiles) return;                           // (split is rounded up)
+    int tmi, tni;
+    tile_order(wg, tiles, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
+    prod_mid_body<T, BM, BN, S, KS, false, false>(
+        p, tmi, tni, lds, [&](const auto &acc, float *stage, int lane, int row0, int col0) __attribute__((always_inline)) {
+            if (second)
+                emit_vgpr(e1, p, acc, stage, lane, row0, col0);
+            else
+                emit_vgpr(e0, p, acc, stage, lane, row0, col0);
+        });
 }
 
 }  // namespace tg

@@ -38,19 +38,25 @@ __device__ __forceinline__ void prod_mfma_agpr(f32x4 &acc, const u32x4 &a, const
 #undef TG_PROD_MFMA
 }
 
-// (operand rows on 16 bytes, KB > 0 a multiple of 16)
-template <int T, bool PAIR, class Epi>
-__global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
+constexpr int kW4Lds = 4 * 256 * 128 + 1024;
+
+// Workgroup wg of nwg that walk the tiles wg, wg + nwg, ... below p.run.
+// reload(): p again, from memory; emit(acc, stage, lane, row0, col0, M, N)
+// stores a quadrant's results, wait_stores() waits for all but their stores.  (Operand rows on 16 bytes, KB > 0 a multiple of
+// 16.)
+template <int T, bool PAIR, bool PREFETCH, class Reload, class Emit, class Wait>
+__device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg, char *smem, Reload &&reload,
+                                             Emit &&emit, Wait &&wait_stores) {
     constexpr int TM = 8, TN = 8, Q = TM * TN, SLOT = 256 * 128, B_BASE = 2 * SLOT;
     constexpr int BN = PAIR ? 128 : 256;               // result columns of a tile
     constexpr int W = BN / 2, STAGE = 16 * kStagePitch<W> * 4;
-    static_assert(2 * STAGE <= SLOT, "staging areas");
-    __shared__ __attribute__((aligned(1024))) char smem[4 * SLOT];
+    constexpr int PF = 3;                              // K tiles ahead
+    static_assert(2 * STAGE <= SLOT && kW4Lds == 4 * SLOT + 1024, "LDS");
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    int vt = blockIdx.x, tmi, tni;
+    int vt = wg, tmi, tni;
     tile_order(vt, p.tiles_m * p.tiles_n, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
     int m0 = tmi * 256, n0 = tni * BN;
     const int KB = p.KB, nt = (KB + 127) / 128;
@@ -81,84 +87,120 @@ __global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
     // the 8 XCDs: with rows a multiple of 4 KiB apart, a K tile's chunks of all
     // rows lie in few memory channels, and the XCDs would meet there (gated 8192
     // x 14336 x 4096: 1342 us, 1446 in step).
-    const int k_first = (int)(blockIdx.x & 7) * nt / 8 * 128;
+    const int k_first = (wg & 7) * nt / 8 * 128;
     auto koff = [&](int t) __attribute__((always_inline)) {
         const int k = t * 128 + k_first;
         return t >= nt ? KB : k >= nt * 128 ? k - nt * 128 : k;
     };
-    auto fetch_a = [&](int t, int j) __attribute__((always_inline)) {
+    // (into slot s: K tile t's is t % 2, a constant in the loop unrolled by two)
+    auto fetch_a = [&](int t, int s, int j) __attribute__((always_inline)) {
         const int k0 = koff(t);
         const uint32_t v = k0 + kc < KB ? aoff + k0 : kOOB;
-        dma(rA, (t & 1) * SLOT + (4 * j + wave) * 1024, v, j * astep);
+        dma(rA, s * SLOT + (4 * j + wave) * 1024, v, j * astep);
     };
-    auto fetch_b = [&](int t, int j) __attribute__((always_inline)) {
+    auto fetch_b = [&](int t, int s, int j) __attribute__((always_inline)) {
         const int k0 = koff(t);
         const uint32_t v = k0 + kc < KB ? boff + k0 : kOOB;
-        dma(rB, B_BASE + (t & 1) * SLOT + (4 * j + wave) * 1024, v, j * bstep);
+        dma(rB, B_BASE + s * SLOT + (4 * j + wave) * 1024, v, j * bstep);
+    };
+
+    // Lines of K tile t + PF brought into this XCD's L2, a 128-byte line a lane:
+    // of each of its panels a workgroup takes the part that falls to it among
+    // those that share the panel (in the tile order 8 share rows of A and 4 rows
+    // of B), 32 rows of A and 64 of B.  Four bytes of each line go to LDS that
+    // nobody reads; the wait at a window's end leaves them in flight.  Hides
+    // what the L2s miss (gradients of 8192 x 14336 x 4096: 3280 -> 3020 us; 2 or
+    // 5 tiles ahead the same).
+    auto pf_off = [&]() __attribute__((always_inline)) {
+        if (wave == 0) return lane < 32 ? (uint32_t)((32 * (tni & 7) + lane) * (int)p.lda) : kOOB;
+        if (PAIR) return wave < 3 && lane < 32 ? (uint32_t)((32 * (tmi & 3) + lane) * (int)ldb) : kOOB;
+        return wave == 1 ? (uint32_t)((64 * (tmi & 3) + lane) * (int)ldb) : kOOB;
+    };
+    uint32_t pfo = pf_off();
+    int pfk = 0;                                       // K offset of the tile next prefetched
+    auto prefetch = [&]() __attribute__((always_inline)) {
+        pfk = pfk + 128 >= nt * 128 ? pfk + 128 - nt * 128 : pfk + 128;    // (past the end: the circle again)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            wave == 0 ? rA : rB, (__attribute__((address_space(3))) void *)(smem + 4 * SLOT + wave * 256), 4, pfo, pfk, 0, 0);
     };
 
     const int fr = lane & 15, fq = lane >> 4, fswz = swz16(fr);
-    const int a_read = (wm * 128 + fr) * 128, b_read = B_BASE + (wn * 128 + fr) * 128;
+    int a_read[2], b_read[2];                          // [step]
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+        a_read[st] = (wm * 128 + fr) * 128 + (((4 * st + fq) ^ fswz) << 4);
+        b_read[st] = B_BASE + (wn * 128 + fr) * 128 + (((4 * st + fq) ^ fswz) << 4);
+    }
     f32x4 acc[TM][TN];
     u32x4 fa[2][TM], fb[2][TN];                        // [step][block]
-    // fragment read k of step st of tile t, in the order the MFMAs use them: A
+    // fragment read k of step st from slot s, in the order the MFMAs use them: A
     // block 0, B blocks 0 .. 7, A blocks 1 .. 7
-    auto read_frag = [&](int t, int st, int k) __attribute__((always_inline)) {
-        const int c = (t & 1) * SLOT + (((4 * st + fq) ^ fswz) << 4);
+    auto read_frag = [&](int s, int st, int k) __attribute__((always_inline)) {
         if (k == 0 || k > TN) {
             const int i = k == 0 ? 0 : k - TN;
-            fa[st][i] = *(const u32x4 *)(smem + a_read + i * 16 * 128 + c);
+            fa[st][i] = *(const u32x4 *)(smem + a_read[st] + (s * SLOT + i * 16 * 128));
         } else {
-            fb[st][k - 1] = *(const u32x4 *)(smem + b_read + (k - 1) * 16 * 128 + c);
+            fb[st][k - 1] = *(const u32x4 *)(smem + b_read[st] + (s * SLOT + (k - 1) * 16 * 128));
         }
     };
     auto mfma = [&](auto zero, int st, int i, int j) __attribute__((always_inline)) {
         prod_mfma_agpr<T, decltype(zero)::value>(acc[i][j], fb[st][j], fa[st][i]);
         __builtin_amdgcn_sched_barrier(0);
     };
-    // One K tile; FIRST: none before it (accumulators start from zero).
-    auto tile = [&](auto first, int t) __attribute__((always_inline)) {
+    // One K tile, in slot S; FIRST: none before it (accumulators start from zero).
+    auto tile = [&](auto first, auto slot, int t) __attribute__((always_inline)) {
+        constexpr int S = decltype(slot)::value;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             if constexpr (!decltype(first)::value) mfma(std::false_type(), 1, q / TN, q % TN);
-            if (q % 4 == 0) read_frag(t, 0, q / 4);
-            if (q % 8 == 2) fetch_a(t + 1, q / 8);
-            if (q % 8 == 6) fetch_b(t + 1, q / 8);
+            if (q % 4 == 0) read_frag(S, 0, q / 4);
+            if (q % 8 == 2) fetch_a(t + 1, 1 - S, q / 8);
+            if (q % 8 == 6) fetch_b(t + 1, 1 - S, q / 8);
+            if (PREFETCH && q == 63) prefetch();
         }
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             mfma(first, 0, q / TN, q % TN);
-            if (q % 3 == 0 && q / 3 < TM + TN) read_frag(t, 1, q / 3);
+            if (q % 3 == 0 && q / 3 < TM + TN) read_frag(S, 1, q / 3);
         }
-        wait_vmcnt<0>();                               // tile t + 1 landed
+        wait_vmcnt<PREFETCH ? 1 : 0>();                // tile t + 1 landed
         wait_lgkmcnt0();
         barrier();
     };
 
 #pragma unroll
-    for (int j = 0; j < 8; ++j) fetch_a(0, j);
+    for (int j = 0; j < 8; ++j) fetch_a(0, 0, j);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) fetch_b(0, j);
+    for (int j = 0; j < 8; ++j) fetch_b(0, 0, j);
     wait_vmcnt<0>();
     barrier();
     float *stage = (float *)(smem + (wave < 2 ? SLOT : B_BASE + SLOT) + (wave & 1) * STAGE);
     while (true) {
-        tile(std::true_type(), 0);
-        for (int t = 1; t < nt; ++t) tile(std::false_type(), t);
+        using even = std::integral_constant<int, 0>;
+        using odd = std::integral_constant<int, 1>;
+        pfk = (k_first + (PF - 1) * 128) % (nt * 128);
+        tile(std::true_type(), even(), 0);
+        int t = 1;
+        for (; t + 1 < nt; t += 2) {
+            tile(std::false_type(), odd(), t);
+            tile(std::false_type(), even(), t + 1);
+        }
+        if (t < nt) tile(std::false_type(), odd(), t);
 #pragma unroll
         for (int q = 0; q < Q; ++q) mfma(std::false_type(), 1, q / TN, q % TN);
         mfma_result_fence<TM, TN>(acc);
         // (every wave is past its last barrier, so past all reads of the slots;
         // the loads of the tile past the end have landed there)
-        const ProdArgs r = kernel_arg0_reloaded<ProdArgs>();
+        const ProdArgs r = reload();
         const int dm0 = m0, dn0 = n0;
-        vt += gridDim.x;
+        vt += nwg;
         const bool more = vt < r.run;
         if (more) {
             tile_order(vt, r.tiles_m * r.tiles_n, r.tiles_m, r.tiles_n, r.group_m, tmi, tni);
             m0 = tmi * 256;
             n0 = tni * BN;
             resources(r);
+            pfo = pf_off();
             int wv = wave;                             // (their LDS addresses are computed here, not held)
             asm volatile("" : "+s"(wv));
             const int k0 = koff(0);
@@ -168,20 +210,73 @@ __global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) dma(rB, B_BASE + (4 * j + wv) * 1024, vb, j * bstep);
         }
-        if (e.vec)
-            e.template block<TM, TN, true, true>(acc, stage, lane, dm0 + wm * 128, dn0 + wn * W, r.M, r.N);
-        else
-            e.template block<TM, TN, true, false>(acc, stage, lane, dm0 + wm * 128, dn0 + wn * W, r.M, r.N);
-        if (!more) break;
+        emit(acc, stage, lane, dm0 + wm * 128, dn0 + wn * W, r.M, r.N);
+        if (!more) {
+            wait_vmcnt<0>();
+            break;
+        }
         // the next tile's first loads landed; the results' stores issued after
         // them may still run
-        if (e.vec)
-            wait_vmcnt<Epi::template stores<TM, TN>()>();
-        else
-            wait_vmcnt<0>();
+        wait_stores();
         wait_lgkmcnt0();
         barrier();
     }
+}
+
+// An epilogue's results, and the wait that leaves their stores in flight.
+template <class Epi, int TM, int TN>
+__device__ __forceinline__ void emit_agpr(const Epi &e, const f32x4 (&acc)[TM][TN], float *stage, int lane, int row0,
+                                          int col0, int M, int N) {
+    if (e.vec)
+        e.template block<TM, TN, true, true>(acc, stage, lane, row0, col0, M, N);
+    else
+        e.template block<TM, TN, true, false>(acc, stage, lane, row0, col0, M, N);
+}
+template <class Epi>
+__device__ __forceinline__ void wait_emitted(const Epi &e) {
+    if (e.vec)
+        wait_vmcnt<Epi::template stores<8, 8>()>();
+    else
+        wait_vmcnt<0>();
+}
+
+template <int T, bool PAIR, bool PREFETCH, class Epi>
+__global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
+    __shared__ __attribute__((aligned(1024))) char smem[kW4Lds];
+    prod_w4_body<T, PAIR, PREFETCH>(
+        p, blockIdx.x, gridDim.x, smem, [] { return kernel_arg0_reloaded<ProdArgs>(); },
+        [&](const auto &acc, float *stage, int lane, int row0, int col0, int M, int N)
+            __attribute__((always_inline)) { emit_agpr(e, acc, stage, lane, row0, col0, M, N); },
+        [&]() __attribute__((always_inline)) { wait_emitted(e); });
+}
+
+// Two products in one launch: the first on workgroups below `split`, the second
+// on the others, each in rounds of its own.
+template <int T, class Epi0, class Epi1>
+__global__ void __launch_bounds__(256) prod_w4_two_kernel(ProdPair q, Epi0 e0, Epi1 e1) {
+    __shared__ __attribute__((aligned(1024))) char smem[kW4Lds];
+    const bool second = (int)blockIdx.x >= q.split;
+    const ProdArgs p = second ? q.p[1] : q.p[0];
+    const int wg = second ? blockIdx.x - q.split : blockIdx.x;
+    if (wg >= p.run) return;                           // (more workgroups than tiles)
+    prod_w4_body<T, false, true>(
+        p, wg, second ? gridDim.x - q.split : q.split, smem,
+        [&]() __attribute__((always_inline)) {
+            const ProdPair r = kernel_arg0_reloaded<ProdPair>();
+            return second ? r.p[1] : r.p[0];
+        },
+        [&](const auto &acc, float *stage, int lane, int row0, int col0, int M, int N) __attribute__((always_inline)) {
+            if (second)
+                emit_agpr(e1, acc, stage, lane, row0, col0, M, N);
+            else
+                emit_agpr(e0, acc, stage, lane, row0, col0, M, N);
+        },
+        [&]() __attribute__((always_inline)) {
+            if (second)
+                wait_emitted(e1);
+            else
+                wait_emitted(e0);
+        });
 }
 
 }  // namespace tg
