@@ -98,49 +98,42 @@ hipError_t launch_prod_aligned(const ProdArgs &p, const Epi &e, hipStream_t s) {
     return launch_prod_tiles<T, false, false, Epi>(p, e, s);
 }
 
-template <int T, int BM, int BN, int S, int KS, class Epi0, class Epi1>
-hipError_t go_mid_two(ProdPair q, const Epi0 &e0, const Epi1 &e1, hipStream_t s) {
-    q.split = (int)(prod_tiles(q.p[0], BM, BN) + 7) / 8 * 8;
-    const unsigned grid = (unsigned)q.split + prod_tiles(q.p[1], BM, BN);
-    hipLaunchKernelGGL((prod_mid_two_kernel<T, BM, BN, S, KS, Epi0, Epi1>), dim3(grid), dim3(256 * KS), 0, s, q, e0, e1);
-    return hipGetLastError();
+// About how long such a product takes by itself, in us.
+inline double prod_estimate(const ProdArgs &p) {
+    const double k = (p.KB + 127) / 128;
+    if (tiles_of(p, 64, 64) <= 256) return 0.4 * k;
+    const int64_t t128 = tiles_of(p, 128, 128), t256 = tiles_of(p, 256, 256), rest = t256 % 256;
+    if (t128 <= 512) return (t128 <= 256 ? 0.75 : 1.1) * k;
+    return 1.41 * k * ((double)(t256 / 256) + (rest == 0 ? 0 : t256 < 256 || rest > 128 ? 1 : rest > 64 ? 0.75 : 0.5));
 }
 
-// Two such products in one launch, which leaves no CU idle between them or in
-// the last round of the first.
+// Two such products.  One launch of 256 x 256 tiles, each product on a share of
+// the CUs, takes longer for a K tile (1.57 us in place of 1.41: two sets of
+// panels share the L2s), but leaves no CU idle in a last round and suits a
+// product with too few tiles for the GPU (gradients of 4096 x 6000 x 2048: 403
+// us, one after the other 478; 8192 x 1000 x 4096 267 and 296; 8192 x 14336 x
+// 4096, whose tiles fill whole rounds, 3281 and 3043).
 template <int T, class Epi0, class Epi1>
 hipError_t launch_prod_two(const ProdArgs &p0, const Epi0 &e0, const ProdArgs &p1, const Epi1 &e1, hipStream_t s) {
     ProdPair q;
     q.p[0] = p0;
     q.p[1] = p1;
+    q.split = 128;
     const int64_t k0 = (p0.KB + 127) / 128, k1 = (p1.KB + 127) / 128;
-    const int64_t a128 = tiles_of(p0, 128, 128), b128 = tiles_of(p1, 128, 128);
-    // 256 x 256 tiles: the workgroups are divided so that the later of the two
-    // ends soonest, in K tiles of 1.4 us; 128 x 128: two a CU, 1.1 us
-    const int64_t a256 = tiles_of(p0, 256, 256), b256 = tiles_of(p1, 256, 256);
-    int64_t best = INT64_MAX;
+    const int64_t a = prod_tiles(q.p[0], 256, 256), b = prod_tiles(q.p[1], 256, 256);
+    int64_t best = INT64_MAX;                          // the share that lets the later one end soonest
     for (int n = 8; n < 256; n += 8) {
-        const int64_t x = (a256 + n - 1) / n * k0, y = (b256 + 255 - n) / (256 - n) * k1, end = x > y ? x : y;
+        const int64_t x = (a + n - 1) / n * k0, y = (b + 255 - n) / (256 - n) * k1, end = x > y ? x : y;
         if (end < best) best = end, q.split = n;
     }
-    const int64_t t128 = a128 + b128, longest = k0 > k1 ? k0 : k1;
-    const int64_t mid = t128 <= 512 ? longest : (a128 * k0 + b128 * k1) / 512 + longest / 2;
-    if (t128 > 256 && best * 14 <= mid * 11 && k0 > 0 && k1 > 0) {
-        prod_tiles(q.p[0], 256, 256);
-        prod_tiles(q.p[1], 256, 256);
-        q.p[0].run = (int)a256;
-        q.p[1].run = (int)b256;
+    if (k0 > 0 && k1 > 0 && 1.57 * (double)best < prod_estimate(p0) + prod_estimate(p1)) {
+        q.p[0].run = (int)a;
+        q.p[1].run = (int)b;
         hipLaunchKernelGGL((prod_w4_two_kernel<T, Epi0, Epi1>), dim3(256), dim3(256), 0, s, q, e0, e1);
         return hipGetLastError();
     }
-    // smaller tiles as launch_prod_tiles takes them
-    const int64_t t64 = tiles_of(p0, 64, 64) + tiles_of(p1, 64, 64);
-    if (t64 <= 64) return go_mid_two<T, 32, 32, 3, 4>(q, e0, e1, s);
-    if (t64 <= 128) return go_mid_two<T, 32, 64, 4, 2>(q, e0, e1, s);
-    if (t64 <= 256) return go_mid_two<T, 64, 64, 4, 2>(q, e0, e1, s);
-    if (t64 <= 512) return go_mid_two<T, 64, 128, 3, 2>(q, e0, e1, s);
-    if (t128 <= 256) return go_mid_two<T, 128, 128, 2, 2>(q, e0, e1, s);
-    return go_mid_two<T, 128, 128, 2, 1>(q, e0, e1, s);
+    const hipError_t err = launch_prod_aligned<T>(p0, e0, s);
+    return err != hipSuccess ? err : launch_prod_aligned<T>(p1, e1, s);
 }
 
 template <int T, int MB, bool PAIR, class Epi>

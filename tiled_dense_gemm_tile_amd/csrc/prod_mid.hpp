@@ -239,24 +239,4 @@ __global__ void __launch_bounds__(256 * KS) prod_mid_kernel(ProdArgs p, Epi e) {
                               __attribute__((always_inline)) { emit_vgpr(e, p, acc, stage, lane, row0, col0); });
 }
 
-// Two products in one launch: workgroups below q.split run the first one's
-// tiles.
-template <int T, int BM, int BN, int S, int KS, class Epi0, class Epi1>
-__global__ void __launch_bounds__(256 * KS) prod_mid_two_kernel(ProdPair q, Epi0 e0, Epi1 e1) {
-    __shared__ __attribute__((aligned(1024))) char lds[kMidLds<BM, BN, S, KS>];
-    const bool second = (int)blockIdx.x >= q.split;
-    const ProdArgs p = second ? q.p[1] : q.p[0];
-    const int wg = second ? blockIdx.x - q.split : blockIdx.x, tiles = p.tiles_m * p.tiles_n;
-    if (wg >= tiles) return;                           // (split is rounded up)
-    int tmi, tni;
-    tile_order(wg, tiles, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
-    prod_mid_body<T, BM, BN, S, KS, false, false>(
-        p, tmi, tni, lds, [&](const auto &acc, float *stage, int lane, int row0, int col0) __attribute__((always_inline)) {
-            if (second)
-                emit_vgpr(e1, p, acc, stage, lane, row0, col0);
-            else
-                emit_vgpr(e0, p, acc, stage, lane, row0, col0);
-        });
-}
-
 }  // namespace tg

@@ -154,8 +154,8 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
         for (int q = 0; q < Q; ++q) {
             if constexpr (!decltype(first)::value) mfma(std::false_type(), 1, q / TN, q % TN);
             if (q % 4 == 0) read_frag(S, 0, q / 4);
-            if (q % 8 == 2) fetch_a(t + 1, 1 - S, q / 8);
-            if (q % 8 == 6) fetch_b(t + 1, 1 - S, q / 8);
+            if (q % 8 == 0) fetch_a(t + 1, 1 - S, q / 8);
+            if (q % 8 == 4) fetch_b(t + 1, 1 - S, q / 8);
             if (PREFETCH && q == 63) prefetch();
         }
 #pragma unroll
