@@ -67,26 +67,25 @@ hipError_t launch_prod_tiles(const ProdArgs &p, const Epi &e, hipStream_t s) {
         // 90 against 66)
         if (t128 > 512 && p.KB > 0) return go_w4<T, PAIR>(p, e, s);
     }
-    // few tiles: small ones, K cut over the waves (int8 64 x 4096 x 14336: 32 x
-    // 32 over four groups 20.7, 64 x 64 over two 37.7, over one 37.4; 128 x 4096
-    // x 4096: 32 x 64 10.2, 64 x 64 12.6; gated 64 x 4096 x 4096 22.1 and 25.7)
+    // The smallest tiles of which every CU has one at most, K cut over the waves
+    // (int8 40 x 4096 x 4096: 256 tiles of 32 x 32 7.8, of 32 x 64 9.4, of 64 x 64
+    // 11.7; 77 x 4096 x 4096: 384 of 32 x 32 13.3, 192 of 32 x 64 9.6; gated 200 x
+    // 2048 x 4096: 64 x 64 17.3, 32 x 64 27.0; int8 300 x 4096 x 4096: 64 x 128
+    // 17.0, 64 x 64 21.5).  Through registers two groups are too many but for
+    // the smallest and the widest (int8 40 x 4099 x 4100: 32 x 64 in one group
+    // 11.6, two 12.5; 130 x 4099 x 4100: 64 x 64 13.8 either way).
     if constexpr (!PAIR)
-        if (t64 <= 64) return go_mid<T, 32, 32, 3, 4, PAIR, ANY>(p, e, s);
-    if (t64 <= 128) return go_mid<T, 32, 64, 4, 2, PAIR, ANY>(p, e, s);
+        if (tiles_of(p, 32, 32) <= 256) return go_mid<T, 32, 32, 3, ANY ? 2 : 4, PAIR, ANY>(p, e, s);
+    if (tiles_of(p, 32, 64 / D) <= 256) return go_mid<T, 32, 64, 4, ANY ? 1 : 2, PAIR, ANY>(p, e, s);
     // (rows for one 64-row tile only: larger ones would be part empty.  int8 48
     // x 65536 x 4096: 59.5, 128 x 128 72.7)
     if (p.M <= 64) return go_mid<T, 64, 64, 4, 1, PAIR, ANY>(p, e, s);
-    // gated 256 x 2048 x 2048: 9.4, over one group 11.0, 64 x 128 11.7
-    if (t64 <= 256) return go_mid<T, 64, 64, 4, 2, PAIR, ANY>(p, e, s);
-    if constexpr (ANY) {
-        if (t64 <= 512) return go_mid<T, 64, 64, 2, 1, PAIR, ANY>(p, e, s);
-    } else {
-        // int8 512 x 4096 x 4096: 15.0; 64 x 64 18.1, 128 x 128 21.1
-        if (t64 <= 512) return go_mid<T, 64, 128, 3, 2, PAIR, ANY>(p, e, s);
-        // int8 1000 x 4096 x 4096: 23.5, over one group 28.7, 64 x 64 32.1;
-        // gated 128 x 14336 x 4096 41 and 47
+    if (t64 <= 256) return go_mid<T, 64, 64, 4, ANY ? 1 : 2, PAIR, ANY>(p, e, s);
+    if (tiles_of(p, 64, 128 / D) <= 256) return go_mid<T, 64, 128, 3, 2, PAIR, ANY>(p, e, s);
+    // int8 1000 x 4096 x 4096: two groups 23.5, one 28.7, 64 x 64 32.1; gated 128
+    // x 14336 x 4096 41 and 47
+    if constexpr (!ANY)
         if (t128 <= 256) return go_mid<T, 128, 128, 2, 2, PAIR, ANY>(p, e, s);
-    }
     // two workgroups a CU (gated 1024 x 2736 x 1008: 19.2; four slots and one
     // workgroup 29.3, 64 x 64 28.4)
     return go_mid<T, 128, 128, 2, 1, PAIR, ANY>(p, e, s);
