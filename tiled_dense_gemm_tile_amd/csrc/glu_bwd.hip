@@ -55,25 +55,33 @@ __global__ void __launch_bounds__(256) glu_bwd_operands_kernel(GluBwdArgs p) {
     const int n_act = p.tm * p.tf;
     if (w < n_act) {
         const int m0 = w / p.tf * kCopyTile, f0 = w % p.tf * kCopyTile;
+        // (all loads first; past the matrix those of its last row or first
+        // features, which become zeros)
+        typename R::V dh[2], g[2], u[2];
+        const int f = f0 + c, fc = f < p.F ? f : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t m = m0 + r0 + 32 * h < p.M ? m0 + r0 + 32 * h : p.M - 1;
+            dh[h] = R::load_raw((const uint16_t *)p.dH + m * p.lddh, fc, p.F);
+            g[h] = R::load_raw((const uint16_t *)p.G + m * p.ldg, fc, p.F);
+            u[h] = R::load_raw((const uint16_t *)p.U + m * p.ldu, fc, p.F);
+        }
         with_act(p.act, [&](auto a) __attribute__((always_inline)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int m = m0 + r0 + 32 * h, f = f0 + c;
-                uint16_t dg[8] = {}, du[8] = {};
-                if (m < p.M && f < p.F) {
-                    const typename R::V dh = R::load((const uint16_t *)p.dH + m * p.lddh, f, p.F);
-                    const typename R::V g = R::load((const uint16_t *)p.G + m * p.ldg, f, p.F);
-                    const typename R::V u = R::load((const uint16_t *)p.U + m * p.ldu, f, p.F);
+                const int m = m0 + r0 + 32 * h;
+                const bool in = m < p.M && f < p.F;
+                const typename R::V d = R::settle(dh[h], fc, p.F), gv = R::settle(g[h], fc, p.F),
+                                    uv = R::settle(u[h], fc, p.F);
+                uint16_t dg[8], du[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float value, slope;
-                        const float d = Elem<T>::up(dh[i]);
-                        act_both<decltype(a)::value>(Elem<T>::up(g[i]), value, slope);
-                        if (f + i < p.F) {
-                            dg[i] = __builtin_bit_cast(uint16_t, Elem<T>::down(d * Elem<T>::up(u[i]) * slope));
-                            du[i] = __builtin_bit_cast(uint16_t, Elem<T>::down(d * value));
-                        }
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    float value, slope;
+                    act_both<decltype(a)::value>(Elem<T>::up(gv[i]), value, slope);
+                    const auto x = Elem<T>::down(Elem<T>::up(d[i]) * Elem<T>::up(uv[i]) * slope);
+                    const auto y = Elem<T>::down(Elem<T>::up(d[i]) * value);
+                    dg[i] = in && f + i < p.F ? __builtin_bit_cast(uint16_t, x) : 0;
+                    du[i] = in && f + i < p.F ? __builtin_bit_cast(uint16_t, y) : 0;
                 }
                 if (p.dgu && m < p.M) {
                     uint16_t *row = p.dgu + (int64_t)m * p.ldf;
@@ -113,20 +121,25 @@ __global__ void __launch_bounds__(256) glu_bwd_operands_kernel(GluBwdArgs p) {
         dst = p.wt + (up ? p.Fp : 0), ldd = p.ldf;
     }
     const int a0 = w / p.tk * kCopyTile, k0 = w % p.tk * kCopyTile;
+    const int k = k0 + c, kk = k < p.K ? k : 0;
+    typename R::V v[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int r = a0 + r0 + 32 * h, k = k0 + c;
-        typename R::V v = {};
-        if (r < rows && k < p.K) v = R::load(src + r * lds_, k, p.K);
-        const u32x4 e = __builtin_bit_cast(u32x4, v);
+        const int64_t r = a0 + r0 + 32 * h < rows ? a0 + r0 + 32 * h : rows - 1;
+        v[h] = R::load_raw(src + r * lds_, kk, p.K);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        u32x4 e = __builtin_bit_cast(u32x4, R::settle(v[h], kk, p.K));
+        if (a0 + r0 + 32 * h >= rows) e = u32x4{0u, 0u, 0u, 0u};    // (columns past K are not stored)
 #pragma unroll
         for (int i = 0; i < 4; ++i) *(uint32_t *)(lds[0] + (r0 + 32 * h) * kCopyPitch + c + 2 * i) = e[i];
     }
     __syncthreads();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int k = r0 + 32 * h, r = c;
-        if (k0 + k < p.K) *(u32x4 *)(dst + (int64_t)(k0 + k) * ldd + a0 + r) = tile_column(lds[0], r, k);
+        const int row = r0 + 32 * h;
+        if (k0 + row < p.K) *(u32x4 *)(dst + (int64_t)(k0 + row) * ldd + a0 + c) = tile_column(lds[0], c, row);
     }
 }
 
