@@ -217,7 +217,8 @@ def test_glu_gradient_is_the_slope(name):
 # ---- 8-bit integers -----------------------------------------------------------------
 
 @pytest.mark.parametrize("rows,n", [(1, 1), (1, 14336), (3, 7), (5, 64), (70, 511), (4, 513), (9, 2048), (33, 4100), (2, 8200),
-                                    (3, 16385), (2, 40000), (1000, 96)])
+                                    (3, 16385), (2, 40000), (1000, 96), (1500, 96), (1100, 700), (1024, 1500),
+                                    (1030, 3001), (1025, 5000), (1025, 9001), (1024, 17000), (7, 1200), (5, 3000), (1, 20000)])
 @pytest.mark.parametrize("dtype", [F32, BF, FP], ids=KIND.get)
 def test_quantize(rows, n, dtype):
     x = rand(rows + n, rows, n, dtype=dtype)

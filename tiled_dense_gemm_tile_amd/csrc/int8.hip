@@ -9,7 +9,7 @@ namespace tg {
 // One row in the registers of NT threads, NV vectors of 16 bytes each; WIDE
 // rows are read twice (the second time from the caches).  The row's largest
 // magnitude as bits: an infinity or a NaN shows as a larger number than any
-// finite one.
+// finite one.  Bound by memory (8192 x 14336 bf16 66 to 75 us, 4.7 to 5.3 TB/s).
 struct QuantArgs {
     const void *X;
     int8_t *Q;
@@ -67,8 +67,8 @@ __device__ __forceinline__ void store_codes(int8_t *q, int c, int n, const typen
 }
 
 template <int T, int NT, int NV, bool WIDE>
-__global__ void __launch_bounds__(NT < 256 ? 256 : NT) int8_quantize_kernel(QuantArgs p) {
-    constexpr int VE = kVE<T>, RPW = NT < 256 ? 256 / NT : 1, NW = NT / 64;    // rows of a workgroup, waves of a row
+__global__ void __launch_bounds__(NT < 128 ? 256 : NT) int8_quantize_kernel(QuantArgs p) {
+    constexpr int VE = kVE<T>, RPW = NT < 128 ? 256 / NT : 1, NW = NT / 64;    // rows of a workgroup, waves of a row
     const int t = threadIdx.x % NT, sub = threadIdx.x / NT;
     const int lane = threadIdx.x & 63, wave = t >> 6;
     __shared__ uint32_t top[NW > 1 ? NW : 1];
@@ -96,11 +96,13 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) int8_quantize_kernel(Quan
                 m = m > b ? m : b;
             }
         }
-#pragma unroll
-        for (int by = 1; by < 64; by *= 2) {
-            const uint32_t b = __shfl_xor(m, by);
-            m = m > b ? m : b;
-        }
+        auto join = [&](uint32_t b) __attribute__((always_inline)) { m = m > b ? m : b; };
+        join(dpp<kXor1>(m));
+        join(dpp<kXor2>(m));
+        join(dpp<kMirror8>(m));
+        join(dpp<kMirror16>(m));
+        join(__shfl_xor(m, 16));
+        join(__shfl_xor(m, 32));
         if constexpr (NW > 1) {
             __syncthreads();                           // (the last row's reads of top)
             if (lane == 0) top[wave] = m;
@@ -130,10 +132,10 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) int8_quantize_kernel(Quan
 
 template <int T, int NT, int NV, bool WIDE = false>
 hipError_t go_quantize(const QuantArgs &p, hipStream_t s) {
-    constexpr int RPW = NT < 256 ? 256 / NT : 1;
+    constexpr int RPW = NT < 128 ? 256 / NT : 1;
     const int64_t want = (p.rows + RPW - 1) / RPW;
     hipLaunchKernelGGL((int8_quantize_kernel<T, NT, NV, WIDE>), dim3((unsigned)(want < kMaxGrid ? want : kMaxGrid)),
-                       dim3(NT < 256 ? 256 : NT), 0, s, p);
+                       dim3(NT < 128 ? 256 : NT), 0, s, p);
     return hipGetLastError();
 }
 
@@ -141,10 +143,24 @@ template <int T>
 hipError_t launch_quantize(const QuantArgs &p, hipStream_t s) {
     const int nvec = (int)(((int64_t)p.N + kVE<T> - 1) / kVE<T>);
     if (nvec <= 64) return go_quantize<T, 64, 1>(p, s);
-    if (nvec <= 256) return go_quantize<T, 256, 1>(p, s);
-    if (nvec <= 512) return go_quantize<T, 256, 2>(p, s);
-    if (nvec <= 1024) return go_quantize<T, 256, 4>(p, s);
-    if (nvec <= 2048) return go_quantize<T, 256, 8>(p, s);
+    // Few rows: as many threads as there are vectors (64 x 14336 bf16: 4.9 us, of
+    // 256 threads 8.1).  Many: more vectors a thread, as joining the threads'
+    // maxima and the division come once a row (16384 x 4096 bf16: 256 x 2 37.3,
+    // 512 x 1 58.5; 20000 x 1024: 64 x 2 14.1, 128 x 1 18.9, 256 x 1 28.2; 8192
+    // x 2048: 128 x 2 12.9, 256 x 1 16.4).
+    if (p.rows < 1024) {
+        if (nvec <= 128) return go_quantize<T, 128, 1>(p, s);
+        if (nvec <= 256) return go_quantize<T, 256, 1>(p, s);
+        if (nvec <= 512) return go_quantize<T, 512, 1>(p, s);
+        if (nvec <= 1024) return go_quantize<T, 1024, 1>(p, s);
+        if (nvec <= 2048) return go_quantize<T, 1024, 2>(p, s);
+    } else {
+        if (nvec <= 128) return go_quantize<T, 64, 2>(p, s);
+        if (nvec <= 256) return go_quantize<T, 128, 2>(p, s);
+        if (nvec <= 512) return go_quantize<T, 256, 2>(p, s);
+        if (nvec <= 1024) return go_quantize<T, 256, 4>(p, s);
+        if (nvec <= 2048) return go_quantize<T, 256, 8>(p, s);
+    }
     if (nvec <= 4096) return go_quantize<T, 512, 8>(p, s);
     return go_quantize<T, 1024, 1, true>(p, s);
 }
