@@ -233,3 +233,49 @@ def test_binding_refuses_host_tensors_and_types():
                  lambda: tg.gemm_int8(x, s, q, s)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_checks_in_cpp_say_what_python_says():
+    """The binding's checks in C++ against their Python form, over every way a matrix or a vector can be wrong."""
+    fast = pytest.importorskip("tiled_dense_gemm_tile_amd._tensors")
+    from tiled_dense_gemm_tile_amd import ops
+    bf, f32 = (torch.bfloat16,), (torch.float32, torch.bfloat16)
+    m = torch.zeros(6, 10).bfloat16()
+    cases = [(m, (6, 10), bf), (m, (6, 10), f32), (m, (6, 10), (torch.float16,)), (m, (5, 10), bf), (m[:, :4], (6, 4), bf),
+             (m.t(), (10, 6), bf), (m[::2], (3, 10), bf), (m[:, ::2], (6, 5), bf), (m[:, :1], (6, 1), bf), (m[:1], (1, 10), bf),
+             (m[2:3, :4], (1, 4), bf), (m[:0], (0, 10), bf), (m[0], (1, 10), bf), (m[:, :0], (6, 0), bf),
+             (m.as_strided((1, 10), (1 << 22, 1)), (1, 10), bf), (m.as_strided((1, 10), (3, 1)), (1, 10), bf)]
+    slow, ops._fast = ops._fast, None
+    try:
+        for t, shape, types in cases:
+            for dev in (-1, 0):
+                try:
+                    want = ops._matrix("t", t, shape, types, dev)
+                except (TypeError, ValueError):
+                    want = None
+                assert fast.matrix(t, shape, types, dev) == want, (t.shape, t.stride(), shape, types, dev)
+        v = torch.zeros(12)
+        for t, n, types in ((v, 12, f32), (v, 11, f32), (v, 12, bf), (v[::2], 6, f32), (v[:1], 1, f32), (v[::12], 1, f32), (m, 6, f32)):
+            for dev in (-1, 0):
+                try:
+                    want = ops._vector("t", t, n, types, dev)
+                except (TypeError, ValueError):
+                    want = None
+                assert fast.vector(t, n, types, dev) == want
+    finally:
+        ops._fast = slow
+    assert fast.matrix(None, (1, 1), bf, -1) is None and fast.matrix(m.to_sparse(), (6, 10), bf, -1) is None
+    # lists on the host, of other types, or empty are left to Python
+    assert fast.gradients([]) is None and fast.gradients([m]) is None and fast.gradients([1]) is None
+
+
+def test_calls_in_cpp_refuse_wrong_counts():
+    fast = pytest.importorskip("tiled_dense_gemm_tile_amd._tensors")
+    from tiled_dense_gemm_tile_amd import layers
+    f = layers._entry("gemm_int8")
+    assert f is fast.gemm_int8
+    with pytest.raises(TypeError):
+        f(1, 2, 3)
+    with pytest.raises(TypeError):
+        f(*["x"] * 15)
+    assert f(-1, 4, 4, 1, 64, 1, 1, 64, 1, None, 0, 1, 64, 0, None) == INVALID_SIZE

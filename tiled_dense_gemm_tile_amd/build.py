@@ -1,4 +1,4 @@
-"""Build libtilegemm.so in-tree with hipcc for gfx950.
+"""Build libtilegemm.so in-tree with hipcc for gfx950, and the binding's _tensors.so with g++.
 
     python -m tiled_dense_gemm_tile_amd.build
 
@@ -25,6 +25,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 OUT = os.path.join(HERE, "libtilegemm.so")
+BINDING = os.path.join(HERE, "_tensors.so")
 OBJDIR = os.path.join(ROOT, "_build")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -85,13 +86,35 @@ def _compile(src):
     return obj, compile_unit(src, obj)
 
 
+def build_binding() -> str:
+    """The binding's part in C++ (csrc/tensors.cpp), against the installed torch."""
+    import sysconfig
+
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I" + inc,
+           "-I" + os.path.join(inc, "torch", "csrc", "api", "include"), "-I" + sysconfig.get_paths()["include"],
+           "-I" + os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"), os.path.join(CSRC, "tensors.cpp"),
+           "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for tensors.cpp:\n%s\n%s" % (r.stdout, r.stderr))
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = True) -> str:
     if shutil.which(HIPCC) is None and not os.path.exists(HIPCC):
         raise RuntimeError("hipcc not found at %s" % HIPCC)
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        binding = ex.submit(build_binding)
         done = list(ex.map(_compile, srcs))
+        binding.result()
     objs = [o for o, _ in done]
     kernels = [k for _, ks in done for k in ks]
     with open(os.path.join(OBJDIR, "resource_usage.txt"), "w") as f:

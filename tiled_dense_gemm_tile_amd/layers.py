@@ -11,15 +11,32 @@ current stream of the tensors' GPU.
 """
 from __future__ import annotations
 
+import ctypes
 from array import array
 
 import torch
 
 from . import _load
-from .ops import _F32, _NONE, _TYPES, _device, _matrix, _new, _rows, _run, _vector, _workspace
+from .ops import _F32, _NONE, _TYPES, _device, _fast, _matrix, _new, _rows, _run, _vector, _workspace
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 _INT8 = (torch.int8,)
+
+
+_entries = {}
+
+
+def _entry(name):
+    """The C function, called without ctypes' conversions where csrc/tensors.cpp
+    is built."""
+    f = _entries.get(name)
+    if f is None:
+        f = getattr(_load(), name)
+        if _fast is not None:
+            _fast.bind(name, ctypes.cast(f, ctypes.c_void_p).value)
+            f = getattr(_fast, name)
+        _entries[name] = f
+    return f
 
 
 def _act(name):
@@ -57,7 +74,7 @@ def gemm_glu(X, Wg, Wu, act="silu", H=None, G=None, U=None, keep=False):
         U = _new((M, F), X.dtype, dev) if U is None else U
     g = _NONE if G is None else _matrix("G", G, (M, F), own, dev)
     u = _NONE if U is None else _matrix("U", U, (M, F), own, dev)
-    _run(_load().gemm_glu, dev, M, F, K, *x, *wg, *wu, _TYPES[X.dtype], _act(act), *_matrix("H", H, (M, F), own, dev),
+    _run(_entry("gemm_glu"), dev, M, F, K, *x, *wg, *wu, _TYPES[X.dtype], _act(act), *_matrix("H", H, (M, F), own, dev),
          *g, *u)
     return H if G is None and U is None else (H, G, U)
 
@@ -110,9 +127,8 @@ def gemm_glu_backward(dH, G, U, X, Wg, Wu, act="silu", Cg=None, Cu=None, dX=None
             cg, cu = _matrix("Cg", Cg, (F, K), grad, dev), _matrix("Cu", Cu, (F, K), grad, dev)
     elif not (dWg is dWu is Cg is Cu is None):
         raise ValueError("dWg, dWu, Cg or Cu given with weight_grad=False")
-    L = _load()
-    workspace, *ws = _workspace(workspace, workspace is None and L.gemm_glu_backward_workspace_bytes(M, F, K), dev)
-    _run(L.gemm_glu_backward, dev, M, F, K, *dh, *g, *u, *x, *wg, *wu, _TYPES[X.dtype], _act(act), *dx, *cg, *cu,
+    workspace, *ws = _workspace(workspace, workspace is None and gemm_glu_backward_workspace_bytes(M, F, K), dev)
+    _run(_entry("gemm_glu_backward"), dev, M, F, K, *dh, *g, *u, *x, *wg, *wu, _TYPES[X.dtype], _act(act), *dx, *cg, *cu,
          *dwg, *dwu, _TYPES[grad_dtype], *ws)
     return dX, dWg, dWu
 
@@ -128,7 +144,7 @@ def int8_quantize(X, Q=None, S=None):
         Q = _new(shape, torch.int8, dev)
     if S is None:
         S = _new(shape[0], torch.float32, dev)
-    _run(_load().int8_quantize, dev, *shape, *x, code, *_matrix("Q", Q, shape, _INT8, dev),
+    _run(_entry("int8_quantize"), dev, *shape, *x, code, *_matrix("Q", Q, shape, _INT8, dev),
          _vector("S", S, shape[0], _F32, dev))
     return Q, S
 
@@ -156,7 +172,7 @@ def gemm_int8(A, SA, B, SB, C=None, out_dtype=None, D=None):
     c = _NONE
     if C is not None:
         c = (_vector("C", C, N, own, dev), 0) if C.dim() == 1 else _matrix("C", C, (M, N), own, dev)
-    _run(_load().gemm_int8, dev, M, N, K, *a, sa, *b, sb, *c, *_matrix("D", D, (M, N), own, dev), _TYPES[out_dtype])
+    _run(_entry("gemm_int8"), dev, M, N, K, *a, sa, *b, sb, *c, *_matrix("D", D, (M, N), own, dev), _TYPES[out_dtype])
     return D
 
 
@@ -177,6 +193,9 @@ def _dense(t):
 def _gradients(name, grads):
     """(device, whether all are contiguous, addresses, sizes, types) of a list
     of tensors: the arrays that the C calls read."""
+    if _fast is not None and (found := _fast.gradients(grads)) is not None:
+        dev, at, sizes, types = found
+        return dev, True, at, memoryview(sizes).cast("q"), types
     if not grads:
         raise ValueError("no %s" % name)
     dev = _device(grads[0])
@@ -194,6 +213,8 @@ def _gradients(name, grads):
 
 def _twice(at, sizes):
     """Whether two tensors with elements start at the same address."""
+    if isinstance(at, bytes):
+        at = memoryview(at).cast("q")
     if len(set(at)) == len(at):
         return False
     at = [a for a, n in zip(at, sizes) if n]
@@ -201,7 +222,10 @@ def _twice(at, sizes):
 
 
 def _at(a):
-    return a.buffer_info()[0]
+    """What a call takes as the address of the array (a bytes object as it is)."""
+    if isinstance(a, memoryview):
+        return a.obj
+    return a if isinstance(a, bytes) else a.buffer_info()[0]
 
 
 def grad_workspace_bytes(n: int) -> int:
@@ -221,7 +245,7 @@ def grad_norm(grads, norm=None, workspace=None):
     dev, _, at, sizes, types = _gradients("gradients", grads)
     norm, to = _norm_out(norm, dev)
     workspace, *ws = _workspace(workspace, workspace is None and grad_workspace_bytes(len(grads)), dev)
-    _run(_load().grad_norm, dev, len(grads), _at(at), _at(sizes), _at(types), to, *ws)
+    _run(_entry("grad_norm"), dev, len(grads), _at(at), _at(sizes), _at(types), to, *ws)
     return norm
 
 
@@ -269,5 +293,5 @@ def clip_grads(grads, max_norm, out=None, norm=None, given=None, workspace=None)
         if norm is not None:
             raise ValueError("norm is an output: give either it or given")
         norm, read, into, ws = given, _scalar("given", given, dev), None, (None, 0)
-    _run(_load().grad_clip, dev, len(grads), _at(at), _at(to), _at(sizes), _at(types), max_norm, read, into, *ws)
+    _run(_entry("grad_clip"), dev, len(grads), _at(at), _at(to), _at(sizes), _at(types), max_norm, read, into, *ws)
     return norm

@@ -17,6 +17,11 @@ import torch
 
 from . import OUT_BF16, OUT_F32, _check, _load
 
+try:                                                   # the checks below in C++ (csrc/tensors.cpp): quicker, not needed
+    from . import _tensors as _fast
+except ImportError:
+    _fast = None
+
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 _E8M0 = (torch.float8_e8m0fnu, torch.uint8)
@@ -57,6 +62,8 @@ def _new(shape, dtype, dev):
 
 def _matrix(name, t, shape, dtypes, dev):
     """(pointer, leading dimension) of a matrix, checked."""
+    if _fast is not None and (found := _fast.matrix(t, shape, dtypes, dev)) is not None:
+        return found
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
     if t.shape != shape:
@@ -73,6 +80,8 @@ def _matrix(name, t, shape, dtypes, dev):
 
 def _vector(name, t, n, dtypes, dev):
     """Pointer of a contiguous vector, checked."""
+    if _fast is not None and (found := _fast.vector(t, n, dtypes, dev)) is not None:
+        return found
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
     if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
