@@ -46,12 +46,19 @@ typedef enum {                   /* activations of the gated block */
  *     otherwise); ldx, ldwg, ldwu >= K, ldh >= F (GEMM_ERR_BAD_LD)
  *   G, U: M x F, g and u rounded to `type`, what gemm_glu_backward reads; NULL:
  *     not kept (each for itself).  ldg, ldu >= F.
+ *   workspace: device memory, 256-byte aligned (GEMM_ERR_MISALIGNED), or NULL.
+ *     With at least gemm_glu_workspace_bytes(M, F, K) bytes, large calls whose
+ *     operand rows do not start on 16 bytes copy them there first; a smaller one
+ *     or NULL runs without, slower (the same result up to summation order).
+ *     Calls sharing it must be ordered.  Its contents need no initialisation.
  * Up to 32 rows of X run a kernel made for the reading of the weights.  M or F
  * == 0: nothing is enqueued; K == 0: g = u = 0.
  */
 gemm_status gemm_glu(int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx, const void *Wg, int64_t ldwg,
                      const void *Wu, int64_t ldwu, int type, int act, void *H, int64_t ldh, void *G, int64_t ldg,
-                     void *U, int64_t ldu, hipStream_t stream);
+                     void *U, int64_t ldu, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t gemm_glu_workspace_bytes(int64_t M, int64_t F, int64_t K);
 
 /*
  * gemm_glu_backward -- gradients of gemm_glu from the gradient dH of H:
@@ -105,12 +112,15 @@ gemm_status int8_quantize(int64_t rows, int64_t N, const void *X, int64_t ldx, i
  *   C: M x N, NULL: 0; ldc >= N, or 0: one row for all (a bias); C == D with
  *     ldc == ldd accumulates in place; C and D overlap in no other way
  *     (GEMM_ERR_UNSUPPORTED)
+ *   workspace as in gemm_glu, gemm_int8_workspace_bytes(M, N, K) bytes
  * Up to 32 rows of A run a kernel made for the reading of B.  M or N == 0:
  * nothing is enqueued; K == 0: D = C, or 0.
  */
 gemm_status gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const float *SA, const void *B,
                       int64_t ldb, const float *SB, const void *C, int64_t ldc, void *D, int64_t ldd, int out_type,
-                      hipStream_t stream);
+                      void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*
  * grad_norm -- norm of n gradients taken together: the root of the sum of all

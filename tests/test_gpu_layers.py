@@ -494,3 +494,25 @@ def test_glu_backward_parts_of_large_grids():
     for got, w, b in zip((dx, dwg, dwu), want, bound):
         within(got, w, half(w, b, got.dtype))
     assert torch.equal(both[0], tg.gemm_glu_backward(*a, grad_dtype=F32)[0])
+
+
+# ---- copies of unaligned operands -----------------------------------------------------
+
+@pytest.mark.parametrize("m,n,k", [(2900, 3000, 77), (3000, 2900, 130), (2560, 4000, 1)])
+def test_unaligned_large_grids(m, n, k):
+    """Rows off 16 bytes in large grids: copied first, and without a workspace."""
+    x, wg, wu = rand(1, m, k), rand(2, n // 2, k, scale=k ** -0.5), rand(3, n // 2, k, scale=k ** -0.5)
+    assert tg.gemm_glu_workspace_bytes(m, n // 2, k) > 0 and tg.gemm_int8_workspace_bytes(m, n, k) > 0
+    tiny = torch.empty(256, dtype=torch.uint8, device=DEV)
+    check_glu(x, wg, wu, "silu")
+    check_glu(x, wg, wu, "silu", workspace=tiny)
+    check_glu(padded(x, k + 3), padded(wg, k + 8), wu, "silu")
+    shifted = rand(1, m * 80 + 1)[1:].reshape(m, 80)
+    check_glu(shifted, *(rand(i, n // 2, 80, scale=0.1) for i in (2, 3)), "gelu")
+    check_int8(m, n, k, BF)
+    check_int8(m, n, k, F32, "row", pads=(3, 16, 1))
+    need = tg.gemm_glu_workspace_bytes(m, n // 2, k)
+    guard = torch.full((need + 256,), 171, dtype=torch.uint8, device=DEV)
+    assert torch.equal(tg.gemm_glu(x, wg, wu, workspace=guard[:need]), tg.gemm_glu(x, wg, wu)) and bool((guard[need:] == 171).all())
+    with pytest.raises(tg.GemmError):
+        tg.gemm_glu(x, wg, wu, workspace=guard[1:])

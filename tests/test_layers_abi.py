@@ -24,8 +24,8 @@ NAN, INF = float("nan"), float("inf")
 def test_header_functions_are_exported():
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = sorted(set(re.findall(r"^[A-Za-z_][\w\s\*]*?\b(\w+)\s*\(", text, flags=re.M)))
-    assert names == ["gemm_glu", "gemm_glu_backward", "gemm_glu_backward_workspace_bytes", "gemm_int8", "grad_clip",
-                     "grad_norm", "grad_workspace_bytes", "int8_quantize"]
+    assert names == ["gemm_glu", "gemm_glu_backward", "gemm_glu_backward_workspace_bytes", "gemm_glu_workspace_bytes", "gemm_int8",
+                     "gemm_int8_workspace_bytes", "grad_clip", "grad_norm", "grad_workspace_bytes", "int8_quantize"]
     out = subprocess.run(["nm", "-D", "--defined-only", tg.library_path()], capture_output=True, text=True,
                          check=True).stdout
     exported = {line.split()[-1] for line in out.splitlines() if " T " in line}
@@ -35,8 +35,8 @@ def test_header_functions_are_exported():
 
 
 def glu(M=4, F=64, K=32, X=P, ldx=32, Wg=P + MB, ldwg=32, Wu=P + 2 * MB, ldwu=32, t=BF16, act=0, H=Q, ldh=64,
-        G=Q + MB, ldg=64, U=Q + 2 * MB, ldu=64):
-    return tg.raw.gemm_glu(M, F, K, X, ldx, Wg, ldwg, Wu, ldwu, t, act, H, ldh, G, ldg, U, ldu, None)
+        G=Q + MB, ldg=64, U=Q + 2 * MB, ldu=64, ws=None, wb=0):
+    return tg.raw.gemm_glu(M, F, K, X, ldx, Wg, ldwg, Wu, ldwu, t, act, H, ldh, G, ldg, U, ldu, ws, wb, None)
 
 
 def test_glu_refusals():
@@ -64,6 +64,16 @@ def test_glu_refusals():
         assert glu(**{bad: P + MB + 64}) == UNSUPPORTED        # over Wg
     assert glu(G=Q) == UNSUPPORTED
     assert glu(U=Q + MB) == UNSUPPORTED
+    assert glu(ws=Q + 4 * MB + 128, wb=MB) == MISALIGNED
+
+
+def test_workspace_bytes_of_copies():
+    """Large grids alone, and copies that few results would read are left out: rows of an odd multiple of 256 bytes."""
+    for f in (tg.gemm_glu_workspace_bytes, tg.gemm_int8_workspace_bytes):
+        for none in ((0, 4096, 4096), (4096, -1, 4096), (4096, 4096, 0), (32, 4096, 4095), (1 << 31, 4096, 64), (256, 1 << 20, 65)):
+            assert f(*none) == 0
+    assert tg.gemm_glu_workspace_bytes(4096, 4095, 1001) == (4096 + 2 * 4095) * 2304
+    assert tg.gemm_int8_workspace_bytes(4096, 4095, 1001) == (4096 + 4095) * 1280
 
 
 def bwd(M=4, F=64, K=32, dH=P, lddh=64, G=P + MB, ldg=64, U=P + 2 * MB, ldu=64, X=P + 3 * MB, ldx=32, Wg=P + 4 * MB,
@@ -147,8 +157,8 @@ def test_quantize_refusals():
 
 
 def int8(M=4, N=64, K=32, A=P, lda=32, SA=P + MB, B=P + 2 * MB, ldb=32, SB=P + 3 * MB, C=None, ldc=64, D=Q, ldd=64,
-         out=F32):
-    return tg.raw.gemm_int8(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, D, ldd, out, None)
+         out=F32, ws=None, wb=0):
+    return tg.raw.gemm_int8(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, D, ldd, out, ws, wb, None)
 
 
 def test_int8_refusals():
@@ -169,6 +179,7 @@ def test_int8_refusals():
     for bad in ("SA", "SB", "D", "C"):
         assert int8(**{bad: P + 5 * MB + 2}) == MISALIGNED
     assert int8(lda=8 * MB) == UNSUPPORTED
+    assert int8(ws=Q + 4 * MB + 8, wb=MB) == MISALIGNED
     assert int8(ldd=2 * MB) == UNSUPPORTED
     assert int8(C=Q, ldc=128) == UNSUPPORTED                   # in place with another leading dimension
     assert int8(C=Q + 64) == UNSUPPORTED
@@ -277,5 +288,5 @@ def test_calls_in_cpp_refuse_wrong_counts():
     with pytest.raises(TypeError):
         f(1, 2, 3)
     with pytest.raises(TypeError):
-        f(*["x"] * 15)
-    assert f(-1, 4, 4, 1, 64, 1, 1, 64, 1, None, 0, 1, 64, 0, None) == INVALID_SIZE
+        f(*["x"] * 17)
+    assert f(-1, 4, 4, 1, 64, 1, 1, 64, 1, None, 0, 1, 64, 0, None, 0, None) == INVALID_SIZE

@@ -30,8 +30,8 @@ __all__ = ["gemm_bf16", "gemm_fp16", "gemm_bf16_splitk", "gemm_fp16_splitk", "sp
            "gemm_mxfp8", "gemm_mxfp4", "gemm_mxfp6", "gemm_mxfp8_splitk", "gemm_mxfp4_splitk", "gemm_mxfp6_splitk", "raw", "GemmError", "LibraryMissing",
            "library_path", "STATUS", "mxfp8_quantize", "rmsnorm", "rmsnorm_mxfp8", "rmsnorm_backward",
            "rmsnorm_backward_workspace_bytes", "gemm_wgrad_mxfp8", "gemm_wgrad_mxfp8_workspace_bytes", "gemv_mxfp4", "gemv_mxfp4_workspace_bytes",
-           "gemm_glu", "gemm_glu_backward", "gemm_glu_backward_workspace_bytes", "int8_quantize", "gemm_int8",
-           "grad_norm", "clip_grads", "grad_workspace_bytes"]
+           "gemm_glu", "gemm_glu_workspace_bytes", "gemm_glu_backward", "gemm_glu_backward_workspace_bytes",
+           "int8_quantize", "gemm_int8", "gemm_int8_workspace_bytes", "grad_norm", "clip_grads", "grad_workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libtilegemm.so")
@@ -165,16 +165,17 @@ def _declare_layers(L):
     m = [vp, i64]                                      # a matrix and its leading dimension
     size = [i64, i64, i64]
     for name, args in (
-            ("gemm_glu", size + m * 3 + [ci, ci] + m * 3 + [vp]),
+            ("gemm_glu", size + m * 3 + [ci, ci] + m * 3 + [vp, sz, vp]),
             ("gemm_glu_backward", size + m * 6 + [ci, ci] + m * 5 + [ci, vp, sz, vp]),
             ("int8_quantize", [i64, i64] + m + [ci] + m + [vp, vp]),
-            ("gemm_int8", size + (m + [vp]) * 2 + m * 2 + [ci, vp]),
+            ("gemm_int8", size + (m + [vp]) * 2 + m * 2 + [ci, vp, sz, vp]),
             ("grad_norm", [i64, vp, vp, vp, vp, vp, sz, vp]),
             ("grad_clip", [i64, vp, vp, vp, vp, f32, vp, vp, vp, sz, vp])):
         f = getattr(L, name)
         f.restype, f.argtypes = ci, args
-    L.gemm_glu_backward_workspace_bytes.restype = sz
-    L.gemm_glu_backward_workspace_bytes.argtypes = size
+    for name in ("gemm_glu_workspace_bytes", "gemm_glu_backward_workspace_bytes", "gemm_int8_workspace_bytes"):
+        f = getattr(L, name)
+        f.restype, f.argtypes = sz, size
     L.grad_workspace_bytes.restype = sz
     L.grad_workspace_bytes.argtypes = [i64]
 
@@ -715,8 +716,8 @@ def gemm_mxfp6_splitk(A, SFA, B, SFB, C=None, out_dtype=None, D=None, fmt="e2m3"
 # The functions of ops.py and layers.py, which need torch at import, load with their first use.
 _OPS = ("mxfp8_quantize", "rmsnorm", "rmsnorm_mxfp8", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes",
         "gemm_wgrad_mxfp8", "gemm_wgrad_mxfp8_workspace_bytes", "gemv_mxfp4", "gemv_mxfp4_workspace_bytes")
-_LAYERS = ("gemm_glu", "gemm_glu_backward", "gemm_glu_backward_workspace_bytes", "int8_quantize", "gemm_int8",
-           "grad_norm", "clip_grads", "grad_workspace_bytes")
+_LAYERS = ("gemm_glu", "gemm_glu_workspace_bytes", "gemm_glu_backward", "gemm_glu_backward_workspace_bytes",
+           "int8_quantize", "gemm_int8", "gemm_int8_workspace_bytes", "grad_norm", "clip_grads", "grad_workspace_bytes")
 
 
 def __getattr__(name):

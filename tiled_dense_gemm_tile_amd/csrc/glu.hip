@@ -3,9 +3,15 @@
 
 using namespace tg_api;
 
+extern "C" size_t gemm_glu_workspace_bytes(int64_t M, int64_t F, int64_t K) {
+    if (M <= 0 || F <= 0 || K <= 0 || M >= kMaxDim || F >= kMaxDim || K * 2 >= kMaxLdBytes) return 0;
+    return prod_copy_bytes(M, F, 2, K * 2);
+}
+
 extern "C" gemm_status gemm_glu(int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx, const void *Wg,
                                 int64_t ldwg, const void *Wu, int64_t ldwu, int type, int act, void *H, int64_t ldh,
-                                void *G, int64_t ldg, void *U, int64_t ldu, hipStream_t stream) {
+                                void *G, int64_t ldg, void *U, int64_t ldu, void *workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
     if (M < 0 || F < 0 || K < 0) return GEMM_ERR_INVALID_SIZE;
     if (M >= kMaxDim || F >= kMaxDim || K >= kMaxDim || !type16(type) || !known_act(act)) return GEMM_ERR_UNSUPPORTED;
     if (M == 0 || F == 0) return GEMM_OK;
@@ -28,6 +34,7 @@ extern "C" gemm_status gemm_glu(int64_t M, int64_t F, int64_t K, const void *X, 
             return GEMM_ERR_UNSUPPORTED;
     }
     if ((G && G == H) || (U && U == H) || (G && G == U)) return GEMM_ERR_UNSUPPORTED;
+    if (workspace && (uintptr_t)workspace % 256 != 0) return GEMM_ERR_MISALIGNED;
     tg::ProdArgs p = {};
     p.A = X;
     p.B = Wg;
@@ -38,6 +45,11 @@ extern "C" gemm_status gemm_glu(int64_t M, int64_t F, int64_t K, const void *X, 
     p.M = (int)M;
     p.N = (int)F;
     p.KB = (int)(K * 2);
+    const size_t need = workspace && !prod_aligned(p) ? prod_copy_bytes(M, F, 2, K * 2) : 0;
+    if (need > 0 && workspace_bytes >= need) {
+        gemm_status st = launched(tg::prod_aligned_copies(p, type, (char *)workspace, stream));
+        if (st != GEMM_OK) return st;
+    }
     const bool vec = tg::emit_whole(H, ldh, F, 2) && (!G || tg::emit_whole(G, ldg, F, 2)) && (!U || tg::emit_whole(U, ldu, F, 2));
     if (type == GEMM_TYPE_BF16) return launched(tg::launch_glu<1>(p, {H, G, U, ldh, ldg, ldu, act, vec}, stream));
     return launched(tg::launch_glu<2>(p, {H, G, U, ldh, ldg, ldu, act, vec}, stream));

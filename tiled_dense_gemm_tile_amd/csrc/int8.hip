@@ -192,9 +192,14 @@ gemm_status int8_quantize(int64_t rows, int64_t N, const void *X, int64_t ldx, i
     }
 }
 
+size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N <= 0 || K <= 0 || M >= kMaxDim || N >= kMaxDim || K >= (int64_t)1 << 17) return 0;
+    return prod_copy_bytes(M, N, 1, K);
+}
+
 gemm_status gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const float *SA, const void *B,
                       int64_t ldb, const float *SB, const void *C, int64_t ldc, void *D, int64_t ldd, int out_type,
-                      hipStream_t stream) {
+                      void *workspace, size_t workspace_bytes, hipStream_t stream) {
     if (M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_SIZE;
     if (M >= kMaxDim || N >= kMaxDim || K >= (int64_t)1 << 17 || !elem_type(out_type)) return GEMM_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return GEMM_OK;
@@ -209,6 +214,7 @@ gemm_status gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, int64_t ld
     if (overlap(D, db, SA, M * 4) || overlap(D, db, SB, N * 4) ||
         (K > 0 && (overlap(D, db, A, matrix_bytes(M, K, lda, 1)) || overlap(D, db, B, matrix_bytes(N, K, ldb, 1)))))
         return GEMM_ERR_UNSUPPORTED;
+    if (workspace && (uintptr_t)workspace % 256 != 0) return GEMM_ERR_MISALIGNED;
     tg::ProdArgs p = {};
     p.A = A;
     p.B = B;
@@ -217,6 +223,11 @@ gemm_status gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, int64_t ld
     p.M = (int)M;
     p.N = (int)N;
     p.KB = (int)K;
+    const size_t need = workspace && !prod_aligned(p) ? prod_copy_bytes(M, N, 1, K) : 0;
+    if (need > 0 && workspace_bytes >= need) {
+        gemm_status st = launched(tg::prod_aligned_copies(p, tg::kI8, (char *)workspace, stream));
+        if (st != GEMM_OK) return st;
+    }
     const bool vec = tg::emit_whole(D, ldd, N, os);
     switch (out_type) {
     case GEMM_TYPE_F32: return launched(tg::launch_int8<0>(p, {SA, SB, C, D, ldc, ldd, vec}, stream));

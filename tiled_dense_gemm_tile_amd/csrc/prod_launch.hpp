@@ -1,6 +1,7 @@
 // The choice of kernel for a product of prod.hpp, and its launch.
 #pragma once
 
+#include "prod_api.hpp"
 #include "prod_mid.hpp"
 #include "prod_rows.hpp"
 #include "prod_w4.hpp"
@@ -12,14 +13,6 @@ inline unsigned prod_tiles(ProdArgs &p, int bm, int bn) {
     p.tiles_n = (p.N + bn - 1) / bn;
     p.group_m = 4;
     return (unsigned)(p.tiles_m * (int64_t)p.tiles_n);
-}
-
-// Direct loads: rows on 16 bytes and whole 16-byte chunks.
-inline bool prod_aligned(const ProdArgs &p) {
-    auto on16 = [](const void *q, int64_t ld, int rows) {
-        return (uintptr_t)q % 16 == 0 && (ld % 16 == 0 || rows == 1);
-    };
-    return p.KB % 16 == 0 && on16(p.A, p.lda, p.M) && on16(p.B, p.ldb, p.N) && (!p.B1 || on16(p.B1, p.ldb1, p.N));
 }
 
 inline int64_t tiles_of(const ProdArgs &p, int bm, int bn) {
@@ -152,7 +145,7 @@ hipError_t launch_prod(const ProdArgs &p, const Epi &e, hipStream_t s) {
     const int64_t t64 = tiles_of(p, 64, PAIR ? 32 : 64);
     if (p.M <= 8 || (p.M <= 16 && t64 < 200)) return go_rows<T, 1, PAIR>(p, e, s);
     if (p.M <= 32 && t64 <= 128) return go_rows<T, 2, PAIR>(p, e, s);
-    if (prod_aligned(p)) return launch_prod_tiles<T, PAIR, false, Epi>(p, e, s);
+    if (tg_api::prod_aligned(p)) return launch_prod_tiles<T, PAIR, false, Epi>(p, e, s);
     return launch_prod_tiles<T, PAIR, true, Epi>(p, e, s);
 }
 

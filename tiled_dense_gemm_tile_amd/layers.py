@@ -51,14 +51,37 @@ def _type16(name, t):
     return (t.dtype,)
 
 
-def gemm_glu(X, Wg, Wu, act="silu", H=None, G=None, U=None, keep=False):
+def _copy_room(need, sizes, unit, workspace, dev, *operands):
+    """(tensor to keep, pointer, bytes) of a product's workspace: given, or
+    allocated here where rows that do not start on 16 bytes would be copied."""
+    if workspace is None:
+        at, off = 0, sizes[2]
+        for p, ld in operands:
+            at |= p
+            off |= ld
+        if at % 16 == 0 and off % unit == 0:
+            return None, None, 0
+        return _workspace(None, need(*sizes), dev)
+    return _workspace(workspace, 0, dev)
+
+
+def gemm_glu_workspace_bytes(M: int, F: int, K: int) -> int:
+    """Workspace bytes with which :func:`gemm_glu` may copy operands whose rows
+    do not start on 16 bytes (0: it would not)."""
+    return _load().gemm_glu_workspace_bytes(M, F, K)
+
+
+def gemm_glu(X, Wg, Wu, act="silu", H=None, G=None, U=None, keep=False, workspace=None):
     """Gated block of a feed-forward layer: H (M, F) = act(X @ Wg^T) * (X @
     Wu^T), X (M, K), Wg and Wu (F, K; two tensors, or the halves of one), all
     bfloat16 or all float16.  ``act``: "silu", "gelu", "gelu_tanh" or "relu".
     Sums and activation in fp32, H rounded once.  ``keep``, or G or U given:
     the two products are given out too, rounded, for
-    :func:`gemm_glu_backward`.  Returns H, or (H, G, U) with those kept (None
-    where one of G and U alone was given)."""
+    :func:`gemm_glu_backward`.  ``workspace``: a device byte tensor, 256-byte
+    aligned, of :func:`gemm_glu_workspace_bytes` bytes (allocated per call when
+    not given and of use; a smaller one runs without copying operands whose
+    rows do not start on 16 bytes).  Returns H, or (H, G, U) with those kept
+    (None where one of G and U alone was given)."""
     own = _type16("X", X)
     dev = _device(X)
     M, K = X.shape
@@ -74,8 +97,9 @@ def gemm_glu(X, Wg, Wu, act="silu", H=None, G=None, U=None, keep=False):
         U = _new((M, F), X.dtype, dev) if U is None else U
     g = _NONE if G is None else _matrix("G", G, (M, F), own, dev)
     u = _NONE if U is None else _matrix("U", U, (M, F), own, dev)
+    workspace, *ws = _copy_room(gemm_glu_workspace_bytes, (M, F, K), 8, workspace, dev, x, wg, wu)
     _run(_entry("gemm_glu"), dev, M, F, K, *x, *wg, *wu, _TYPES[X.dtype], _act(act), *_matrix("H", H, (M, F), own, dev),
-         *g, *u)
+         *g, *u, *ws)
     return H if G is None and U is None else (H, G, U)
 
 
@@ -149,12 +173,19 @@ def int8_quantize(X, Q=None, S=None):
     return Q, S
 
 
-def gemm_int8(A, SA, B, SB, C=None, out_dtype=None, D=None):
+def gemm_int8_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Workspace bytes with which :func:`gemm_int8` may copy operands whose rows
+    do not start on 16 bytes (0: it would not)."""
+    return _load().gemm_int8_workspace_bytes(M, N, K)
+
+
+def gemm_int8(A, SA, B, SB, C=None, out_dtype=None, D=None, workspace=None):
     """D (M, N) = SA[m] * SB[n] * (A @ B^T) + C, A (M, K) and B (N, K) int8, SA
     (M,) and SB (N,) float32: the operands that :func:`int8_quantize` makes, of
     tokens and of a weight's channels.  The integer sums are exact (K below
     2^17).  ``out_dtype`` float32 (default), bfloat16 or float16; C of that
-    type, (M, N) or (N,) (a bias); C may be D."""
+    type, (M, N) or (N,) (a bias); C may be D.  ``workspace`` as in
+    :func:`gemm_glu`, of :func:`gemm_int8_workspace_bytes` bytes."""
     if A.dim() != 2 or A.dtype != torch.int8 or B.dim() != 2:
         raise TypeError("A and B must be 2-D int8 tensors")
     dev = _device(A)
@@ -172,7 +203,9 @@ def gemm_int8(A, SA, B, SB, C=None, out_dtype=None, D=None):
     c = _NONE
     if C is not None:
         c = (_vector("C", C, N, own, dev), 0) if C.dim() == 1 else _matrix("C", C, (M, N), own, dev)
-    _run(_entry("gemm_int8"), dev, M, N, K, *a, sa, *b, sb, *c, *_matrix("D", D, (M, N), own, dev), _TYPES[out_dtype])
+    workspace, *ws = _copy_room(gemm_int8_workspace_bytes, (M, N, K), 16, workspace, dev, a, b)
+    _run(_entry("gemm_int8"), dev, M, N, K, *a, sa, *b, sb, *c, *_matrix("D", D, (M, N), own, dev), _TYPES[out_dtype],
+         *ws)
     return D
 
 
