@@ -41,9 +41,8 @@ inline bool prod_aligned(const tg::ProdArgs &p) {
 
 // Workspace bytes of the copies of unaligned operands (M and D * N rows of
 // `kbytes`), 0 where they do not pay: in grids of 256 x 256 tiles, which only
-// aligned operands have (gated 4096 x 4095 x 1001: 120 us without, 78 with; with 384 tiles of
-// 128 x 128 the same), if
-// results per row copied are many.
+// aligned operands have (gated 4096 x 4095 x 1001: 120 us without, 78 with; 384
+// tiles of 128 x 128: the same), if results per row copied are many.
 inline size_t prod_copy_bytes(int64_t M, int64_t N, int D, int64_t kbytes) {
     const int64_t bn = 128 / D, t128 = ((M + 127) / 128) * ((N + bn - 1) / bn);
     if (kbytes == 0 || t128 <= 512 || (double)M * (double)N * D < 300.0 * (double)(M + D * N)) return 0;
