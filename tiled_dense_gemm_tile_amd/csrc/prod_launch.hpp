@@ -28,13 +28,16 @@ hipError_t go_mid(ProdArgs p, const Epi &e, hipStream_t s) {
 }
 
 // 256 x 256 tiles in whole rounds of one a CU; what is left of up to half a
-// round in 128 x 128 tiles (four times as many: gated 8256 features).
+// round in 128 x 128 tiles (four times as many: weight gradients of 8192 x 8256
+// x 4096, 16 tiles past four rounds, 973 -> 917 us).  8-bit operands without the
+// lines brought ahead (8192 x 14336 x 4096 359 us, with them 364; the gated
+// block 1356 without, 1348 with).
 template <int T, bool PAIR, class Epi>
 hipError_t go_w4(ProdArgs p, const Epi &e, hipStream_t s) {
     const unsigned tiles = prod_tiles(p, 256, PAIR ? 128 : 256), cus = 256, rest = tiles % cus;
     const bool cut = tiles > cus && rest > 0 && rest <= cus / 2;
     p.run = (int)(cut ? tiles - rest : tiles);
-    hipLaunchKernelGGL((prod_w4_kernel<T, PAIR, !PAIR && T != kI8, Epi>), dim3(tiles < cus ? tiles : cus), dim3(256), 0, s, p, e);
+    hipLaunchKernelGGL((prod_w4_kernel<T, PAIR, T != kI8, Epi>), dim3(tiles < cus ? tiles : cus), dim3(256), 0, s, p, e);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || !cut) return err;
     // (one a CU; more of them two a CU)
