@@ -1,0 +1,113 @@
+"""The waits of the 256 x 256-tile products, checked in the gfx950 assembly of
+their sources (CPU only: compiled, never run).
+
+Operands come by direct loads into LDS, which nothing but a count of outstanding
+vector-memory operations says to have landed: a K tile's barrier leaves one
+operation in flight where lines are brought ahead (that one), the barrier before
+the next output tile leaves the finished tile's stores.  Here every path through
+the kernels is followed with the queue of outstanding operations (they return in
+order): none of those loads may be in it at a barrier, and nothing that writes
+LDS at the kernel's end, where the LDS is another workgroup's next."""
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+from test_wgrad_waits import VMEM, blocks_of, count_of
+from tiled_dense_gemm_tile_amd import build as B
+
+pytestmark = pytest.mark.skipif(shutil.which(B.HIPCC) is None and not os.path.exists(B.HIPCC),
+                                reason="hipcc not available")
+
+# (The kernel of two products has the same body; its paths by which product it is are too many here.)
+# An epilogue whose results are known, when it is compiled, to lie in whole pieces or not: the kernels choose at run time,
+# and paths that mix the one's stores with the other's wait do not exist.
+SOURCE = """
+#include "prod_w4.hpp"
+namespace tg {
+template <class E, bool V> struct Known : E {
+    static constexpr bool vec = V;
+};
+#define ONE(T, PAIR, AHEAD, E)                                                                          \\
+    template __global__ void prod_w4_kernel<T, PAIR, AHEAD, Known<E, true>>(ProdArgs, Known<E, true>); \\
+    template __global__ void prod_w4_kernel<T, PAIR, AHEAD, Known<E, false>>(ProdArgs, Known<E, false>);
+ONE(1, true, true, GluEpi<1>)
+ONE(2, true, true, GluEpi<2>)
+ONE(3, false, false, Int8Epi<0>)
+ONE(3, false, false, Int8Epi<1>)
+ONE(1, false, true, PlainEpi<0>)
+ONE(2, false, true, PlainEpi<2>)
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def assembly(tmp_path_factory):
+    d = tmp_path_factory.mktemp("asm")
+    (d / "w4.hip").write_text(SOURCE)
+    subprocess.run([B.HIPCC] + B.FLAGS + ["-I" + B.CSRC, "-S", "--cuda-device-only", str(d / "w4.hip"), "-o", str(d / "w4.s")],
+                   check=True, capture_output=True)
+    return (d / "w4.s").read_text()
+
+
+def follow(text, name, at_barrier, at_end):
+    """Every path, with the queue of outstanding operations: 2 a load of 16 bytes a lane into LDS, 1 a smaller one, 0 any
+    other.  Only the queue from its oldest LDS load on is kept."""
+    blocks, first = blocks_of(text, name)
+    todo, seen, barriers = [(first, ())], set(), 0
+    while todo:
+        state = todo.pop()
+        if state in seen:
+            continue
+        seen.add(state)
+        assert len(seen) < 400000
+        label, queue = state
+        ins, after = blocks[label]
+        for line in ins:
+            if VMEM.match(line):
+                queue += ((2 if "dwordx4" in line else 1) if line.endswith(" lds") else 0,)
+            elif line.startswith("s_waitcnt"):
+                n = count_of(line)
+                queue = queue[len(queue) - n:] if 0 < n < len(queue) else queue if n else ()
+            elif line.startswith("s_barrier"):
+                at_barrier(queue)
+                barriers += 1
+            elif line.startswith("s_endpgm"):
+                at_end(queue)
+            while queue and queue[0] == 0:
+                queue = queue[1:]
+            if len(queue) > 96:                        # (an LDS load this old is outstanding for good)
+                queue = queue[:1] + queue[-95:]
+        todo.extend((b, queue) for b in after)
+    return barriers
+
+
+def at_barrier(queue):
+    assert 2 not in queue, "an operand's load may still be on its way behind this barrier"
+
+
+def at_end(queue):
+    assert not any(queue), "a load may write LDS after the workgroup's end"
+
+
+def kernels(text):
+    return sorted(set(re.findall(r"^(_ZN2tg\w*prod_w4_\w+):", text, re.M)))
+
+
+def test_operands_have_landed_at_every_barrier(assembly):
+    names = kernels(assembly)
+    assert len(names) == 12
+    for name in names:
+        assert follow(assembly, name, at_barrier, at_end) > 4, name
+
+
+def test_the_check_sees_waits_that_are_too_short(assembly):
+    """The same text with one operation more left in flight, at the K tiles' ends or behind the results."""
+    for kernel, wait, longer in (("prod_w4_kernelILi3ELb0ELb0ENS_5KnownINS_7Int8EpiILi1EEELb1", 0, 1),
+                                 ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1", 1, 2),
+                                 ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1", 16, 17)):
+        name = [k for k in kernels(assembly) if kernel in k][0]
+        with pytest.raises(AssertionError):
+            follow(assembly.replace("vmcnt(%d)" % wait, "vmcnt(%d)" % longer), name, at_barrier, at_end)

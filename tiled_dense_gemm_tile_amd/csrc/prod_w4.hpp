@@ -42,11 +42,11 @@ constexpr int kW4Lds = 4 * 256 * 128 + 1024;
 
 // Workgroup wg of nwg that walk the tiles wg, wg + nwg, ... below p.run.
 // reload(): p again, from memory; emit(acc, stage, lane, row0, col0, M, N)
-// stores a quadrant's results, wait_stores() waits for all but their stores.  (Operand rows on 16 bytes, KB > 0 a multiple of
-// 16.)
-template <int T, bool PAIR, bool PREFETCH, class Reload, class Emit, class Wait>
+// stores a quadrant's results and waits for all that was issued before their
+// last stores.  (Operand rows on 16 bytes, KB > 0 a multiple of 16.)
+template <int T, bool PAIR, bool PREFETCH, class Reload, class Emit>
 __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg, char *smem, Reload &&reload,
-                                             Emit &&emit, Wait &&wait_stores) {
+                                             Emit &&emit) {
     constexpr int TM = 8, TN = 8, Q = TM * TN, SLOT = 256 * 128, B_BASE = 2 * SLOT;
     constexpr int BN = PAIR ? 128 : 256;               // result columns of a tile
     constexpr int W = BN / 2, STAGE = 16 * kStagePitch<W> * 4;
@@ -215,29 +215,24 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
             wait_vmcnt<0>();
             break;
         }
-        // the next tile's first loads landed; the results' stores issued after
-        // them may still run
-        wait_stores();
         wait_lgkmcnt0();
         barrier();
     }
 }
 
-// An epilogue's results, and the wait that leaves their stores in flight.
+// An epilogue's results.  The next tile's first loads have landed then; the
+// results' stores issued after them, of which there are at least stores(), may
+// still run.
 template <class Epi, int TM, int TN>
 __device__ __forceinline__ void emit_agpr(const Epi &e, const f32x4 (&acc)[TM][TN], float *stage, int lane, int row0,
                                           int col0, int M, int N) {
-    if (e.vec)
+    if (e.vec) {
         e.template block<TM, TN, true, true>(acc, stage, lane, row0, col0, M, N);
-    else
+        wait_vmcnt<Epi::template stores<TM, TN>()>();
+    } else {
         e.template block<TM, TN, true, false>(acc, stage, lane, row0, col0, M, N);
-}
-template <class Epi>
-__device__ __forceinline__ void wait_emitted(const Epi &e) {
-    if (e.vec)
-        wait_vmcnt<Epi::template stores<8, 8>()>();
-    else
         wait_vmcnt<0>();
+    }
 }
 
 template <int T, bool PAIR, bool PREFETCH, class Epi>
@@ -246,8 +241,7 @@ __global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
     prod_w4_body<T, PAIR, PREFETCH>(
         p, blockIdx.x, gridDim.x, smem, [] { return kernel_arg0_reloaded<ProdArgs>(); },
         [&](const auto &acc, float *stage, int lane, int row0, int col0, int M, int N)
-            __attribute__((always_inline)) { emit_agpr(e, acc, stage, lane, row0, col0, M, N); },
-        [&]() __attribute__((always_inline)) { wait_emitted(e); });
+            __attribute__((always_inline)) { emit_agpr(e, acc, stage, lane, row0, col0, M, N); });
 }
 
 // Two products in one launch: the first on workgroups below `split`, the second
@@ -270,12 +264,6 @@ __global__ void __launch_bounds__(256) prod_w4_two_kernel(ProdPair q, Epi0 e0, E
                 emit_agpr(e1, acc, stage, lane, row0, col0, M, N);
             else
                 emit_agpr(e0, acc, stage, lane, row0, col0, M, N);
-        },
-        [&]() __attribute__((always_inline)) {
-            if (second)
-                wait_emitted(e1);
-            else
-                wait_emitted(e0);
         });
 }
 
