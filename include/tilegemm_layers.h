@@ -16,9 +16,12 @@
  * dimensions count elements; matrices are row-major; pointers are aligned to
  * their element size (GEMM_ERR_MISALIGNED) and need no more than that, though
  * operands whose rows start on 16 bytes run faster.  Sizes are below 2^31 and
- * leading dimensions below 8 MiB in bytes (GEMM_ERR_UNSUPPORTED).  Outputs
- * overlap neither inputs nor each other unless a call says so.  The same call
- * on the same values gives the same bits.
+ * leading dimensions below 8 MiB in bytes (GEMM_ERR_UNSUPPORTED).  Outputs and
+ * workspaces overlap neither inputs nor each other (GEMM_ERR_UNSUPPORTED)
+ * unless a call says so: an input's piece of memory, from its first element to
+ * its last, holds no result.  Results of one leading dimension may lie row by
+ * row next to each other, as the halves of one tensor.  The same call on the
+ * same values gives the same bits.
  */
 #ifndef TILEGEMM_LAYERS_H
 #define TILEGEMM_LAYERS_H
@@ -51,8 +54,8 @@ typedef enum {                   /* activations of the gated block */
  *     operand rows do not start on 16 bytes copy them there first; a smaller one
  *     or NULL runs without, slower (the same result up to summation order).
  *     Calls sharing it must be ordered.  Its contents need no initialisation.
- * Up to 32 rows of X run a kernel made for the reading of the weights.  M or F
- * == 0: nothing is enqueued; K == 0: g = u = 0.
+ * Up to 32 rows of X run a kernel made for the reading of the weights.  M and F
+ * below 2^27.  M or F == 0: nothing is enqueued; K == 0: g = u = 0.
  */
 gemm_status gemm_glu(int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx, const void *Wg, int64_t ldwg,
                      const void *Wu, int64_t ldwu, int type, int act, void *H, int64_t ldh, void *G, int64_t ldg,
@@ -113,8 +116,8 @@ gemm_status int8_quantize(int64_t rows, int64_t N, const void *X, int64_t ldx, i
  *     ldc == ldd accumulates in place; C and D overlap in no other way
  *     (GEMM_ERR_UNSUPPORTED)
  *   workspace as in gemm_glu, gemm_int8_workspace_bytes(M, N, K) bytes
- * Up to 32 rows of A run a kernel made for the reading of B.  M or N == 0:
- * nothing is enqueued; K == 0: D = C, or 0.
+ * Up to 32 rows of A run a kernel made for the reading of B.  M and N below
+ * 2^27.  M or N == 0: nothing is enqueued; K == 0: D = C, or 0.
  */
 gemm_status gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const float *SA, const void *B,
                       int64_t ldb, const float *SB, const void *C, int64_t ldc, void *D, int64_t ldd, int out_type,
@@ -146,7 +149,8 @@ gemm_status grad_norm(int64_t n, const void *const *grads, const int64_t *sizes,
  *     otherwise one float, read in its place (a norm that ranks have summed),
  *     and norm may be NULL (else it receives a copy; it may be `given`)
  *   out: n tensors of the same sizes and types; out NULL or out[i] == grads[i]:
- *     in place, where a factor of 1 leaves them untouched
+ *     in place, where a factor of 1 leaves them untouched.  No result shares
+ *     memory with another or with another's gradient (GEMM_ERR_UNSUPPORTED).
  *   max_norm >= 0, not NaN (GEMM_ERR_UNSUPPORTED otherwise)
  *   Everything else as grad_norm; workspace is needed without `given` only.
  * A norm that is NaN makes every gradient NaN; an infinite one zeros (NaN for

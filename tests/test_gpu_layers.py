@@ -516,3 +516,42 @@ def test_unaligned_large_grids(m, n, k):
     assert torch.equal(tg.gemm_glu(x, wg, wu, workspace=guard[:need]), tg.gemm_glu(x, wg, wu)) and bool((guard[need:] == 171).all())
     with pytest.raises(tg.GemmError):
         tg.gemm_glu(x, wg, wu, workspace=guard[1:])
+
+
+@pytest.mark.parametrize("m", [3, 150])
+def test_matrices_next_to_each_other_in_one(m):
+    """Operands as columns of one tensor, results as those of another: none is another's, and what lies behind them
+    stays."""
+    f, k = 96, 64
+    ins, outs = torch.zeros(m, k + f, dtype=BF, device=DEV), torch.full((m, 3 * f + 8), 7.0, dtype=BF, device=DEV)
+    x, dh, h, g, u = ins[:, :k], ins[:, k:], outs[:, :f], outs[:, f:2 * f], outs[:, 2 * f:3 * f]
+    x.copy_(rand(1, m, k))
+    dh.copy_(rand(2, m, f))
+    w = rand(3, f, 2 * k)
+    wg, wu = w[:, :k], w[:, k:]
+    check_glu(x, wg, wu, "silu", H=h, G=g, U=u)
+    dw = torch.full((f, 2 * k + 8), 7.0, device=DEV)
+    dx, _, _ = tg.gemm_glu_backward(dh, g, u, x, wg, wu, dWg=dw[:, :k], dWu=dw[:, k:2 * k])
+    alone = tg.gemm_glu_backward(dh.clone(), g.clone(), u.clone(), x.clone(), wg.clone(), wu.clone(), grad_dtype=F32)
+    for got, want in zip((dx, dw[:, :k], dw[:, k:2 * k]), alone):
+        assert torch.equal(got, want)
+    tg.gemm_glu_backward(dh, g, u, x, wg, wu, Cg=dw[:, :k], Cu=dw[:, k:2 * k], dWg=dw[:, :k], dWu=dw[:, k:2 * k])
+    for got, want in zip((dw[:, :k], dw[:, k:2 * k]), alone[1:]):
+        # (one sum taken twice: exact)
+        assert torch.equal(got, 2 * want)
+    assert (outs[:, 3 * f:] == 7).all() and (dw[:, 2 * k:] == 7).all()
+
+
+def test_clip_into_other_tensors_in_any_order():
+    """Many tensors, results in another order in memory, some in place."""
+    n = 600
+    src = torch.randn(n, 40, device=DEV)
+    dst = torch.zeros(n, 40, device=DEV)
+    grads = [src[(7 * i) % n, :1 + i % 40] for i in range(n)]
+    want, total = [g.clone() for g in grads], math.sqrt(sum(float((g.double() ** 2).sum()) for g in grads))
+    out = [g if i % 3 == 0 else dst[(11 * i) % n, :1 + i % 40] for i, g in enumerate(grads)]
+    norm = tg.clip_grads(grads, 1.0, out=out)
+    assert abs(float(norm) - total) <= 2 * U * total
+    for got, w in zip(out, want):
+        # the factor's two roundings and the norm's, the product's
+        within(got, w.double() / (total + 1e-6), 5 * U * w.double().abs() / total)

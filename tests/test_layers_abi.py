@@ -290,3 +290,54 @@ def test_calls_in_cpp_refuse_wrong_counts():
     with pytest.raises(TypeError):
         f(*["x"] * 17)
     assert f(-1, 4, 4, 1, 64, 1, 1, 64, 1, None, 0, 1, 64, 0, None, 0, None) == INVALID_SIZE
+
+
+def test_shared_memory_is_refused():
+    """Matrices that share elements; those of one leading dimension that lie next to each other row by row do not."""
+    assert glu(G=Q + 64) == UNSUPPORTED                        # rows of 128 bytes, half a row on
+    assert glu(ldh=128, ldg=128, G=Q + 126) == UNSUPPORTED     # one element too near
+    assert glu(ldh=128, ldg=130, G=Q + 128) == UNSUPPORTED     # rows that drift apart
+    assert glu(ldu=128, ldg=128, U=Q + MB + 130) == UNSUPPORTED    # the last element is the next row's first
+    assert bwd(dWu=Q + MB + 32) == UNSUPPORTED
+    assert bwd(lddwg=64, lddwu=64, dWu=Q + MB + 62) == UNSUPPORTED
+    assert bwd(dX=Q + MB + 64) == UNSUPPORTED
+    assert bwd(Cg=P + 6 * MB, Cu=Q + MB + 64) == UNSUPPORTED   # Cu in the other's result
+    for at in (P, P + 3 * MB, P + 5 * MB, Q, Q + 2 * MB):      # the workspace over an operand, a result
+        assert bwd(ws=at) == UNSUPPORTED
+    assert int8(ldc=128, ldd=128, C=Q + 252) == UNSUPPORTED
+    big = dict(M=4096, N=4095, K=1001, lda=1001, ldb=1001, ldd=4095, SA=P + 32 * MB, SB=P + 33 * MB, B=P + 16 * MB)
+    need = tg.gemm_int8_workspace_bytes(4096, 4095, 1001)
+    for at in (P, P + 16 * MB, P + 32 * MB, Q, Q + 63 * MB):   # where operands are copied
+        assert int8(**big, ws=at, wb=need) == UNSUPPORTED
+    big = dict(M=4096, F=4095, K=1001, ldx=1001, ldwg=1001, ldwu=1001, ldh=4095, G=None, U=None, Wg=P + 16 * MB, Wu=P + 32 * MB)
+    need = tg.gemm_glu_workspace_bytes(4096, 4095, 1001)
+    for at in (P, P + 16 * MB, P + 32 * MB, Q, Q + 31 * MB):
+        assert glu(**big, ws=at, wb=need) == UNSUPPORTED
+
+
+def test_gradients_that_share_memory_are_refused():
+    two = dict(sizes=(10, 20), types=(BF16, F32))
+    assert grads(at=(P + 4, P), **two) == UNSUPPORTED          # the first inside the second
+    assert grads(at=(P, P + 16), **two) == UNSUPPORTED         # the second in the first's last elements
+    assert grads(out=(Q + 2 * MB, Q + 2 * MB + 16), **two) == UNSUPPORTED
+    assert grads(out=(P + MB, Q + 2 * MB), **two) == UNSUPPORTED   # a result over the other's gradient
+    assert grads(out=(P + 2, P + MB), **two) == UNSUPPORTED    # over its own, shifted
+    assert grads(norm=P + MB + 76) == UNSUPPORTED
+    assert grads(given=P + 8, norm=None) == UNSUPPORTED
+    assert grads(at=(P, Q + MB + 64)) == UNSUPPORTED           # in the workspace
+    n = 1000                                                   # many: one overlap at a time, anywhere
+    for k in (0, 1, 500, 998):
+        at = [P + 4096 * ((7 * i) % n) for i in range(n)]
+        at[k + 1] = at[k] + 16
+        assert grads(at=at, sizes=[8] * n, types=[F32] * n) == UNSUPPORTED
+
+
+def test_sizes_that_no_grid_holds():
+    assert glu(M=1 << 27) == UNSUPPORTED
+    assert glu(F=1 << 27, ldh=1 << 27) == UNSUPPORTED
+    assert int8(M=1 << 27) == UNSUPPORTED
+    assert int8(N=1 << 27, ldd=1 << 27) == UNSUPPORTED
+    assert tg.gemm_glu_workspace_bytes(1 << 27, 4096, 65) == 0
+    # copies' rows: 2 K bytes rounded up to an odd multiple of 256, the largest of which below 8 MiB is 8 MiB - 256
+    assert tg.gemm_glu_workspace_bytes(4096, 4095, 4 * MB - 127) == 0
+    assert tg.gemm_glu_workspace_bytes(4096, 4095, 4 * MB - 129) == (4096 + 2 * 4095) * (8 * MB - 256)

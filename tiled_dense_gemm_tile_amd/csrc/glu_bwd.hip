@@ -237,32 +237,20 @@ gemm_status gemm_glu_backward(int64_t M, int64_t F, int64_t K, const void *dH, i
     for (int64_t ld : {dw ? lddwg : 0, dw ? lddwu : 0, Cg ? ldcg : 0, Cg ? ldcu : 0})
         if (ld * gs >= kMaxLdBytes) return GEMM_ERR_UNSUPPORTED;
     // (K is a row of the weights, so below 8 MiB too)
-    const int64_t mf = M > 0 && F > 0;
-    struct Piece {
-        const void *p;
-        int64_t bytes;
-    };
-    const Piece in[] = {{dH, mf ? matrix_bytes(M, F, lddh, 2) : 0}, {G, mf ? matrix_bytes(M, F, ldg, 2) : 0},
-                        {U, mf ? matrix_bytes(M, F, ldu, 2) : 0},   {dw && M > 0 ? X : nullptr, matrix_bytes(M, K, ldx, 2)},
-                        {dx && F > 0 ? Wg : nullptr, matrix_bytes(F, K, ldwg, 2)},
-                        {dx && F > 0 ? Wu : nullptr, matrix_bytes(F, K, ldwu, 2)}};
-    const Piece out[] = {{dx ? dX : nullptr, matrix_bytes(M, K, lddx, 2)},
-                         {dw ? dWg : nullptr, matrix_bytes(F, K, lddwg, gs)},
-                         {dw ? dWu : nullptr, matrix_bytes(F, K, lddwu, gs)}};
+    // (each operand that the call reads; then Cg, Cu and the results)
+    const void *const no = nullptr;
+    const Area in[] = {{dH, M, F, lddh, 2}, {G, M, F, ldg, 2}, {U, M, F, ldu, 2}, {dw ? X : no, M, K, ldx, 2},
+                       {dx ? Wg : no, F, K, ldwg, 2}, {dx ? Wu : no, F, K, ldwu, 2},
+                       {dw ? Cg : no, F, K, ldcg, gs}, {dw ? Cu : no, F, K, ldcu, gs}};
+    const Area out[] = {{dx ? dX : no, M, K, lddx, 2}, {dw ? dWg : no, F, K, lddwg, gs}, {dw ? dWu : no, F, K, lddwu, gs}};
+    const bool same[] = {Cg && Cg == dWg, Cu && Cu == dWu};
+    if (dw && ((same[0] && ldcg != lddwg && F > 1) || (same[1] && ldcu != lddwu && F > 1))) return GEMM_ERR_UNSUPPORTED;
     for (int i = 0; i < 3; ++i) {
-        for (const Piece &q : in)
-            if (q.bytes > 0 && overlap(out[i].p, out[i].bytes, q.p, q.bytes)) return GEMM_ERR_UNSUPPORTED;
+        for (int j = 0; j < 8; ++j)
+            if (j < 6 ? near(out[i], in[j]) : !(i == j - 5 && same[j - 6]) && meet(out[i], in[j])) return GEMM_ERR_UNSUPPORTED;
         for (int j = 0; j < i; ++j)
-            // (the halves of one tensor may lie row by row next to each other)
-            if (out[i].p == out[j].p && out[i].p) return GEMM_ERR_UNSUPPORTED;
+            if (meet(out[i], out[j])) return GEMM_ERR_UNSUPPORTED;
     }
-    const Piece c[] = {{dw ? Cg : nullptr, matrix_bytes(F, K, ldcg, gs)}, {dw ? Cu : nullptr, matrix_bytes(F, K, ldcu, gs)}};
-    if (dw && ((Cg == dWg && Cg && ldcg != lddwg) || (Cu == dWu && Cu && ldcu != lddwu) || (Cg && (Cg == dWu || Cu == dWg))))
-        return GEMM_ERR_UNSUPPORTED;
-    for (int i = 0; i < 2; ++i)
-        if ((c[i].p != out[1 + i].p && overlap(c[i].p, c[i].bytes, out[1 + i].p, out[1 + i].bytes)) ||
-            overlap(c[i].p, c[i].bytes, out[0].p, out[0].bytes))
-            return GEMM_ERR_UNSUPPORTED;
     if (F == 0) {                                      // (a product without a sum: zeros)
         tg::GluBwdArgs a = {};
         a.M = (int)M;
@@ -272,6 +260,11 @@ gemm_status gemm_glu_backward(int64_t M, int64_t F, int64_t K, const void *dH, i
     }
     if (!workspace || workspace_bytes < gemm_glu_backward_workspace_bytes(M, F, K)) return GEMM_ERR_WORKSPACE;
     if ((uintptr_t)workspace % 256 != 0) return GEMM_ERR_MISALIGNED;
+    const size_t used = gemm_glu_backward_workspace_bytes(M, F, K);
+    for (const Area &x : in)
+        if (near(x, workspace, used)) return GEMM_ERR_UNSUPPORTED;
+    for (const Area &x : out)
+        if (near(x, workspace, used)) return GEMM_ERR_UNSUPPORTED;
     tg::GluBwdArgs a = {};
     a.M = (int)M;
     a.F = (int)F;

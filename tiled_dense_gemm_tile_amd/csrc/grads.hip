@@ -9,6 +9,11 @@
 // sum.  The scaling's workgroups add the partial sums for themselves, which
 // costs less than a launch between the two, and walk the chunks from the last
 // to the first: the last ones read are still in the caches.
+#include <algorithm>
+#include <cstdlib>
+#include <initializer_list>
+#include <memory>
+
 #include "rows_api.hpp"
 #include "rows.hpp"
 
@@ -213,6 +218,47 @@ gemm_status squares(int64_t n, const void *const *src, const int64_t *sizes, con
     return GEMM_OK;
 }
 
+// Whether a result shares memory with another one, with a gradient that is not
+// its own, or with the call's other memory: results in the order of their
+// addresses, then each piece looked up among them.
+struct Span {
+    uintptr_t from, to;
+    int64_t i;
+};
+gemm_status check_shared(int64_t n, const void *const *src, void *const *dst, const int64_t *sizes, const int *types,
+                         std::initializer_list<Span> others) {
+    constexpr int64_t kFew = 256;
+    Span few[kFew];
+    std::unique_ptr<Span, void (*)(void *)> many(nullptr, free);
+    if (n > kFew) many.reset((Span *)malloc((size_t)n * sizeof(Span)));
+    Span *const at = n > kFew ? many.get() : few;
+    if (!at) return GEMM_ERR_UNSUPPORTED;
+    int64_t count = 0;
+    bool apart = false;
+    for (int64_t i = 0; i < n; ++i) {
+        if (sizes[i] == 0) continue;
+        const uintptr_t from = (uintptr_t)(dst ? dst[i] : src[i]);
+        at[count++] = {from, from + (uintptr_t)(sizes[i] * elem_size(types[i])), i};
+        apart = apart || (dst && dst[i] != src[i]);
+    }
+    std::sort(at, at + count, [](const Span &a, const Span &b) { return a.from < b.from; });
+    for (int64_t k = 1; k < count; ++k)
+        if (at[k].from < at[k - 1].to) return GEMM_ERR_UNSUPPORTED;
+    auto hit = [&](uintptr_t from, uintptr_t to) -> const Span * {
+        const Span *s = std::lower_bound(at, at + count, to, [](const Span &a, uintptr_t v) { return a.from < v; });
+        return s != at && s[-1].to > from ? s - 1 : nullptr;
+    };
+    for (int64_t i = 0; apart && i < n; ++i) {
+        if (sizes[i] == 0) continue;
+        const uintptr_t from = (uintptr_t)src[i];
+        const Span *s = hit(from, from + (uintptr_t)(sizes[i] * elem_size(types[i])));
+        if (s && !(s->i == i && s->from == from)) return GEMM_ERR_UNSUPPORTED;
+    }
+    for (const Span &o : others)
+        if (o.from && hit(o.from, o.to)) return GEMM_ERR_UNSUPPORTED;
+    return GEMM_OK;
+}
+
 gemm_status check_room(int64_t n, const void *ws, size_t bytes) {
     if (!ws || bytes < grad_workspace_bytes(n)) return GEMM_ERR_WORKSPACE;
     return (uintptr_t)ws % 256 != 0 ? GEMM_ERR_MISALIGNED : GEMM_OK;
@@ -248,6 +294,9 @@ gemm_status grad_clip(int64_t n, const void *const *grads, void *const *out, con
     if (!(max_norm >= 0.0f)) return GEMM_ERR_UNSUPPORTED;
     if (!given && !norm) return GEMM_ERR_NULL_POINTER;
     if (misaligned(given, 4) || misaligned(norm, 4)) return GEMM_ERR_MISALIGNED;
+    const uintptr_t g = (uintptr_t)given, o = (uintptr_t)norm, w = given ? 0 : (uintptr_t)workspace;
+    st = check_shared(n, grads, out, sizes, types, {{g, g + 4, 0}, {o, o + 4, 0}, {w, w + grad_workspace_bytes(n), 0}});
+    if (st != GEMM_OK) return st;
     int parts = 0;
     if (!given) {
         if ((st = check_room(n, workspace, workspace_bytes)) != GEMM_OK) return st;

@@ -193,7 +193,7 @@ gemm_status int8_quantize(int64_t rows, int64_t N, const void *X, int64_t ldx, i
 }
 
 size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    if (M <= 0 || N <= 0 || K <= 0 || M >= kMaxDim || N >= kMaxDim || K >= (int64_t)1 << 17) return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || M >= kMostRows || N >= kMostRows || K >= (int64_t)1 << 17) return 0;
     return prod_copy_bytes(M, N, 1, K);
 }
 
@@ -201,7 +201,7 @@ gemm_status gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, int64_t ld
                       int64_t ldb, const float *SB, const void *C, int64_t ldc, void *D, int64_t ldd, int out_type,
                       void *workspace, size_t workspace_bytes, hipStream_t stream) {
     if (M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_SIZE;
-    if (M >= kMaxDim || N >= kMaxDim || K >= (int64_t)1 << 17 || !elem_type(out_type)) return GEMM_ERR_UNSUPPORTED;
+    if (M >= kMostRows || N >= kMostRows || K >= (int64_t)1 << 17 || !elem_type(out_type)) return GEMM_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return GEMM_OK;
     if (lda < K || ldb < K || ldd < N || (C && ldc != 0 && ldc < N)) return GEMM_ERR_BAD_LD;
     if (!D || !SA || !SB || (K > 0 && (!A || !B))) return GEMM_ERR_NULL_POINTER;
@@ -209,11 +209,11 @@ gemm_status gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, int64_t ld
     if (misaligned(SA, 4) || misaligned(SB, 4) || misaligned(C, os) || misaligned(D, os)) return GEMM_ERR_MISALIGNED;
     if (lda >= kMaxLdBytes || ldb >= kMaxLdBytes || ldd * os >= kMaxLdBytes || (C && ldc * os >= kMaxLdBytes))
         return GEMM_ERR_UNSUPPORTED;
-    const int64_t db = matrix_bytes(M, N, ldd, os);
-    if (C == D ? C && ldc != ldd && M > 1 : overlap(C, matrix_bytes(M, N, ldc, os), D, db)) return GEMM_ERR_UNSUPPORTED;
-    if (overlap(D, db, SA, M * 4) || overlap(D, db, SB, N * 4) ||
-        (K > 0 && (overlap(D, db, A, matrix_bytes(M, K, lda, 1)) || overlap(D, db, B, matrix_bytes(N, K, ldb, 1)))))
-        return GEMM_ERR_UNSUPPORTED;
+    const Area d{D, M, N, ldd, os}, in[5] = {{A, M, K, lda, 1}, {B, N, K, ldb, 1}, {SA, 1, M, M, 4}, {SB, 1, N, N, 4},
+                                             {C, ldc ? M : 1, N, ldc ? ldc : N, os}};
+    if (C && C == D && ldc != ldd && M > 1) return GEMM_ERR_UNSUPPORTED;
+    for (int i = 0; i < (C == D ? 4 : 5); ++i)
+        if (near(d, in[i])) return GEMM_ERR_UNSUPPORTED;
     if (workspace && (uintptr_t)workspace % 256 != 0) return GEMM_ERR_MISALIGNED;
     tg::ProdArgs p = {};
     p.A = A;
@@ -225,6 +225,9 @@ gemm_status gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, int64_t ld
     p.KB = (int)K;
     const size_t need = workspace && !prod_aligned(p) ? prod_copy_bytes(M, N, 1, K) : 0;
     if (need > 0 && workspace_bytes >= need) {
+        if (near(d, workspace, need)) return GEMM_ERR_UNSUPPORTED;
+        for (const Area &a : in)
+            if (near(a, workspace, need)) return GEMM_ERR_UNSUPPORTED;
         gemm_status st = launched(tg::prod_aligned_copies(p, tg::kI8, (char *)workspace, stream));
         if (st != GEMM_OK) return st;
     }
