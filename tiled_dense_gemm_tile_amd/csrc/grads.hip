@@ -23,23 +23,25 @@ using namespace tg_api;
 
 namespace tg {
 
-constexpr int kGradTable = 128, kGradGroups = 2048;
+constexpr int kGradTable = 128, kGradFew = 16, kGradGroups = 2048;
 // Elements of a chunk: 32 KiB, 8 vectors of each of 256 threads (half of that:
 // 16-bit sums at 5.3 TB/s in place of 6.0).
 template <int T> constexpr int kGradChunk = 8 * 256 * kVE<T>;
 
+template <int MOST>
 struct GradTable {
-    const void *src[kGradTable];
-    void *dst[kGradTable];
-    int64_t n[kGradTable];
-    uint32_t first[kGradTable + 1];                    // first chunk of each tensor; [count]: all chunks
-    uint8_t type[kGradTable];
+    const void *src[MOST];
+    void *dst[MOST];
+    int64_t n[MOST];
+    uint32_t first[MOST + 1];                          // first chunk of each tensor; [count]: all chunks
+    uint8_t type[MOST];
     int count;
 };
-static_assert(sizeof(GradTable) <= 3800, "kernel arguments");
+static_assert(sizeof(GradTable<kGradTable>) <= 3800, "kernel arguments");
 
 // The tensor whose chunk c is.
-__device__ __forceinline__ int grad_tensor(const GradTable &t, uint32_t c) {
+template <int MOST>
+__device__ __forceinline__ int grad_tensor(const GradTable<MOST> &t, uint32_t c) {
     int lo = 0, hi = t.count;                          // first[lo] <= c < first[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
@@ -77,7 +79,8 @@ __device__ __forceinline__ double group_sum(double v, double *lds) {
     return lds[0] + lds[1] + lds[2] + lds[3];
 }
 
-__global__ void __launch_bounds__(256) grad_squares_kernel(GradTable t, double *part) {
+template <int MOST>
+__global__ void __launch_bounds__(256) grad_squares_kernel(GradTable<MOST> t, double *part) {
     __shared__ double lds[4];
     double s[4] = {};                                  // (four chains of additions)
     const uint32_t chunks = t.first[t.count];
@@ -117,7 +120,8 @@ __global__ void __launch_bounds__(256) grad_norm_kernel(const double *part, int 
     if (threadIdx.x == 0) *norm = v;
 }
 
-__global__ void __launch_bounds__(256) grad_scale_kernel(GradTable t, const double *part, int parts,
+template <int MOST>
+__global__ void __launch_bounds__(256) grad_scale_kernel(GradTable<MOST> t, const double *part, int parts,
                                                          const float *given, float max_norm, float *norm, bool stream_out) {
     __shared__ double lds[4];
     const float v = given ? *given : grad_total(part, parts, lds);
@@ -179,11 +183,12 @@ gemm_status check_grads(int64_t n, const void *const *src, void *const *dst, con
 
 // Tensors [at, next) in one launch's table; a tensor of more chunks than a
 // launch counts in 32 bits takes none (sizes below 2^40 have 2^27).
-int64_t fill(tg::GradTable &t, int64_t at, int64_t n, const void *const *src, void *const *dst, const int64_t *sizes,
+template <int MOST>
+int64_t fill(tg::GradTable<MOST> &t, int64_t at, int64_t n, const void *const *src, void *const *dst, const int64_t *sizes,
              const int *types) {
     t.count = 0;
     t.first[0] = 0;
-    for (; at < n && t.count < tg::kGradTable; ++at) {
+    for (; at < n && t.count < MOST; ++at) {
         if (sizes[at] == 0) continue;
         const int c = t.count++;
         t.src[c] = src[at];
@@ -196,21 +201,23 @@ int64_t fill(tg::GradTable &t, int64_t at, int64_t n, const void *const *src, vo
     return at;
 }
 
-unsigned groups(const tg::GradTable &t) {
+template <int MOST>
+unsigned groups(const tg::GradTable<MOST> &t) {
     const uint32_t c = t.first[t.count];
     return c < (uint32_t)tg::kGradGroups ? c : tg::kGradGroups;
 }
 
 // Partial sums of all tensors; *parts: how many.
+template <int MOST>
 gemm_status squares(int64_t n, const void *const *src, const int64_t *sizes, const int *types, double *part,
                     int *parts, hipStream_t s) {
-    tg::GradTable t;
+    tg::GradTable<MOST> t;
     *parts = 0;
     for (int64_t at = 0; at < n;) {
         at = fill(t, at, n, src, nullptr, sizes, types);
         if (t.count == 0) break;
         const unsigned g = groups(t);
-        hipLaunchKernelGGL(tg::grad_squares_kernel, dim3(g), dim3(256), 0, s, t, part + *parts);
+        hipLaunchKernelGGL(tg::grad_squares_kernel<MOST>, dim3(g), dim3(256), 0, s, t, part + *parts);
         const gemm_status st = launched(hipGetLastError());
         if (st != GEMM_OK) return st;
         *parts += (int)g;
@@ -259,6 +266,49 @@ gemm_status check_shared(int64_t n, const void *const *src, void *const *dst, co
     return GEMM_OK;
 }
 
+// The scaling of all tensors, the last table first.
+template <int MOST>
+gemm_status scale(int64_t n, const void *const *src, void *const *dst, const int64_t *sizes, const int *types,
+                  float max_norm, const float *given, float *norm, const double *part, int parts, hipStream_t s) {
+    // Results beyond the caches' size are streamed past them (fp32 1 GiB: 583 ->
+    // 556 us for norm and scaling).
+    int64_t bytes = 0;
+    for (int64_t i = 0; i < n; ++i) bytes += sizes[i] * elem_size(types[i]);
+    const bool stream_out = bytes >= (int64_t)256 << 20;
+    int64_t starts[kMostGrads / tg::kGradTable + 1];
+    int tables = 0;
+    tg::GradTable<MOST> t;
+    for (int64_t at = 0; at < n;) {
+        const int64_t next = fill(t, at, n, src, dst, sizes, types);
+        if (t.count == 0) break;
+        starts[tables++] = at;
+        at = next;
+    }
+    if (tables == 0) {                                 // (no elements: the norm alone)
+        t.count = 0;
+        t.first[0] = 0;
+        hipLaunchKernelGGL(tg::grad_scale_kernel<MOST>, dim3(1), dim3(256), 0, s, t, part, parts, given, max_norm, norm,
+                           false);
+        return launched(hipGetLastError());
+    }
+    for (int k = tables - 1; k >= 0; --k) {
+        if (k < tables - 1) fill(t, starts[k], n, src, dst, sizes, types);
+        hipLaunchKernelGGL(tg::grad_scale_kernel<MOST>, dim3(groups(t)), dim3(256), 0, s, t, part, parts, given,
+                           max_norm, k == 0 ? norm : nullptr, stream_out);
+        const gemm_status st = launched(hipGetLastError());
+        if (st != GEMM_OK) return st;
+    }
+    return GEMM_OK;
+}
+
+// f(integral_constant<int, MOST>): the table for n tensors.  A launch with the
+// small one passes 0.5 KiB of arguments in place of 3.7.
+template <class F>
+gemm_status with_table(int64_t n, F &&f) {
+    if (n <= tg::kGradFew) return f(std::integral_constant<int, tg::kGradFew>());
+    return f(std::integral_constant<int, tg::kGradTable>());
+}
+
 gemm_status check_room(int64_t n, const void *ws, size_t bytes) {
     if (!ws || bytes < grad_workspace_bytes(n)) return GEMM_ERR_WORKSPACE;
     return (uintptr_t)ws % 256 != 0 ? GEMM_ERR_MISALIGNED : GEMM_OK;
@@ -281,7 +331,10 @@ gemm_status grad_norm(int64_t n, const void *const *grads, const int64_t *sizes,
     if (misaligned(norm, 4)) return GEMM_ERR_MISALIGNED;
     if ((st = check_room(n, workspace, workspace_bytes)) != GEMM_OK) return st;
     int parts;
-    if ((st = squares(n, grads, sizes, types, (double *)workspace, &parts, stream)) != GEMM_OK) return st;
+    st = with_table(n, [&](auto most) {
+        return squares<decltype(most)::value>(n, grads, sizes, types, (double *)workspace, &parts, stream);
+    });
+    if (st != GEMM_OK) return st;
     hipLaunchKernelGGL(tg::grad_norm_kernel, dim3(1), dim3(256), 0, stream, (const double *)workspace, parts, norm);
     return launched(hipGetLastError());
 }
@@ -300,37 +353,15 @@ gemm_status grad_clip(int64_t n, const void *const *grads, void *const *out, con
     int parts = 0;
     if (!given) {
         if ((st = check_room(n, workspace, workspace_bytes)) != GEMM_OK) return st;
-        if ((st = squares(n, grads, sizes, types, (double *)workspace, &parts, stream)) != GEMM_OK) return st;
+        st = with_table(n, [&](auto most) {
+            return squares<decltype(most)::value>(n, grads, sizes, types, (double *)workspace, &parts, stream);
+        });
+        if (st != GEMM_OK) return st;
     }
-    // Results beyond the caches' size are streamed past them (fp32 1 GiB: 583 ->
-    // 556 us for norm and scaling).
-    int64_t bytes = 0;
-    for (int64_t i = 0; i < n; ++i) bytes += sizes[i] * elem_size(types[i]);
-    const bool stream_out = bytes >= (int64_t)256 << 20;
-    // the tables again, the last first
-    int64_t starts[kMostGrads / tg::kGradTable + 1];
-    int tables = 0;
-    tg::GradTable t;
-    for (int64_t at = 0; at < n;) {
-        const int64_t next = fill(t, at, n, grads, out, sizes, types);
-        if (t.count == 0) break;
-        starts[tables++] = at;
-        at = next;
-    }
-    if (tables == 0) {                                 // (no elements: the norm alone)
-        t.count = 0;
-        t.first[0] = 0;
-        hipLaunchKernelGGL(tg::grad_scale_kernel, dim3(1), dim3(256), 0, stream, t, (const double *)workspace, parts,
-                           given, max_norm, norm, false);
-        return launched(hipGetLastError());
-    }
-    for (int k = tables - 1; k >= 0; --k) {
-        fill(t, starts[k], n, grads, out, sizes, types);
-        hipLaunchKernelGGL(tg::grad_scale_kernel, dim3(groups(t)), dim3(256), 0, stream, t, (const double *)workspace,
-                           parts, given, max_norm, k == 0 ? norm : nullptr, stream_out);
-        if ((st = launched(hipGetLastError())) != GEMM_OK) return st;
-    }
-    return GEMM_OK;
+    return with_table(n, [&](auto most) {
+        return scale<decltype(most)::value>(n, grads, out, sizes, types, max_norm, given, norm, (const double *)workspace,
+                                            parts, stream);
+    });
 }
 
 }  // extern "C"

@@ -68,7 +68,7 @@ def _copy_room(need, sizes, unit, workspace, dev, *operands):
 def gemm_glu_workspace_bytes(M: int, F: int, K: int) -> int:
     """Workspace bytes with which :func:`gemm_glu` may copy operands whose rows
     do not start on 16 bytes (0: it would not)."""
-    return _load().gemm_glu_workspace_bytes(M, F, K)
+    return _entry("gemm_glu_workspace_bytes")(M, F, K)
 
 
 def gemm_glu(X, Wg, Wu, act="silu", H=None, G=None, U=None, keep=False, workspace=None):
@@ -105,7 +105,7 @@ def gemm_glu(X, Wg, Wu, act="silu", H=None, G=None, U=None, keep=False, workspac
 
 def gemm_glu_backward_workspace_bytes(M: int, F: int, K: int) -> int:
     """Workspace bytes :func:`gemm_glu_backward` needs."""
-    return _load().gemm_glu_backward_workspace_bytes(M, F, K)
+    return _entry("gemm_glu_backward_workspace_bytes")(M, F, K)
 
 
 def gemm_glu_backward(dH, G, U, X, Wg, Wu, act="silu", Cg=None, Cu=None, dX=None, dWg=None, dWu=None,
@@ -176,7 +176,7 @@ def int8_quantize(X, Q=None, S=None):
 def gemm_int8_workspace_bytes(M: int, N: int, K: int) -> int:
     """Workspace bytes with which :func:`gemm_int8` may copy operands whose rows
     do not start on 16 bytes (0: it would not)."""
-    return _load().gemm_int8_workspace_bytes(M, N, K)
+    return _entry("gemm_int8_workspace_bytes")(M, N, K)
 
 
 def gemm_int8(A, SA, B, SB, C=None, out_dtype=None, D=None, workspace=None):
@@ -264,7 +264,7 @@ def _at(a):
 def grad_workspace_bytes(n: int) -> int:
     """Workspace bytes :func:`grad_norm` and :func:`clip_grads` need for n
     tensors."""
-    return _load().grad_workspace_bytes(n)
+    return _entry("grad_workspace_bytes")(n)
 
 
 def grad_norm(grads, norm=None, workspace=None):

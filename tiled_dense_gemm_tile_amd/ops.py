@@ -57,7 +57,8 @@ _GPUS = [torch.device("cuda", i) for i in range(64)]
 
 
 def _new(shape, dtype, dev):
-    return torch.empty(shape, dtype=dtype, device=_GPUS[dev])
+    t = None if _fast is None else _fast.empty(shape, dtype, dev)
+    return torch.empty(shape, dtype=dtype, device=_GPUS[dev]) if t is None else t
 
 
 def _matrix(name, t, shape, dtypes, dev):
