@@ -22,23 +22,30 @@ pytestmark = pytest.mark.skipif(shutil.which(B.HIPCC) is None and not os.path.ex
                                 reason="hipcc not available")
 
 # (The kernel of two products has the same body; its paths by which product it is are too many here.)
-# An epilogue whose results are known, when it is compiled, to lie in whole pieces or not: the kernels choose at run time,
-# and paths that mix the one's stores with the other's wait do not exist.
+# An epilogue of which it is known, when it is compiled, whether its results lie in whole pieces and whether they are added
+# to something: the kernels choose at run time, and paths that mix the one's stores with the other's wait do not exist.
 SOURCE = """
 #include "prod_w4.hpp"
 namespace tg {
-template <class E, bool V> struct Known : E {
-    static constexpr bool vec = V;
+template <class E, bool V, bool A> struct Known : E {
+    static constexpr bool vec = V, add = A;
 };
-#define ONE(T, PAIR, AHEAD, E)                                                                          \\
-    template __global__ void prod_w4_kernel<T, PAIR, AHEAD, Known<E, true>>(ProdArgs, Known<E, true>); \\
-    template __global__ void prod_w4_kernel<T, PAIR, AHEAD, Known<E, false>>(ProdArgs, Known<E, false>);
+#define ONE(T, PAIR, AHEAD, E)                                                                                        \\
+    template __global__ void prod_w4_kernel<T, PAIR, AHEAD, Known<E, true, false>>(ProdArgs, Known<E, true, false>); \\
+    template __global__ void prod_w4_kernel<T, PAIR, AHEAD, Known<E, false, false>>(ProdArgs, Known<E, false, false>);
+#define ADDING(T, PAIR, AHEAD, E)                                                                                     \\
+    template __global__ void prod_w4_kernel<T, PAIR, AHEAD, Known<E, true, true>>(ProdArgs, Known<E, true, true>);    \\
+    template __global__ void prod_w4_kernel<T, PAIR, AHEAD, Known<E, false, true>>(ProdArgs, Known<E, false, true>);
 ONE(1, true, true, GluEpi<1>)
 ONE(2, true, true, GluEpi<2>)
 ONE(3, false, false, Int8Epi<0>)
 ONE(3, false, false, Int8Epi<1>)
 ONE(1, false, true, PlainEpi<0>)
 ONE(2, false, true, PlainEpi<2>)
+ADDING(3, false, false, Int8Epi<0>)
+ADDING(3, false, false, Int8Epi<1>)
+ADDING(1, false, true, PlainEpi<0>)
+ADDING(2, false, true, PlainEpi<2>)
 }
 """
 
@@ -98,16 +105,16 @@ def kernels(text):
 
 def test_operands_have_landed_at_every_barrier(assembly):
     names = kernels(assembly)
-    assert len(names) == 12
+    assert len(names) == 20
     for name in names:
         assert follow(assembly, name, at_barrier, at_end) > 4, name
 
 
 def test_the_check_sees_waits_that_are_too_short(assembly):
     """The same text with one operation more left in flight, at the K tiles' ends or behind the results."""
-    for kernel, wait, longer in (("prod_w4_kernelILi3ELb0ELb0ENS_5KnownINS_7Int8EpiILi1EEELb1", 0, 1),
-                                 ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1", 1, 2),
-                                 ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1", 16, 17)):
+    for kernel, wait, longer in (("prod_w4_kernelILi3ELb0ELb0ENS_5KnownINS_7Int8EpiILi1EEELb1ELb0", 0, 1),
+                                 ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1ELb0", 1, 2),
+                                 ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1ELb0", 16, 17)):
         name = [k for k in kernels(assembly) if kernel in k][0]
         with pytest.raises(AssertionError):
             follow(assembly.replace("vmcnt(%d)" % wait, "vmcnt(%d)" % longer), name, at_barrier, at_end)

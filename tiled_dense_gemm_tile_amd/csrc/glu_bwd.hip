@@ -172,7 +172,7 @@ gemm_status products(const tg::GluBwdArgs &a, void *dX, int64_t lddx, const tg::
     w.N = a.K;
     w.KB = a.Mp * 2;
     const tg::PlainEpi<T> ex{{nullptr, nullptr}, {dX, nullptr}, {0, 0}, {lddx, 0}, 0x7fffffff, a.M,
-                             tg::emit_whole(dX, lddx, a.K, 2)};
+                             tg::emit_whole(dX, lddx, a.K, 2), false};
     if (!e.D[0]) return launched(tg::launch_plain<T, T>(x, ex, s));
     if (!dX) return launched(tg::launch_plain<T, OT>(w, e, s));
     return launched(tg::launch_plain_two<T, OT>(x, ex, w, e, s));
@@ -194,8 +194,8 @@ gemm_status run(const tg::GluBwdArgs &a, void *dX, int64_t lddx, const void *Cg,
     const int gs = f32 ? 4 : 2;
     const bool vec = tg::emit_whole(dWg, lddwg, a.K, gs) && tg::emit_whole(dWu, lddwu, a.K, gs);
     if (f32)
-        return products<T, 0>(a, dX, lddx, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F, vec}, s);
-    return products<T, T>(a, dX, lddx, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F, vec}, s);
+        return products<T, 0>(a, dX, lddx, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F, vec, Cg != nullptr}, s);
+    return products<T, T>(a, dX, lddx, {{Cg, Cu}, {dWg, dWu}, {ldcg, ldcu}, {lddwg, lddwu}, a.Fp, a.F, vec, Cg != nullptr}, s);
 }
 
 }  // namespace

@@ -233,9 +233,9 @@ gemm_status gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, int64_t ld
     }
     const bool vec = tg::emit_whole(D, ldd, N, os);
     switch (out_type) {
-    case GEMM_TYPE_F32: return launched(tg::launch_int8<0>(p, {SA, SB, C, D, ldc, ldd, vec}, stream));
-    case GEMM_TYPE_BF16: return launched(tg::launch_int8<1>(p, {SA, SB, C, D, ldc, ldd, vec}, stream));
-    default: return launched(tg::launch_int8<2>(p, {SA, SB, C, D, ldc, ldd, vec}, stream));
+    case GEMM_TYPE_F32: return launched(tg::launch_int8<0>(p, {SA, SB, C, D, ldc, ldd, vec, C != nullptr}, stream));
+    case GEMM_TYPE_BF16: return launched(tg::launch_int8<1>(p, {SA, SB, C, D, ldc, ldd, vec, C != nullptr}, stream));
+    default: return launched(tg::launch_int8<2>(p, {SA, SB, C, D, ldc, ldd, vec, C != nullptr}, stream));
     }
 }
 

@@ -124,14 +124,39 @@ template <int W> constexpr int kStagePitch = W + 4;
 // Store instructions of a lane for 16 staged rows of W columns.
 template <int OT, int W> constexpr int kEmitStores = 16 / (64 / (W / kVE<OT>) < 16 ? 64 / (W / kVE<OT>) : 16);
 
-// 16 staged rows of W fp32 values as rows row0 .. of D (element type OT), plus
-// C's: whole 16-byte pieces of a row at any element alignment (C: NULL or the
-// same type; ldc 0: one row for all).  VEC: D's rows start on 16 bytes and hold
-// whole pieces; the stores are then always issued, kEmitStores of them (past
-// the matrix: beyond the resource), and stream past the caches.
+// A lane's part of 16 rows of C (element type OT, as stored).
+template <int OT, int W>
+struct RowsOfC {
+    typename RowVec<OT>::V v[kEmitStores<OT, W>];
+};
+
+// Rows row0 .. of C (ldc 0: one row for all), loaded without a branch and ahead
+// of their use: past the matrix another row's or column's.  VEC as below.
 template <int OT, int W, bool VEC>
+__device__ __forceinline__ void fetch_rows(RowsOfC<OT, W> &c, int lane, int row0, int col0, int M, int N, const void *C,
+                                           int64_t ldc) {
+    typedef RowVec<OT> R;
+    constexpr int LPR = W / R::VE, RPI = 64 / LPR;
+    const int lr0 = lane / LPR, col = col0 + (lane % LPR) * R::VE, at = col < N ? col : 0;
+#pragma unroll
+    for (int q = 0; q < kEmitStores<OT, W>; ++q) {
+        const int row = row0 + q * RPI + lr0;
+        const typename R::S *p = (const typename R::S *)C + (int64_t)(row < M ? row : M - 1) * ldc;
+        if constexpr (VEC)
+            c.v[q] = R::load_whole(p, at);
+        else
+            c.v[q] = R::load_raw(p, at, N);
+    }
+}
+
+// 16 staged rows of W fp32 values as rows row0 .. of D (element type OT), ADD:
+// plus C's: whole 16-byte pieces of a row at any element alignment.  VEC: D's
+// rows start on 16 bytes and hold whole pieces; the stores are then always
+// issued, kEmitStores of them (past the matrix: beyond the resource), and
+// stream past the caches.
+template <int OT, int W, bool VEC, bool ADD>
 __device__ __forceinline__ void emit_rows(const float *stage, int lane, int row0, int col0, int M, int N, void *D,
-                                          int64_t ldd, const void *C, int64_t ldc) {
+                                          int64_t ldd, const RowsOfC<OT, W> &add) {
     typedef RowVec<OT> R;
     typedef typename R::S S;
     constexpr int VE = R::VE, LPR = W / VE, RPI = 64 / LPR;
@@ -151,9 +176,8 @@ __device__ __forceinline__ void emit_rows(const float *stage, int lane, int row0
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[h + r] = t[r];
         }
-        const bool in = row < M && col < N;
-        if (C && (!VEC || in)) {
-            const typename R::V a = R::load((const S *)C + (int64_t)row * ldc, col, N);
+        if constexpr (ADD) {
+            const typename R::V a = VEC ? add.v[q] : R::settle(add.v[q], col, N);
 #pragma unroll
             for (int i = 0; i < VE; ++i) v[i] += Elem<OT>::up(a[i]);
         }
@@ -162,8 +186,8 @@ __device__ __forceinline__ void emit_rows(const float *stage, int lane, int row0
         for (int i = 0; i < VE; ++i) o[i] = Elem<OT>::down(v[i]);
         if constexpr (VEC)
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), rD,
-                                                   in ? (uint32_t)(lr * ldd + col) * (uint32_t)sizeof(S) : kOOB, 0,
-                                                   kStoreStream);
+                                                   row < M && col < N ? (uint32_t)(lr * ldd + col) * (uint32_t)sizeof(S) : kOOB,
+                                                   0, kStoreStream);
         else
             R::store((S *)D + (int64_t)row * ldd, col, N, o);
     }
@@ -180,6 +204,29 @@ __device__ __forceinline__ void stage_fence() {
     asm volatile("" ::: "memory");
 }
 
+// An epilogue has prepare(), which loads into `Regs` what its results need,
+// before the next tile's loads are issued, behind which it would wait
+// (operations are counted in order), and block(), which computes and stores
+// them.  C's rows are loaded two blocks of 16 ahead, and nothing else is loaded
+// between a tile's stores: a load there waits for the stores before it (with
+// C's rows loaded where they are added, int8 8192 x 14336 x 4096 took 492 us, 390
+// so, and 370 without C; gradients of 4096 x 6000 x 2048 added in place in fp32
+// 490 and 418).
+// (32-bit rows of 128 columns: 32 registers a block)
+template <int OT> constexpr int kAheadC = OT == 0 ? 1 : 2;
+
+// one(i, c) for the blocks in turn, fetch(c, i) AHEAD of it.
+template <int TM, bool ADD, int AHEAD, class C, class Fetch, class One>
+__device__ __forceinline__ void emit_blocks(C (&c)[AHEAD + 1], Fetch &&fetch, One &&one) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (ADD)
+            if (i + AHEAD < TM) fetch(c[(i + AHEAD) % (AHEAD + 1)], i + AHEAD);
+        one(i, c[i % (AHEAD + 1)]);
+    }
+}
+
 // D[m][n] = C[m][n] + sa[m] * sb[n] * sum, the int32 sum rounded to fp32 once
 // (exact below 2^24) and multiplied by sa * sb, C added, then rounded to OT.
 template <int OT>
@@ -188,39 +235,59 @@ struct Int8Epi {
     const void *C;
     void *D;
     int64_t ldc, ldd;
-    bool vec;                                          // emit_whole
+    bool vec, add;                                     // emit_whole; C given
     template <int TM, int TN> static constexpr int stores() { return TM * kEmitStores<OT, TN * 16> < 63 ? TM * kEmitStores<OT, TN * 16> : 63; }
 
-    template <int TM, int TN, bool AGPR, bool VEC>
-    __device__ __forceinline__ void block(const f32x4 (&acc)[TM][TN], float *stage, int lane, int row0, int col0, int M,
-                                          int N) const {
-        constexpr int W = TN * 16;
-        const int fr = lane & 15, fq = lane >> 4;
+    template <int TM, int TN>
+    struct Regs {
         f32x4 cs[TN];
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int n = col0 + 16 * j + 4 * fq + r;
-                cs[j][r] = n < N ? sb[n] : 0.0f;
-            }
+        float rs[TM];
+        RowsOfC<OT, TN * 16> c[kAheadC<OT> + 1];
+    };
+    template <int TM, int TN, bool VEC, bool ADD>
+    __device__ __forceinline__ void prepare(Regs<TM, TN> &g, int lane, int row0, int col0, int M, int N) const {
+        const int fr = lane & 15, fq = lane >> 4;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            __builtin_amdgcn_sched_barrier(0);
             const int m = row0 + 16 * i + fr;
-            const float rs = m < M ? sa[m] : 0.0f;
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const i32x4 s = __builtin_bit_cast(i32x4, acc_value<AGPR>(acc[i][j]));
-                f32x4 v;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = (float)s[r] * (rs * cs[j][r]);
-                *(f32x4 *)(stage + fr * kStagePitch<W> + 16 * j + 4 * fq) = v;
-            }
-            stage_fence();
-            emit_rows<OT, W, VEC>(stage, lane, row0 + 16 * i, col0, M, N, D, ldd, C, ldc);
-            stage_fence();
+            g.rs[i] = sa[m < M ? m : M - 1];
         }
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            g.cs[j] = RowVec<0>::load_raw(sb, col0 + 16 * j + 4 * fq < N ? col0 + 16 * j + 4 * fq : 0, N);
+        if constexpr (ADD)
+#pragma unroll
+            for (int i = 0; i < kAheadC<OT> && i < TM; ++i)
+                fetch_rows<OT, TN * 16, VEC>(g.c[i], lane, row0 + 16 * i, col0, M, N, C, ldc);
+    }
+    template <int TM, int TN, bool AGPR, bool VEC, bool ADD>
+    __device__ __forceinline__ void block(Regs<TM, TN> &g, const f32x4 (&acc)[TM][TN], float *stage, int lane, int row0,
+                                          int col0, int M, int N) const {
+        constexpr int W = TN * 16;
+        const int fr = lane & 15, fq = lane >> 4;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int n = col0 + 16 * j + 4 * fq;
+            g.cs[j] = RowVec<0>::settle(g.cs[j], n < N ? n : 0, N);
+        }
+        emit_blocks<TM, ADD, kAheadC<OT>>(
+            g.c,
+            [&](RowsOfC<OT, W> &c, int i) __attribute__((always_inline)) {
+                fetch_rows<OT, W, VEC>(c, lane, row0 + 16 * i, col0, M, N, C, ldc);
+            },
+            [&](int i, const RowsOfC<OT, W> &c) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const i32x4 s = __builtin_bit_cast(i32x4, acc_value<AGPR>(acc[i][j]));
+                    f32x4 v;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] = (float)s[r] * (g.rs[i] * g.cs[j][r]);
+                    *(f32x4 *)(stage + fr * kStagePitch<W> + 16 * j + 4 * fq) = v;
+                }
+                stage_fence();
+                emit_rows<OT, W, VEC, ADD>(stage, lane, row0 + 16 * i, col0, M, N, D, ldd, c);
+                stage_fence();
+            });
     }
     // (result m, n of a sum's bits)
     __device__ __forceinline__ void one(int m, int n, int32_t sum) const {
@@ -295,11 +362,15 @@ struct GluEpi {
     int64_t ldh, ldg, ldu;
     int act;
     bool vec;
+    static constexpr bool add = false;
     template <int TM, int TN> static constexpr int stores() { return TM * kEmitStores<OT, TN * 8>; }    // (H alone)
 
-    template <int TM, int TN, bool AGPR, bool VEC>
-    __device__ __forceinline__ void block(const f32x4 (&acc)[TM][TN], float *stage, int lane, int row0, int col0, int M,
-                                          int N) const {
+    template <int TM, int TN> struct Regs {};
+    template <int TM, int TN, bool VEC, bool ADD>
+    __device__ __forceinline__ void prepare(Regs<TM, TN> &, int, int, int, int, int) const {}
+    template <int TM, int TN, bool AGPR, bool VEC, bool ADD>
+    __device__ __forceinline__ void block(Regs<TM, TN> &, const f32x4 (&acc)[TM][TN], float *stage, int lane, int row0,
+                                          int col0, int M, int N) const {
         constexpr int W = TN * 8;
         const int fr = lane & 15, fq = lane >> 4;
 #pragma unroll
@@ -315,7 +386,7 @@ struct GluEpi {
 #pragma unroll
                 for (int j = 0; j < TN / 2; ++j) *(f32x4 *)(stage + fr * kStagePitch<W> + 16 * j + 4 * fq) = v[j];
                 stage_fence();
-                emit_rows<OT, W, VEC>(stage, lane, row0 + 16 * i, col0, M, N, D, ldd, nullptr, 0);
+                emit_rows<OT, W, VEC, false>(stage, lane, row0 + 16 * i, col0, M, N, D, ldd, {});
                 stage_fence();
             };
             if (G) put(g, G, ldg);
@@ -348,28 +419,56 @@ struct PlainEpi {
     void *D[2];
     int64_t ldc[2], ldd[2];
     int split, rows;
-    bool vec;
+    bool vec, add;
     template <int TM, int TN> static constexpr int stores() { return TM * kEmitStores<OT, TN * 16> < 63 ? TM * kEmitStores<OT, TN * 16> : 63; }
 
-    template <int TM, int TN, bool AGPR, bool VEC>
-    __device__ __forceinline__ void block(const f32x4 (&acc)[TM][TN], float *stage, int lane, int row0, int col0, int M,
-                                          int N) const {
+    template <int TM, int TN>
+    struct Regs {
+        RowsOfC<OT, TN * 16> c[kAheadC<OT> + 1];
+    };
+    // (split is a multiple of 16: 16 rows lie on one side)
+    template <int W, bool VEC>
+    __device__ __forceinline__ void fetch(RowsOfC<OT, W> &c, int lane, int r0, int col0, int N) const {
+        const int h = r0 >= split ? 1 : 0;
+        fetch_rows<OT, W, VEC>(c, lane, h ? r0 - split : r0, col0, rows, N, h ? C[1] : C[0], h ? ldc[1] : ldc[0]);
+    }
+    template <int TM, int TN, bool VEC, bool ADD>
+    __device__ __forceinline__ void prepare(Regs<TM, TN> &g, int lane, int row0, int col0, int, int N) const {
+        if constexpr (ADD)
+#pragma unroll
+            for (int i = 0; i < kAheadC<OT> && i < TM; ++i) fetch<TN * 16, VEC>(g.c[i], lane, row0 + 16 * i, col0, N);
+    }
+    template <int TM, int TN, bool AGPR, bool VEC, bool ADD>
+    __device__ __forceinline__ void block(Regs<TM, TN> &g, const f32x4 (&acc)[TM][TN], float *stage, int lane, int row0,
+                                          int col0, int, int N) const {
         constexpr int W = TN * 16;
         const int fr = lane & 15, fq = lane >> 4;
+        emit_blocks<TM, ADD, kAheadC<OT>>(
+            g.c,
+            [&](RowsOfC<OT, W> &c, int i) __attribute__((always_inline)) { fetch<W, VEC>(c, lane, row0 + 16 * i, col0, N); },
+            [&](int i, const RowsOfC<OT, W> &c) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                *(f32x4 *)(stage + fr * kStagePitch<W> + 16 * j + 4 * fq) = acc_value<AGPR>(acc[i][j]);
-            stage_fence();
-            // (split is a multiple of 16: the 16 rows lie on one side)
-            const int r0 = row0 + 16 * i, h = r0 >= split ? 1 : 0;
-            emit_rows<OT, W, VEC>(stage, lane, h ? r0 - split : r0, col0, rows, N, h ? D[1] : D[0], h ? ldd[1] : ldd[0],
-                             h ? C[1] : C[0], h ? ldc[1] : ldc[0]);
-            stage_fence();
-        }
+                for (int j = 0; j < TN; ++j)
+                    *(f32x4 *)(stage + fr * kStagePitch<W> + 16 * j + 4 * fq) = acc_value<AGPR>(acc[i][j]);
+                stage_fence();
+                const int r0 = row0 + 16 * i, h = r0 >= split ? 1 : 0;
+                emit_rows<OT, W, VEC, ADD>(stage, lane, h ? r0 - split : r0, col0, rows, N, h ? D[1] : D[0],
+                                           h ? ldd[1] : ldd[0], c);
+                stage_fence();
+            });
     }
 };
+
+// f(VEC, ADD), as constants, of an epilogue's `vec` and `add` (C given).
+template <class Epi, class F>
+__device__ __forceinline__ void with_form(const Epi &e, F &&f) {
+    if (e.vec) {
+        if (e.add) f(std::true_type(), std::true_type());
+        else f(std::true_type(), std::false_type());
+    } else {
+        if (e.add) f(std::false_type(), std::true_type());
+        else f(std::false_type(), std::false_type());
+    }
+}
 
 }  // namespace tg

@@ -23,9 +23,9 @@ namespace tg {
 
 template <int BM, int BN, int S, int KS> constexpr int kMidLds = KS * S * (BM + BN) * 128;
 
-// Tile (tmi, tni); emit(acc, stage, lane, row0, col0) stores a wave's results.
-template <int T, int BM, int BN, int S, int KS, bool PAIR, bool ANY, class Emit>
-__device__ __forceinline__ void prod_mid_body(const ProdArgs &p, int tmi, int tni, char *lds, Emit &&emit) {
+// Tile (tmi, tni).
+template <int T, int BM, int BN, int S, int KS, bool PAIR, bool ANY, class Epi>
+__device__ __forceinline__ void prod_mid_body(const ProdArgs &p, int tmi, int tni, char *lds, const Epi &e) {
     constexpr int WTM = BM / 2, WTN = BN / 2, TM = WTM / 16, TN = WTN / 16;
     constexpr int LA = BM / 32, LB = BN / 32;          // load instructions of a wave a tile
     constexpr int SLOT_A = BM * 128, SLOT_B = BN * 128, B_BASE = S * SLOT_A;
@@ -184,6 +184,12 @@ __device__ __forceinline__ void prod_mid_body(const ProdArgs &p, int tmi, int tn
         wait_vmcnt<0>();                               // no load still writes a slot
         barrier();
     }
+    typename Epi::template Regs<TM, TN> regs;
+    const int row0 = m0 + wm * WTM, col0 = n0 + wn * W;
+    if (e.add)
+        e.template prepare<TM, TN, false, true>(regs, lane, row0, col0, p.M, p.N);
+    else
+        e.template prepare<TM, TN, false, false>(regs, lane, row0, col0, p.M, p.N);
     if constexpr (KS > 1) {
         // (every wave is past the last reads of the slots)
         if (group > 0) {
@@ -209,14 +215,11 @@ __device__ __forceinline__ void prod_mid_body(const ProdArgs &p, int tmi, int tn
                 }
         stage_fence();
     }
-    emit(acc, (float *)(KS > 1 ? lds + (KS - 1) * 4 * SUMS + wave * STAGE : lds + wave * STAGE), lane, m0 + wm * WTM,
-         n0 + wn * W);
-}
-
-template <class Epi, int TM, int TN>
-__device__ __forceinline__ void emit_vgpr(const Epi &e, const ProdArgs &p, const f32x4 (&acc)[TM][TN], float *stage,
-                                          int lane, int row0, int col0) {
-    e.template block<TM, TN, false, false>(acc, stage, lane, row0, col0, p.M, p.N);
+    float *stage = (float *)(KS > 1 ? lds + (KS - 1) * 4 * SUMS + wave * STAGE : lds + wave * STAGE);
+    if (e.add)
+        e.template block<TM, TN, false, false, true>(regs, acc, stage, lane, row0, col0, p.M, p.N);
+    else
+        e.template block<TM, TN, false, false, false>(regs, acc, stage, lane, row0, col0, p.M, p.N);
 }
 
 // QUARTERS: the tiles are the quarters of those 256 x 256 tiles (in prod_w4's
@@ -234,9 +237,7 @@ __global__ void __launch_bounds__(256 * KS) prod_mid_kernel(ProdArgs p, Epi e) {
     } else {
         tile_order(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
     }
-    prod_mid_body<T, BM, BN, S, KS, PAIR, ANY>(
-        p, tmi, tni, lds, [&](const auto &acc, float *stage, int lane, int row0, int col0)
-                              __attribute__((always_inline)) { emit_vgpr(e, p, acc, stage, lane, row0, col0); });
+    prod_mid_body<T, BM, BN, S, KS, PAIR, ANY>(p, tmi, tni, lds, e);
 }
 
 }  // namespace tg

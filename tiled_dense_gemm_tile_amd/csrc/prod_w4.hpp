@@ -41,12 +41,13 @@ __device__ __forceinline__ void prod_mfma_agpr(f32x4 &acc, const u32x4 &a, const
 constexpr int kW4Lds = 4 * 256 * 128 + 1024;
 
 // Workgroup wg of nwg that walk the tiles wg, wg + nwg, ... below p.run.
-// reload(): p again, from memory; emit(acc, stage, lane, row0, col0, M, N)
-// stores a quadrant's results and waits for all that was issued before their
-// last stores.  (Operand rows on 16 bytes, KB > 0 a multiple of 16.)
-template <int T, bool PAIR, bool PREFETCH, class Reload, class Emit>
+// reload(): p again, from memory; prepare(lane, row0, col0, M, N) loads what a
+// quadrant's results need, before the tile's last MFMAs and the next one's first
+// loads; emit(regs, acc, stage, lane, row0, col0, M, N) stores them and waits for
+// all that was issued before their last stores.  (Operand rows on 16 bytes, KB > 0 a multiple of 16.)
+template <int T, bool PAIR, bool PREFETCH, class Reload, class Prepare, class Emit>
 __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg, char *smem, Reload &&reload,
-                                             Emit &&emit) {
+                                             Prepare &&prepare, Emit &&emit) {
     constexpr int TM = 8, TN = 8, Q = TM * TN, SLOT = 256 * 128, B_BASE = 2 * SLOT;
     constexpr int BN = PAIR ? 128 : 256;               // result columns of a tile
     constexpr int W = BN / 2, STAGE = 16 * kStagePitch<W> * 4;
@@ -186,13 +187,14 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
             tile(std::false_type(), even(), t + 1);
         }
         if (t < nt) tile(std::false_type(), odd(), t);
+        const ProdArgs r = reload();
+        const int dm0 = m0, dn0 = n0;
+        auto regs = prepare(lane, dm0 + wm * 128, dn0 + wn * W, r.M, r.N);
 #pragma unroll
         for (int q = 0; q < Q; ++q) mfma(std::false_type(), 1, q / TN, q % TN);
         mfma_result_fence<TM, TN>(acc);
         // (every wave is past its last barrier, so past all reads of the slots;
         // the loads of the tile past the end have landed there)
-        const ProdArgs r = reload();
-        const int dm0 = m0, dn0 = n0;
         vt += nwg;
         const bool more = vt < r.run;
         if (more) {
@@ -210,7 +212,7 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
 #pragma unroll
             for (int j = 0; j < 8; ++j) dma(rB, B_BASE + (4 * j + wv) * 1024, vb, j * bstep);
         }
-        emit(acc, stage, lane, dm0 + wm * 128, dn0 + wn * W, r.M, r.N);
+        emit(regs, acc, stage, lane, dm0 + wm * 128, dn0 + wn * W, r.M, r.N);
         if (!more) {
             wait_vmcnt<0>();
             break;
@@ -220,28 +222,38 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
     }
 }
 
+template <class Epi, class Regs>
+__device__ __forceinline__ void prepare_agpr(const Epi &e, Regs &regs, int lane, int row0, int col0, int M, int N) {
+    with_form(e, [&](auto vec, auto add) __attribute__((always_inline)) {
+        e.template prepare<8, 8, vec, add>(regs, lane, row0, col0, M, N);
+    });
+}
+
 // An epilogue's results.  The next tile's first loads have landed then; the
 // results' stores issued after them, of which there are at least stores(), may
 // still run.
 template <class Epi, int TM, int TN>
-__device__ __forceinline__ void emit_agpr(const Epi &e, const f32x4 (&acc)[TM][TN], float *stage, int lane, int row0,
-                                          int col0, int M, int N) {
-    if (e.vec) {
-        e.template block<TM, TN, true, true>(acc, stage, lane, row0, col0, M, N);
-        wait_vmcnt<Epi::template stores<TM, TN>()>();
-    } else {
-        e.template block<TM, TN, true, false>(acc, stage, lane, row0, col0, M, N);
-        wait_vmcnt<0>();
-    }
+__device__ __forceinline__ void emit_agpr(const Epi &e, typename Epi::template Regs<TM, TN> &regs, const f32x4 (&acc)[TM][TN],
+                                          float *stage, int lane, int row0, int col0, int M, int N) {
+    with_form(e, [&](auto vec, auto add) __attribute__((always_inline)) {
+        e.template block<TM, TN, true, vec, add>(regs, acc, stage, lane, row0, col0, M, N);
+        wait_vmcnt<vec ? Epi::template stores<TM, TN>() : 0>();
+    });
 }
 
 template <int T, bool PAIR, bool PREFETCH, class Epi>
 __global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
     __shared__ __attribute__((aligned(1024))) char smem[kW4Lds];
+    typedef typename Epi::template Regs<8, 8> Regs;
     prod_w4_body<T, PAIR, PREFETCH>(
         p, blockIdx.x, gridDim.x, smem, [] { return kernel_arg0_reloaded<ProdArgs>(); },
-        [&](const auto &acc, float *stage, int lane, int row0, int col0, int M, int N)
-            __attribute__((always_inline)) { emit_agpr(e, acc, stage, lane, row0, col0, M, N); });
+        [&](int lane, int row0, int col0, int M, int N) __attribute__((always_inline)) {
+            Regs r;
+            prepare_agpr(e, r, lane, row0, col0, M, N);
+            return r;
+        },
+        [&](Regs &regs, const auto &acc, float *stage, int lane, int row0, int col0, int M, int N)
+            __attribute__((always_inline)) { emit_agpr(e, regs, acc, stage, lane, row0, col0, M, N); });
 }
 
 // Two products in one launch: the first on workgroups below `split`, the second
@@ -253,17 +265,29 @@ __global__ void __launch_bounds__(256) prod_w4_two_kernel(ProdPair q, Epi0 e0, E
     const ProdArgs p = second ? q.p[1] : q.p[0];
     const int wg = second ? blockIdx.x - q.split : blockIdx.x;
     if (wg >= p.run) return;                           // (more workgroups than tiles)
+    struct Regs {
+        typename Epi0::template Regs<8, 8> a;
+        typename Epi1::template Regs<8, 8> b;
+    };
     prod_w4_body<T, false, true>(
         p, wg, second ? gridDim.x - q.split : q.split, smem,
         [&]() __attribute__((always_inline)) {
             const ProdPair r = kernel_arg0_reloaded<ProdPair>();
             return second ? r.p[1] : r.p[0];
         },
-        [&](const auto &acc, float *stage, int lane, int row0, int col0, int M, int N) __attribute__((always_inline)) {
+        [&](int lane, int row0, int col0, int M, int N) __attribute__((always_inline)) {
+            Regs r;
             if (second)
-                emit_agpr(e1, acc, stage, lane, row0, col0, M, N);
+                prepare_agpr(e1, r.b, lane, row0, col0, M, N);
             else
-                emit_agpr(e0, acc, stage, lane, row0, col0, M, N);
+                prepare_agpr(e0, r.a, lane, row0, col0, M, N);
+            return r;
+        },
+        [&](Regs &regs, const auto &acc, float *stage, int lane, int row0, int col0, int M, int N) __attribute__((always_inline)) {
+            if (second)
+                emit_agpr(e1, regs.b, acc, stage, lane, row0, col0, M, N);
+            else
+                emit_agpr(e0, regs.a, acc, stage, lane, row0, col0, M, N);
         });
 }
 
