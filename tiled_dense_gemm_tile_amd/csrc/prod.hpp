@@ -204,10 +204,10 @@ __device__ __forceinline__ void stage_fence() {
     asm volatile("" ::: "memory");
 }
 
-// An epilogue has prepare(), which loads into `Regs` what its results need,
-// before the next tile's loads are issued, behind which it would wait
-// (operations are counted in order), and block(), which computes and stores
-// them.  C's rows are loaded two blocks of 16 ahead, and nothing else is loaded
+// An epilogue has scales() and prepare(), which load into `Regs` what its
+// results need and the first of C's rows, before the next tile's loads are
+// issued, behind which they would wait (operations are counted in order), and
+// block(), which computes and stores the results.  C's rows are loaded two blocks of 16 ahead, and nothing else is loaded
 // between a tile's stores: a load there waits for the stores before it (with
 // C's rows loaded where they are added, int8 8192 x 14336 x 4096 took 492 us, 390
 // so, and 370 without C; gradients of 4096 x 6000 x 2048 added in place in fp32
@@ -244,8 +244,8 @@ struct Int8Epi {
         float rs[TM];
         RowsOfC<OT, TN * 16> c[kAheadC<OT> + 1];
     };
-    template <int TM, int TN, bool VEC, bool ADD>
-    __device__ __forceinline__ void prepare(Regs<TM, TN> &g, int lane, int row0, int col0, int M, int N) const {
+    template <int TM, int TN>
+    __device__ __forceinline__ void scales(Regs<TM, TN> &g, int lane, int row0, int col0, int M, int N) const {
         const int fr = lane & 15, fq = lane >> 4;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
@@ -255,6 +255,9 @@ struct Int8Epi {
 #pragma unroll
         for (int j = 0; j < TN; ++j)
             g.cs[j] = RowVec<0>::load_raw(sb, col0 + 16 * j + 4 * fq < N ? col0 + 16 * j + 4 * fq : 0, N);
+    }
+    template <int TM, int TN, bool VEC, bool ADD>
+    __device__ __forceinline__ void prepare(Regs<TM, TN> &g, int lane, int row0, int col0, int M, int N) const {
         if constexpr (ADD)
 #pragma unroll
             for (int i = 0; i < kAheadC<OT> && i < TM; ++i)
@@ -366,6 +369,8 @@ struct GluEpi {
     template <int TM, int TN> static constexpr int stores() { return TM * kEmitStores<OT, TN * 8>; }    // (H alone)
 
     template <int TM, int TN> struct Regs {};
+    template <int TM, int TN>
+    __device__ __forceinline__ void scales(Regs<TM, TN> &, int, int, int, int, int) const {}
     template <int TM, int TN, bool VEC, bool ADD>
     __device__ __forceinline__ void prepare(Regs<TM, TN> &, int, int, int, int, int) const {}
     template <int TM, int TN, bool AGPR, bool VEC, bool ADD>
@@ -426,6 +431,8 @@ struct PlainEpi {
     struct Regs {
         RowsOfC<OT, TN * 16> c[kAheadC<OT> + 1];
     };
+    template <int TM, int TN>
+    __device__ __forceinline__ void scales(Regs<TM, TN> &, int, int, int, int, int) const {}
     // (split is a multiple of 16: 16 rows lie on one side)
     template <int W, bool VEC>
     __device__ __forceinline__ void fetch(RowsOfC<OT, W> &c, int lane, int r0, int col0, int N) const {

@@ -133,6 +133,10 @@ __device__ __forceinline__ void prod_mid_body(const ProdArgs &p, int tmi, int tn
         }
     };
 
+    typename Epi::template Regs<TM, TN> regs;
+    const int row0 = m0 + wm * WTM, col0 = n0 + wn * W;
+    e.template scales<TM, TN>(regs, lane, row0, col0, p.M, p.N);
+
     if constexpr (ANY) {
         // tile t's chunks are in registers t % PD until they are written to slot
         // t % 2, before the barrier that opens it; that slot's last reads were
@@ -184,12 +188,8 @@ __device__ __forceinline__ void prod_mid_body(const ProdArgs &p, int tmi, int tn
         wait_vmcnt<0>();                               // no load still writes a slot
         barrier();
     }
-    typename Epi::template Regs<TM, TN> regs;
-    const int row0 = m0 + wm * WTM, col0 = n0 + wn * W;
     if (e.add)
         e.template prepare<TM, TN, false, true>(regs, lane, row0, col0, p.M, p.N);
-    else
-        e.template prepare<TM, TN, false, false>(regs, lane, row0, col0, p.M, p.N);
     if constexpr (KS > 1) {
         // (every wave is past the last reads of the slots)
         if (group > 0) {

@@ -224,6 +224,7 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
 
 template <class Epi, class Regs>
 __device__ __forceinline__ void prepare_agpr(const Epi &e, Regs &regs, int lane, int row0, int col0, int M, int N) {
+    e.template scales<8, 8>(regs, lane, row0, col0, M, N);
     with_form(e, [&](auto vec, auto add) __attribute__((always_inline)) {
         e.template prepare<8, 8, vec, add>(regs, lane, row0, col0, M, N);
     });
