@@ -555,3 +555,35 @@ def test_clip_into_other_tensors_in_any_order():
     for got, w in zip(out, want):
         # the factor's two roundings and the norm's, the product's
         within(got, w.double() / (total + 1e-6), 5 * U * w.double().abs() / total)
+
+
+# ---- 256 x 128 tiles -------------------------------------------------------------------
+
+# 235, 256 and 130 tiles, K of 8 to 33 tiles that ends inside one, results in whole pieces and not
+@pytest.mark.parametrize("m,n", [(1100, 6000), (2048, 4096), (300, 8300), (1100, 5999)])
+@pytest.mark.parametrize("k", [912, 1040, 2944, 4160])
+def test_int8_narrow_tiles(m, n, k):
+    for out in (BF, F32):
+        check_int8(m, n, k, out)
+        check_int8(m, n, k, out, "matrix", pads=(16, 32, 0))
+    check_int8(m, n, k, FP, "matrix", pads=(0, 0, 3))
+    check_int8(m, n, k, BF, "row")
+
+
+@pytest.mark.parametrize("m,f,k", [(1100, 3000, 520), (2048, 2048, 464), (300, 4150, 1480), (1100, 2999, 1608)])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=KIND.get)
+def test_glu_narrow_tiles(m, f, k, dtype):
+    x, wg, wu = rand(1, m, k, dtype=dtype), rand(2, f, k, dtype=dtype, scale=k ** -0.5), rand(3, f, k, dtype=dtype, scale=k ** -0.5)
+    check_glu(x, wg, wu, "gelu")
+    out = [padded(torch.zeros(m, f, dtype=dtype, device=DEV), f + 8 + i, 7.0) for i in range(3)]
+    check_glu(x, wg, wu, "silu", H=out[0], G=out[1], U=out[2])
+    for o in out:
+        whole = o.as_strided((m + 1, o.stride(0)), (o.stride(0), 1))
+        assert bool((whole[:, f:] == 7).all()) and bool((whole[m] == 7).all())
+
+
+@pytest.mark.parametrize("m,f,k", [(1000, 2728, 1024), (1001, 2731, 1003), (1600, 2731, 1003), (1100, 300, 6000)])
+@pytest.mark.parametrize("dtype,grad", [(BF, BF), (BF, F32), (FP, FP)])
+def test_glu_backward_narrow_tiles(m, f, k, dtype, grad):
+    check_backward(m, f, k, dtype, grad=grad)
+    check_backward(m, f, k, dtype, grad=grad, acc=True)

@@ -46,6 +46,15 @@ ADDING(3, false, false, Int8Epi<0>)
 ADDING(3, false, false, Int8Epi<1>)
 ADDING(1, false, true, PlainEpi<0>)
 ADDING(2, false, true, PlainEpi<2>)
+#define NARROW(T, PAIR, E, ...) template __global__ void prod_w4_kernel<T, PAIR, true, Known<E, __VA_ARGS__>, 4>(ProdArgs, Known<E, __VA_ARGS__>);
+NARROW(1, true, GluEpi<1>, true, false)
+NARROW(2, true, GluEpi<2>, false, false)
+NARROW(3, false, Int8Epi<0>, true, true)
+NARROW(3, false, Int8Epi<1>, false, true)
+NARROW(3, false, Int8Epi<1>, true, false)
+NARROW(1, false, PlainEpi<0>, false, true)
+NARROW(2, false, PlainEpi<2>, true, true)
+NARROW(2, false, PlainEpi<2>, true, false)
 }
 """
 
@@ -105,16 +114,16 @@ def kernels(text):
 
 def test_operands_have_landed_at_every_barrier(assembly):
     names = kernels(assembly)
-    assert len(names) == 20
+    assert len(names) == 28
     for name in names:
         assert follow(assembly, name, at_barrier, at_end) > 4, name
 
 
 def test_the_check_sees_waits_that_are_too_short(assembly):
     """The same text with one operation more left in flight, at the K tiles' ends or behind the results."""
-    for kernel, wait, longer in (("prod_w4_kernelILi3ELb0ELb0ENS_5KnownINS_7Int8EpiILi1EEELb1ELb0", 0, 1),
-                                 ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1ELb0", 1, 2),
-                                 ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1ELb0", 16, 17)):
+    for kernel, wait, longer in (("prod_w4_kernelILi3ELb0ELb0ENS_5KnownINS_7Int8EpiILi1EEELb1ELb0EEELi8", 0, 1),
+                                 ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1ELb0EEELi8", 1, 2),
+                                 ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1ELb0EEELi8", 16, 17)):
         name = [k for k in kernels(assembly) if kernel in k][0]
         with pytest.raises(AssertionError):
             follow(assembly.replace("vmcnt(%d)" % wait, "vmcnt(%d)" % longer), name, at_barrier, at_end)

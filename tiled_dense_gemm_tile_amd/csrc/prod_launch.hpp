@@ -50,6 +50,14 @@ hipError_t go_w4(ProdArgs p, const Epi &e, hipStream_t s) {
     return hipGetLastError();
 }
 
+// 256 x 128 tiles (PAIR: 64 columns), one a CU.
+template <int T, bool PAIR, class Epi>
+hipError_t go_w4_narrow(ProdArgs p, const Epi &e, hipStream_t s) {
+    p.run = (int)prod_tiles(p, 256, PAIR ? 64 : 128);
+    hipLaunchKernelGGL((prod_w4_kernel<T, PAIR, true, Epi, 4>), dim3(p.run), dim3(256), 0, s, p, e);
+    return hipGetLastError();
+}
+
 // Tiles by how many of them there are (a K tile's loads bound a workgroup, 31
 // to 44 bytes a clock and CU, until all CUs have work; times in us, weights
 // that no cache holds, int8 M x N x K or the gated block's M x F x K in bf16).
@@ -82,6 +90,15 @@ hipError_t launch_prod_tiles(const ProdArgs &p, const Epi &e, hipStream_t s) {
     // x 14336 x 4096 41 and 47
     if constexpr (!ANY)
         if (t128 <= 256) return go_mid<T, 128, 128, 2, 2, PAIR, ANY>(p, e, s);
+    if constexpr (!ANY) {
+        // 256 x 128 on one round of CUs, for K that covers the longer way to the
+        // first and the last K tile, and the results' stores by half the waves
+        // (K tiles of 128 bytes; int8 2000 x 4096 x 4096 34.4 us, 128 x 128 43.7;
+        // gated 256 x 14336 x 4096 62 and 73, 2048 x 2048 x 2048 32 and 38, x 512
+        // 13.1 and 13.9, 1200 x 2048 x 256 9.3 and 8.8; results at any alignment:
+        // int8 2000 x 4095 x 4096 36.8 and 44.0, with C x 1024 21.0 and 18.3)
+        if (tiles_of(p, 256, 128 / D) <= 256 && p.KB > (e.vec ? 7 : 23) * 128) return go_w4_narrow<T, PAIR>(p, e, s);
+    }
     // two workgroups a CU (gated 1024 x 2736 x 1008: 19.2; four slots and one
     // workgroup 29.3, 64 x 64 28.4)
     return go_mid<T, 128, 128, 2, 1, PAIR, ANY>(p, e, s);
@@ -106,8 +123,9 @@ inline double prod_estimate(const ProdArgs &p) {
 // the CUs, takes longer for a K tile (1.57 us in place of 1.41: two sets of
 // panels share the L2s), but leaves no CU idle in a last round and suits a
 // product with too few tiles for the GPU (gradients of 4096 x 6000 x 2048: 403
-// us, one after the other 478; 8192 x 1000 x 4096 267 and 296; 8192 x 14336 x
-// 4096, whose tiles fill whole rounds, 3281 and 3043).
+// us, one after the other 478; 8192 x 1000 x 4096 267 and 296; 3000 x 2000 x 1504
+// 103 and 121; 8192 x 14336 x 4096, whose tiles fill whole rounds, 3281 and
+// 3043).
 template <int T, class Epi0, class Epi1>
 hipError_t launch_prod_two(const ProdArgs &p0, const Epi0 &e0, const ProdArgs &p1, const Epi1 &e1, hipStream_t s) {
     ProdPair q;

@@ -15,7 +15,6 @@
 // and stored from the other slots.
 #pragma once
 
-#include "gemm_f16_w4.hpp"                             // mfma_result_fence
 #include "prod.hpp"
 
 namespace tg {
@@ -38,21 +37,37 @@ __device__ __forceinline__ void prod_mfma_agpr(f32x4 &acc, const u32x4 &a, const
 #undef TG_PROD_MFMA
 }
 
-constexpr int kW4Lds = 4 * 256 * 128 + 1024;
+// The last MFMAs' results are in their registers behind this (a 16x16 one's 8
+// passes and the longest wait that a read of its result needs: 36 cycles).
+template <int TM, int TN>
+__device__ __forceinline__ void prod_result_fence(f32x4 (&acc)[TM][TN]) {
+    asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 3" : "+a"(acc[0][0]), "+a"(acc[0][1]), "+a"(acc[0][2]), "+a"(acc[0][3]));
+#pragma unroll
+    for (int k = 4; k < TM * TN; k += 4) {
+        f32x4 *a = &acc[k / TN][k % TN];
+        asm volatile("" : "+a"(a[0]), "+a"(a[1]), "+a"(a[2]), "+a"(a[3]));
+    }
+}
+
+// LDS of a workgroup with 16 TN rows of B a wave (TN 8 as above; 4: 256 x 128
+// tiles, PAIR 64 columns): two slots an operand, and what lines brought ahead
+// leave behind.
+template <int TN> constexpr int kW4Lds = 2 * (256 + 32 * TN) * 128 + 1024;
 
 // Workgroup wg of nwg that walk the tiles wg, wg + nwg, ... below p.run.
 // reload(): p again, from memory; prepare(lane, row0, col0, M, N) loads what a
 // quadrant's results need, before the tile's last MFMAs and the next one's first
 // loads; emit(regs, acc, stage, lane, row0, col0, M, N) stores them and waits for
 // all that was issued before their last stores.  (Operand rows on 16 bytes, KB > 0 a multiple of 16.)
-template <int T, bool PAIR, bool PREFETCH, class Reload, class Prepare, class Emit>
+template <int T, bool PAIR, bool PREFETCH, int TN, class Reload, class Prepare, class Emit>
 __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg, char *smem, Reload &&reload,
                                              Prepare &&prepare, Emit &&emit) {
-    constexpr int TM = 8, TN = 8, Q = TM * TN, SLOT = 256 * 128, B_BASE = 2 * SLOT;
-    constexpr int BN = PAIR ? 128 : 256;               // result columns of a tile
+    constexpr int TM = 8, Q = TM * TN, SLOT = 256 * 128, B_SLOT = 32 * TN * 128, B_BASE = 2 * SLOT;
+    constexpr int BN = PAIR ? 16 * TN : 32 * TN;       // result columns of a tile
     constexpr int W = BN / 2, STAGE = 16 * kStagePitch<W> * 4;
     constexpr int PF = 3;                              // K tiles ahead
-    static_assert(2 * STAGE <= SLOT && kW4Lds == 4 * SLOT + 1024, "LDS");
+    static_assert(TN == 8 || TN == 4, "schedule");
+    static_assert(2 * STAGE <= B_SLOT && kW4Lds<TN> == B_BASE + 2 * B_SLOT + 1024, "LDS");
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -102,27 +117,27 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
     auto fetch_b = [&](int t, int s, int j) __attribute__((always_inline)) {
         const int k0 = koff(t);
         const uint32_t v = k0 + kc < KB ? boff + k0 : kOOB;
-        dma(rB, B_BASE + s * SLOT + (4 * j + wave) * 1024, v, j * bstep);
+        dma(rB, B_BASE + s * B_SLOT + (4 * j + wave) * 1024, v, j * bstep);
     };
 
     // Lines of K tile t + PF brought into this XCD's L2, a 128-byte line a lane:
     // of each of its panels a workgroup takes the part that falls to it among
     // those that share the panel (in the tile order 8 share rows of A and 4 rows
-    // of B), 32 rows of A and 64 of B.  Four bytes of each line go to LDS that
+    // of B), 32 rows of A and 64 of B (TN 4: 32).  Four bytes of each line go to LDS that
     // nobody reads; the wait at a window's end leaves them in flight.  Hides
     // what the L2s miss (gradients of 8192 x 14336 x 4096: 3280 -> 3020 us; 2 or
     // 5 tiles ahead the same).
     auto pf_off = [&]() __attribute__((always_inline)) {
         if (wave == 0) return lane < 32 ? (uint32_t)((32 * (tni & 7) + lane) * (int)p.lda) : kOOB;
-        if (PAIR) return wave < 3 && lane < 32 ? (uint32_t)((32 * (tmi & 3) + lane) * (int)ldb) : kOOB;
-        return wave == 1 ? (uint32_t)((64 * (tmi & 3) + lane) * (int)ldb) : kOOB;
+        constexpr int OF_B = PAIR ? 4 * TN : 8 * TN;
+        return wave < (PAIR ? 3 : 2) && lane < OF_B ? (uint32_t)((OF_B * (tmi & 3) + lane) * (int)ldb) : kOOB;
     };
     uint32_t pfo = pf_off();
     int pfk = 0;                                       // K offset of the tile next prefetched
     auto prefetch = [&]() __attribute__((always_inline)) {
         pfk = pfk + 128 >= nt * 128 ? pfk + 128 - nt * 128 : pfk + 128;    // (past the end: the circle again)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            wave == 0 ? rA : rB, (__attribute__((address_space(3))) void *)(smem + 4 * SLOT + wave * 256), 4, pfo, pfk, 0, 0);
+            wave == 0 ? rA : rB, (__attribute__((address_space(3))) void *)(smem + B_BASE + 2 * B_SLOT + wave * 256), 4, pfo, pfk, 0, 0);
     };
 
     const int fr = lane & 15, fq = lane >> 4, fswz = swz16(fr);
@@ -130,18 +145,18 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
         a_read[st] = (wm * 128 + fr) * 128 + (((4 * st + fq) ^ fswz) << 4);
-        b_read[st] = B_BASE + (wn * 128 + fr) * 128 + (((4 * st + fq) ^ fswz) << 4);
+        b_read[st] = B_BASE + (wn * 16 * TN + fr) * 128 + (((4 * st + fq) ^ fswz) << 4);
     }
     f32x4 acc[TM][TN];
     u32x4 fa[2][TM], fb[2][TN];                        // [step][block]
     // fragment read k of step st from slot s, in the order the MFMAs use them: A
-    // block 0, B blocks 0 .. 7, A blocks 1 .. 7
+    // block 0, the B blocks, A blocks 1 .. 7
     auto read_frag = [&](int s, int st, int k) __attribute__((always_inline)) {
         if (k == 0 || k > TN) {
             const int i = k == 0 ? 0 : k - TN;
             fa[st][i] = *(const u32x4 *)(smem + a_read[st] + (s * SLOT + i * 16 * 128));
         } else {
-            fb[st][k - 1] = *(const u32x4 *)(smem + b_read[st] + (s * SLOT + (k - 1) * 16 * 128));
+            fb[st][k - 1] = *(const u32x4 *)(smem + b_read[st] + (s * B_SLOT + (k - 1) * 16 * 128));
         }
     };
     auto mfma = [&](auto zero, int st, int i, int j) __attribute__((always_inline)) {
@@ -154,15 +169,22 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             if constexpr (!decltype(first)::value) mfma(std::false_type(), 1, q / TN, q % TN);
-            if (q % 4 == 0) read_frag(S, 0, q / 4);
-            if (q % 8 == 0) fetch_a(t + 1, 1 - S, q / 8);
-            if (q % 8 == 4) fetch_b(t + 1, 1 - S, q / 8);
-            if (PREFETCH && q == 63) prefetch();
+            if constexpr (TN == 8) {
+                if (q % 4 == 0) read_frag(S, 0, q / 4);
+                if (q % 8 == 0) fetch_a(t + 1, 1 - S, q / 8);
+                if (q % 8 == 4) fetch_b(t + 1, 1 - S, q / 8);
+            } else {
+                if (q % 2 == 0 && q / 2 < TM + TN) read_frag(S, 0, q / 2);
+                if (q % 4 == 1) fetch_a(t + 1, 1 - S, q / 4);
+                if (q % 8 == 3) fetch_b(t + 1, 1 - S, q / 8);
+            }
+            if (PREFETCH && q == Q - 1) prefetch();
         }
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             mfma(first, 0, q / TN, q % TN);
-            if (q % 3 == 0 && q / 3 < TM + TN) read_frag(S, 1, q / 3);
+            constexpr int EVERY = TN == 8 ? 3 : 2;
+            if (q % EVERY == 0 && q / EVERY < TM + TN) read_frag(S, 1, q / EVERY);
         }
         wait_vmcnt<PREFETCH ? 1 : 0>();                // tile t + 1 landed
         wait_lgkmcnt0();
@@ -172,10 +194,10 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
 #pragma unroll
     for (int j = 0; j < 8; ++j) fetch_a(0, 0, j);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) fetch_b(0, 0, j);
+    for (int j = 0; j < TN; ++j) fetch_b(0, 0, j);
     wait_vmcnt<0>();
     barrier();
-    float *stage = (float *)(smem + (wave < 2 ? SLOT : B_BASE + SLOT) + (wave & 1) * STAGE);
+    float *stage = (float *)(smem + (wave < 2 ? SLOT : B_BASE + B_SLOT) + (wave & 1) * STAGE);
     while (true) {
         using even = std::integral_constant<int, 0>;
         using odd = std::integral_constant<int, 1>;
@@ -192,7 +214,7 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
         auto regs = prepare(lane, dm0 + wm * 128, dn0 + wn * W, r.M, r.N);
 #pragma unroll
         for (int q = 0; q < Q; ++q) mfma(std::false_type(), 1, q / TN, q % TN);
-        mfma_result_fence<TM, TN>(acc);
+        prod_result_fence<TM, TN>(acc);
         // (every wave is past its last barrier, so past all reads of the slots;
         // the loads of the tile past the end have landed there)
         vt += nwg;
@@ -210,7 +232,7 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
 #pragma unroll
             for (int j = 0; j < 8; ++j) dma(rA, (4 * j + wv) * 1024, va, j * astep);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dma(rB, B_BASE + (4 * j + wv) * 1024, vb, j * bstep);
+            for (int j = 0; j < TN; ++j) dma(rB, B_BASE + (4 * j + wv) * 1024, vb, j * bstep);
         }
         emit(regs, acc, stage, lane, dm0 + wm * 128, dn0 + wn * W, r.M, r.N);
         if (!more) {
@@ -222,11 +244,12 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
     }
 }
 
-template <class Epi, class Regs>
-__device__ __forceinline__ void prepare_agpr(const Epi &e, Regs &regs, int lane, int row0, int col0, int M, int N) {
-    e.template scales<8, 8>(regs, lane, row0, col0, M, N);
+template <class Epi, int TN>
+__device__ __forceinline__ void prepare_agpr(const Epi &e, typename Epi::template Regs<8, TN> &regs, int lane, int row0,
+                                             int col0, int M, int N) {
+    e.template scales<8, TN>(regs, lane, row0, col0, M, N);
     with_form(e, [&](auto vec, auto add) __attribute__((always_inline)) {
-        e.template prepare<8, 8, vec, add>(regs, lane, row0, col0, M, N);
+        e.template prepare<8, TN, vec, add>(regs, lane, row0, col0, M, N);
     });
 }
 
@@ -242,15 +265,15 @@ __device__ __forceinline__ void emit_agpr(const Epi &e, typename Epi::template R
     });
 }
 
-template <int T, bool PAIR, bool PREFETCH, class Epi>
+template <int T, bool PAIR, bool PREFETCH, class Epi, int TN = 8>
 __global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
-    __shared__ __attribute__((aligned(1024))) char smem[kW4Lds];
-    typedef typename Epi::template Regs<8, 8> Regs;
-    prod_w4_body<T, PAIR, PREFETCH>(
+    __shared__ __attribute__((aligned(1024))) char smem[kW4Lds<TN>];
+    typedef typename Epi::template Regs<8, TN> Regs;
+    prod_w4_body<T, PAIR, PREFETCH, TN>(
         p, blockIdx.x, gridDim.x, smem, [] { return kernel_arg0_reloaded<ProdArgs>(); },
         [&](int lane, int row0, int col0, int M, int N) __attribute__((always_inline)) {
             Regs r;
-            prepare_agpr(e, r, lane, row0, col0, M, N);
+            prepare_agpr<Epi, TN>(e, r, lane, row0, col0, M, N);
             return r;
         },
         [&](Regs &regs, const auto &acc, float *stage, int lane, int row0, int col0, int M, int N)
@@ -261,7 +284,7 @@ __global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
 // on the others, each in rounds of its own.
 template <int T, class Epi0, class Epi1>
 __global__ void __launch_bounds__(256) prod_w4_two_kernel(ProdPair q, Epi0 e0, Epi1 e1) {
-    __shared__ __attribute__((aligned(1024))) char smem[kW4Lds];
+    __shared__ __attribute__((aligned(1024))) char smem[kW4Lds<8>];
     const bool second = (int)blockIdx.x >= q.split;
     const ProdArgs p = second ? q.p[1] : q.p[0];
     const int wg = second ? blockIdx.x - q.split : blockIdx.x;
@@ -270,7 +293,7 @@ __global__ void __launch_bounds__(256) prod_w4_two_kernel(ProdPair q, Epi0 e0, E
         typename Epi0::template Regs<8, 8> a;
         typename Epi1::template Regs<8, 8> b;
     };
-    prod_w4_body<T, false, true>(
+    prod_w4_body<T, false, true, 8>(
         p, wg, second ? gridDim.x - q.split : q.split, smem,
         [&]() __attribute__((always_inline)) {
             const ProdPair r = kernel_arg0_reloaded<ProdPair>();
@@ -279,9 +302,9 @@ __global__ void __launch_bounds__(256) prod_w4_two_kernel(ProdPair q, Epi0 e0, E
         [&](int lane, int row0, int col0, int M, int N) __attribute__((always_inline)) {
             Regs r;
             if (second)
-                prepare_agpr(e1, r.b, lane, row0, col0, M, N);
+                prepare_agpr<Epi1, 8>(e1, r.b, lane, row0, col0, M, N);
             else
-                prepare_agpr(e0, r.a, lane, row0, col0, M, N);
+                prepare_agpr<Epi0, 8>(e0, r.a, lane, row0, col0, M, N);
             return r;
         },
         [&](Regs &regs, const auto &acc, float *stage, int lane, int row0, int col0, int M, int N) __attribute__((always_inline)) {
