@@ -3,8 +3,9 @@ their sources (CPU only: compiled, never run).
 
 Operands come by direct loads into LDS, which nothing but a count of outstanding
 vector-memory operations says to have landed: a K tile's barrier leaves one
-operation in flight where lines are brought ahead (that one), the barrier before
-the next output tile leaves the finished tile's stores.  Here every path through
+operation in flight where lines are brought ahead (that one; with three slots
+also the next but one K tile's loads), the barrier before the next output tile
+leaves the finished tile's stores.  Here every path through
 the kernels is followed with the queue of outstanding operations (they return in
 order): none of those loads may be in it at a barrier, and nothing that writes
 LDS at the kernel's end, where the LDS is another workgroup's next."""
@@ -24,7 +25,7 @@ pytestmark = pytest.mark.skipif(shutil.which(B.HIPCC) is None and not os.path.ex
 # (The kernel of two products has the same body; its paths by which product it is are too many here.)
 # An epilogue of which it is known, when it is compiled, whether its results lie in whole pieces and whether they are added
 # to something: the kernels choose at run time, and paths that mix the one's stores with the other's wait do not exist.
-SOURCE = """
+HEAD = """
 #include "prod_w4.hpp"
 namespace tg {
 template <class E, bool V, bool A> struct Known : E {
@@ -36,41 +37,34 @@ template <class E, bool V, bool A> struct Known : E {
 #define ADDING(T, PAIR, AHEAD, E)                                                                                     \\
     template __global__ void prod_w4_kernel<T, PAIR, AHEAD, Known<E, true, true>>(ProdArgs, Known<E, true, true>);    \\
     template __global__ void prod_w4_kernel<T, PAIR, AHEAD, Known<E, false, true>>(ProdArgs, Known<E, false, true>);
-ONE(1, true, true, GluEpi<1>)
-ONE(2, true, true, GluEpi<2>)
-ONE(3, false, false, Int8Epi<0>)
-ONE(3, false, false, Int8Epi<1>)
-ONE(1, false, true, PlainEpi<0>)
-ONE(2, false, true, PlainEpi<2>)
-ADDING(3, false, false, Int8Epi<0>)
-ADDING(3, false, false, Int8Epi<1>)
-ADDING(1, false, true, PlainEpi<0>)
-ADDING(2, false, true, PlainEpi<2>)
-#define NARROW(T, PAIR, E, ...) template __global__ void prod_w4_kernel<T, PAIR, true, Known<E, __VA_ARGS__>, 4>(ProdArgs, Known<E, __VA_ARGS__>);
-NARROW(1, true, GluEpi<1>, true, false)
-NARROW(2, true, GluEpi<2>, false, false)
-NARROW(3, false, Int8Epi<0>, true, true)
-NARROW(3, false, Int8Epi<1>, false, true)
-NARROW(3, false, Int8Epi<1>, true, false)
-NARROW(1, false, PlainEpi<0>, false, true)
-NARROW(2, false, PlainEpi<2>, true, true)
-NARROW(2, false, PlainEpi<2>, true, false)
-}
+#define NARROW(T, PAIR, E, ...)                                                                                       \\
+    template __global__ void prod_w4_kernel<T, PAIR, true, Known<E, __VA_ARGS__>, 4>(ProdArgs, Known<E, __VA_ARGS__>);
 """
+# compiled apart, at the same time
+PARTS = [
+    ["ONE(1, true, true, GluEpi<1>)", "ONE(2, false, true, PlainEpi<2>)", "NARROW(1, true, GluEpi<1>, true, false)", "NARROW(1, false, PlainEpi<0>, false, true)"],
+    ["ONE(2, true, true, GluEpi<2>)", "ADDING(3, false, false, Int8Epi<0>)", "NARROW(2, true, GluEpi<2>, false, false)", "NARROW(2, false, PlainEpi<2>, true, true)"],
+    ["ONE(3, false, false, Int8Epi<0>)", "ADDING(3, false, false, Int8Epi<1>)", "NARROW(3, false, Int8Epi<0>, true, true)", "NARROW(2, false, PlainEpi<2>, true, false)"],
+    ["ONE(3, false, false, Int8Epi<1>)", "ADDING(1, false, true, PlainEpi<0>)", "NARROW(3, false, Int8Epi<1>, false, true)"],
+    ["ONE(1, false, true, PlainEpi<0>)", "ADDING(2, false, true, PlainEpi<2>)", "NARROW(3, false, Int8Epi<1>, true, false)"],
+]
 
 
 @pytest.fixture(scope="module")
 def assembly(tmp_path_factory):
     d = tmp_path_factory.mktemp("asm")
-    (d / "w4.hip").write_text(SOURCE)
-    subprocess.run([B.HIPCC] + B.FLAGS + ["-I" + B.CSRC, "-S", "--cuda-device-only", str(d / "w4.hip"), "-o", str(d / "w4.s")],
-                   check=True, capture_output=True)
-    return (d / "w4.s").read_text()
+    runs = []
+    for i, part in enumerate(PARTS):
+        (d / ("w4_%d.hip" % i)).write_text(HEAD + "\n".join(part) + "\n}\n")
+        runs.append(subprocess.Popen([B.HIPCC] + B.FLAGS + ["-I" + B.CSRC, "-S", "--cuda-device-only", str(d / ("w4_%d.hip" % i)),
+                                                            "-o", str(d / ("w4_%d.s" % i))], stderr=subprocess.DEVNULL))
+    assert [r.wait() for r in runs] == [0] * len(runs)
+    return "".join((d / ("w4_%d.s" % i)).read_text() for i in range(len(PARTS)))
 
 
 def follow(text, name, at_barrier, at_end):
-    """Every path, with the queue of outstanding operations: 2 a load of 16 bytes a lane into LDS, 1 a smaller one, 0 any
-    other.  Only the queue from its oldest LDS load on is kept."""
+    """Every path, with the queue of outstanding operations: 2 a load of 16 bytes a lane into LDS (3 from the next barrier
+    on), 1 a smaller one, 0 any other.  Only the queue from its oldest LDS load on is kept."""
     blocks, first = blocks_of(text, name)
     todo, seen, barriers = [(first, ())], set(), 0
     while todo:
@@ -88,7 +82,8 @@ def follow(text, name, at_barrier, at_end):
                 n = count_of(line)
                 queue = queue[len(queue) - n:] if 0 < n < len(queue) else queue if n else ()
             elif line.startswith("s_barrier"):
-                at_barrier(queue)
+                at_barrier(name, queue)
+                queue = tuple(3 if q == 2 else q for q in queue)
                 barriers += 1
             elif line.startswith("s_endpgm"):
                 at_end(queue)
@@ -100,8 +95,15 @@ def follow(text, name, at_barrier, at_end):
     return barriers
 
 
-def at_barrier(queue):
-    assert 2 not in queue, "an operand's load may still be on its way behind this barrier"
+NARROW_LOADS = 12                                      # of a K tile and wave
+
+
+def at_barrier(name, queue):
+    """256 x 256 tiles: the next K tile is the last one issued.  256 x 128: one more is on its way, issued since the
+    barrier before (at the start both are)."""
+    late = "an operand's load may still be on its way behind this barrier"
+    assert 3 not in queue, late
+    assert queue.count(2) <= (NARROW_LOADS if "ELi4EEEv" in name else 0), late
 
 
 def at_end(queue):
@@ -123,7 +125,10 @@ def test_the_check_sees_waits_that_are_too_short(assembly):
     """The same text with one operation more left in flight, at the K tiles' ends or behind the results."""
     for kernel, wait, longer in (("prod_w4_kernelILi3ELb0ELb0ENS_5KnownINS_7Int8EpiILi1EEELb1ELb0EEELi8", 0, 1),
                                  ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1ELb0EEELi8", 1, 2),
-                                 ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1ELb0EEELi8", 16, 17)):
+                                 ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1ELb0EEELi8", 16, 17),
+                                 ("prod_w4_kernelILi2ELb0ELb1ENS_5KnownINS_8PlainEpiILi2EEELb1ELb0EEELi4", 14, 15),
+                                 ("prod_w4_kernelILi2ELb0ELb1ENS_5KnownINS_8PlainEpiILi2EEELb1ELb0EEELi4", 13, 14),
+                                 ("prod_w4_kernelILi2ELb0ELb1ENS_5KnownINS_8PlainEpiILi2EEELb1ELb0EEELi4", 12, 13)):
         name = [k for k in kernels(assembly) if kernel in k][0]
         with pytest.raises(AssertionError):
             follow(assembly.replace("vmcnt(%d)" % wait, "vmcnt(%d)" % longer), name, at_barrier, at_end)

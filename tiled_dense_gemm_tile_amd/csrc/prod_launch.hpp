@@ -93,9 +93,9 @@ hipError_t launch_prod_tiles(const ProdArgs &p, const Epi &e, hipStream_t s) {
     if constexpr (!ANY) {
         // 256 x 128 on one round of CUs, for K that covers the longer way to the
         // first and the last K tile, and the results' stores by half the waves
-        // (K tiles of 128 bytes; int8 2000 x 4096 x 4096 34.4 us, 128 x 128 43.7;
-        // gated 256 x 14336 x 4096 62 and 73, 2048 x 2048 x 2048 32 and 38, x 512
-        // 13.1 and 13.9, 1200 x 2048 x 256 9.3 and 8.8; results at any alignment:
+        // (K tiles of 128 bytes; int8 2000 x 4096 x 4096 33.8 us, 128 x 128 43.7;
+        // gated 256 x 14336 x 4096 58 and 73, 2048 x 2048 x 2048 32 and 38, x 512
+        // 12.9 and 13.9, 1200 x 2048 x 256 9.3 and 8.8; results at any alignment:
         // int8 2000 x 4095 x 4096 36.8 and 44.0, with C x 1024 21.0 and 18.3)
         if (tiles_of(p, 256, 128 / D) <= 256 && p.KB > (e.vec ? 7 : 23) * 128) return go_w4_narrow<T, PAIR>(p, e, s);
     }

@@ -50,9 +50,10 @@ __device__ __forceinline__ void prod_result_fence(f32x4 (&acc)[TM][TN]) {
 }
 
 // LDS of a workgroup with 16 TN rows of B a wave (TN 8 as above; 4: 256 x 128
-// tiles, PAIR 64 columns): two slots an operand, and what lines brought ahead
-// leave behind.
-template <int TN> constexpr int kW4Lds = 2 * (256 + 32 * TN) * 128 + 1024;
+// tiles, PAIR 64 columns): slots of K tiles, and what lines brought ahead leave
+// behind.
+template <int TN> constexpr int kW4Slots = TN == 8 ? 2 : 3;
+template <int TN> constexpr int kW4Lds = kW4Slots<TN> * (256 + 32 * TN) * 128 + 1024;
 
 // Workgroup wg of nwg that walk the tiles wg, wg + nwg, ... below p.run.
 // reload(): p again, from memory; prepare(lane, row0, col0, M, N) loads what a
@@ -62,12 +63,13 @@ template <int TN> constexpr int kW4Lds = 2 * (256 + 32 * TN) * 128 + 1024;
 template <int T, bool PAIR, bool PREFETCH, int TN, class Reload, class Prepare, class Emit>
 __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg, char *smem, Reload &&reload,
                                              Prepare &&prepare, Emit &&emit) {
-    constexpr int TM = 8, Q = TM * TN, SLOT = 256 * 128, B_SLOT = 32 * TN * 128, B_BASE = 2 * SLOT;
+    constexpr int TM = 8, Q = TM * TN, SLOT = 256 * 128, B_SLOT = 32 * TN * 128;
+    constexpr int NS = kW4Slots<TN>, B_BASE = NS * SLOT, LOADS = 8 + TN;
     constexpr int BN = PAIR ? 16 * TN : 32 * TN;       // result columns of a tile
     constexpr int W = BN / 2, STAGE = 16 * kStagePitch<W> * 4;
-    constexpr int PF = 3;                              // K tiles ahead
+    constexpr int PF = NS + 1;                         // K tiles ahead
     static_assert(TN == 8 || TN == 4, "schedule");
-    static_assert(2 * STAGE <= B_SLOT && kW4Lds<TN> == B_BASE + 2 * B_SLOT + 1024, "LDS");
+    static_assert(2 * STAGE <= B_SLOT && kW4Lds<TN> == B_BASE + NS * B_SLOT + 1024, "LDS");
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -137,7 +139,7 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
     auto prefetch = [&]() __attribute__((always_inline)) {
         pfk = pfk + 128 >= nt * 128 ? pfk + 128 - nt * 128 : pfk + 128;    // (past the end: the circle again)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            wave == 0 ? rA : rB, (__attribute__((address_space(3))) void *)(smem + B_BASE + 2 * B_SLOT + wave * 256), 4, pfo, pfk, 0, 0);
+            wave == 0 ? rA : rB, (__attribute__((address_space(3))) void *)(smem + B_BASE + NS * B_SLOT + wave * 256), 4, pfo, pfk, 0, 0);
     };
 
     const int fr = lane & 15, fq = lane >> 4, fswz = swz16(fr);
@@ -163,20 +165,20 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
         prod_mfma_agpr<T, decltype(zero)::value>(acc[i][j], fb[st][j], fa[st][i]);
         __builtin_amdgcn_sched_barrier(0);
     };
-    // One K tile, in slot S; FIRST: none before it (accumulators start from zero).
+    // One K tile, in slot S, the one NS - 1 ahead into the last one's; FIRST: none before it (accumulators start from zero).
     auto tile = [&](auto first, auto slot, int t) __attribute__((always_inline)) {
-        constexpr int S = decltype(slot)::value;
+        constexpr int S = decltype(slot)::value, FREE = (S + NS - 1) % NS;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             if constexpr (!decltype(first)::value) mfma(std::false_type(), 1, q / TN, q % TN);
             if constexpr (TN == 8) {
                 if (q % 4 == 0) read_frag(S, 0, q / 4);
-                if (q % 8 == 0) fetch_a(t + 1, 1 - S, q / 8);
-                if (q % 8 == 4) fetch_b(t + 1, 1 - S, q / 8);
+                if (q % 8 == 0) fetch_a(t + NS - 1, FREE, q / 8);
+                if (q % 8 == 4) fetch_b(t + NS - 1, FREE, q / 8);
             } else {
                 if (q % 2 == 0 && q / 2 < TM + TN) read_frag(S, 0, q / 2);
-                if (q % 4 == 1) fetch_a(t + 1, 1 - S, q / 4);
-                if (q % 8 == 3) fetch_b(t + 1, 1 - S, q / 8);
+                if (q % 4 == 1) fetch_a(t + NS - 1, FREE, q / 4);
+                if (q % 8 == 3) fetch_b(t + NS - 1, FREE, q / 8);
             }
             if (PREFETCH && q == Q - 1) prefetch();
         }
@@ -186,29 +188,33 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
             constexpr int EVERY = TN == 8 ? 3 : 2;
             if (q % EVERY == 0 && q / EVERY < TM + TN) read_frag(S, 1, q / EVERY);
         }
-        wait_vmcnt<PREFETCH ? 1 : 0>();                // tile t + 1 landed
+        // tile t + 1 landed; what was issued behind its loads may be on its way (in
+        // an output tile's first K tile one line less: no K tile was before it)
+        wait_vmcnt<(NS - 2) * LOADS + (!PREFETCH ? 0 : decltype(first)::value ? 1 : NS - 1)>();
         wait_lgkmcnt0();
         barrier();
     };
 
+    static_for<0, NS - 1>([&](auto t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) fetch_a(0, 0, j);
+        for (int j = 0; j < 8; ++j) fetch_a(t, t, j);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) fetch_b(0, 0, j);
-    wait_vmcnt<0>();
+        for (int j = 0; j < TN; ++j) fetch_b(t, t, j);
+    });
+    wait_vmcnt<(NS - 2) * LOADS>();
     barrier();
-    float *stage = (float *)(smem + (wave < 2 ? SLOT : B_BASE + B_SLOT) + (wave & 1) * STAGE);
+    float *stage = (float *)(smem + (wave < 2 ? (NS - 1) * SLOT : B_BASE + (NS - 1) * B_SLOT) + (wave & 1) * STAGE);
     while (true) {
-        using even = std::integral_constant<int, 0>;
-        using odd = std::integral_constant<int, 1>;
         pfk = (k_first + (PF - 1) * 128) % (nt * 128);
-        tile(std::true_type(), even(), 0);
+        tile(std::true_type(), std::integral_constant<int, 0>(), 0);
         int t = 1;
-        for (; t + 1 < nt; t += 2) {
-            tile(std::false_type(), odd(), t);
-            tile(std::false_type(), even(), t + 1);
-        }
-        if (t < nt) tile(std::false_type(), odd(), t);
+        for (; t + NS - 1 < nt; t += NS)
+            static_for<0, NS>([&](auto k) __attribute__((always_inline)) {
+                tile(std::false_type(), std::integral_constant<int, (k + 1) % NS>(), t + k);
+            });
+        static_for<0, NS - 1>([&](auto k) __attribute__((always_inline)) {
+            if (t + k < nt) tile(std::false_type(), std::integral_constant<int, (k + 1) % NS>(), t + k);
+        });
         const ProdArgs r = reload();
         const int dm0 = m0, dn0 = n0;
         auto regs = prepare(lane, dm0 + wm * 128, dn0 + wn * W, r.M, r.N);
@@ -216,7 +222,11 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
         for (int q = 0; q < Q; ++q) mfma(std::false_type(), 1, q / TN, q % TN);
         prod_result_fence<TM, TN>(acc);
         // (every wave is past its last barrier, so past all reads of the slots;
-        // the loads of the tile past the end have landed there)
+        // the loads of the tiles past the end have landed there)
+        if constexpr (NS > 2) {
+            wait_vmcnt<0>();
+            barrier();
+        }
         vt += nwg;
         const bool more = vt < r.run;
         if (more) {
@@ -227,12 +237,14 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
             pfo = pf_off();
             int wv = wave;                             // (their LDS addresses are computed here, not held)
             asm volatile("" : "+s"(wv));
-            const int k0 = koff(0);
-            const uint32_t va = k0 + kc < KB ? aoff + k0 : kOOB, vb = k0 + kc < KB ? boff + k0 : kOOB;
+            static_for<0, NS - 1>([&](auto t) __attribute__((always_inline)) {
+                const int k0 = koff(t);
+                const uint32_t va = k0 + kc < KB ? aoff + k0 : kOOB, vb = k0 + kc < KB ? boff + k0 : kOOB;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dma(rA, (4 * j + wv) * 1024, va, j * astep);
+                for (int j = 0; j < 8; ++j) dma(rA, t * SLOT + (4 * j + wv) * 1024, va, j * astep);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) dma(rB, B_BASE + (4 * j + wv) * 1024, vb, j * bstep);
+                for (int j = 0; j < TN; ++j) dma(rB, B_BASE + t * B_SLOT + (4 * j + wv) * 1024, vb, j * bstep);
+            });
         }
         emit(regs, acc, stage, lane, dm0 + wm * 128, dn0 + wn * W, r.M, r.N);
         if (!more) {
