@@ -587,3 +587,27 @@ def test_glu_narrow_tiles(m, f, k, dtype):
 def test_glu_backward_narrow_tiles(m, f, k, dtype, grad):
     check_backward(m, f, k, dtype, grad=grad)
     check_backward(m, f, k, dtype, grad=grad, acc=True)
+
+
+# ---- 128 x 128 tiles, one a CU ------------------------------------------------------
+
+# 256 and 252 tiles; 1 to 5 K tiles and 17, which is once around the slots and more
+@pytest.mark.parametrize("m,n", [(900, 4096), (500, 8000), (897, 4095)])
+@pytest.mark.parametrize("k", [16, 144, 272, 400, 528, 2064])
+def test_int8_single_tiles(m, n, k):
+    check_int8(m, n, k, BF)
+    check_int8(m, n, k, F32, "matrix", pads=(16, 32, 0))
+    check_int8(m, n, k, FP, "matrix", pads=(0, 0, 3))
+
+
+@pytest.mark.parametrize("m,f,k", [(1000, 2048, 64), (500, 4000, 136), (897, 2047, 200), (128, 14336, 264), (1000, 2048, 1040)])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=KIND.get)
+def test_glu_single_tiles(m, f, k, dtype):
+    x, wg, wu = rand(1, m, k, dtype=dtype), rand(2, f, k, dtype=dtype, scale=k ** -0.5), rand(3, f, k, dtype=dtype, scale=k ** -0.5)
+    check_glu(x, wg, wu, "gelu_tanh")
+
+
+@pytest.mark.parametrize("k", [1280, 1424])
+def test_int8_narrow_tiles_of_other_counts(k):
+    check_int8(2048, 4096, k, BF, "matrix")
+    check_int8(1100, 6000, k, F32)

@@ -37,8 +37,9 @@ template <class E, bool V, bool A> struct Known : E {
 #define ADDING(T, PAIR, AHEAD, E)                                                                                     \\
     template __global__ void prod_w4_kernel<T, PAIR, AHEAD, Known<E, true, true>>(ProdArgs, Known<E, true, true>);    \\
     template __global__ void prod_w4_kernel<T, PAIR, AHEAD, Known<E, false, true>>(ProdArgs, Known<E, false, true>);
-#define NARROW(T, PAIR, E, ...)                                                                                       \\
-    template __global__ void prod_w4_kernel<T, PAIR, true, Known<E, __VA_ARGS__>, 4>(ProdArgs, Known<E, __VA_ARGS__>);
+#define NARROW(T, PAIR, E, ...)                                                                                          \\
+    template __global__ void prod_w4_kernel<T, PAIR, true, Known<E, __VA_ARGS__>, 4>(ProdArgs, Known<E, __VA_ARGS__>);   \\
+    template __global__ void prod_w4_kernel<T, PAIR, true, Known<E, __VA_ARGS__>, 4, 4>(ProdArgs, Known<E, __VA_ARGS__>);
 """
 # compiled apart, at the same time
 PARTS = [
@@ -63,8 +64,8 @@ def assembly(tmp_path_factory):
 
 
 def follow(text, name, at_barrier, at_end):
-    """Every path, with the queue of outstanding operations: 2 a load of 16 bytes a lane into LDS (3 from the next barrier
-    on), 1 a smaller one, 0 any other.  Only the queue from its oldest LDS load on is kept."""
+    """Every path, with the queue of outstanding operations: 2 a load of 16 bytes a lane into LDS (3 behind the next
+    barrier, 4 behind the one after it, ...), 1 a smaller one, 0 any other.  Only the queue from its oldest LDS load on is kept."""
     blocks, first = blocks_of(text, name)
     todo, seen, barriers = [(first, ())], set(), 0
     while todo:
@@ -83,7 +84,7 @@ def follow(text, name, at_barrier, at_end):
                 queue = queue[len(queue) - n:] if 0 < n < len(queue) else queue if n else ()
             elif line.startswith("s_barrier"):
                 at_barrier(name, queue)
-                queue = tuple(3 if q == 2 else q for q in queue)
+                queue = tuple(q + 1 if q >= 2 else q for q in queue)
                 barriers += 1
             elif line.startswith("s_endpgm"):
                 at_end(queue)
@@ -95,15 +96,13 @@ def follow(text, name, at_barrier, at_end):
     return barriers
 
 
-NARROW_LOADS = 12                                      # of a K tile and wave
-
-
 def at_barrier(name, queue):
-    """256 x 256 tiles: the next K tile is the last one issued.  256 x 128: one more is on its way, issued since the
-    barrier before (at the start both are)."""
+    """256 x 256 tiles: the next K tile is the last one issued.  256 x 128 and 128 x 128: one and two more, of 12 and 8
+    loads each, are on their way, the latest issued since the barrier before (at the start all of them)."""
+    ahead, loads = {"ELi8ELi8EEEv": (0, 0), "ELi4ELi8EEEv": (1, 12), "ELi4ELi4EEEv": (2, 8)}[re.search(r"(ELi\dELi\dEEEv)", name).group(1)]
     late = "an operand's load may still be on its way behind this barrier"
-    assert 3 not in queue, late
-    assert queue.count(2) <= (NARROW_LOADS if "ELi4EEEv" in name else 0), late
+    assert all(q < 2 + ahead for q in queue if q >= 2), late
+    assert sum(q >= 2 for q in queue) <= ahead * loads, late
 
 
 def at_end(queue):
@@ -116,7 +115,7 @@ def kernels(text):
 
 def test_operands_have_landed_at_every_barrier(assembly):
     names = kernels(assembly)
-    assert len(names) == 28
+    assert len(names) == 36
     for name in names:
         assert follow(assembly, name, at_barrier, at_end) > 4, name
 
@@ -126,9 +125,10 @@ def test_the_check_sees_waits_that_are_too_short(assembly):
     for kernel, wait, longer in (("prod_w4_kernelILi3ELb0ELb0ENS_5KnownINS_7Int8EpiILi1EEELb1ELb0EEELi8", 0, 1),
                                  ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1ELb0EEELi8", 1, 2),
                                  ("prod_w4_kernelILi1ELb1ELb1ENS_5KnownINS_6GluEpiILi1EEELb1ELb0EEELi8", 16, 17),
-                                 ("prod_w4_kernelILi2ELb0ELb1ENS_5KnownINS_8PlainEpiILi2EEELb1ELb0EEELi4", 14, 15),
-                                 ("prod_w4_kernelILi2ELb0ELb1ENS_5KnownINS_8PlainEpiILi2EEELb1ELb0EEELi4", 13, 14),
-                                 ("prod_w4_kernelILi2ELb0ELb1ENS_5KnownINS_8PlainEpiILi2EEELb1ELb0EEELi4", 12, 13)):
+                                 ("prod_w4_kernelILi2ELb0ELb1ENS_5KnownINS_8PlainEpiILi2EEELb1ELb0EEELi4ELi8", 14, 15),
+                                 ("prod_w4_kernelILi2ELb0ELb1ENS_5KnownINS_8PlainEpiILi2EEELb1ELb0EEELi4ELi8", 13, 14),
+                                 ("prod_w4_kernelILi2ELb0ELb1ENS_5KnownINS_8PlainEpiILi2EEELb1ELb0EEELi4ELi4", 19, 20),
+                                 ("prod_w4_kernelILi2ELb0ELb1ENS_5KnownINS_8PlainEpiILi2EEELb1ELb0EEELi4ELi4", 18, 19)):
         name = [k for k in kernels(assembly) if kernel in k][0]
         with pytest.raises(AssertionError):
             follow(assembly.replace("vmcnt(%d)" % wait, "vmcnt(%d)" % longer), name, at_barrier, at_end)

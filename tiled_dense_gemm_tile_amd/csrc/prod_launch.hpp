@@ -50,11 +50,11 @@ hipError_t go_w4(ProdArgs p, const Epi &e, hipStream_t s) {
     return hipGetLastError();
 }
 
-// 256 x 128 tiles (PAIR: 64 columns), one a CU.
-template <int T, bool PAIR, class Epi>
-hipError_t go_w4_narrow(ProdArgs p, const Epi &e, hipStream_t s) {
-    p.run = (int)prod_tiles(p, 256, PAIR ? 64 : 128);
-    hipLaunchKernelGGL((prod_w4_kernel<T, PAIR, true, Epi, 4>), dim3(p.run), dim3(256), 0, s, p, e);
+// 32 TM x 128 tiles (PAIR: 64 columns), one a CU.
+template <int T, bool PAIR, int TM, class Epi>
+hipError_t go_w4_once(ProdArgs p, const Epi &e, hipStream_t s) {
+    p.run = (int)prod_tiles(p, 32 * TM, PAIR ? 64 : 128);
+    hipLaunchKernelGGL((prod_w4_kernel<T, PAIR, true, Epi, 4, TM>), dim3(p.run), dim3(256), 0, s, p, e);
     return hipGetLastError();
 }
 
@@ -86,18 +86,18 @@ hipError_t launch_prod_tiles(const ProdArgs &p, const Epi &e, hipStream_t s) {
     if (p.M <= 64) return go_mid<T, 64, 64, 4, 1, PAIR, ANY>(p, e, s);
     if (t64 <= 256) return go_mid<T, 64, 64, 4, ANY ? 1 : 2, PAIR, ANY>(p, e, s);
     if (tiles_of(p, 64, 128 / D) <= 256) return go_mid<T, 64, 128, 3, 2, PAIR, ANY>(p, e, s);
-    // int8 1000 x 4096 x 4096: two groups 23.5, one 28.7, 64 x 64 32.1; gated 128
-    // x 14336 x 4096 41 and 47
-    if constexpr (!ANY)
-        if (t128 <= 256) return go_mid<T, 128, 128, 2, 2, PAIR, ANY>(p, e, s);
     if constexpr (!ANY) {
+        // 128 x 128, one a CU, in the large tiles' schedule (int8 1000 x 4096 x 4096
+        // 20.8, K cut over two groups of waves 23.8; gated 128 x 14336 x 4096 39 and
+        // 42, 1024 x 2048 x 256 6.8 and 6.6)
+        if (t128 <= 256 && p.KB > 0) return go_w4_once<T, PAIR, 4>(p, e, s);
         // 256 x 128 on one round of CUs, for K that covers the longer way to the
         // first and the last K tile, and the results' stores by half the waves
         // (K tiles of 128 bytes; int8 2000 x 4096 x 4096 33.8 us, 128 x 128 43.7;
         // gated 256 x 14336 x 4096 58 and 73, 2048 x 2048 x 2048 32 and 38, x 512
         // 12.9 and 13.9, 1200 x 2048 x 256 9.3 and 8.8; results at any alignment:
         // int8 2000 x 4095 x 4096 36.8 and 44.0, with C x 1024 21.0 and 18.3)
-        if (tiles_of(p, 256, 128 / D) <= 256 && p.KB > (e.vec ? 7 : 23) * 128) return go_w4_narrow<T, PAIR>(p, e, s);
+        if (tiles_of(p, 256, 128 / D) <= 256 && p.KB > (e.vec ? 7 : 23) * 128) return go_w4_once<T, PAIR, 8>(p, e, s);
     }
     // two workgroups a CU (gated 1024 x 2736 x 1008: 19.2; four slots and one
     // workgroup 29.3, 64 x 64 28.4)

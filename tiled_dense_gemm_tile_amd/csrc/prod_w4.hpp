@@ -12,7 +12,16 @@
 //                     wait for the loads; barrier t + 1
 // After a tile's last K step the next tile's first loads are issued, into the
 // slots K tile 0 always uses, and then the finished tile's results are staged
-// and stored from the other slots.
+// and stored from the last slots.
+//
+// A K tile takes 1.37 to 1.41 us (MFMAs busy 71 to 83 % of the cycles; LDS three
+// quarters of them): int8 8192^3 2.95 POP/s, bf16 8192 x 4096 x 28672 1.57
+// PFLOP/s.
+//
+// Grids of one round at most run the same schedule in tiles of 256 x 128 and 128
+// x 128 (TN 4; TM 8 and 4) with three and four slots: a K tile's MFMAs take half
+// the time and a quarter of it, so its loads are issued two and three K tiles
+// ahead (256 x 128: two slots 0.86 us a K tile with 160 workgroups, three 0.73).
 #pragma once
 
 #include "prod.hpp"
@@ -52,31 +61,32 @@ __device__ __forceinline__ void prod_result_fence(f32x4 (&acc)[TM][TN]) {
 // LDS of a workgroup with 16 TN rows of B a wave (TN 8 as above; 4: 256 x 128
 // tiles, PAIR 64 columns): slots of K tiles, and what lines brought ahead leave
 // behind.
-template <int TN> constexpr int kW4Slots = TN == 8 ? 2 : 3;
-template <int TN> constexpr int kW4Lds = kW4Slots<TN> * (256 + 32 * TN) * 128 + 1024;
+template <int TM, int TN> constexpr int kW4Slots = TN == 8 ? 2 : TM == 8 ? 3 : 4;
+template <int TM, int TN> constexpr int kW4Lds = kW4Slots<TM, TN> * 32 * (TM + TN) * 128 + 1024;
 
 // Workgroup wg of nwg that walk the tiles wg, wg + nwg, ... below p.run.
 // reload(): p again, from memory; prepare(lane, row0, col0, M, N) loads what a
 // quadrant's results need, before the tile's last MFMAs and the next one's first
 // loads; emit(regs, acc, stage, lane, row0, col0, M, N) stores them and waits for
 // all that was issued before their last stores.  (Operand rows on 16 bytes, KB > 0 a multiple of 16.)
-template <int T, bool PAIR, bool PREFETCH, int TN, class Reload, class Prepare, class Emit>
+template <int T, bool PAIR, bool PREFETCH, int TM, int TN, class Reload, class Prepare, class Emit>
 __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg, char *smem, Reload &&reload,
                                              Prepare &&prepare, Emit &&emit) {
-    constexpr int TM = 8, Q = TM * TN, SLOT = 256 * 128, B_SLOT = 32 * TN * 128;
-    constexpr int NS = kW4Slots<TN>, B_BASE = NS * SLOT, LOADS = 8 + TN;
+    constexpr int Q = TM * TN, SLOT = 32 * TM * 128, B_SLOT = 32 * TN * 128;
+    constexpr int NS = kW4Slots<TM, TN>, B_BASE = NS * SLOT, LOADS = TM + TN;
+    constexpr int BM = 32 * TM;
     constexpr int BN = PAIR ? 16 * TN : 32 * TN;       // result columns of a tile
     constexpr int W = BN / 2, STAGE = 16 * kStagePitch<W> * 4;
     constexpr int PF = NS + 1;                         // K tiles ahead
-    static_assert(TN == 8 || TN == 4, "schedule");
-    static_assert(2 * STAGE <= B_SLOT && kW4Lds<TN> == B_BASE + NS * B_SLOT + 1024, "LDS");
+    static_assert((TM == 8 && TN == 8) || TN == 4, "schedule");
+    static_assert(2 * STAGE <= B_SLOT && 2 * STAGE <= SLOT && kW4Lds<TM, TN> == B_BASE + NS * B_SLOT + 1024, "LDS");
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     int vt = wg, tmi, tni;
     tile_order(vt, p.tiles_m * p.tiles_n, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
-    int m0 = tmi * 256, n0 = tni * BN;
+    int m0 = tmi * BM, n0 = tni * BN;
     const int KB = p.KB, nt = (KB + 127) / 128;
 
     // Load instruction j of a wave: A rows 32 j + 8 wave + lane / 8, B the same
@@ -125,12 +135,12 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
     // Lines of K tile t + PF brought into this XCD's L2, a 128-byte line a lane:
     // of each of its panels a workgroup takes the part that falls to it among
     // those that share the panel (in the tile order 8 share rows of A and 4 rows
-    // of B), 32 rows of A and 64 of B (TN 4: 32).  Four bytes of each line go to LDS that
+    // of B), an eighth of A's rows and a quarter of B's.  Four bytes of each line go to LDS that
     // nobody reads; the wait at a window's end leaves them in flight.  Hides
     // what the L2s miss (gradients of 8192 x 14336 x 4096: 3280 -> 3020 us; 2 or
     // 5 tiles ahead the same).
     auto pf_off = [&]() __attribute__((always_inline)) {
-        if (wave == 0) return lane < 32 ? (uint32_t)((32 * (tni & 7) + lane) * (int)p.lda) : kOOB;
+        if (wave == 0) return lane < BM / 8 ? (uint32_t)((BM / 8 * (tni & 7) + lane) * (int)p.lda) : kOOB;
         constexpr int OF_B = PAIR ? 4 * TN : 8 * TN;
         return wave < (PAIR ? 3 : 2) && lane < OF_B ? (uint32_t)((OF_B * (tmi & 3) + lane) * (int)ldb) : kOOB;
     };
@@ -146,13 +156,13 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
     int a_read[2], b_read[2];                          // [step]
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
-        a_read[st] = (wm * 128 + fr) * 128 + (((4 * st + fq) ^ fswz) << 4);
+        a_read[st] = (wm * 16 * TM + fr) * 128 + (((4 * st + fq) ^ fswz) << 4);
         b_read[st] = B_BASE + (wn * 16 * TN + fr) * 128 + (((4 * st + fq) ^ fswz) << 4);
     }
     f32x4 acc[TM][TN];
     u32x4 fa[2][TM], fb[2][TN];                        // [step][block]
     // fragment read k of step st from slot s, in the order the MFMAs use them: A
-    // block 0, the B blocks, A blocks 1 .. 7
+    // block 0, the B blocks, the other A blocks
     auto read_frag = [&](int s, int st, int k) __attribute__((always_inline)) {
         if (k == 0 || k > TN) {
             const int i = k == 0 ? 0 : k - TN;
@@ -178,34 +188,35 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
             } else {
                 if (q % 2 == 0 && q / 2 < TM + TN) read_frag(S, 0, q / 2);
                 if (q % 4 == 1) fetch_a(t + NS - 1, FREE, q / 4);
-                if (q % 8 == 3) fetch_b(t + NS - 1, FREE, q / 8);
+                if (q % TM == 3) fetch_b(t + NS - 1, FREE, q / TM);
             }
             if (PREFETCH && q == Q - 1) prefetch();
         }
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             mfma(first, 0, q / TN, q % TN);
-            constexpr int EVERY = TN == 8 ? 3 : 2;
+            constexpr int EVERY = TN == 8 ? 3 : TM == 8 ? 2 : 1;
             if (q % EVERY == 0 && q / EVERY < TM + TN) read_frag(S, 1, q / EVERY);
         }
-        // tile t + 1 landed; what was issued behind its loads may be on its way (in
-        // an output tile's first K tile one line less: no K tile was before it)
-        wait_vmcnt<(NS - 2) * LOADS + (!PREFETCH ? 0 : decltype(first)::value ? 1 : NS - 1)>();
+        // tile t + 1 landed; what was issued behind its loads may be on its way
+        wait_vmcnt<(NS - 2) * LOADS + (PREFETCH ? NS - 1 : 0)>();
         wait_lgkmcnt0();
         barrier();
     };
 
+    // (in the order of the loop: K tile t's lines behind the loads of t + NS - 1)
+    pfk = (k_first + 2 * 128) % (nt * 128);
     static_for<0, NS - 1>([&](auto t) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) fetch_a(t, t, j);
+        for (int j = 0; j < TM; ++j) fetch_a(t, t, j);
 #pragma unroll
         for (int j = 0; j < TN; ++j) fetch_b(t, t, j);
+        if (PREFETCH && t > 0) prefetch();
     });
-    wait_vmcnt<(NS - 2) * LOADS>();
+    wait_vmcnt<(NS - 2) * (LOADS + (PREFETCH ? 1 : 0))>();
     barrier();
     float *stage = (float *)(smem + (wave < 2 ? (NS - 1) * SLOT : B_BASE + (NS - 1) * B_SLOT) + (wave & 1) * STAGE);
     while (true) {
-        pfk = (k_first + (PF - 1) * 128) % (nt * 128);
         tile(std::true_type(), std::integral_constant<int, 0>(), 0);
         int t = 1;
         for (; t + NS - 1 < nt; t += NS)
@@ -217,7 +228,7 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
         });
         const ProdArgs r = reload();
         const int dm0 = m0, dn0 = n0;
-        auto regs = prepare(lane, dm0 + wm * 128, dn0 + wn * W, r.M, r.N);
+        auto regs = prepare(lane, dm0 + wm * 16 * TM, dn0 + wn * W, r.M, r.N);
 #pragma unroll
         for (int q = 0; q < Q; ++q) mfma(std::false_type(), 1, q / TN, q % TN);
         prod_result_fence<TM, TN>(acc);
@@ -231,22 +242,24 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
         const bool more = vt < r.run;
         if (more) {
             tile_order(vt, r.tiles_m * r.tiles_n, r.tiles_m, r.tiles_n, r.group_m, tmi, tni);
-            m0 = tmi * 256;
+            m0 = tmi * BM;
             n0 = tni * BN;
             resources(r);
             pfo = pf_off();
             int wv = wave;                             // (their LDS addresses are computed here, not held)
             asm volatile("" : "+s"(wv));
+            pfk = (k_first + 2 * 128) % (nt * 128);
             static_for<0, NS - 1>([&](auto t) __attribute__((always_inline)) {
                 const int k0 = koff(t);
                 const uint32_t va = k0 + kc < KB ? aoff + k0 : kOOB, vb = k0 + kc < KB ? boff + k0 : kOOB;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) dma(rA, t * SLOT + (4 * j + wv) * 1024, va, j * astep);
+                for (int j = 0; j < TM; ++j) dma(rA, t * SLOT + (4 * j + wv) * 1024, va, j * astep);
 #pragma unroll
                 for (int j = 0; j < TN; ++j) dma(rB, B_BASE + t * B_SLOT + (4 * j + wv) * 1024, vb, j * bstep);
+                if (PREFETCH && t > 0) prefetch();
             });
         }
-        emit(regs, acc, stage, lane, dm0 + wm * 128, dn0 + wn * W, r.M, r.N);
+        emit(regs, acc, stage, lane, dm0 + wm * 16 * TM, dn0 + wn * W, r.M, r.N);
         if (!more) {
             wait_vmcnt<0>();
             break;
@@ -256,12 +269,12 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
     }
 }
 
-template <class Epi, int TN>
-__device__ __forceinline__ void prepare_agpr(const Epi &e, typename Epi::template Regs<8, TN> &regs, int lane, int row0,
+template <class Epi, int TM, int TN>
+__device__ __forceinline__ void prepare_agpr(const Epi &e, typename Epi::template Regs<TM, TN> &regs, int lane, int row0,
                                              int col0, int M, int N) {
-    e.template scales<8, TN>(regs, lane, row0, col0, M, N);
+    e.template scales<TM, TN>(regs, lane, row0, col0, M, N);
     with_form(e, [&](auto vec, auto add) __attribute__((always_inline)) {
-        e.template prepare<8, TN, vec, add>(regs, lane, row0, col0, M, N);
+        e.template prepare<TM, TN, vec, add>(regs, lane, row0, col0, M, N);
     });
 }
 
@@ -277,15 +290,15 @@ __device__ __forceinline__ void emit_agpr(const Epi &e, typename Epi::template R
     });
 }
 
-template <int T, bool PAIR, bool PREFETCH, class Epi, int TN = 8>
+template <int T, bool PAIR, bool PREFETCH, class Epi, int TN = 8, int TM = 8>
 __global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
-    __shared__ __attribute__((aligned(1024))) char smem[kW4Lds<TN>];
-    typedef typename Epi::template Regs<8, TN> Regs;
-    prod_w4_body<T, PAIR, PREFETCH, TN>(
+    __shared__ __attribute__((aligned(1024))) char smem[kW4Lds<TM, TN>];
+    typedef typename Epi::template Regs<TM, TN> Regs;
+    prod_w4_body<T, PAIR, PREFETCH, TM, TN>(
         p, blockIdx.x, gridDim.x, smem, [] { return kernel_arg0_reloaded<ProdArgs>(); },
         [&](int lane, int row0, int col0, int M, int N) __attribute__((always_inline)) {
             Regs r;
-            prepare_agpr<Epi, TN>(e, r, lane, row0, col0, M, N);
+            prepare_agpr<Epi, TM, TN>(e, r, lane, row0, col0, M, N);
             return r;
         },
         [&](Regs &regs, const auto &acc, float *stage, int lane, int row0, int col0, int M, int N)
@@ -296,7 +309,7 @@ __global__ void __launch_bounds__(256) prod_w4_kernel(ProdArgs p, Epi e) {
 // on the others, each in rounds of its own.
 template <int T, class Epi0, class Epi1>
 __global__ void __launch_bounds__(256) prod_w4_two_kernel(ProdPair q, Epi0 e0, Epi1 e1) {
-    __shared__ __attribute__((aligned(1024))) char smem[kW4Lds<8>];
+    __shared__ __attribute__((aligned(1024))) char smem[kW4Lds<8, 8>];
     const bool second = (int)blockIdx.x >= q.split;
     const ProdArgs p = second ? q.p[1] : q.p[0];
     const int wg = second ? blockIdx.x - q.split : blockIdx.x;
@@ -305,7 +318,7 @@ __global__ void __launch_bounds__(256) prod_w4_two_kernel(ProdPair q, Epi0 e0, E
         typename Epi0::template Regs<8, 8> a;
         typename Epi1::template Regs<8, 8> b;
     };
-    prod_w4_body<T, false, true, 8>(
+    prod_w4_body<T, false, true, 8, 8>(
         p, wg, second ? gridDim.x - q.split : q.split, smem,
         [&]() __attribute__((always_inline)) {
             const ProdPair r = kernel_arg0_reloaded<ProdPair>();
@@ -314,9 +327,9 @@ __global__ void __launch_bounds__(256) prod_w4_two_kernel(ProdPair q, Epi0 e0, E
         [&](int lane, int row0, int col0, int M, int N) __attribute__((always_inline)) {
             Regs r;
             if (second)
-                prepare_agpr<Epi1, 8>(e1, r.b, lane, row0, col0, M, N);
+                prepare_agpr<Epi1, 8, 8>(e1, r.b, lane, row0, col0, M, N);
             else
-                prepare_agpr<Epi0, 8>(e0, r.a, lane, row0, col0, M, N);
+                prepare_agpr<Epi0, 8, 8>(e0, r.a, lane, row0, col0, M, N);
             return r;
         },
         [&](Regs &regs, const auto &acc, float *stage, int lane, int row0, int col0, int M, int N) __attribute__((always_inline)) {
