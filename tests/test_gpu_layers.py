@@ -611,3 +611,21 @@ def test_glu_single_tiles(m, f, k, dtype):
 def test_int8_narrow_tiles_of_other_counts(k):
     check_int8(2048, 4096, k, BF, "matrix")
     check_int8(1100, 6000, k, F32)
+
+
+# ---- both products of a small backward pass in one launch -----------------------------
+
+# up to 256 tiles of 64 x 64 and up to 1024, the longest sums and one K tile more, each gradient by itself
+@pytest.mark.parametrize("m,f,k", [(64, 64, 64), (1, 30, 500), (355, 256, 1520), (179, 768, 1768), (200, 1024, 500), (200, 1025, 500),
+                                   (2048, 64, 300), (2049, 64, 300), (500, 500, 500)])
+@pytest.mark.parametrize("dtype,grad", [(BF, F32), (FP, FP)])
+def test_glu_backward_small(m, f, k, dtype, grad):
+    check_backward(m, f, k, dtype, grad=grad)
+    check_backward(m, f, k, dtype, grad=grad, acc=True, name="gelu")
+    a = [rand(i, m, f, dtype=dtype) for i in range(3)] + [rand(3, m, k, dtype=dtype), rand(4, f, k, dtype=dtype, scale=0.05),
+                                                          rand(5, f, k, dtype=dtype, scale=0.05)]
+    want, bound = ref.glu_backward(*a, "silu")
+    dx, _, _ = tg.gemm_glu_backward(*a, weight_grad=False)
+    _, dwg, dwu = tg.gemm_glu_backward(*a, input_grad=False, grad_dtype=grad)
+    for got, w, b in zip((dx, dwg, dwu), want, bound):
+        within(got, w, half(w, b, got.dtype))

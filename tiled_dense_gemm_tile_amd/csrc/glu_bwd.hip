@@ -155,7 +155,7 @@ int64_t padded(int64_t n) { return (n + tg::kCopyTile - 1) / tg::kCopyTile * tg:
 int64_t pitch(int64_t n) { return n + (256 + 128 - n % 256) % 256; }
 int64_t part(int64_t elements) { return (elements * 2 + 255) / 256 * 256; }
 
-// The products: the input gradient where dX is given, the weights' where e.D is.
+// The products, the input gradient and the weights', each where it is wanted.
 template <int T, int OT>
 gemm_status products(const tg::GluBwdArgs &a, void *dX, int64_t lddx, const tg::PlainEpi<OT> &e, hipStream_t s) {
     tg::ProdArgs x = {}, w = {};
@@ -173,8 +173,6 @@ gemm_status products(const tg::GluBwdArgs &a, void *dX, int64_t lddx, const tg::
     w.KB = a.Mp * 2;
     const tg::PlainEpi<T> ex{{nullptr, nullptr}, {dX, nullptr}, {0, 0}, {lddx, 0}, 0x7fffffff, a.M,
                              tg::emit_whole(dX, lddx, a.K, 2), false};
-    if (!e.D[0]) return launched(tg::launch_plain<T, T>(x, ex, s));
-    if (!dX) return launched(tg::launch_plain<T, OT>(w, e, s));
     return launched(tg::launch_plain_two<T, OT>(x, ex, w, e, s));
 }
 

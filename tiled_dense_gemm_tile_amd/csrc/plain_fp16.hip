@@ -4,10 +4,6 @@
 
 #define TG_PLAIN(OT)                                                                                           \
     template <>                                                                                                \
-    hipError_t tg::launch_plain<2, OT>(const ProdArgs &p, const PlainEpi<OT> &e, hipStream_t s) {              \
-        return launch_prod_aligned<2>(p, e, s);                                                                \
-    }                                                                                                          \
-    template <>                                                                                                \
     hipError_t tg::launch_plain_two<2, OT>(const ProdArgs &p0, const PlainEpi<2> &e0, const ProdArgs &p1,      \
                                            const PlainEpi<OT> &e1, hipStream_t s) {                            \
         return launch_prod_two<2>(p0, e0, p1, e1, s);                                                          \

@@ -14,9 +14,8 @@ namespace tg {
 template <int T> hipError_t launch_glu(const ProdArgs &p, const GluEpi<T> &e, hipStream_t s);
 // OT: element type of D
 template <int OT> hipError_t launch_int8(const ProdArgs &p, const Int8Epi<OT> &e, hipStream_t s);
-// operands with rows on 16 bytes, whole K tiles of 128 bytes
-template <int T, int OT> hipError_t launch_plain(const ProdArgs &p, const PlainEpi<OT> &e, hipStream_t s);
-// two of them, in one launch where that is sooner
+// two products whose operands have rows on 16 bytes and whole K tiles of 128
+// bytes, in one launch where that is sooner; one whose D is NULL is left out
 template <int T, int OT>
 hipError_t launch_plain_two(const ProdArgs &p0, const PlainEpi<T> &e0, const ProdArgs &p1, const PlainEpi<OT> &e1,
                             hipStream_t s);

@@ -119,13 +119,13 @@ inline double prod_estimate(const ProdArgs &p) {
     return 1.41 * k * ((double)(t256 / 256) + (rest == 0 ? 0 : t256 < 256 || rest > 128 ? 1 : rest > 64 ? 0.75 : 0.5));
 }
 
-// Two such products.  One launch of 256 x 256 tiles, each product on a share of
-// the CUs, takes longer for a K tile (1.57 us in place of 1.41: two sets of
-// panels share the L2s), but leaves no CU idle in a last round and suits a
-// product with too few tiles for the GPU (gradients of 4096 x 6000 x 2048: 403
-// us, one after the other 478; 8192 x 1000 x 4096 267 and 296; 3000 x 2000 x 1504
-// 103 and 121; 8192 x 14336 x 4096, whose tiles fill whole rounds, 3281 and
-// 3043).
+// Two such products (D NULL: left out).  One launch of 256 x 256 tiles, each
+// product on a share of the CUs, takes longer for a K tile (1.57 us in place of
+// 1.41: two sets of panels share the L2s), but leaves no CU idle in a last round
+// and suits a product with too few tiles for the GPU (gradients of 4096 x 6000 x
+// 2048: 403 us, one after the other 478; 8192 x 1000 x 4096 267 and 296; 3000 x
+// 2000 x 1504 103 and 121; 8192 x 14336 x 4096, whose tiles fill whole rounds,
+// 3281 and 3043).
 template <int T, class Epi0, class Epi1>
 hipError_t launch_prod_two(const ProdArgs &p0, const Epi0 &e0, const ProdArgs &p1, const Epi1 &e1, hipStream_t s) {
     ProdPair q;
@@ -133,6 +133,22 @@ hipError_t launch_prod_two(const ProdArgs &p0, const Epi0 &e0, const ProdArgs &p
     q.p[1] = p1;
     q.split = 128;
     const int64_t k0 = (p0.KB + 127) / 128, k1 = (p1.KB + 127) / 128;
+    const int64_t few = tiles_of(p0, 64, 64) + tiles_of(p1, 64, 64);
+    // Small ones in 64 x 64 tiles: a launch less (gradients of 64 x 64 x 64 10.5
+    // us, 13.5 in two; 179 x 768 x 1768, 756 tiles of 24 and 3 K tiles, 18.0 and
+    // 22.8; 2 x 1792 x 189, 56 K tiles, 17.5 and 16.0).
+    if (few <= 1024 && k0 <= 32 && k1 <= 32) {
+        const unsigned n0 = prod_tiles(q.p[0], 64, 64), n1 = prod_tiles(q.p[1], 64, 64);
+        q.split = e0.D[0] ? (int)n0 : 0;
+        const dim3 grid(q.split + (e1.D[0] ? n1 : 0));
+        if (few <= 256)
+            hipLaunchKernelGGL((prod_mid_two_kernel<T, 64, 64, 4, 2, Epi0, Epi1>), grid, dim3(512), 0, s, q, e0, e1);
+        else
+            hipLaunchKernelGGL((prod_mid_two_kernel<T, 64, 64, 4, 1, Epi0, Epi1>), grid, dim3(256), 0, s, q, e0, e1);
+        return hipGetLastError();
+    }
+    if (!e0.D[0] || !e1.D[0])
+        return e0.D[0] ? launch_prod_aligned<T>(p0, e0, s) : launch_prod_aligned<T>(p1, e1, s);
     const int64_t a = prod_tiles(q.p[0], 256, 256), b = prod_tiles(q.p[1], 256, 256);
     int64_t best = INT64_MAX;                          // the share that lets the later one end soonest
     for (int n = 8; n < 256; n += 8) {

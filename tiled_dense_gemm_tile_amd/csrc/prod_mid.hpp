@@ -240,4 +240,20 @@ __global__ void __launch_bounds__(256 * KS) prod_mid_kernel(ProdArgs p, Epi e) {
     prod_mid_body<T, BM, BN, S, KS, PAIR, ANY>(p, tmi, tni, lds, e);
 }
 
+// Two products in one launch: the first on workgroups below `split`, the second
+// on the others, each with as many as it has tiles.
+template <int T, int BM, int BN, int S, int KS, class Epi0, class Epi1>
+__global__ void __launch_bounds__(256 * KS) prod_mid_two_kernel(ProdPair q, Epi0 e0, Epi1 e1) {
+    __shared__ __attribute__((aligned(1024))) char lds[kMidLds<BM, BN, S, KS>];
+    const bool second = (int)blockIdx.x >= q.split;
+    const ProdArgs p = second ? q.p[1] : q.p[0];
+    const int wg = second ? blockIdx.x - q.split : blockIdx.x;
+    int tmi, tni;
+    tile_order(wg, p.tiles_m * p.tiles_n, p.tiles_m, p.tiles_n, p.group_m, tmi, tni);
+    if (second)
+        prod_mid_body<T, BM, BN, S, KS, false, false>(p, tmi, tni, lds, e1);
+    else
+        prod_mid_body<T, BM, BN, S, KS, false, false>(p, tmi, tni, lds, e0);
+}
+
 }  // namespace tg
