@@ -1,0 +1,42 @@
+"""Edges of the feed-forward layer's operators that sizes and random inputs do
+not reach: scales next to the smallest one, infinite bounds, many tensors."""
+import pytest
+import torch
+
+import layersref as ref
+import tiled_dense_gemm_tile_amd as tg
+from layersref import DEV, KIND, rand
+
+pytestmark = pytest.mark.gpu
+
+BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+# ---- codes of rows whose scale is next to 2^-126 ----------------------------------------
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=KIND.get)
+@pytest.mark.parametrize("binade", [-128, -127, -126, -125, -124, -100])
+def test_quantize_codes_of_tiny_rows(binade, dtype):
+    """Elements at the codes' borders and their neighbours, in rows whose scale lies in [2^binade, 2^(binade + 1)): the
+    remainder at a border of a scale just over 2^-126 is below the least subnormal."""
+    g = torch.Generator(DEV).manual_seed(11)
+    top = ((torch.rand(200, 1, generator=g, device=DEV) + 1) * 127 * 2.0 ** binade).to(dtype).float()
+    scale = ref.quantize(top)[1].double()[:, None]
+    k = torch.arange(-126, 126, device=DEV, dtype=torch.float64) + 0.5
+    near = (k * scale).to(dtype)
+    steps = near.view(torch.int32 if dtype == F32 else torch.int16)
+    x = torch.cat([top.to(dtype), near, (steps + 1).view(dtype), (steps - 1).view(dtype)], 1)
+    # (a neighbour of a border past the row's largest number would change its scale)
+    x = torch.where(x.float().abs() <= top, x, torch.zeros_like(x))
+    q, s = tg.int8_quantize(x)
+    wq, ws = ref.quantize(x)
+    assert torch.equal(s, ws)
+    assert torch.equal(q, wq), "%d codes off" % int((q != wq).sum())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=KIND.get)
+def test_quantize_remainder_below_the_least_subnormal(dtype):
+    """A quotient of 63.5 - 3.4e-8, whose remainder is -2^-150: no tie."""
+    x = torch.tensor([[float.fromhex("0x1.bcp-119"), float.fromhex("0x1.bcp-120")]], device=DEV).to(dtype)
+    q, s = tg.int8_quantize(x)
+    assert q.tolist() == [[127, 63]] and torch.equal(s, ref.quantize(x)[1])

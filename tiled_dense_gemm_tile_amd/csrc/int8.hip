@@ -20,12 +20,14 @@ struct QuantArgs {
 
 // x / s rounded to nearest even, exactly: x * (1 / s) is off by 2^-16 at most
 // (three roundings of a number up to 127), so only within 2^-14 of a border the
-// remainder's sign decides.
+// remainder's sign decides.  It is a multiple of half of s's last place, so both
+// are scaled up first where that may be below the least subnormal, 2^-149.
 __device__ __forceinline__ int int8_code(float x, float s, float inv) {
     const float y = x * inv;
     float r = rintf(y);
     if (fabsf(y - r) > 0.5f - 0x1p-14f) {
-        const float h = floorf(y) + 0.5f, d = fmaf(-h, s, x);
+        const float up = s < 1.0f ? 0x1p24f : 1.0f;
+        const float h = floorf(y) + 0.5f, d = fmaf(-h, s * up, x * up);
         r = d > 0.0f ? h + 0.5f : d < 0.0f ? h - 0.5f : rintf(h);
     }
     return (int)r;
