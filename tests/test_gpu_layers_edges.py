@@ -40,3 +40,21 @@ def test_quantize_remainder_below_the_least_subnormal(dtype):
     x = torch.tensor([[float.fromhex("0x1.bcp-119"), float.fromhex("0x1.bcp-120")]], device=DEV).to(dtype)
     q, s = tg.int8_quantize(x)
     assert q.tolist() == [[127, 63]] and torch.equal(s, ref.quantize(x)[1])
+
+
+# ---- memory next to each other -----------------------------------------------------------
+
+def test_norm_next_to_the_gradients():
+    """Gradients that are views of each other, the norm between two of them, the workspace behind."""
+    room = tg.grad_workspace_bytes(3)
+    flat = rand(1, 1 << 18, dtype=F32)
+    grads, norm = [flat[:1001], flat[500:1001], flat[1002:30000]], flat[1001:1002]
+    want = torch.linalg.vector_norm(torch.cat(grads), dtype=torch.float64)
+    ws = flat[30016:].view(torch.uint8)[:room + 64]
+    ws = ws[-ws.data_ptr() % 256:][:room]
+    got = tg.grad_norm(grads, norm=norm, workspace=ws)
+    assert abs(float(got) - float(want)) <= 2.0 ** -23 * float(want)
+    for over in (dict(norm=flat[1000:1001]), dict(norm=ws[:4].view(F32), workspace=ws),
+                 dict(workspace=flat.view(torch.uint8)[:room])):
+        with pytest.raises(tg.GemmError):
+            tg.grad_norm(grads, **over)

@@ -1,0 +1,13 @@
+"""Edges of the feed-forward layer's operators on the CPU: memory that a call
+may not share, sizes next to the limits (no compute call is made)."""
+from test_layers_abi import MB, P, Q, UNSUPPORTED, grads
+
+import tiled_dense_gemm_tile_amd as tg
+
+
+def test_norm_and_workspace_apart_from_the_gradients():
+    """What grad_norm writes lies neither in a gradient nor in its workspace."""
+    room = tg.grad_workspace_bytes(2)
+    for over in (dict(norm=P), dict(norm=P + 16), dict(norm=P + MB + 76), dict(ws=P), dict(ws=P + MB), dict(at=(P, Q + MB + 64)),
+                 dict(at=(Q + MB + room - 4, P)), dict(norm=Q + MB), dict(norm=Q + MB + room - 4)):
+        assert grads(clip=False, **over) == UNSUPPORTED, over

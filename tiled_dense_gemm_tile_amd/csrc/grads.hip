@@ -233,6 +233,8 @@ struct Span {
     uintptr_t from, to;
     int64_t i;
 };
+Span span_of(const void *p, size_t bytes) { return {(uintptr_t)p, (uintptr_t)p + bytes, 0}; }
+
 gemm_status check_shared(int64_t n, const void *const *src, void *const *dst, const int64_t *sizes, const int *types,
                          std::initializer_list<Span> others) {
     constexpr int64_t kFew = 256;
@@ -264,6 +266,19 @@ gemm_status check_shared(int64_t n, const void *const *src, void *const *dst, co
     }
     for (const Span &o : others)
         if (o.from && hit(o.from, o.to)) return GEMM_ERR_UNSUPPORTED;
+    return GEMM_OK;
+}
+
+// Whether the norm or the workspace, which a call writes, shares memory with a
+// gradient or with the other.
+gemm_status check_written(int64_t n, const void *const *src, const int64_t *sizes, const int *types, Span norm, Span ws) {
+    auto meet = [](const Span &a, const Span &b) { return a.from && b.from && a.from < b.to && b.from < a.to; };
+    if (meet(norm, ws)) return GEMM_ERR_UNSUPPORTED;
+    for (int64_t i = 0; i < n; ++i) {
+        if (sizes[i] == 0) continue;
+        const Span g = span_of(src[i], (size_t)(sizes[i] * elem_size(types[i])));
+        if (meet(g, norm) || meet(g, ws)) return GEMM_ERR_UNSUPPORTED;
+    }
     return GEMM_OK;
 }
 
@@ -331,6 +346,8 @@ gemm_status grad_norm(int64_t n, const void *const *grads, const int64_t *sizes,
     if (!norm) return GEMM_ERR_NULL_POINTER;
     if (misaligned(norm, 4)) return GEMM_ERR_MISALIGNED;
     if ((st = check_room(n, workspace, workspace_bytes)) != GEMM_OK) return st;
+    st = check_written(n, grads, sizes, types, span_of(norm, 4), span_of(workspace, grad_workspace_bytes(n)));
+    if (st != GEMM_OK) return st;
     int parts;
     st = with_table(n, [&](auto most) {
         return squares<decltype(most)::value>(n, grads, sizes, types, (double *)workspace, &parts, stream);
