@@ -11,3 +11,15 @@ def test_norm_and_workspace_apart_from_the_gradients():
     for over in (dict(norm=P), dict(norm=P + 16), dict(norm=P + MB + 76), dict(ws=P), dict(ws=P + MB), dict(at=(P, Q + MB + 64)),
                  dict(at=(Q + MB + room - 4, P)), dict(norm=Q + MB), dict(norm=Q + MB + room - 4)):
         assert grads(clip=False, **over) == UNSUPPORTED, over
+
+
+def test_clip_writes_apart_from_what_it_reads():
+    """With results of their own: the norm and the workspace lie in no gradient either, and, in place too, not in each
+    other."""
+    room, apart = tg.grad_workspace_bytes(2), dict(out=(Q + 2 * MB, Q + 3 * MB))
+    for over in (dict(norm=P), dict(norm=P + 16), dict(norm=P + MB + 76), dict(ws=P), dict(ws=P + MB), dict(at=(P, Q + MB + 64)),
+                 dict(at=(Q + MB + room - 4, P)), dict(given=Q + 4 * MB, norm=P + 16), dict(given=Q + 4 * MB, norm=P + MB + 76)):
+        assert grads(**over, **apart) == UNSUPPORTED, over
+    for over in (dict(norm=Q + MB), dict(norm=Q + MB + room - 4)):
+        assert grads(**over) == UNSUPPORTED, over
+        assert grads(**over, **apart) == UNSUPPORTED, over

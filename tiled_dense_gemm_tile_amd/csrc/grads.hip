@@ -228,7 +228,8 @@ gemm_status squares(int64_t n, const void *const *src, const int64_t *sizes, con
 
 // Whether a result shares memory with another one, with a gradient that is not
 // its own, or with the call's other memory: results in the order of their
-// addresses, then each piece looked up among them.
+// addresses, then each piece looked up among them.  (What else is written:
+// check_written.)
 struct Span {
     uintptr_t from, to;
     int64_t i;
@@ -365,9 +366,9 @@ gemm_status grad_clip(int64_t n, const void *const *grads, void *const *out, con
     if (!(max_norm >= 0.0f)) return GEMM_ERR_UNSUPPORTED;
     if (!given && !norm) return GEMM_ERR_NULL_POINTER;
     if (misaligned(given, 4) || misaligned(norm, 4)) return GEMM_ERR_MISALIGNED;
-    const uintptr_t g = (uintptr_t)given, o = (uintptr_t)norm, w = given ? 0 : (uintptr_t)workspace;
-    st = check_shared(n, grads, out, sizes, types, {{g, g + 4, 0}, {o, o + 4, 0}, {w, w + grad_workspace_bytes(n), 0}});
-    if (st != GEMM_OK) return st;
+    const Span to = span_of(norm, 4), room = span_of(given ? nullptr : workspace, grad_workspace_bytes(n));
+    if ((st = check_shared(n, grads, out, sizes, types, {span_of(given, 4), to, room})) != GEMM_OK) return st;
+    if ((st = check_written(n, grads, sizes, types, to, room)) != GEMM_OK) return st;
     int parts = 0;
     if (!given) {
         if ((st = check_room(n, workspace, workspace_bytes)) != GEMM_OK) return st;
