@@ -151,10 +151,11 @@ gemm_status grad_norm(int64_t n, const void *const *grads, const int64_t *sizes,
  *   out: n tensors of the same sizes and types; out NULL or out[i] == grads[i]:
  *     in place, where a factor of 1 leaves them untouched.  No result shares
  *     memory with another or with another's gradient (GEMM_ERR_UNSUPPORTED).
- *   max_norm >= 0, not NaN (GEMM_ERR_UNSUPPORTED otherwise)
+ *   max_norm >= 0, not NaN (GEMM_ERR_UNSUPPORTED otherwise); infinite: the
+ *     factor is 1 for an infinite norm too
  *   Everything else as grad_norm; workspace is needed without `given` only.
- * A norm that is NaN makes every gradient NaN; an infinite one zeros (NaN for
- * infinities).
+ * A norm that is NaN makes every gradient NaN; an infinite one under a finite
+ * max_norm zeros (NaN for infinities).
  */
 gemm_status grad_clip(int64_t n, const void *const *grads, void *const *out, const int64_t *sizes, const int *types,
                       float max_norm, const float *given, float *norm, void *workspace, size_t workspace_bytes,

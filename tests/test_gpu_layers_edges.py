@@ -58,3 +58,25 @@ def test_norm_next_to_the_gradients():
                  dict(workspace=flat.view(torch.uint8)[:room])):
         with pytest.raises(tg.GemmError):
             tg.grad_norm(grads, **over)
+
+
+# ---- an infinite bound ------------------------------------------------------------------
+
+def test_clip_by_an_infinite_bound():
+    """The norm alone: gradients stay, whatever the norm is, unless that is a NaN."""
+    for bad, want in ((None, None), (float("inf"), "same"), (float("nan"), "nan")):
+        g = [rand(1, 9000, dtype=BF), rand(2, 70001, dtype=F32)]
+        if bad is not None:
+            g[1][69999] = bad
+        keep = [t.clone() for t in g]
+        out = [torch.full_like(t, 7) for t in g]
+        n = tg.clip_grads(g, float("inf"), out=out)
+        given = tg.clip_grads([t.clone() for t in g], float("inf"), given=n)
+        assert given is n and torch.equal(n, tg.grad_norm(g)) or want == "nan"
+        n2 = tg.clip_grads(g, float("inf"))
+        assert torch.equal(n, n2) or want == "nan"
+        for t, k, o in zip(g, keep, out):
+            if want == "nan":
+                assert bool(t.isnan().all()) and bool(o.isnan().all())
+            else:
+                assert torch.equal(t, k) and torch.equal(o, k)

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(256) grad_scale_kernel(GradTable<MOST> t, cons
     const float v = given ? *given : grad_total(part, parts, lds);
     if (norm && norm != given && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
     float by = max_norm / (v + 1e-6f);
-    by = by > 1.0f ? 1.0f : by;                        // (a NaN stays one)
+    by = by > 1.0f || (isinf(max_norm) && v == v) ? 1.0f : by;    // (a NaN stays one; inf / inf bounds nothing)
     const uint32_t chunks = t.first[t.count];
     for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
         const uint32_t c = chunks - 1 - k;

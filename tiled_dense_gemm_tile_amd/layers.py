@@ -300,7 +300,8 @@ def clip_grads(grads, max_norm, out=None, norm=None, given=None, workspace=None)
     gradients are, else of the same strides).  The norm is that
     of :func:`grad_norm`, computed here, or ``given``: one float32 on the GPU,
     such as a norm whose square the ranks have summed.  Returns the norm
-    (``given`` where it was).  No two gradients may share memory."""
+    (``given`` where it was).  An infinite ``max_norm`` leaves every gradient as
+    it is (unless the norm is NaN).  No two gradients may share memory."""
     grads = list(grads)
     dev, whole, at, sizes, types = _gradients("gradients", grads)
     if _twice(at, sizes):
