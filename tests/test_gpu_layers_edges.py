@@ -80,3 +80,39 @@ def test_clip_by_an_infinite_bound():
                 assert bool(t.isnan().all()) and bool(o.isnan().all())
             else:
                 assert torch.equal(t, k) and torch.equal(o, k)
+
+
+# ---- many tensors -----------------------------------------------------------------------
+
+def milliseconds(f, rounds=5):
+    f()
+    best = float("inf")
+    for _ in range(rounds):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+def test_clip_of_many_tensors_costs_its_parts():
+    """Thousands of tensors are scaled over many launches: the norm is computed once for all of them, so that the whole
+    call costs about what the norm and a scaling by a given norm do."""
+    n, size = 6000, 1 << 17
+    flat = rand(1, n * size, dtype=BF)
+    grads = [flat[i * size:(i + 1) * size] for i in range(n)]
+    out = torch.empty_like(flat)
+    outs = [out[i * size:(i + 1) * size] for i in range(n)]
+    norm = tg.grad_norm(grads)
+    whole = milliseconds(lambda: tg.clip_grads(grads, 1.0, out=outs))
+    parts = milliseconds(lambda: tg.grad_norm(grads)) + milliseconds(lambda: tg.clip_grads(grads, 1.0, out=outs, given=norm))
+    print("clip %.2f ms, its parts %.2f" % (whole, parts))
+    assert whole <= 1.5 * parts, "%.2f ms against %.2f" % (whole, parts)
+    want = torch.linalg.vector_norm(flat, dtype=torch.float64)
+    assert abs(float(norm) - float(want)) <= 2.0 ** -23 * float(want)
+    got = tg.clip_grads(grads, 1.0, out=outs)
+    assert torch.equal(got, norm)
+    by = torch.clamp(1.0 / (norm + 1e-6), max=1.0)
+    assert torch.equal(out, (flat.float() * by).to(BF))

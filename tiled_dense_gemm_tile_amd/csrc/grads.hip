@@ -7,9 +7,11 @@
 // tensors in its arguments (so that nothing is copied to the GPU and a captured
 // graph holds what it needs), cut into chunks of 32 KiB that a fixed
 // number of workgroups walks; each keeps its sum in fp64 and writes one partial
-// sum.  The scaling's workgroups add the partial sums for themselves, which
-// costs less than a launch between the two, and walk the chunks from the last
-// to the first: the last ones read are still in the caches.
+// sum.  The scaling's workgroups add up to kGradGroups partial sums for
+// themselves, which costs less than a launch between the two; more of them one
+// workgroup adds for all (each workgroup of each launch for itself: 6000 tensors
+// of 128 K bf16 3.4 ms, so 1.2).  The scaling walks the chunks from the last to
+// the first: the last ones read are still in the caches.
 #include <algorithm>
 #include <cstdlib>
 #include <initializer_list>
@@ -376,6 +378,11 @@ gemm_status grad_clip(int64_t n, const void *const *grads, void *const *out, con
             return squares<decltype(most)::value>(n, grads, sizes, types, (double *)workspace, &parts, stream);
         });
         if (st != GEMM_OK) return st;
+    }
+    if (parts > tg::kGradGroups) {
+        hipLaunchKernelGGL(tg::grad_norm_kernel, dim3(1), dim3(256), 0, stream, (const double *)workspace, parts, norm);
+        if ((st = launched(hipGetLastError())) != GEMM_OK) return st;
+        given = norm;
     }
     return with_table(n, [&](auto most) {
         return scale<decltype(most)::value>(n, grads, out, sizes, types, max_norm, given, norm, (const double *)workspace,
