@@ -6,6 +6,7 @@ import torch
 import layersref as ref
 import tiled_dense_gemm_tile_amd as tg
 from layersref import DEV, KIND, rand
+from tiled_dense_gemm_tile_amd import layers, ops
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +117,38 @@ def test_clip_of_many_tensors_costs_its_parts():
     assert torch.equal(got, norm)
     by = torch.clamp(1.0 / (norm + 1e-6), max=1.0)
     assert torch.equal(out, (flat.float() * by).to(BF))
+
+
+# ---- the binding without its part in C++ ---------------------------------------------------
+
+@pytest.fixture
+def plain_binding(monkeypatch):
+    monkeypatch.setattr(ops, "_fast", None)
+    monkeypatch.setattr(layers, "_fast", None)
+    monkeypatch.setattr(layers, "_entries", {})
+
+
+def every_operator():
+    x, wg, wu, dh = rand(1, 40, 72), rand(2, 56, 72), rand(3, 56, 72), rand(4, 40, 56)
+    h, g, u = tg.gemm_glu(x, wg, wu, keep=True)
+    odd = tg.gemm_glu(x[:, 1:], wg[:, 1:], wu[:, 1:], act="relu", workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+    dx, dwg, dwu = tg.gemm_glu_backward(dh, g, u, x, wg, wu, grad_dtype=F32)
+    q, s = tg.int8_quantize(x)
+    wq, ws = tg.int8_quantize(wg)
+    d, b = tg.gemm_int8(q, s, wq, ws, C=dh, out_dtype=BF), tg.gemm_int8(q, s, wq, ws, C=torch.ones(56, device=DEV))
+    norm = tg.grad_norm([dwg, dwu.t(), dx])
+    outs = [torch.empty_like(dwg), torch.empty_like(dwu), torch.empty_like(dx)]
+    n2 = tg.clip_grads([dwg, dwu, dx], 0.5, out=outs)
+    n3 = tg.clip_grads([dwg, dwu.t()], 0.5, given=norm)
+    y = tg.rmsnorm(x, rand(5, 72), 1e-5)
+    return [h, g, u, odd, dx, dwg, dwu, q, s, wq, ws, d, b, norm, n2, n3, *outs, *y]
+
+
+def test_operators_through_ctypes(plain_binding, request):
+    got = every_operator()
+    with pytest.raises(ValueError):
+        tg.gemm_glu(rand(1, 4, 8), rand(2, 4, 9), rand(3, 4, 8))
+    assert all(isinstance(f, type(layers._load().gemm_glu)) for f in layers._entries.values())
+    request.getfixturevalue("monkeypatch").undo()
+    for a, b in zip(got, every_operator()):
+        assert torch.equal(a, b)
