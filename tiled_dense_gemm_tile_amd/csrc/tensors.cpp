@@ -6,6 +6,7 @@
 //
 // Checks say yes or no: where one fails, or torch throws, the function returns
 // None, and the Python form of the same check raises the error that names it.
+// An error that Python code raised below is passed on.
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -39,6 +40,7 @@ PyObject *or_none(F &&f) {
     try {
         return f();
     } catch (...) {
+        if (PyErr_Occurred()) return nullptr;          // (thrown by Python code that torch called)
         Py_RETURN_NONE;
     }
 }
