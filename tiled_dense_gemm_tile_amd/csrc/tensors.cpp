@@ -83,6 +83,13 @@ PyObject *vector(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return or_none([&] { return checked_vector(a, n); });
 }
 
+// Without the interpreter's lock, as torch's own functions run: an allocation
+// may wait for the GPU.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // empty(length or shape, dtype, device index) -> tensor
 PyObject *checked_empty(PyObject *const *a, Py_ssize_t n) {
     if (n != 3 || !THPDtype_Check(a[1])) Py_RETURN_NONE;
@@ -97,8 +104,13 @@ PyObject *checked_empty(PyObject *const *a, Py_ssize_t n) {
     }
     const long long dev = PyLong_AsLongLong(a[2]);
     if (PyErr_Occurred()) return nullptr;
-    return THPVariable_Wrap(at::empty(c10::IntArrayRef(size, dims),
-                                      at::TensorOptions(((THPDtype *)a[1])->scalar_type).device(at::kCUDA, (int8_t)dev)));
+    const auto options = at::TensorOptions(((THPDtype *)a[1])->scalar_type).device(at::kCUDA, (int8_t)dev);
+    at::Tensor t;
+    {
+        Unlocked u;
+        t = at::empty(c10::IntArrayRef(size, dims), options);
+    }
+    return THPVariable_Wrap(std::move(t));
 }
 
 PyObject *empty(PyObject *, PyObject *const *a, Py_ssize_t n) {
