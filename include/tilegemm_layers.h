@@ -16,7 +16,8 @@
  * dimensions count elements; matrices are row-major; pointers are aligned to
  * their element size (GEMM_ERR_MISALIGNED) and need no more than that, though
  * operands whose rows start on 16 bytes run faster.  Sizes are below 2^31 and
- * leading dimensions below 8 MiB in bytes (GEMM_ERR_UNSUPPORTED).  Outputs and
+ * leading dimensions below 8 MiB in bytes, but for int8_quantize's
+ * (GEMM_ERR_UNSUPPORTED).  Outputs and
  * workspaces overlap neither inputs nor each other (GEMM_ERR_UNSUPPORTED)
  * unless a call says so: an input's piece of memory, from its first element to
  * its last, holds no result.  Results of one leading dimension may lie row by
@@ -68,7 +69,8 @@ size_t gemm_glu_workspace_bytes(int64_t M, int64_t F, int64_t K);
  *     dg = dH * u * act'(g)      du = dH * act(g)
  *     dX = dg.Wg + du.Wu         dWg = Cg + dg^T.X      dWu = Cu + du^T.X
  * dg and du are computed in fp32 from the kept G and U and rounded to `type`
- * (the products' operands); the products are summed in fp32.  relu'(0) = 0.
+ * (the products' operands): in fp16 past 65504 they are infinities, below 2^-14
+ * multiples of 2^-24.  The products are summed in fp32.  relu'(0) = 0.
  *   dH, G, U: M x F, X: M x K, Wg, Wu: F x K of `type` as in gemm_glu
  *   dX: M x K of `type`, or NULL: not computed (Wg and Wu are not read)
  *   dWg, dWu: F x K of grad_type, which is `type` or GEMM_TYPE_F32
@@ -80,7 +82,9 @@ size_t gemm_glu_workspace_bytes(int64_t M, int64_t F, int64_t K);
  *     (GEMM_ERR_WORKSPACE): dg and du, and copies of X and the weights, rows
  *     laid along the sums.  Calls sharing it must be ordered.  Its contents
  *     need no initialisation.
- * M < 2^21 and F < 2^20.  M == 0: dWg = Cg and dWu = Cu, or zeros.
+ * M < 2^21, F < 2^20, and m f + (m + 2 f) k < 2^24, where m, f, k are M, F, K
+ * divided by 64 and rounded up (GEMM_ERR_UNSUPPORTED).  M == 0: dWg = Cg and dWu
+ * = Cu, or zeros.
  */
 gemm_status gemm_glu_backward(int64_t M, int64_t F, int64_t K, const void *dH, int64_t lddh, const void *G,
                               int64_t ldg, const void *U, int64_t ldu, const void *X, int64_t ldx, const void *Wg,

@@ -152,3 +152,21 @@ def test_operators_through_ctypes(plain_binding, request):
     request.getfixturevalue("monkeypatch").undo()
     for a, b in zip(got, every_operator()):
         assert torch.equal(a, b)
+
+
+# ---- the range of the gated block's inner gradients ---------------------------------------
+
+def test_glu_backward_range_of_fp16():
+    """dg and du as the products' operands, rounded to fp16: 300 x 300 is an infinity, 2^-13 x 1.5 2^-12 rounds to 2^-24
+    (du there is 0: act(g) = 2^-14 and dh 2^-13); bf16 holds both."""
+    for dtype, big, small in ((FP, float("inf"), 2.0 ** -24), (BF, 300.0 * 300.0, 1.5 * 2.0 ** -25)):
+        one = torch.ones(1, 1, device=DEV, dtype=dtype)
+        zero = 0 * one
+        dx, dwg, _ = tg.gemm_glu_backward(300 * one, one, 300 * one, one, one, zero, act="relu", grad_dtype=F32)
+        if dtype == FP:
+            assert float(dwg) == big
+        else:
+            assert abs(float(dwg) / big - 1) <= 2.0 ** -8
+        _, dwg, dwu = tg.gemm_glu_backward(2.0 ** -13 * one, 2.0 ** -14 * one, 1.5 * 2.0 ** -12 * one, one, one, zero, act="relu",
+                                           grad_dtype=F32)
+        assert float(dwg) == small and (float(dwu) == 0 if dtype == FP else float(dwu) == 2.0 ** -27)

@@ -114,7 +114,9 @@ def gemm_glu_backward(dH, G, U, X, Wg, Wu, act="silu", Cg=None, Cu=None, dX=None
     the G and U that it kept: dX (M, K) of X's type, dWg and dWu (F, K) of
     ``grad_dtype`` (X's type, the default, or float32), Cg and Cu of that type
     added to them (both or neither; Cg may be dWg and Cu dWu: gradients
-    accumulated in place).  ``input_grad=False`` / ``weight_grad=False``: not
+    accumulated in place).  The gradients of G and U, the products' operands, are
+    rounded to X's type: scale the loss so that float16 holds them.
+    ``input_grad=False`` / ``weight_grad=False``: not
     computed, returned as None.  ``workspace``: a device byte tensor of at
     least :func:`gemm_glu_backward_workspace_bytes` bytes, 256-byte aligned
     (allocated per call when not given).  Returns (dX, dWg, dWu)."""
