@@ -77,7 +77,8 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
     constexpr int BM = 32 * TM;
     constexpr int BN = PAIR ? 16 * TN : 32 * TN;       // result columns of a tile
     constexpr int W = BN / 2, STAGE = 16 * kStagePitch<W> * 4;
-    constexpr int PF = NS + 1;                         // K tiles ahead
+    // K tile t brings the lines of tile t + PF; NS - 2 tiles' come ahead of the loop, behind tile PF0
+    constexpr int PF = NS + 1, PF0 = PF - (NS - 2) - 1;
     static_assert((TM == 8 && TN == 8) || TN == 4, "schedule");
     static_assert(2 * STAGE <= B_SLOT && 2 * STAGE <= SLOT && kW4Lds<TM, TN> == B_BASE + NS * B_SLOT + 1024, "LDS");
 
@@ -204,8 +205,8 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
         barrier();
     };
 
-    // (in the order of the loop: K tile t's lines behind the loads of t + NS - 1)
-    pfk = (k_first + 2 * 128) % (nt * 128);
+    // (in the order of the loop: a K tile's lines behind the loads of another)
+    pfk = (k_first + PF0 * 128) % (nt * 128);
     static_for<0, NS - 1>([&](auto t) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < TM; ++j) fetch_a(t, t, j);
@@ -248,7 +249,7 @@ __device__ __forceinline__ void prod_w4_body(const ProdArgs &p, int wg, int nwg,
             pfo = pf_off();
             int wv = wave;                             // (their LDS addresses are computed here, not held)
             asm volatile("" : "+s"(wv));
-            pfk = (k_first + 2 * 128) % (nt * 128);
+            pfk = (k_first + PF0 * 128) % (nt * 128);
             static_for<0, NS - 1>([&](auto t) __attribute__((always_inline)) {
                 const int k0 = koff(t);
                 const uint32_t va = k0 + kc < KB ? aoff + k0 : kOOB, vb = k0 + kc < KB ? boff + k0 : kOOB;
