@@ -210,8 +210,8 @@ __device__ __forceinline__ void stage_fence() {
 // block(), which computes and stores the results.  C's rows are loaded two blocks of 16 ahead, and nothing else is loaded
 // between a tile's stores: a load there waits for the stores before it (with
 // C's rows loaded where they are added, int8 8192 x 14336 x 4096 took 492 us, 390
-// so, and 370 without C; gradients of 4096 x 6000 x 2048 added in place in fp32
-// 490 and 418).
+// to 414 so, and 354 to 372 without C; gradients of 4096 x 6000 x 2048 added in
+// place in fp32 490 and 418 to 430).
 // (32-bit rows of 128 columns: 32 registers a block)
 template <int OT> constexpr int kAheadC = OT == 0 ? 1 : 2;
 

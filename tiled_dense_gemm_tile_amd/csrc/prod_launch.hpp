@@ -30,8 +30,9 @@ hipError_t go_mid(ProdArgs p, const Epi &e, hipStream_t s) {
 // 256 x 256 tiles in whole rounds of one a CU; what is left of up to half a
 // round in 128 x 128 tiles (four times as many: weight gradients of 8192 x 8256
 // x 4096, 16 tiles past four rounds, 973 -> 917 us).  8-bit operands without the
-// lines brought ahead (8192 x 14336 x 4096 359 us, with them 364; the gated
-// block 1356 without, 1348 with).
+// lines brought ahead (8192 x 14336 x 4096 359 us, with them 364: more than two
+// runs in turn differ, less than two boxes; the gradients' products gain, 3280 ->
+// 3020, the gated block neither way, 1356 without, 1348 with).
 template <int T, bool PAIR, class Epi>
 hipError_t go_w4(ProdArgs p, const Epi &e, hipStream_t s) {
     const unsigned tiles = prod_tiles(p, 256, PAIR ? 128 : 256), cus = 256, rest = tiles % cus;
@@ -59,8 +60,10 @@ hipError_t go_w4_once(ProdArgs p, const Epi &e, hipStream_t s) {
 }
 
 // Tiles by how many of them there are (a K tile's loads bound a workgroup, 31
-// to 44 bytes a clock and CU, until all CUs have work; times in us, weights
-// that no cache holds, int8 M x N x K or the gated block's M x F x K in bf16).
+// to 44 bytes a clock and CU, until all CUs have work; times in us, int8 M x N x
+// K or the gated block's M x F x K in bf16, of weights that no cache holds; F
+// 14336: of one set, which the Infinity Cache keeps.  From HBM 64 rows take 51,
+// 128 55, 256 73, 512 101).
 template <int T, bool PAIR, bool ANY, class Epi>
 hipError_t launch_prod_tiles(const ProdArgs &p, const Epi &e, hipStream_t s) {
     constexpr int D = PAIR ? 2 : 1;                    // a tile's columns of B for one of the results

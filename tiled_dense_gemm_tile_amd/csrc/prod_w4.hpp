@@ -14,9 +14,10 @@
 // slots K tile 0 always uses, and then the finished tile's results are staged
 // and stored from the last slots.
 //
-// A K tile takes 1.37 to 1.41 us (MFMAs busy 71 to 83 % of the cycles; LDS three
-// quarters of them): int8 8192^3 2.95 POP/s, bf16 8192 x 4096 x 28672 1.57
-// PFLOP/s.
+// A K tile takes 1.37 to 1.41 us (MFMAs busy 71 to 83 % of the cycles, 61 % where
+// K is short for the results, int8 8192 x 14336 x 4096; LDS three quarters of
+// them): int8 8192^3 373 to 407 us, 2.7 to 2.95 POP/s, bf16 8192 x 4096 x 28672
+// 1.57 PFLOP/s.
 //
 // Grids of one round at most run the same schedule in tiles of 256 x 128 and 128
 // x 128 (TN 4; TM 8 and 4) with three and four slots: a K tile's MFMAs take half
