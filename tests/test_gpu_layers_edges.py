@@ -170,3 +170,39 @@ def test_glu_backward_range_of_fp16():
         _, dwg, dwu = tg.gemm_glu_backward(2.0 ** -13 * one, 2.0 ** -14 * one, 1.5 * 2.0 ** -12 * one, one, one, zero, act="relu",
                                            grad_dtype=F32)
         assert float(dwg) == small and (float(dwu) == 0 if dtype == FP else float(dwu) == 2.0 ** -27)
+
+
+def test_clip_over_several_launches_captured():
+    """The norm of several launches, added up once, in a graph: replays with new gradients give what the eager call
+    gives, in place and into other tensors."""
+    n, size = 140, 300001
+    flat = torch.zeros(n * size, dtype=BF, device=DEV)
+    grads = [flat[i * size:(i + 1) * size] for i in range(n)]
+    out, norm, norm2 = torch.zeros_like(flat), torch.zeros((), device=DEV), torch.zeros((), device=DEV)
+    outs = [out[i * size:(i + 1) * size] for i in range(n)]
+    ws = torch.empty(tg.grad_workspace_bytes(n), dtype=torch.uint8, device=DEV)
+
+    def step():
+        tg.clip_grads(grads, 0.75, out=outs, norm=norm, workspace=ws)
+        tg.clip_grads(grads, 0.75, norm=norm2)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        new = rand(i, n * size, scale=i + 1)
+        flat.copy_(new)
+        graph.replay()
+        again = new.clone()
+        want = tg.clip_grads([again[k * size:(k + 1) * size] for k in range(n)], 0.75)
+        torch.cuda.synchronize()
+        assert torch.equal(norm, want) and torch.equal(norm2, want), "replay %d" % i
+        assert torch.equal(flat, again) and torch.equal(out, again), "replay %d" % i
+        by = torch.clamp(0.75 / (want + 1e-6), max=1.0)
+        assert torch.equal(out, (new.float() * by).to(BF))
+        assert abs(float(want) / float(torch.linalg.vector_norm(new, dtype=torch.float64)) - 1) <= 2.0 ** -23

@@ -31,7 +31,7 @@ hipError_t go_mid(ProdArgs p, const Epi &e, hipStream_t s) {
 // round in 128 x 128 tiles (four times as many: weight gradients of 8192 x 8256
 // x 4096, 16 tiles past four rounds, 973 -> 917 us).  8-bit operands without the
 // lines brought ahead (8192 x 14336 x 4096 359 us, with them 364: more than two
-// runs in turn differ, less than two boxes; the gradients' products gain, 3280 ->
+// runs in turn differ, less than two cards; the gradients' products gain, 3280 ->
 // 3020, the gated block neither way, 1356 without, 1348 with).
 template <int T, bool PAIR, class Epi>
 hipError_t go_w4(ProdArgs p, const Epi &e, hipStream_t s) {
