@@ -114,7 +114,7 @@ hipError_t launch_prod_aligned(const ProdArgs &p, const Epi &e, hipStream_t s) {
 }
 
 // About how long such a product takes by itself, in us: enough to tell which of
-// launch_prod_two's forms ends sooner (84 sizes of 600 to 8192: the one taken was
+// launch_prod_two's forms ends sooner (81 sizes of 600 to 8192: the one taken was
 // never 3 % behind the other).
 inline double prod_estimate(const ProdArgs &p) {
     const double k = (p.KB + 127) / 128;
